@@ -22,6 +22,14 @@ bool diag_h_fits(int64_t Tk, int I) { return g_diag_h == nullptr || g_diag_h_byt
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// elements a row stride is a multiple of, so that every row starts 16-byte aligned
+int row_unit(int in_dtype) { return in_dtype == MX_IN_BF16 ? 8 : 4; }
+
+// alignment of scale rows of K elements: dwords where every row is whole dwords, else bytes
+uintptr_t scale_unit(int K) { return K % 128 == 0 ? 4 : 1; }
+
+constexpr int64_t MAX_CHUNKS = int64_t(1) << 38;  // 8-element chunks of one call: 2^30 workgroups of 256 threads
+
 mx_status from_hip(hipError_t e) { return e == hipSuccess ? MX_OK : MX_EHIP; }
 
 }  // namespace
@@ -332,6 +340,112 @@ mx_status moe_shared_expert(const uint8_t* x, const uint8_t* x_sc, int T, int H,
   const char* v = "";
   const hipError_t e = mx::launch_shared_expert(x, x_sc, T, H, w13, w13_sc, w2, w2_sc, I, y, ws,
                                                 static_cast<hipStream_t>(stream), &v);
+  if (e == hipSuccess) g_variant = v;
+  return from_hip(e);
+}
+
+mx_status mx_dequantize(const uint8_t* q, const uint8_t* sc, int fmt, int64_t rows, int64_t cols, void* out,
+                        int out_dtype, void* stream) {
+  if (rows < 0 || cols < 0 || cols % 32 != 0) return MX_EINVAL;
+  if (fmt != MX_FMT_E4M3 && fmt != MX_FMT_E2M1) return MX_EINVAL;
+  if (out_dtype != MX_OUT_BF16 && out_dtype != MX_OUT_F32) return MX_EINVAL;
+  if (rows == 0 || cols == 0) { g_variant = "dequantize:empty"; return MX_OK; }
+  if (!q || !sc || !out) return MX_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16)) return MX_EINVAL;
+  if (cols / 8 > MAX_CHUNKS / rows) return MX_EUNSUPPORTED;
+  const hipError_t e = mx::launch_dequantize(q, sc, fmt == MX_FMT_E2M1, rows, cols, out, out_dtype == MX_OUT_BF16,
+                                             static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = fmt == MX_FMT_E2M1 ? "dequantize:e2m1_block32" : "dequantize:e4m3_block32";
+  return from_hip(e);
+}
+
+mx_status mx_swiglu_quantize(const void* gu, int in_dtype, int64_t gu_ld, int64_t T, int I, int fmt, uint8_t* q,
+                             uint8_t* sc, void* stream) {
+  if (T < 0 || I < 32 || I % 32 != 0) return MX_EINVAL;
+  if (in_dtype != MX_IN_F32 && in_dtype != MX_IN_BF16) return MX_EINVAL;
+  if (fmt != MX_FMT_E4M3 && fmt != MX_FMT_E2M1) return MX_EINVAL;
+  if (gu_ld < 2 * (int64_t)I || gu_ld % row_unit(in_dtype) != 0) return MX_EINVAL;
+  if (T == 0) { g_variant = "swiglu_quantize:empty"; return MX_OK; }
+  if (!gu || !q || !sc) return MX_EINVAL;
+  if (!aligned(gu, 16) || !aligned(q, 16)) return MX_EINVAL;
+  if (I / 8 > MAX_CHUNKS / T || gu_ld > (int64_t(1) << 60) / T) return MX_EUNSUPPORTED;
+  const hipError_t e = mx::launch_swiglu_quantize(gu, in_dtype == MX_IN_BF16, gu_ld, T, I, fmt == MX_FMT_E2M1, q, sc,
+                                                  static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = fmt == MX_FMT_E2M1 ? "swiglu_quantize:e2m1_block32" : "swiglu_quantize:e4m3_block32";
+  return from_hip(e);
+}
+
+mx_status mx_add_rmsnorm(const void* x, const void* x2, int x_dtype, int64_t x_ld, const void* residual, void* h,
+                         int res_dtype, int64_t res_ld, const void* weight, int w_dtype, int T, int H, float eps,
+                         uint16_t* n, uint8_t* q, uint8_t* sc, int fmt, void* stream) {
+  if (T < 0 || H < 32 || H % 32 != 0) return MX_EINVAL;
+  const bool res = residual != nullptr || h != nullptr;
+  if (x_dtype != MX_IN_F32 && x_dtype != MX_IN_BF16) return MX_EINVAL;
+  if (res && res_dtype != MX_IN_F32 && res_dtype != MX_IN_BF16) return MX_EINVAL;
+  if (weight && w_dtype != MX_IN_F32 && w_dtype != MX_IN_BF16) return MX_EINVAL;
+  if (q && fmt != MX_FMT_E4M3 && fmt != MX_FMT_E2M1) return MX_EINVAL;
+  if (!(eps > 0.0f) || eps > 3.0e38f) return MX_EINVAL;                    // eps = 0 would make a zero row NaN
+  if (x_ld < H || x_ld % row_unit(x_dtype) != 0) return MX_EINVAL;
+  if (res && (res_ld < H || res_ld % row_unit(res_dtype) != 0)) return MX_EINVAL;
+  if (H > mx::NORM_MAX_H) return MX_EUNSUPPORTED;
+  if (T == 0) { g_variant = "add_rmsnorm:empty"; return MX_OK; }
+  if (x_ld > (int64_t(1) << 60) / T || (res && res_ld > (int64_t(1) << 60) / T)) return MX_EUNSUPPORTED;
+  if (!x || (!h && !n && !q) || (q == nullptr) != (sc == nullptr)) return MX_EINVAL;
+  if (!aligned(x, 16) || !aligned(x2, 16) || !aligned(residual, 16) || !aligned(h, 16) || !aligned(weight, 16) ||
+      !aligned(n, 16) || !aligned(q, 16))
+    return MX_EINVAL;
+  const mx::NormArgs a{x, x2, x_ld, x_dtype == MX_IN_BF16, residual, h, res_ld, res && res_dtype == MX_IN_BF16,
+                       weight, w_dtype == MX_IN_BF16, n, q, sc, fmt == MX_FMT_E2M1, H, eps};
+  const hipError_t e = mx::launch_add_rmsnorm(a, T, static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = "add_rmsnorm:row";
+  return from_hip(e);
+}
+
+mx_status fp4_block_gemm(const uint8_t* a, const uint8_t* a_sc, int a_fmt, const uint8_t* w, const uint8_t* w_sc,
+                         int M, int N, int K, void* y, int y_dtype, void* stream) {
+  if (M < 0 || N < 1 || K < 32 || K % 32 != 0) return MX_EINVAL;
+  if (a_fmt != MX_FMT_E4M3 && a_fmt != MX_FMT_E2M1) return MX_EINVAL;
+  if (y_dtype != MX_OUT_BF16 && y_dtype != MX_OUT_F32) return MX_EINVAL;
+  if (K > mx::FP4_MAX_K || (int64_t)M * N >= (int64_t(1) << 40)) return MX_EUNSUPPORTED;
+  if (!w || !w_sc || (M > 0 && (!a || !a_sc || !y))) return MX_EINVAL;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 4)) return MX_EINVAL;
+  if (!aligned(a_sc, scale_unit(K)) || !aligned(w_sc, scale_unit(K))) return MX_EINVAL;
+  if (M == 0) { g_variant = "fp4:empty"; return MX_OK; }
+  const char* v = "";
+  const hipError_t e = mx::launch_fp4_gemm(a, a_sc, a_fmt == MX_FMT_E2M1, w, w_sc, M, N, K, y, y_dtype == MX_OUT_BF16,
+                                           static_cast<hipStream_t>(stream), &v);
+  if (e == hipSuccess) g_variant = v;
+  return from_hip(e);
+}
+
+namespace {
+bool fp4_ffn_shape(int T, int H, int I, int mid_fmt) {
+  return T >= 0 && H >= 32 && I >= 32 && H % 32 == 0 && I % 32 == 0 && (mid_fmt == MX_FMT_E4M3 || mid_fmt == MX_FMT_E2M1);
+}
+}  // namespace
+
+size_t fp4_dense_ffn_workspace_bytes(int T, int H, int I, int mid_fmt) {
+  if (!fp4_ffn_shape(T, H, I, mid_fmt)) return 0;
+  return mx::fp4_ffn_ws_bytes(T, H, I, mid_fmt == MX_FMT_E2M1);
+}
+
+mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T, int H, const uint8_t* w13,
+                        const uint8_t* w13_sc, const uint8_t* w2, const uint8_t* w2_sc, int I, int mid_fmt, void* y,
+                        int y_dtype, void* ws, size_t ws_bytes, void* stream) {
+  if (!fp4_ffn_shape(T, H, I, mid_fmt) || (x_fmt != MX_FMT_E4M3 && x_fmt != MX_FMT_E2M1)) return MX_EINVAL;
+  if (y_dtype != MX_OUT_BF16 && y_dtype != MX_OUT_F32) return MX_EINVAL;
+  if (H > mx::FP4_MAX_K || I > mx::FP4_MAX_K || (int64_t)T * 2 * I >= (int64_t(1) << 40) ||
+      (int64_t)T * H >= (int64_t(1) << 40))
+    return MX_EUNSUPPORTED;
+  if (!w13 || !w13_sc || !w2 || !w2_sc || (T > 0 && (!x || !x_sc || !y))) return MX_EINVAL;
+  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(y, 4) || !aligned(ws, 256)) return MX_EINVAL;
+  if (!aligned(x_sc, scale_unit(H)) || !aligned(w13_sc, scale_unit(H)) || !aligned(w2_sc, scale_unit(I))) return MX_EINVAL;
+  if (T == 0) { g_variant = "fp4_ffn:empty"; return MX_OK; }
+  if (!ws || ws_bytes < mx::fp4_ffn_ws_bytes(T, H, I, mid_fmt == MX_FMT_E2M1)) return MX_EWORKSPACE;
+  const char* v = "";
+  const hipError_t e = mx::launch_fp4_ffn(x, x_sc, x_fmt == MX_FMT_E2M1, T, H, w13, w13_sc, w2, w2_sc, I,
+                                          mid_fmt == MX_FMT_E2M1, y, y_dtype == MX_OUT_BF16, ws,
+                                          static_cast<hipStream_t>(stream), &v);
   if (e == hipSuccess) g_variant = v;
   return from_hip(e);
 }

@@ -222,4 +222,73 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// ---------------------------------------------------------------------------
+// Rows in chunks of 8 consecutive elements per lane: four neighbouring lanes
+// (a quad) hold one block of 32.
+
+// 8 fp32 or bf16 elements from element i on (i % 8 == 0, 16-byte aligned).
+__device__ __forceinline__ void load8(const void* p, bool bf16, int64_t i, float* v) {
+  if (bf16) {
+    const u32x4 d = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(d[j] << 16);
+      v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
+    }
+  } else {
+    const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const u32x4 d = s[q];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * q + j] = __uint_as_float(d[j]);
+    }
+  }
+}
+
+__device__ __forceinline__ void store8(void* p, bool bf16, int64_t i, const float* v) {
+  if (bf16) {
+    u32x4 d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      d[j] = (uint32_t)f32_to_bf16_rne(v[2 * j]) | ((uint32_t)f32_to_bf16_rne(v[2 * j + 1]) << 16);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = d;
+  } else {
+    u32x4* d = reinterpret_cast<u32x4*>(static_cast<float*>(p) + i);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      d[q] = u32x4{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                   __float_as_uint(v[4 * q + 3])};
+  }
+}
+
+// Maximum over a quad (lanes 4 r .. 4 r + 3), in registers.
+__device__ __forceinline__ float quad_max(float m) {
+  m = fmaxf(m, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(m), 0xB1, 0xF, 0xF, false)));   // quad [1,0,3,2]
+  m = fmaxf(m, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(m), 0x4E, 0xF, 0xF, false)));   // quad [2,3,0,1]
+  return m;
+}
+
+// Codes of this lane's chunk of a block-32 row (all four lanes of its quad
+// active): chunk number `chunk` of the code array (8 or 4 bytes each), and
+// one scale byte per quad.
+__device__ __forceinline__ void store8_codes(bool fp4, const float* v, uint8_t* q, uint8_t* sc, int64_t chunk) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, __builtin_fabsf(v[j]));
+  const uint32_t s = e8m0_code_for_amax(quad_max(amax), fp4 ? 2 : 8);
+  if (fp4) {
+    uint32_t d = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d |= encode_e2m1(v[j], s) << (4 * j);
+    *reinterpret_cast<uint32_t*>(q + chunk * 4) = d;
+  } else {
+    uint2 d;
+    d.x = requant2_e4m3(v[0], v[1], s) | (requant2_e4m3(v[2], v[3], s) << 16);
+    d.y = requant2_e4m3(v[4], v[5], s) | (requant2_e4m3(v[6], v[7], s) << 16);
+    *reinterpret_cast<uint2*>(q + chunk * 8) = d;
+  }
+  if ((chunk & 3) == 0) sc[chunk >> 2] = (uint8_t)s;
+}
+
 }  // namespace mx

@@ -20,6 +20,30 @@ constexpr int KPART_MAX_SHARED1 = 1024; // one-row shared expert: its down proje
 hipError_t launch_quantize(const void* src, bool bf16, int64_t rows, int64_t cols, bool fp4,
                            uint8_t* q, uint8_t* sc, hipStream_t stream);
 
+hipError_t launch_dequantize(const uint8_t* q, const uint8_t* sc, bool fp4, int64_t rows, int64_t cols, void* out,
+                             bool bf16, hipStream_t stream);
+hipError_t launch_swiglu_quantize(const void* gu, bool bf16, int64_t ld, int64_t T, int I, bool fp4, uint8_t* q,
+                                  uint8_t* sc, hipStream_t stream);
+
+constexpr int NORM_MAX_H = 16384;
+struct NormArgs {                                 // strides in elements; x2, residual, w, h, n, q (with sc) may be NULL
+  const void* x; const void* x2; int64_t x_ld; bool x_bf16;
+  const void* residual; void* h; int64_t r_ld; bool r_bf16;
+  const void* w; bool w_bf16;
+  uint16_t* n; uint8_t* q; uint8_t* sc; bool fp4;
+  int H; float eps;
+};
+hipError_t launch_add_rmsnorm(const NormArgs& a, int T, hipStream_t stream);
+
+// products with FP4 weights; a is E4M3 (fp4a false) or E2M1
+constexpr int FP4_MAX_K = 16384;
+hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
+                           int M, int N, int K, void* y, bool bf16_out, hipStream_t stream, const char** variant);
+size_t fp4_ffn_ws_bytes(int T, int H, int I, bool fp4mid);
+hipError_t launch_fp4_ffn(const uint8_t* x, const uint8_t* x_sc, bool fp4x, int T, int H, const uint8_t* w13,
+                          const uint8_t* w13_sc, const uint8_t* w2, const uint8_t* w2_sc, int I, bool fp4mid, void* y,
+                          bool bf16_out, void* ws, hipStream_t stream, const char** variant);
+
 size_t route_ws_bytes(int T, int E);
 // anchor == NULL: skip mode; otherwise router-live mode
 hipError_t launch_route(const float* logits, int T, int E, int k, const float* survival, float skip_below,

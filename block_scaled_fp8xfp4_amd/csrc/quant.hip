@@ -72,6 +72,80 @@ hipError_t launch_quantize(const void* src, bool bf16, int64_t rows, int64_t col
   return hipGetLastError();
 }
 
+// Codes and scales back to the values they stand for (exact in fp32; bf16
+// holds every element times its scale too, except where the product falls
+// under bf16's smallest values, rounded to nearest even there): the inverse
+// of the casts above, for a caller's own operations on quantized rows.  One
+// thread per 8 elements, so a wave reads 256 or 512 contiguous bytes and
+// writes 1 or 2 KB.
+template <bool FP4>
+__global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc,
+                                                         int64_t nchunks, void* __restrict__ out, bool bf16) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= nchunks) return;
+  const int e = (int)sc[c >> 2] - 127;
+  float v[8];
+  if (FP4) {
+    const uint32_t d = *reinterpret_cast<const uint32_t*>(q + c * 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t code = (d >> (4 * j)) & 15u, m = code & 7u;
+      const uint32_t mag = m == 0 ? 0u : (m == 1 ? 0x3F000000u : (((m >> 1) + 126u) << 23) | ((m & 1u) << 22));
+      v[j] = __builtin_ldexpf(__uint_as_float(mag | ((code & 8u) << 28)), e);
+    }
+  } else {
+    const uint2 d = *reinterpret_cast<const uint2*>(q + c * 8);
+    v[0] = __builtin_amdgcn_cvt_f32_fp8(d.x, 0); v[1] = __builtin_amdgcn_cvt_f32_fp8(d.x, 1);
+    v[2] = __builtin_amdgcn_cvt_f32_fp8(d.x, 2); v[3] = __builtin_amdgcn_cvt_f32_fp8(d.x, 3);
+    v[4] = __builtin_amdgcn_cvt_f32_fp8(d.y, 0); v[5] = __builtin_amdgcn_cvt_f32_fp8(d.y, 1);
+    v[6] = __builtin_amdgcn_cvt_f32_fp8(d.y, 2); v[7] = __builtin_amdgcn_cvt_f32_fp8(d.y, 3);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __builtin_ldexpf(v[j], e);
+  }
+  store8(out, bf16, c * 8, v);
+}
+
+hipError_t launch_dequantize(const uint8_t* q, const uint8_t* sc, bool fp4, int64_t rows, int64_t cols, void* out,
+                             bool bf16, hipStream_t stream) {
+  const int64_t n = rows * (cols / 8);
+  if (n == 0) return hipSuccess;
+  const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+  if (fp4) hipLaunchKernelGGL(dequantize_kernel<true>, grid, block, 0, stream, q, sc, n, out, bf16);
+  else hipLaunchKernelGGL(dequantize_kernel<false>, grid, block, 0, stream, q, sc, n, out, bf16);
+  return hipGetLastError();
+}
+
+// SwiGLU + block-32 codes of gate/up rows [T][2I] (gate, then up): what lies
+// between the two products of an FFN.  a = silu(gate) * up in double, rounded
+// once to fp32 (swiglu, as in every other kernel of the library), then the
+// block's codes.  One thread per 8 columns of one row.
+template <bool BF16, bool FP4>
+__global__ __launch_bounds__(256) void swiglu_quantize_kernel(const void* __restrict__ gu, int64_t ld, int64_t nchunks,
+                                                              int I, uint8_t* __restrict__ q, uint8_t* __restrict__ sc) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= nchunks) return;                                     // whole quads are in or out (I % 32 == 0)
+  const int per_row = I / 8;
+  const int64_t t = c / per_row, i = (c - t * per_row) * 8;
+  float g[8], u[8];
+  load8(gu, BF16, t * ld + i, g);
+  load8(gu, BF16, t * ld + I + i, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = swiglu(g[j], u[j]);
+  store8_codes(FP4, g, q, sc, c);
+}
+
+hipError_t launch_swiglu_quantize(const void* gu, bool bf16, int64_t ld, int64_t T, int I, bool fp4, uint8_t* q,
+                                  uint8_t* sc, hipStream_t stream) {
+  const int64_t n = T * (I / 8);
+  if (n == 0) return hipSuccess;
+  const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+#define MX_SQ(B, F) hipLaunchKernelGGL((swiglu_quantize_kernel<B, F>), grid, block, 0, stream, gu, ld, n, I, q, sc)
+  if (bf16) { if (fp4) MX_SQ(true, true); else MX_SQ(true, false); }
+  else { if (fp4) MX_SQ(false, true); else MX_SQ(false, false); }
+#undef MX_SQ
+  return hipGetLastError();
+}
+
 // Diagnostic: the finite floats whose magnitude bits lie in [lo, hi), with
 // both signs, through both E4M3 encoders of the intermediate: the hardware
 // conversion of requant2_e4m3 and the integer rounding of encode_e4m3 (scale

@@ -95,3 +95,58 @@ class ExpertFFN:
         sc = self.ws[oqs:oqs + Tk * (I // 32)].view(Tk, I // 32)
         o = self.ws[oo:oo + Tk * H * 4].view(torch.float32).view(Tk, H)
         return q, sc, o
+
+
+class AddNorm:
+    """Residual addition + root-mean-square norm (mx_add_rmsnorm) with a weight [H]."""
+
+    def __init__(self, weight, eps=1e-6):
+        self.weight, self.eps = weight, eps
+
+    def __call__(self, x, residual=None, x2=None, fmt=None, hidden=False, stream=None):
+        """(h, ...) with the codes and scales of the normed rows when fmt is given, then with the rows themselves in
+        bf16 when hidden is set.  h is the new residual stream, in the residual's type (x's without one)."""
+        T, H = x.shape
+        h = torch.empty((T, H), dtype=x.dtype if residual is None else residual.dtype, device=x.device)
+        if residual is not None and T > 1 and residual.stride(0) != H:
+            residual = residual.contiguous()
+        out, q, sc, n = [h], None, None, None
+        if fmt is not None:
+            q = torch.empty((T, H if fmt == mxmoe.MX_FMT_E4M3 else H // 2), dtype=torch.uint8, device=x.device)
+            sc = torch.empty((T, H // 32), dtype=torch.uint8, device=x.device)
+            out += [q, sc]
+        if hidden:
+            n = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+            out.append(n)
+        mxmoe.mx_add_rmsnorm(x, self.weight, self.eps, residual, x2, h, n, q, sc,
+                             mxmoe.MX_FMT_E4M3 if fmt is None else fmt, stream)
+        return tuple(out)
+
+
+class FP4Linear:
+    """A dense projection with MXFP4 weights [N, K/2] + scales [N, K/32] (fp4_block_gemm)."""
+
+    def __init__(self, w, w_sc):
+        self.w, self.w_sc = w, w_sc
+
+    def __call__(self, a, a_sc, a_fmt, dtype=torch.bfloat16, stream=None):
+        y = torch.empty((a.shape[0], self.w.shape[0]), dtype=dtype, device=a.device)
+        mxmoe.fp4_block_gemm(a, a_sc, a_fmt, self.w, self.w_sc, y, stream)
+        return y
+
+
+class DenseFFN:
+    """A dense SwiGLU FFN with MXFP4 weights (fp4_dense_ffn); owns the workspace of up to T rows."""
+
+    def __init__(self, w13, w13_sc, w2, w2_sc, T, mid_fmt=mxmoe.MX_FMT_E4M3):
+        self.weights, self.T, self.mid_fmt = (w13, w13_sc, w2, w2_sc), T, mid_fmt
+        self.H, self.I = w2.shape[0], w2.shape[1] * 2
+        n = max(mxmoe.fp4_dense_ffn_workspace_bytes(t, self.H, self.I, mid_fmt) for t in (1, T))
+        self.ws = torch.empty(max(n, 256), dtype=torch.uint8, device=w13.device)
+
+    def __call__(self, x, x_sc, x_fmt, dtype=torch.bfloat16, stream=None):
+        if x.shape[0] > self.T:
+            raise ValueError("DenseFFN: more rows than sized for")
+        y = torch.empty((x.shape[0], self.H), dtype=dtype, device=x.device)
+        mxmoe.fp4_dense_ffn(x, x_sc, x_fmt, *self.weights, self.mid_fmt, y, self.ws, stream)
+        return y

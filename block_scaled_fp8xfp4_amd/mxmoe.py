@@ -21,7 +21,9 @@ EXPORTS = ("mx_quantize", "moe_router_logits_workspace_bytes", "moe_router_logit
            "mx_last_variant", "mx_set_ffn_path", "mx_set_layer1_single_launch", "mx_check_requant", "mx_set_phase_events",
            "moe_shared_expert_workspace_bytes", "moe_shared_expert", "mx_prefetch",
            "moe_layer_decode1", "mx_set_ffn_diag", "moe_expert_ffn_noalloc", "moe_expert_ffn_noalloc_max_bytes",
-           "moe_layer_decode1_shared_workspace_bytes", "moe_layer_decode1_shared")
+           "moe_layer_decode1_shared_workspace_bytes", "moe_layer_decode1_shared",
+           "mx_dequantize", "mx_swiglu_quantize", "mx_add_rmsnorm", "fp4_block_gemm",
+           "fp4_dense_ffn_workspace_bytes", "fp4_dense_ffn")
 
 _lib = None
 
@@ -78,6 +80,18 @@ def load():
     lib.moe_layer_decode1_shared.restype = I32
     lib.moe_layer_decode1_shared.argtypes = [P, I32, I32, P, F32, P, P, I32, P, P, P, P, I32, P, P, P, P, I32,
                                              P, P, P, P, P, P, P, P, SZ, P]
+    lib.mx_dequantize.restype = I32
+    lib.mx_dequantize.argtypes = [P, P, I32, I64, I64, P, I32, P]
+    lib.mx_swiglu_quantize.restype = I32
+    lib.mx_swiglu_quantize.argtypes = [P, I32, I64, I64, I32, I32, P, P, P]
+    lib.mx_add_rmsnorm.restype = I32
+    lib.mx_add_rmsnorm.argtypes = [P, P, I32, I64, P, P, I32, I64, P, I32, I32, I32, F32, P, P, P, I32, P]
+    lib.fp4_block_gemm.restype = I32
+    lib.fp4_block_gemm.argtypes = [P, P, I32, P, P, I32, I32, I32, P, I32, P]
+    lib.fp4_dense_ffn_workspace_bytes.restype = SZ
+    lib.fp4_dense_ffn_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    lib.fp4_dense_ffn.restype = I32
+    lib.fp4_dense_ffn.argtypes = [P, P, I32, I32, I32, P, P, P, P, I32, I32, P, I32, P, SZ, P]
     lib.mx_prefetch.restype = I32
     lib.mx_prefetch.argtypes = [P, ctypes.c_uint64, ctypes.c_uint64, P]
     lib.mx_status_string.restype = ctypes.c_char_p
@@ -279,6 +293,164 @@ def moe_shared_expert(x, x_sc, w13, w13_sc, w2, w2_sc, y, ws, stream=None):
     _check(load().moe_shared_expert(_ptr(x), _ptr(x_sc), T, H, _ptr(w13), _ptr(w13_sc), _ptr(w2), _ptr(w2_sc), I,
                                     _ptr(y), _ptr(ws), ws.nbytes, _stream(stream)),
            "moe_shared_expert")
+
+
+# ------------------------------------------- dense block in microscaled formats
+# These calls check their tensors here (type, shape, layout, device): a wrong
+# one raises ValueError before anything is launched.
+def _rows(name, what, t, dtypes, rows, cols):
+    """The row stride of t, a 2-D tensor [rows, cols] of one of dtypes with contiguous rows."""
+    if t.dim() != 2 or t.dtype not in dtypes or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, expected ({rows}, {cols}) {dtypes}")
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: {what} must have contiguous rows")
+    return t.stride(0) if rows > 1 else _padded(cols)
+
+
+def _padded(cols):
+    return (cols + 7) // 8 * 8
+
+
+def _packed(name, what, t, dtypes, shape):
+    """t is contiguous, of one of dtypes and of this shape."""
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, expected contiguous {tuple(shape)} {dtypes}")
+
+
+def _on_current_device(name, *tensors):
+    import torch
+    d = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{d}")
+
+
+_types = None
+
+
+def _torch_types():
+    """(uint8 only, {fp32, bf16}, MX_IN_* by dtype, MX_OUT_* by dtype)"""
+    global _types
+    if _types is None:
+        import torch
+        _types = ((torch.uint8,), (torch.float32, torch.bfloat16), {torch.float32: MX_IN_F32, torch.bfloat16: MX_IN_BF16},
+                  {torch.bfloat16: MX_OUT_BF16, torch.float32: MX_OUT_F32}, (torch.bfloat16,))
+    return _types
+
+
+def _code_cols(name, fmt, cols):
+    """Code bytes of a row of cols elements."""
+    if fmt not in (MX_FMT_E4M3, MX_FMT_E2M1):
+        raise ValueError(f"{name}: unknown format {fmt}")
+    return cols if fmt == MX_FMT_E4M3 else cols // 2
+
+
+def mx_dequantize(q, sc, fmt, out, stream=None):
+    """out [rows, cols] (fp32 or bf16) = the values of codes q and scales sc."""
+    name = "mx_dequantize"
+    u8, real, _, outs, _ = _torch_types()
+    if out.dim() != 2:
+        raise ValueError(f"{name}: out must be 2-D")
+    rows, cols = out.shape
+    _packed(name, "out", out, real, (rows, cols))
+    _packed(name, "q", q, u8, (rows, _code_cols(name, fmt, cols)))
+    _packed(name, "sc", sc, u8, (rows, cols // 32))
+    _on_current_device(name, q, sc, out)
+    _check(load().mx_dequantize(_ptr(q), _ptr(sc), fmt, rows, cols, _ptr(out), outs[out.dtype], _stream(stream)), name)
+
+
+def mx_swiglu_quantize(gu, q, sc, fmt, stream=None):
+    """q, sc = codes of silu(gate) * up; gu [T, 2I] (fp32 or bf16, any row stride that keeps rows 16-byte
+    aligned), gate in the first I columns."""
+    name = "mx_swiglu_quantize"
+    u8, real, ins, _, _ = _torch_types()
+    if gu.dim() != 2:
+        raise ValueError(f"{name}: gu must be 2-D")
+    T, I = gu.shape[0], gu.shape[1] // 2
+    ld = _rows(name, "gu", gu, real, T, 2 * I)
+    _packed(name, "q", q, u8, (T, _code_cols(name, fmt, I)))
+    _packed(name, "sc", sc, u8, (T, I // 32))
+    _on_current_device(name, gu, q, sc)
+    _check(load().mx_swiglu_quantize(_ptr(gu), ins[gu.dtype], ld, T, I, fmt, _ptr(q), _ptr(sc), _stream(stream)), name)
+
+
+def mx_add_rmsnorm(x, weight, eps, residual=None, x2=None, h=None, n=None, q=None, sc=None, fmt=MX_FMT_E4M3,
+                   stream=None):
+    """v = (residual + x) + x2; h = v in the residual's type; n = h / sqrt(mean(h^2) + eps) * weight.
+    x, x2, residual, h [T, H] fp32 or bf16 (x and x2 of one type and row stride, residual and h too; h may be
+    residual); weight [H] fp32 or bf16 or None; n [T, H] bf16; q, sc the codes of n in fmt.  The outputs that are
+    given are written."""
+    name = "mx_add_rmsnorm"
+    u8, real, ins, _, bf16 = _torch_types()
+    if x.dim() != 2:
+        raise ValueError(f"{name}: x must be 2-D")
+    T, H = x.shape
+    x_ld = _rows(name, "x", x, real, T, H)
+    if x2 is not None and _rows(name, "x2", x2, (x.dtype,), T, H) != x_ld:
+        raise ValueError(f"{name}: x2 must have x's row stride")
+    r = residual if residual is not None else h
+    r_ld, r_dtype = H, MX_IN_F32
+    if r is not None:
+        r_ld, r_dtype = _rows(name, "residual", r, real, T, H), ins[r.dtype]
+        if h is not None and h is not r and _rows(name, "h", h, (r.dtype,), T, H) != r_ld:
+            raise ValueError(f"{name}: h must have the residual's row stride")
+    if weight is not None:
+        _packed(name, "weight", weight, real, (H,))
+    if n is not None:
+        _packed(name, "n", n, bf16, (T, H))
+    if (q is None) != (sc is None):
+        raise ValueError(f"{name}: q and sc come together")
+    if q is not None:
+        _packed(name, "q", q, u8, (T, _code_cols(name, fmt, H)))
+        _packed(name, "sc", sc, u8, (T, H // 32))
+    _on_current_device(name, x, weight, residual, x2, h, n, q, sc)
+    _check(load().mx_add_rmsnorm(_ptr(x), _ptr(x2), ins[x.dtype], x_ld, _ptr(residual), _ptr(h), r_dtype, r_ld,
+                                 _ptr(weight), MX_IN_F32 if weight is None else ins[weight.dtype], T, H, eps, _ptr(n),
+                                 _ptr(q), _ptr(sc), fmt, _stream(stream)), name)
+
+
+def fp4_block_gemm(a, a_sc, a_fmt, w, w_sc, y, stream=None):
+    """y [M, N] (bf16 or fp32) = a . w^T; a codes of K elements a row in a_fmt, w E2M1 [N, K/2], scales [., K/32]."""
+    name = "fp4_block_gemm"
+    u8, real, _, outs, _ = _torch_types()
+    if w.dim() != 2 or y.dim() != 2:
+        raise ValueError(f"{name}: w and y must be 2-D")
+    (N, K), M = w.shape, y.shape[0]
+    K *= 2
+    _packed(name, "w", w, u8, (N, K // 2))
+    _packed(name, "w_sc", w_sc, u8, (N, K // 32))
+    _packed(name, "a", a, u8, (M, _code_cols(name, a_fmt, K)))
+    _packed(name, "a_sc", a_sc, u8, (M, K // 32))
+    _packed(name, "y", y, real, (M, N))
+    _on_current_device(name, a, a_sc, w, w_sc, y)
+    _check(load().fp4_block_gemm(_ptr(a), _ptr(a_sc), a_fmt, _ptr(w), _ptr(w_sc), M, N, K, _ptr(y), outs[y.dtype],
+                                 _stream(stream)), name)
+
+
+def fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt):
+    return load().fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt)
+
+
+def fp4_dense_ffn(x, x_sc, x_fmt, w13, w13_sc, w2, w2_sc, mid_fmt, y, ws, stream=None):
+    """y [T, H] (bf16 or fp32) = SwiGLU FFN of x (codes in x_fmt) with E2M1 weights w13 [2I, H/2] (gate, then up),
+    w2 [H, I/2]; the intermediate in mid_fmt; ws a uint8 tensor of fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt)."""
+    name = "fp4_dense_ffn"
+    u8, real, _, outs, _ = _torch_types()
+    if w2.dim() != 2 or y.dim() != 2:
+        raise ValueError(f"{name}: w2 and y must be 2-D")
+    T, H, I = y.shape[0], w2.shape[0], w2.shape[1] * 2
+    _packed(name, "x", x, u8, (T, _code_cols(name, x_fmt, H)))
+    _packed(name, "x_sc", x_sc, u8, (T, H // 32))
+    _packed(name, "w13", w13, u8, (2 * I, H // 2))
+    _packed(name, "w13_sc", w13_sc, u8, (2 * I, H // 32))
+    _packed(name, "w2", w2, u8, (H, I // 2))
+    _packed(name, "w2_sc", w2_sc, u8, (H, I // 32))
+    _packed(name, "y", y, real, (T, H))
+    if not ws.is_contiguous():
+        raise ValueError(f"{name}: ws must be contiguous")
+    _on_current_device(name, x, x_sc, w13, w13_sc, w2, w2_sc, y, ws)
+    _check(load().fp4_dense_ffn(_ptr(x), _ptr(x_sc), x_fmt, T, H, _ptr(w13), _ptr(w13_sc), _ptr(w2), _ptr(w2_sc), I,
+                                mid_fmt, _ptr(y), outs[y.dtype], _ptr(ws), ws.nbytes, _stream(stream)), name)
 
 
 def prefetch(t, chunk_bytes=0, stream=None, nbytes=None):

@@ -83,6 +83,58 @@ mx_status mx_quantize(const void* src, int src_dtype, int64_t rows, int64_t cols
                       uint8_t* q, uint8_t* sc, void* stream);
 
 /*
+ * The inverse of mx_quantize: out[r][c] = element * 2^(sc - 127), bf16 or
+ * fp32 (out_dtype MX_OUT_*), [rows][cols] contiguous.  Exact in fp32 while
+ * the value fits its range (beyond it: infinity); bf16 is that fp32 value
+ * rounded to nearest even (it holds every value of bf16's normal range).
+ * E4M3's NaN codes (S.1111.111) give NaN.  cols % 32 == 0; rows or cols 0:
+ * nothing to do.  q and out 16-byte aligned; sc needs no alignment.
+ * Supported: rows * cols <= 2^41.
+ */
+mx_status mx_dequantize(const uint8_t* q, const uint8_t* sc, int fmt, int64_t rows, int64_t cols, void* out,
+                        int out_dtype, void* stream);
+
+/*
+ * SwiGLU + block-32 codes (post #6, "Why TileLang": per-block FP8/FP4 casts
+ * with fused SwiGLU), the step between an FFN's two products:
+ *   q, sc = quantize(silu(gate) * up),  silu(g) = g / (1 + e^-g),
+ * evaluated in double and rounded once to fp32 before the cast (the routed
+ * and shared experts' own evaluation); the cast as mx_quantize.
+ * gu: fp32 or bf16 (in_dtype) rows of gu_ld elements, gate in [0, I), up in
+ * [I, 2I); gu_ld >= 2I, a multiple of 4 (fp32) or 8 (bf16).  q: E4M3 [T][I]
+ * or E2M1 [T][I/2]; sc [T][I/32].  I % 32 == 0, T >= 0; gu, q 16-byte
+ * aligned.  q and sc must not overlap gu.  Supported: T * I <= 2^41.
+ */
+mx_status mx_swiglu_quantize(const void* gu, int in_dtype, int64_t gu_ld, int64_t T, int I, int fmt, uint8_t* q,
+                             uint8_t* sc, void* stream);
+
+/*
+ * Residual addition + root-mean-square norm + block-32 codes (post #6,
+ * "Kernel by kernel against B12X": the step's quantization and norms): makes
+ * the rows that the layers of this header read out of what they wrote.
+ *   v = (residual + x) + x2            fp32, absent addends left out
+ *   h = v rounded to res_dtype         (when residual or h is given; else v)
+ *   n = (h / sqrt(mean(h^2) + eps)) * weight
+ * The sum of squares, the root and the products are evaluated in double and
+ * n is rounded once to fp32.  Outputs, each optional, at least one:
+ *   h   fp32 or bf16 (res_dtype), rows of res_ld elements; may be residual
+ *       itself (in place), otherwise must not overlap an input;
+ *   n   bf16 [T][H] (moe_router_logits' hidden rows);
+ *   q + sc  the codes of n's fp32 value, as mx_quantize: E4M3 [T][H] or E2M1
+ *       [T][H/2] (fmt), sc [T][H/32].
+ * x, x2: fp32 or bf16 (x_dtype), rows of x_ld elements (x2 may be NULL: e.g.
+ * y and y_shared of moe_layer_decode1_shared).  residual: res_dtype, rows of
+ * res_ld elements, or NULL.  weight: fp32 or bf16 [H], or NULL (ones).
+ * x_ld, res_ld >= H, multiples of 4 (fp32) or 8 (bf16); res_ld and res_dtype
+ * are ignored without residual and h, fmt without q, w_dtype without weight.
+ * H % 32 == 0, 32 <= H <= 16384 (beyond: MX_EUNSUPPORTED), T >= 0, eps > 0.
+ * All pointers but sc 16-byte aligned.
+ */
+mx_status mx_add_rmsnorm(const void* x, const void* x2, int x_dtype, int64_t x_ld, const void* residual, void* h,
+                         int res_dtype, int64_t res_ld, const void* weight, int w_dtype, int T, int H, float eps,
+                         uint16_t* n, uint8_t* q, uint8_t* sc, int fmt, void* stream);
+
+/*
  * Router logits, the scores the top-k gate ranks (post #6 "How it works"
  * item 3: the MoE top-k gate; "Kernel by kernel against B12X": the router's
  * time per step).  A linear map without bias:
@@ -318,6 +370,43 @@ mx_status moe_layer_decode1_shared(const float* logits, int E, int k, const floa
 mx_status fp8_block_gemm(const uint8_t* a, const uint8_t* a_sc,
                          const uint8_t* w, const uint8_t* w_sc,
                          int M, int N, int K, void* y, int y_dtype, void* stream);
+
+/*
+ * Dense product with MXFP4 weights (post #6 "How it works": block-scaled
+ * MMAs for FP8 x FP4 and MXFP4), the dense sibling of the routed experts'
+ * products:
+ *   y[m][n] = sum_k a[m][k] * w[n][k]   (decoded values)
+ * a: E4M3 [M][K] or E2M1 [M][K/2] (a_fmt) + a_sc SC [M][K/32]; w: E2M1
+ * [N][K/2] + w_sc SC [N][K/32]; y [M][N] bf16 (RNE of the fp32 result) or
+ * fp32 (y_dtype MX_OUT_*).  Accumulated in fp32 on the matrix cores, one
+ * chain over K in order per element, the same for every M and kernel.
+ * E2M1 x E2M1 sums are exact while they fit 24 bits; the matrix cores' sum of
+ * E4M3 x E2M1 products is a few 1e-6 off relative to the result's norm.
+ * Supported: M >= 0, any N >= 1, K % 32 == 0, 32 <= K <= 16384, M*N < 2^40;
+ * beyond these MX_EUNSUPPORTED.  a, w 16-byte, y 4-byte aligned; a_sc, w_sc
+ * 4-byte where K % 128 == 0, else at any byte.
+ */
+mx_status fp4_block_gemm(const uint8_t* a, const uint8_t* a_sc, int a_fmt, const uint8_t* w, const uint8_t* w_sc,
+                         int M, int N, int K, void* y, int y_dtype, void* stream);
+
+/*
+ * Dense SwiGLU FFN with MXFP4 weights (the shared expert's computation on
+ * the experts' weight format):
+ *   y = quantize(silu(x . gate^T) * (x . up^T)) . w2^T
+ * x: E4M3 [T][H] or E2M1 [T][H/2] (x_fmt) + x_sc SC [T][H/32]; w13 E2M1
+ * [2I][H/2] + SC [2I][H/32] (rows [0, I) gate, [I, 2I) up); w2 E2M1 [H][I/2]
+ * + SC [H][I/32]; the intermediate is cast to mid_fmt; y [T][H] bf16 or fp32
+ * (y_dtype).  Results, bit for bit, those of fp4_block_gemm (fp32 out),
+ * mx_swiglu_quantize, fp4_block_gemm.  Supported: T >= 0; H, I % 32 == 0, at
+ * most 16384; T*H, T*2I < 2^40.  x, w13, w2 16-byte, y 4-byte aligned;
+ * scales as in fp4_block_gemm.  ws: fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt) bytes (0 for
+ * an invalid shape), 256-byte aligned, contents ignored; calls that share a
+ * workspace must not overlap.
+ */
+size_t    fp4_dense_ffn_workspace_bytes(int T, int H, int I, int mid_fmt);
+mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T, int H, const uint8_t* w13,
+                        const uint8_t* w13_sc, const uint8_t* w2, const uint8_t* w2_sc, int I, int mid_fmt, void* y,
+                        int y_dtype, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Shared expert: a dense SwiGLU MLP on every row with block-32 FP8 operands
