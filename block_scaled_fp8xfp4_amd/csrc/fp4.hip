@@ -73,8 +73,312 @@ __global__ __launch_bounds__(256) void fp4_rows_kernel(const uint8_t* __restrict
     }
 }
 
+// Many rows: BM x BN output tiles staged through LDS.  A stage holds K = 128
+// of the tile's activation rows, weight rows and scale dwords, brought by LDS
+// DMA NST stages ahead of the matrix cores and ordered by vmcnt waits and
+// LDS-only barriers, one barrier per stage.  Inside a stage two steps of
+// 32x32x64, the shape in which E2M1 x E2M1 runs at its full rate; the next
+// step's operands are read from LDS while the current one multiplies, across
+// the stage's barrier too.
+//
+// The weights take the instruction's A side and the activations its B side,
+// so a lane holds one row of y and four consecutive columns per register
+// quad: lane l has row l % 32 and columns 8 q + 4 (l / 32) + [0, 4), q = 0..3.
+//
+// LDS rows are 64 bytes (E2M1) or 128 (E4M3) in 16-byte chunks; the chunk
+// index is XORed with bits of the row so that 8 (and 16) consecutive rows'
+// reads of one chunk fall on different banks.
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+__device__ __forceinline__ int swz4(int r) { return (((r >> 1) ^ (r >> 3)) & 1) | ((r >> 1) & 2); }
+__device__ __forceinline__ int swz8(int r) { return ((r >> 1) & 3) | (((r ^ (r >> 3)) & 1) << 2); }
+
+__device__ __forceinline__ u32x4 lds_read16(uint32_t addr) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(addr);
+}
+__device__ __forceinline__ uint32_t lds_read4(uint32_t addr) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) uint32_t*>(addr);
+}
+__device__ __forceinline__ v8i operand(const u32x4& lo) {
+  return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], 0, 0, 0, 0};
+}
+__device__ __forceinline__ v8i operand(const u32x4& lo, const u32x4& hi) {
+  return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+constexpr int KS = 128;                           // K per stage
+constexpr int XCDS = 8;
+
+// WM x WN wavefronts of TM x TN 32 x 32 tiles each.
+template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
+struct TileShape {
+  static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
+  static constexpr int RA = FP4A ? KS / 2 : KS;   // bytes of an activation row per stage
+  static constexpr int CA = RA / 16;              // its chunks
+  static constexpr uint32_t OFF_W = BM * RA, OFF_XS = OFF_W + BN * (KS / 2), OFF_WS = OFF_XS + BM * 4;
+  static constexpr uint32_t STAGE = OFF_WS + BN * 4;
+  static constexpr int NX = BM * RA / 1024 / NW, NWT = BN * (KS / 2) / 1024 / NW;   // DMA instructions per wavefront
+  static constexpr int NSC = ((BM + BN) / 64 + NW - 1) / NW;
+  static constexpr int NV = NX + NWT + NSC;       // vector-memory operations per wavefront and stage
+  static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * (KS / 2), "whole DMA instructions");
+  static_assert(STAGE * NST <= 160 * 1024 && NV * (NST - 1) < 63, "LDS and vmcnt");
+};
+
+template <int N> __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
+
+// at most `left` (0 .. NST - 1) whole stages may still be in flight
+template <int NV, int NST> __device__ __forceinline__ void wait_stages(int left) {
+  if (NST > 3 && left >= 3) wait_vm<3 * NV>();
+  else if (NST > 2 && left >= 2) wait_vm<2 * NV>();
+  else if (left >= 1) wait_vm<NV>();
+  else wait_vm<0>();
+}
+
+template <bool FP4A, int WM, int WN, int TM, int TN, int NST, bool TAIL>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_sc,
+                                                                   const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_sc,
+                                                                   int M, int N, int K, void* __restrict__ y, bool bf16_out) {
+  using S = TileShape<FP4A, WM, WN, TM, TN, NST>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::STAGE * NST];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 31, g = lane >> 5;
+  const int wm = wave / WN, wn = wave % WN;
+  const int nblk = K / 32, ns = (K + KS - 1) / KS;
+  const int rowa = FP4A ? K / 2 : K, roww = K / 2;
+
+  // XCD-aware order: each XCD takes a run of consecutive tiles, which go down 8 row tiles before the next column tile
+  const int nrt = (M + S::BM - 1) / S::BM, nct = (N + S::BN - 1) / S::BN;
+  const int64_t tiles = (int64_t)nrt * nct, per = (tiles + XCDS - 1) / XCDS;
+  const int64_t t = (int64_t)(blockIdx.x % XCDS) * per + blockIdx.x / XCDS;
+  if (t >= tiles) return;
+  const int grp = (int)(t / (8 * (int64_t)nct)), in = (int)(t - grp * 8 * (int64_t)nct);
+  const int rows_in = min(8, nrt - grp * 8);
+  const int rt = grp * 8 + in % rows_in, ct = in / rows_in;
+  const int64_t m0 = (int64_t)rt * S::BM, n0 = (int64_t)ct * S::BN;
+  const int mlast = (int)(M - 1 - m0), nlast = (int)(N - 1 - n0);   // rows past the end repeat the last one
+
+  // this lane's DMA sources: byte offsets from the tile's first row
+  uint32_t xoff[S::NX], woff[S::NWT], xc[S::NX], wc[S::NWT], soff[S::NSC];
+#pragma unroll
+  for (int i = 0; i < S::NX; ++i) {
+    const int p = (i * S::NW + wave) * 64 + lane, r = p / S::CA;
+    const int c = (p % S::CA) ^ (FP4A ? swz4(r) : swz8(r));
+    xc[i] = c * (FP4A ? 32 : 16);
+    xoff[i] = (uint32_t)min(r, mlast) * (uint32_t)rowa + c * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < S::NWT; ++i) {
+    const int p = (i * S::NW + wave) * 64 + lane, r = p / 4, c = (p % 4) ^ swz4(r);
+    wc[i] = c * 32;
+    woff[i] = (uint32_t)min(r, nlast) * (uint32_t)roww + c * 16;
+  }
+  int sslot[S::NSC];
+#pragma unroll
+  for (int i = 0; i < S::NSC; ++i) {
+    sslot[i] = min(i * S::NW + wave, (S::BM + S::BN) / 64 - 1);      // surplus wavefronts repeat the last slot
+    const int r = sslot[i] * 64 + lane;
+    soff[i] = (uint32_t)(sslot[i] < S::BM / 64 ? min(r, mlast) : min(r - S::BM, nlast)) * (uint32_t)nblk;
+  }
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  const uint8_t* at = a + m0 * rowa;
+  const uint8_t* wt = w + n0 * roww;
+  const uint8_t* ast = a_sc + m0 * nblk;
+  const uint8_t* wst = w_sc + n0 * nblk;
+  auto issue = [&](int s, uint32_t base) {
+    const bool cut = TAIL && s == ns - 1;                             // chunks past K read the stage's first chunk
+#pragma unroll
+    for (int i = 0; i < S::NX; ++i) {
+      const uint32_t off = cut && s * KS + (int)xc[i] >= K ? xoff[i] - xc[i] / (FP4A ? 2 : 1) : xoff[i];
+      dma16_to_lds(at + (int64_t)s * S::RA, off, base + (i * S::NW + wave) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < S::NWT; ++i) {
+      const uint32_t off = cut && s * KS + (int)wc[i] >= K ? woff[i] - wc[i] / 2 : woff[i];
+      dma16_to_lds(wt + (int64_t)s * (KS / 2), off, base + S::OFF_W + (i * S::NW + wave) * 1024);
+    }
+    if (!TAIL) {
+#pragma unroll
+      for (int i = 0; i < S::NSC; ++i)
+        dma4_to_lds((sslot[i] < S::BM / 64 ? ast : wst) + s * 4, soff[i], base + S::OFF_XS + sslot[i] * 256);
+    }
+  };
+
+  struct Regs { u32x4 xlo[TM], xhi[FP4A ? 1 : TM], w[TN]; };
+  const uint32_t xrow = (uint32_t)(wm * TM * 32 + lr), wrow = (uint32_t)(wn * TN * 32 + lr);
+  const int fx = FP4A ? swz4(lr) : swz8(lr), fw = swz4(lr);
+  auto load = [&](Regs& R, uint32_t base, int ks) {
+    if (FP4A) {
+      const uint32_t p = base + xrow * S::RA + ((2 * ks + g) ^ fx) * 16;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) R.xlo[i] = lds_read16(p + i * 32 * S::RA);
+    } else {
+      const uint32_t p = base + xrow * S::RA + ((4 * ks + g) ^ fx) * 16, p2 = base + xrow * S::RA + ((4 * ks + 2 + g) ^ fx) * 16;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        R.xlo[i] = lds_read16(p + i * 32 * S::RA);
+        R.xhi[FP4A ? 0 : i] = lds_read16(p2 + i * 32 * S::RA);
+      }
+    }
+    const uint32_t pw = base + S::OFF_W + wrow * 64 + ((2 * ks + g) ^ fw) * 16;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) R.w[i] = lds_read16(pw + i * 2048);
+  };
+  // scale dwords of a stage, shifted so that bytes 0 and 2 are the blocks of this lane's half in steps 0 and 1
+  auto scales = [&](uint32_t* sx, uint32_t* sw, uint32_t base) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sx[i] = lds_read4(base + S::OFF_XS + (xrow + i * 32) * 4) >> (8 * g);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) sw[i] = lds_read4(base + S::OFF_WS + (wrow + i * 32) * 4) >> (8 * g);
+  };
+  v16f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  auto cut_step = [&](Regs& R, int s, int ks) {                       // zero elements past K (activations; E2M1 weights are finite)
+    const int b = s * 4 + 2 * ks;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      if (b + (FP4A ? g : 0) >= nblk) R.xlo[i] = u32x4{0, 0, 0, 0};
+      if (!FP4A && b + 1 >= nblk) R.xhi[FP4A ? 0 : i] = u32x4{0, 0, 0, 0};
+    }
+  };
+#define MX_STEP(R, KSI)                                                                                              \
+  _Pragma("unroll") for (int i = 0; i < TM; ++i) {                                                                   \
+    const v8i xv = FP4A ? operand(R.xlo[i]) : operand(R.xlo[i], R.xhi[FP4A ? 0 : i]);                                \
+    _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(      \
+        operand(R.w[j]), xv, acc[i][j], 4, FP4A ? 4 : 0, 2 * KSI, (int)sw[j], 2 * KSI, (int)sx[i]);                  \
+  }
+
+  // K % 128 != 0: scale rows are not dword-aligned; each lane keeps its slots' next dword in registers and writes it
+  // to the stage's LDS before the barrier that publishes the stage (bytes past K: 127)
+  uint32_t sreg[S::NSC];
+  auto fetch_scales = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < S::NSC; ++i) {
+      const uint8_t* p = (sslot[i] < S::BM / 64 ? ast : wst) + soff[i] + s * 4;
+      uint32_t v = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) v |= (uint32_t)(s * 4 + b < nblk ? p[b] : 127) << (8 * b);
+      sreg[i] = v;
+    }
+  };
+  auto put_scales = [&](uint32_t base) {
+#pragma unroll
+    for (int i = 0; i < S::NSC; ++i)
+      *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>(base + S::OFF_XS + sslot[i] * 256 + lane * 4) = sreg[i];
+  };
+
+  auto buf = [&](int s) { return lds0 + (uint32_t)(s % NST) * S::STAGE; };
+#pragma unroll
+  for (int s = 0; s < NST; ++s)
+    if (s < ns) issue(s, lds0 + s * S::STAGE);
+  if (TAIL) {
+    fetch_scales(0);
+    put_scales(lds0);
+    if (ns > 1) fetch_scales(1);
+  }
+  if (TAIL) wait_vm<0>();
+  else wait_stages<S::NV, NST>(min(ns - 1, NST - 1));
+  lds_barrier();
+  Regs R0, R1;
+  uint32_t sx[TM], sw[TN], sxn[TM], swn[TN];
+  load(R0, lds0, 0);
+  scales(sx, sw, lds0);
+  if (TAIL && ns == 1) cut_step(R0, 0, 0);
+  for (int s = 0; s < ns; ++s) {
+    const uint32_t b0 = buf(s), b1 = buf(s + 1);
+    load(R1, b0, 1);
+    if (TAIL && s == ns - 1) cut_step(R1, s, 1);
+    MX_STEP(R0, 0)
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + 1 < ns) {
+      if (TAIL) {
+        put_scales(b1);
+        wait_vm<0>();
+      } else {
+        wait_stages<S::NV, NST>(min(ns - 2 - s, NST - 2));
+      }
+      lds_barrier();
+      if (s + NST < ns) issue(s + NST, b0);
+      if (TAIL && s + 2 < ns) fetch_scales(s + 2);
+      load(R0, b1, 0);
+      scales(sxn, swn, b1);
+      if (TAIL && s + 1 == ns - 1) cut_step(R0, s + 1, 0);
+    }
+    MX_STEP(R1, 1)
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sx[i] = sxn[i];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) sw[j] = swn[j];
+  }
+#undef MX_STEP
+
+  const bool quads = (N & 3) == 0;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = m0 + wm * TM * 32 + i * 32 + lr;
+    if (m >= M) continue;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t n = n0 + wn * TN * 32 + j * 32 + 8 * q + 4 * g;
+        const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2], v3 = acc[i][j][4 * q + 3];
+        if (quads) {
+          if (n >= N) continue;
+          if (bf16_out) {
+            const u32x2_a4 d = {(uint32_t)f32_to_bf16_rne(v0) | ((uint32_t)f32_to_bf16_rne(v1) << 16),
+                                (uint32_t)f32_to_bf16_rne(v2) | ((uint32_t)f32_to_bf16_rne(v3) << 16)};
+            *reinterpret_cast<u32x2_a4*>(static_cast<uint16_t*>(y) + m * N + n) = d;
+          } else {
+            *reinterpret_cast<f32x4_a4*>(static_cast<float*>(y) + m * N + n) = f32x4_a4{v0, v1, v2, v3};
+          }
+        } else {
+          const float v[4] = {v0, v1, v2, v3};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < N) {
+              if (bf16_out) static_cast<uint16_t*>(y)[m * N + n + e] = f32_to_bf16_rne(v[e]);
+              else static_cast<float*>(y)[m * N + n + e] = v[e];
+            }
+        }
+      }
+  }
+}
+
+constexpr int FP4_TILE_MIN_M = 64;
+
+template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
+static void launch_tile(const uint8_t* a, const uint8_t* a_sc, const uint8_t* w, const uint8_t* w_sc, int M, int N, int K,
+                        void* y, bool bf16_out, hipStream_t stream) {
+  using S = TileShape<FP4A, WM, WN, TM, TN, NST>;
+  const int64_t tiles = (int64_t)((M + S::BM - 1) / S::BM) * ((N + S::BN - 1) / S::BN);
+  const dim3 grid((unsigned)((tiles + XCDS - 1) / XCDS * XCDS)), block(64 * S::NW);
+  if (K % KS) hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, NST, true>), grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
+  else hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, NST, false>), grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
+}
+
 hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
                            int M, int N, int K, void* y, bool bf16_out, hipStream_t stream, const char** variant) {
+  if (M >= FP4_TILE_MIN_M) {
+    const int64_t big = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
+    if (big >= 192) {
+      if (fp4a) launch_tile<true, 2, 4, 4, 2, 4>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
+      else launch_tile<false, 4, 2, 2, 4, 3>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
+      *variant = fp4a ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
+    } else {
+      if (fp4a) launch_tile<true, 2, 2, 2, 2, 4>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
+      else launch_tile<false, 2, 2, 2, 2, 3>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
+      *variant = fp4a ? "fp4:tile128x128_a4" : "fp4:tile128x128_a8";
+    }
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16)), block(256);
   if (fp4a) hipLaunchKernelGGL(fp4_rows_kernel<true>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
   else hipLaunchKernelGGL(fp4_rows_kernel<false>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
