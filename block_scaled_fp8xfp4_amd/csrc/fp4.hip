@@ -108,6 +108,8 @@ __device__ __forceinline__ v8i operand(const u32x4& lo, const u32x4& hi) {
   return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+template <int V> struct Int { static constexpr int value = V; };
+
 constexpr int KS = 128;                           // K per stage
 constexpr int XCDS = 8;
 
@@ -206,32 +208,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(const uint8_t
     }
   };
 
+  // Operands of one step, and the scale dwords of a stage shifted so that bytes 0 and 2 are the blocks of this lane's
+  // half in steps 0 and 1.
   struct Regs { u32x4 xlo[TM], xhi[FP4A ? 1 : TM], w[TN]; };
+  struct Scales { uint32_t x[TM], w[TN]; };
   const uint32_t xrow = (uint32_t)(wm * TM * 32 + lr), wrow = (uint32_t)(wn * TN * 32 + lr);
   const int fx = FP4A ? swz4(lr) : swz8(lr), fw = swz4(lr);
-  auto load = [&](Regs& R, uint32_t base, int ks) {
-    if (FP4A) {
-      const uint32_t p = base + xrow * S::RA + ((2 * ks + g) ^ fx) * 16;
-#pragma unroll
-      for (int i = 0; i < TM; ++i) R.xlo[i] = lds_read16(p + i * 32 * S::RA);
-    } else {
-      const uint32_t p = base + xrow * S::RA + ((4 * ks + g) ^ fx) * 16, p2 = base + xrow * S::RA + ((4 * ks + 2 + g) ^ fx) * 16;
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        R.xlo[i] = lds_read16(p + i * 32 * S::RA);
-        R.xhi[FP4A ? 0 : i] = lds_read16(p2 + i * 32 * S::RA);
-      }
+  constexpr int NLD = TN + TM * (FP4A ? 1 : 2), NMM = TM * TN;       // LDS reads and matrix operations of a step
+  // the it-th LDS read of step ks (weights first: every matrix operation row needs them)
+  auto load1 = [&](Regs& R, uint32_t base, int ks, int it) {
+    if (it < TN) R.w[it] = lds_read16(base + S::OFF_W + wrow * 64 + ((2 * ks + g) ^ fw) * 16 + it * 2048);
+    else if (FP4A) R.xlo[it - TN] = lds_read16(base + xrow * S::RA + ((2 * ks + g) ^ fx) * 16 + (it - TN) * 32 * S::RA);
+    else {
+      const int i = (it - TN) / 2;
+      if ((it - TN) % 2 == 0) R.xlo[i] = lds_read16(base + xrow * S::RA + ((4 * ks + g) ^ fx) * 16 + i * 32 * S::RA);
+      else R.xhi[i] = lds_read16(base + xrow * S::RA + ((4 * ks + 2 + g) ^ fx) * 16 + i * 32 * S::RA);
     }
-    const uint32_t pw = base + S::OFF_W + wrow * 64 + ((2 * ks + g) ^ fw) * 16;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) R.w[i] = lds_read16(pw + i * 2048);
   };
-  // scale dwords of a stage, shifted so that bytes 0 and 2 are the blocks of this lane's half in steps 0 and 1
-  auto scales = [&](uint32_t* sx, uint32_t* sw, uint32_t base) {
+  auto load_scales = [&](Scales& C, uint32_t base) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sx[i] = lds_read4(base + S::OFF_XS + (xrow + i * 32) * 4) >> (8 * g);
+    for (int i = 0; i < TM; ++i) C.x[i] = lds_read4(base + S::OFF_XS + (xrow + i * 32) * 4);
 #pragma unroll
-    for (int i = 0; i < TN; ++i) sw[i] = lds_read4(base + S::OFF_WS + (wrow + i * 32) * 4) >> (8 * g);
+    for (int i = 0; i < TN; ++i) C.w[i] = lds_read4(base + S::OFF_WS + (wrow + i * 32) * 4);
+  };
+  auto shift_scales = [&](Scales& C) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) C.x[i] >>= 8 * g;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) C.w[i] >>= 8 * g;
   };
   v16f acc[TM][TN];
 #pragma unroll
@@ -248,12 +252,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(const uint8_t
       if (!FP4A && b + 1 >= nblk) R.xhi[FP4A ? 0 : i] = u32x4{0, 0, 0, 0};
     }
   };
-#define MX_STEP(R, KSI)                                                                                              \
-  _Pragma("unroll") for (int i = 0; i < TM; ++i) {                                                                   \
-    const v8i xv = FP4A ? operand(R.xlo[i]) : operand(R.xlo[i], R.xhi[FP4A ? 0 : i]);                                \
-    _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(      \
-        operand(R.w[j]), xv, acc[i][j], 4, FP4A ? 4 : 0, 2 * KSI, (int)sw[j], 2 * KSI, (int)sx[i]);                  \
-  }
+  auto mma = [&](const Regs& R, const Scales& C, auto step, int q) {   // the q-th matrix operation of step `step`
+    constexpr int B = 2 * decltype(step)::value;
+    const int i = q / TN, j = q % TN;
+    const v8i xv = FP4A ? operand(R.xlo[i]) : operand(R.xlo[i], R.xhi[FP4A ? 0 : i]);
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(R.w[j]), xv, acc[i][j], 4, FP4A ? 4 : 0, B,
+                                                                (int)C.w[j], B, (int)C.x[i]);
+  };
+  // One step's matrix operations with the next step's LDS reads between them (the order is held by scheduling barriers).
+  auto step_with_loads = [&](const Regs& R, const Scales& C, auto step, Regs& Rn, uint32_t base, int ks) {
+#pragma unroll
+    for (int q = 0; q < NMM; ++q) {
+#pragma unroll
+      for (int it = q * NLD / NMM; it < (q + 1) * NLD / NMM; ++it) load1(Rn, base, ks, it);
+      mma(R, C, step, q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  const Int<0> Step0;
+  const Int<1> Step1;
 
   // K % 128 != 0: scale rows are not dword-aligned; each lane keeps its slots' next dword in registers and writes it
   // to the stage's LDS before the barrier that publishes the stage (bytes past K: 127)
@@ -274,7 +291,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(const uint8_t
       *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>(base + S::OFF_XS + sslot[i] * 256 + lane * 4) = sreg[i];
   };
 
-  auto buf = [&](int s) { return lds0 + (uint32_t)(s % NST) * S::STAGE; };
 #pragma unroll
   for (int s = 0; s < NST; ++s)
     if (s < ns) issue(s, lds0 + s * S::STAGE);
@@ -287,37 +303,47 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(const uint8_t
   else wait_stages<S::NV, NST>(min(ns - 1, NST - 1));
   lds_barrier();
   Regs R0, R1;
-  uint32_t sx[TM], sw[TN], sxn[TM], swn[TN];
-  load(R0, lds0, 0);
-  scales(sx, sw, lds0);
+  Scales C, Cn;
+#pragma unroll
+  for (int it = 0; it < NLD; ++it) load1(R0, lds0, 0, it);
+  load_scales(C, lds0);
+  shift_scales(C);
   if (TAIL && ns == 1) cut_step(R0, 0, 0);
-  for (int s = 0; s < ns; ++s) {
-    const uint32_t b0 = buf(s), b1 = buf(s + 1);
-    load(R1, b0, 1);
-    if (TAIL && s == ns - 1) cut_step(R1, s, 1);
-    MX_STEP(R0, 0)
-    __builtin_amdgcn_sched_barrier(0);
-    if (s + 1 < ns) {
-      if (TAIL) {
-        put_scales(b1);
-        wait_vm<0>();
-      } else {
-        wait_stages<S::NV, NST>(min(ns - 2 - s, NST - 2));
-      }
-      lds_barrier();
-      if (s + NST < ns) issue(s + NST, b0);
-      if (TAIL && s + 2 < ns) fetch_scales(s + 2);
-      load(R0, b1, 0);
-      scales(sxn, swn, b1);
-      if (TAIL && s + 1 == ns - 1) cut_step(R0, s + 1, 0);
+  uint32_t b0 = lds0;
+  // Stage s: step 0 while step 1's operands are read; then the next stage's data is waited for and published, this
+  // stage's buffer (read out by every wavefront) refilled, and step 1 multiplies while the next stage's are read.
+  auto stage = [&](int s, auto refill) {
+    const uint32_t b1 = b0 + S::STAGE == lds0 + NST * S::STAGE ? lds0 : b0 + S::STAGE;
+    step_with_loads(R0, C, Step0, R1, b0, 1);
+    if (TAIL) {
+      put_scales(b1);
+      wait_vm<0>();
+    } else if (decltype(refill)::value) {
+      wait_vm<S::NV * (NST - 2)>();
+    } else {
+      wait_stages<S::NV, NST>(min(ns - 2 - s, NST - 2));
     }
-    MX_STEP(R1, 1)
+    lds_barrier();
+    if (decltype(refill)::value) issue(s + NST, b0);
+    if (TAIL && s + 2 < ns) fetch_scales(s + 2);
+    load_scales(Cn, b1);
+    __builtin_amdgcn_sched_barrier(0);
+    step_with_loads(R1, C, Step1, R0, b1, 0);
+    if (TAIL && s + 1 == ns - 1) cut_step(R0, s + 1, 0);
+    shift_scales(Cn);
+    C = Cn;
+    b0 = b1;
+  };
+  int s = 0;
+  for (; s + NST < ns; ++s) stage(s, Step1);
+  for (; s + 1 < ns; ++s) stage(s, Step0);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sx[i] = sxn[i];
+  for (int it = 0; it < NLD; ++it) load1(R1, b0, 1, it);
+  if (TAIL) cut_step(R1, s, 1);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) sw[j] = swn[j];
-  }
-#undef MX_STEP
+  for (int q = 0; q < NMM; ++q) mma(R0, C, Step0, q);
+#pragma unroll
+  for (int q = 0; q < NMM; ++q) mma(R1, C, Step1, q);
 
   const bool quads = (N & 3) == 0;
 #pragma unroll
