@@ -30,8 +30,9 @@ __global__ __launch_bounds__(256) void fp4_rows_kernel(const uint8_t* __restrict
                                                        int M, int N, int K, void* __restrict__ y, bool bf16_out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, g = lane >> 4;
-  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16;
-  const int64_t m0 = (int64_t)blockIdx.y * 16;
+  const uint32_t nct = (N + 63) / 64;                            // workgroups per row tile
+  const int64_t n0 = ((int64_t)(blockIdx.x % nct) * 4 + wave) * 16;
+  const int64_t m0 = (int64_t)(blockIdx.x / nct) * 16;
   if (n0 >= N) return;
   const int64_t n = n0 + col < N ? n0 + col : N - 1, m = m0 + col < M ? m0 + col : M - 1;
   const int nblk = K / 32;
@@ -73,33 +74,40 @@ __global__ __launch_bounds__(256) void fp4_rows_kernel(const uint8_t* __restrict
     }
 }
 
-// Many rows: BM x BN output tiles staged through LDS.  A stage holds K = 128
-// of the tile's activation rows, weight rows and scale dwords, brought by LDS
-// DMA NST stages ahead of the matrix cores and ordered by vmcnt waits and
-// LDS-only barriers, one barrier per stage.  Inside a stage two steps of
-// 32x32x64, the shape in which E2M1 x E2M1 runs at its full rate; the next
-// step's operands are read from LDS while the current one multiplies, across
-// the stage's barrier too.
+// Many rows: BM x BN output tiles staged through LDS.  A stage holds K = KS
+// (256 with E2M1 activations, 128 with E4M3) of the tile's activation and
+// weight rows, brought by LDS DMA NST stages ahead of the matrix cores and
+// ordered by vmcnt waits and LDS-only barriers, one barrier per stage.  A
+// stage's steps are 32x32x64, the shape in which E2M1 x E2M1 runs at its full
+// rate; every step's matrix operations carry the LDS reads of the next step's
+// operands between them, across the stage's barrier too.
+//
+// Rows go to LDS in pieces of 128 bytes where they can: the vector memory
+// path takes a lookup per row piece, and with pieces of 64 bytes and a dword
+// of scales per row and stage the lookups, not the matrix cores, set the time
+// (109 us at 8192 x 4096 x 4096 in E2M1).  For the same reason a lane reads
+// 16 scale bytes of its row at a time (K = 512) and writes them to LDS.
 //
 // The weights take the instruction's A side and the activations its B side,
 // so a lane holds one row of y and four consecutive columns per register
 // quad: lane l has row l % 32 and columns 8 q + 4 (l / 32) + [0, 4), q = 0..3.
 //
-// LDS rows are 64 bytes (E2M1) or 128 (E4M3) in 16-byte chunks; the chunk
-// index is XORed with bits of the row so that 8 (and 16) consecutive rows'
-// reads of one chunk fall on different banks.
+// LDS rows are 64 or 128 bytes in 16-byte chunks; the chunk index is XORed
+// with bits of the row so that 8 (and 16) consecutive rows' reads of one
+// chunk fall on different banks (no conflicts counted).
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
 
 __device__ __forceinline__ int swz4(int r) { return (((r >> 1) ^ (r >> 3)) & 1) | ((r >> 1) & 2); }
 __device__ __forceinline__ int swz8(int r) { return ((r >> 1) & 3) | (((r ^ (r >> 3)) & 1) << 2); }
 
-__device__ __forceinline__ u32x4 lds_read16(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(addr);
+template <typename V> __device__ __forceinline__ V lds_read(uint32_t addr) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) V*>(addr);
 }
-__device__ __forceinline__ uint32_t lds_read4(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) uint32_t*>(addr);
+template <typename V> __device__ __forceinline__ void lds_write(uint32_t addr, const V& v) {
+  *reinterpret_cast<__attribute__((address_space(3))) V*>(addr) = v;
 }
 __device__ __forceinline__ v8i operand(const u32x4& lo) {
   return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], 0, 0, 0, 0};
@@ -108,128 +116,160 @@ __device__ __forceinline__ v8i operand(const u32x4& lo, const u32x4& hi) {
   return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-template <int V> struct Int { static constexpr int value = V; };
+// Holds the computation of v before what follows (no instruction).
+__device__ __forceinline__ void pin(v16f& v) { asm volatile("" : "+v"(v)); }
 
-constexpr int KS = 128;                           // K per stage
+template <int V> struct Int { static constexpr int value = V; };
+template <int N> __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
+
 constexpr int XCDS = 8;
+constexpr int SCK = 512;                          // K whose scales (16 bytes a row) are fetched at a time
 
 // WM x WN wavefronts of TM x TN 32 x 32 tiles each.
 template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
 struct TileShape {
   static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
-  static constexpr int RA = FP4A ? KS / 2 : KS;   // bytes of an activation row per stage
-  static constexpr int CA = RA / 16;              // its chunks
-  static constexpr uint32_t OFF_W = BM * RA, OFF_XS = OFF_W + BN * (KS / 2), OFF_WS = OFF_XS + BM * 4;
-  static constexpr uint32_t STAGE = OFF_WS + BN * 4;
-  static constexpr int NX = BM * RA / 1024 / NW, NWT = BN * (KS / 2) / 1024 / NW;   // DMA instructions per wavefront
-  static constexpr int NSC = ((BM + BN) / 64 + NW - 1) / NW;
-  static constexpr int NV = NX + NWT + NSC;       // vector-memory operations per wavefront and stage
-  static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * (KS / 2), "whole DMA instructions");
-  static_assert(STAGE * NST <= 160 * 1024 && NV * (NST - 1) < 63, "LDS and vmcnt");
+  static constexpr int KS = FP4A ? 256 : 128, STEPS = KS / 64;
+  static constexpr int RA = 128, RW = KS / 2;     // bytes of an activation / a weight row per stage
+  static constexpr int CW = RW / 16;              // chunks of a weight row
+  static constexpr uint32_t OFF_W = BM * RA, STAGE = OFF_W + BN * RW;
+  static constexpr uint32_t OFF_S = STAGE * NST, SCALES = (BM + BN) * 16, LDS = OFF_S + 2 * SCALES;
+  static constexpr int NX = BM * RA / 1024 / NW, NWT = BN * RW / 1024 / NW;   // DMA instructions per wavefront and stage
+  static constexpr int NV = NX + NWT;
+  static constexpr int NSC = (BM + BN) / 64 / NW; // scale rows per lane
+  static constexpr int SPC = SCK / KS;            // stages per scale chunk
+  static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * RW && NSC * NW * 64 == BM + BN, "whole rows");
+  static_assert(LDS <= 160 * 1024 && NV * (NST - 1) < 63, "LDS and vmcnt");
 };
 
-template <int N> __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
+struct TileArgs {
+  const uint8_t* x; const uint8_t* x_sc;          // activations [M][K]
+  const uint8_t* w; const uint8_t* w_sc;          // weights [N][K]
+  int M, N, K;
+  void* y; bool bf16_out;                         // [M][N]
+};
 
-// at most `left` (0 .. NST - 1) whole stages may still be in flight
-template <int NV, int NST> __device__ __forceinline__ void wait_stages(int left) {
-  if (NST > 3 && left >= 3) wait_vm<3 * NV>();
-  else if (NST > 2 && left >= 2) wait_vm<2 * NV>();
-  else if (left >= 1) wait_vm<NV>();
-  else wait_vm<0>();
-}
-
-template <bool FP4A, int WM, int WN, int TM, int TN, int NST, bool TAIL>
-__global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_sc,
-                                                                   const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_sc,
-                                                                   int M, int N, int K, void* __restrict__ y, bool bf16_out) {
+template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
+__global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   using S = TileShape<FP4A, WM, WN, TM, TN, NST>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::STAGE * NST];
+  constexpr int KS = S::KS, STEPS = S::STEPS;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 31, g = lane >> 5;
   const int wm = wave / WN, wn = wave % WN;
+  const int M = A.M, N = A.N, K = A.K;
   const int nblk = K / 32, ns = (K + KS - 1) / KS;
-  const int rowa = FP4A ? K / 2 : K, roww = K / 2;
+  const int rowx = FP4A ? K / 2 : K, roww = K / 2;
 
   // XCD-aware order: each XCD takes a run of consecutive tiles, which go down 8 row tiles before the next column tile
   const int nrt = (M + S::BM - 1) / S::BM, nct = (N + S::BN - 1) / S::BN;
-  const int64_t tiles = (int64_t)nrt * nct, per = (tiles + XCDS - 1) / XCDS;
-  const int64_t t = (int64_t)(blockIdx.x % XCDS) * per + blockIdx.x / XCDS;
+  const uint32_t tiles = (uint32_t)nrt * nct, per = (tiles + XCDS - 1) / XCDS;   // M N < 2^40: fewer than 2^27 tiles
+  const uint32_t t = blockIdx.x % XCDS * per + blockIdx.x / XCDS;
   if (t >= tiles) return;
-  const int grp = (int)(t / (8 * (int64_t)nct)), in = (int)(t - grp * 8 * (int64_t)nct);
-  const int rows_in = min(8, nrt - grp * 8);
-  const int rt = grp * 8 + in % rows_in, ct = in / rows_in;
+  const uint32_t grp = t / (8u * nct), in = t - grp * 8u * nct, rows_in = min(8u, nrt - grp * 8u);
+  const int rt = __builtin_amdgcn_readfirstlane(grp * 8 + in % rows_in), ct = __builtin_amdgcn_readfirstlane(in / rows_in);
   const int64_t m0 = (int64_t)rt * S::BM, n0 = (int64_t)ct * S::BN;
-  const int mlast = (int)(M - 1 - m0), nlast = (int)(N - 1 - n0);   // rows past the end repeat the last one
+  const int mlast = (int)min((int64_t)S::BM, M - m0) - 1, nlast = (int)min((int64_t)S::BN, N - n0) - 1;   // rows past the end repeat the last one
+  const uint8_t* xt = A.x + m0 * rowx;
+  const uint8_t* wt = A.w + n0 * roww;
 
   // this lane's DMA sources: byte offsets from the tile's first row
-  uint32_t xoff[S::NX], woff[S::NWT], xc[S::NX], wc[S::NWT], soff[S::NSC];
+  uint32_t xoff[S::NX], woff[S::NWT];
+  const int cx = (lane % 8) ^ swz8(wave * 8 + lane / 8);              // its chunk of a row piece, the same for every i
+  const int cw = S::CW == 8 ? cx : (lane % 4) ^ swz4(lane / 4);
 #pragma unroll
   for (int i = 0; i < S::NX; ++i) {
-    const int p = (i * S::NW + wave) * 64 + lane, r = p / S::CA;
-    const int c = (p % S::CA) ^ (FP4A ? swz4(r) : swz8(r));
-    xc[i] = c * (FP4A ? 32 : 16);
-    xoff[i] = (uint32_t)min(r, mlast) * (uint32_t)rowa + c * 16;
+    const int r = (i * S::NW + wave) * 8 + lane / 8;                  // NW is 4 or 8: i * NW * 8 leaves the row's swizzle bits alone
+    xoff[i] = (uint32_t)min(r, mlast) * (uint32_t)rowx + cx * 16;
   }
 #pragma unroll
   for (int i = 0; i < S::NWT; ++i) {
-    const int p = (i * S::NW + wave) * 64 + lane, r = p / 4, c = (p % 4) ^ swz4(r);
-    wc[i] = c * 32;
-    woff[i] = (uint32_t)min(r, nlast) * (uint32_t)roww + c * 16;
+    const int r = (i * S::NW + wave) * (64 / S::CW) + lane / S::CW;
+    woff[i] = (uint32_t)min(r, nlast) * (uint32_t)roww + cw * 16;
   }
-  int sslot[S::NSC];
+  const uint8_t* srow[S::NSC];                                        // this lane's scale rows: activations, then weights
 #pragma unroll
   for (int i = 0; i < S::NSC; ++i) {
-    sslot[i] = min(i * S::NW + wave, (S::BM + S::BN) / 64 - 1);      // surplus wavefronts repeat the last slot
-    const int r = sslot[i] * 64 + lane;
-    soff[i] = (uint32_t)(sslot[i] < S::BM / 64 ? min(r, mlast) : min(r - S::BM, nlast)) * (uint32_t)nblk;
+    const int r = (i * S::NW + wave) * 64 + lane;
+    srow[i] = r < S::BM ? A.x_sc + (m0 + min(r, mlast)) * nblk : A.w_sc + (n0 + min(r - S::BM, nlast)) * nblk;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  const uint8_t* at = a + m0 * rowa;
-  const uint8_t* wt = w + n0 * roww;
-  const uint8_t* ast = a_sc + m0 * nblk;
-  const uint8_t* wst = w_sc + n0 * nblk;
+  const bool ragged = K % KS != 0;                                    // the last stage runs past K
   auto issue = [&](int s, uint32_t base) {
-    const bool cut = TAIL && s == ns - 1;                             // chunks past K read the stage's first chunk
+    if (ragged && s == ns - 1) {                                      // chunks past K read the stage's first chunk
 #pragma unroll
-    for (int i = 0; i < S::NX; ++i) {
-      const uint32_t off = cut && s * KS + (int)xc[i] >= K ? xoff[i] - xc[i] / (FP4A ? 2 : 1) : xoff[i];
-      dma16_to_lds(at + (int64_t)s * S::RA, off, base + (i * S::NW + wave) * 1024);
-    }
+      for (int i = 0; i < S::NX; ++i)
+        dma16_to_lds(xt + (int64_t)s * S::RA, s * KS + cx * (FP4A ? 32 : 16) < K ? xoff[i] : xoff[i] - cx * 16,
+                     base + (i * S::NW + wave) * 1024);
 #pragma unroll
-    for (int i = 0; i < S::NWT; ++i) {
-      const uint32_t off = cut && s * KS + (int)wc[i] >= K ? woff[i] - wc[i] / 2 : woff[i];
-      dma16_to_lds(wt + (int64_t)s * (KS / 2), off, base + S::OFF_W + (i * S::NW + wave) * 1024);
-    }
-    if (!TAIL) {
+      for (int i = 0; i < S::NWT; ++i)
+        dma16_to_lds(wt + (int64_t)s * S::RW, s * KS + cw * 32 < K ? woff[i] : woff[i] - cw * 16,
+                     base + S::OFF_W + (i * S::NW + wave) * 1024);
+    } else {
 #pragma unroll
-      for (int i = 0; i < S::NSC; ++i)
-        dma4_to_lds((sslot[i] < S::BM / 64 ? ast : wst) + s * 4, soff[i], base + S::OFF_XS + sslot[i] * 256);
+      for (int i = 0; i < S::NX; ++i)
+        dma16_to_lds(xt + (int64_t)s * S::RA, xoff[i], base + (i * S::NW + wave) * 1024);
+#pragma unroll
+      for (int i = 0; i < S::NWT; ++i)
+        dma16_to_lds(wt + (int64_t)s * S::RW, woff[i], base + S::OFF_W + (i * S::NW + wave) * 1024);
     }
   };
+  // Scales of K = 512 c + [0, 512) of this lane's rows, to the buffer c % 2: by DMA where the 16 bytes are the row's and
+  // dword-aligned, else through registers, written to LDS when the chunk is published (put).  Blocks past K get 127;
+  // the dword that holds a row's last blocks is read from the row's last four bytes (K >= 128), so no read leaves the
+  // row.  Rows start at any byte where K % 128 != 0.
+  u32x4 sreg[S::NSC];
+  auto by_dma = [&](int c) { return K % 128 == 0 && c * 16 + 16 <= nblk; };
+  auto fetch_scales = [&](int c) {
+    const int b0 = c * 16;
+    if (by_dma(c)) {
+#pragma unroll
+      for (int i = 0; i < S::NSC; ++i)
+        dma16_to_lds(srow[i] + b0, lds + S::OFF_S + (c & 1) * S::SCALES + (i * S::NW + wave) * 1024);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::NSC; ++i)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int at = min(b0 + 4 * d, nblk - 4), cut = b0 + 4 * d - at;
+          const uint32_t v = *reinterpret_cast<const u32_a1*>(srow[i] + at);
+          sreg[i][d] = cut == 0 ? v : cut < 4 ? (v >> (8 * cut)) | (0x7F7F7F7Fu << (32 - 8 * cut)) : 0x7F7F7F7Fu;
+        }
+    }
+  };
+  auto put_scales = [&](int c) {
+    if (by_dma(c)) return;
+#pragma unroll
+    for (int i = 0; i < S::NSC; ++i)
+      lds_write(lds0 + S::OFF_S + (c & 1) * S::SCALES + ((i * S::NW + wave) * 64 + lane) * 16, sreg[i]);
+  };
 
-  // Operands of one step, and the scale dwords of a stage shifted so that bytes 0 and 2 are the blocks of this lane's
-  // half in steps 0 and 1.
+  // Operands of one step, and the scale dwords of 128 of K shifted so that bytes 0 and 2 are the blocks of this lane's
+  // half in their two steps.
   struct Regs { u32x4 xlo[TM], xhi[FP4A ? 1 : TM], w[TN]; };
   struct Scales { uint32_t x[TM], w[TN]; };
   const uint32_t xrow = (uint32_t)(wm * TM * 32 + lr), wrow = (uint32_t)(wn * TN * 32 + lr);
-  const int fx = FP4A ? swz4(lr) : swz8(lr), fw = swz4(lr);
+  const uint32_t xp = xrow * S::RA + (g ^ swz8(lr)) * 16, wp = S::OFF_W + wrow * S::RW + (g ^ (S::CW == 8 ? swz8(lr) : swz4(lr))) * 16;
+  const uint32_t sp = lds0 + S::OFF_S + xrow * 16, sw = lds0 + S::OFF_S + (S::BM + wrow) * 16;
   constexpr int NLD = TN + TM * (FP4A ? 1 : 2), NMM = TM * TN;       // LDS reads and matrix operations of a step
-  // the it-th LDS read of step ks (weights first: every matrix operation row needs them)
+  // the it-th LDS read of step ks (weights first: every matrix operation row needs them); the step's chunk is an XOR
+  // of bits that the row leaves zero
   auto load1 = [&](Regs& R, uint32_t base, int ks, int it) {
-    if (it < TN) R.w[it] = lds_read16(base + S::OFF_W + wrow * 64 + ((2 * ks + g) ^ fw) * 16 + it * 2048);
-    else if (FP4A) R.xlo[it - TN] = lds_read16(base + xrow * S::RA + ((2 * ks + g) ^ fx) * 16 + (it - TN) * 32 * S::RA);
+    if (it < TN) R.w[it] = lds_read<u32x4>(base + (wp ^ (ks * 32)) + it * 32 * S::RW);
+    else if (FP4A) R.xlo[it - TN] = lds_read<u32x4>(base + (xp ^ (ks * 32)) + (it - TN) * 32 * S::RA);
     else {
       const int i = (it - TN) / 2;
-      if ((it - TN) % 2 == 0) R.xlo[i] = lds_read16(base + xrow * S::RA + ((4 * ks + g) ^ fx) * 16 + i * 32 * S::RA);
-      else R.xhi[i] = lds_read16(base + xrow * S::RA + ((4 * ks + 2 + g) ^ fx) * 16 + i * 32 * S::RA);
+      if ((it - TN) % 2 == 0) R.xlo[i] = lds_read<u32x4>(base + (xp ^ (ks * 64)) + i * 32 * S::RA);
+      else R.xhi[FP4A ? 0 : i] = lds_read<u32x4>(base + (xp ^ (ks * 64 + 32)) + i * 32 * S::RA);
     }
   };
-  auto load_scales = [&](Scales& C, uint32_t base) {
+  auto load_scales = [&](Scales& C, int k128) {                       // k128: K / 128
+    const uint32_t off = ((k128 >> 2) & 1) * S::SCALES + (k128 & 3) * 4;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) C.x[i] = lds_read4(base + S::OFF_XS + (xrow + i * 32) * 4);
+    for (int i = 0; i < TM; ++i) C.x[i] = lds_read<uint32_t>(sp + off + i * 32 * 16);
 #pragma unroll
-    for (int i = 0; i < TN; ++i) C.w[i] = lds_read4(base + S::OFF_WS + (wrow + i * 32) * 4);
+    for (int i = 0; i < TN; ++i) C.w[i] = lds_read<uint32_t>(sw + off + i * 32 * 16);
   };
   auto shift_scales = [&](Scales& C) {
 #pragma unroll
@@ -244,168 +284,183 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(const uint8_t
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  auto cut_step = [&](Regs& R, int s, int ks) {                       // zero elements past K (activations; E2M1 weights are finite)
-    const int b = s * 4 + 2 * ks;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      if (b + (FP4A ? g : 0) >= nblk) R.xlo[i] = u32x4{0, 0, 0, 0};
-      if (!FP4A && b + 1 >= nblk) R.xhi[FP4A ? 0 : i] = u32x4{0, 0, 0, 0};
-    }
-  };
-  auto mma = [&](const Regs& R, const Scales& C, auto step, int q) {   // the q-th matrix operation of step `step`
-    constexpr int B = 2 * decltype(step)::value;
+  auto mma = [&](const Regs& R, const Scales& C, auto half, int q) {  // the q-th matrix operation; half: step % 2
+    constexpr int B = 2 * decltype(half)::value;
     const int i = q / TN, j = q % TN;
     const v8i xv = FP4A ? operand(R.xlo[i]) : operand(R.xlo[i], R.xhi[FP4A ? 0 : i]);
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(R.w[j]), xv, acc[i][j], 4, FP4A ? 4 : 0, B,
                                                                 (int)C.w[j], B, (int)C.x[i]);
   };
-  // One step's matrix operations with the next step's LDS reads between them (the order is held by scheduling barriers).
-  auto step_with_loads = [&](const Regs& R, const Scales& C, auto step, Regs& Rn, uint32_t base, int ks) {
+  // One step's matrix operations with the next step's LDS reads between them.  The order is held by scheduling
+  // barriers inside a block of code, and by the empty statements at the end (no instruction) beyond it: without them
+  // the compiler moves the matrix operations past the next branch, behind the wait for the next stage.
+  auto step_with_loads = [&](const Regs& R, const Scales& C, auto half, Regs& Rn, uint32_t base, int ks) {
 #pragma unroll
     for (int q = 0; q < NMM; ++q) {
 #pragma unroll
       for (int it = q * NLD / NMM; it < (q + 1) * NLD / NMM; ++it) load1(Rn, base, ks, it);
-      mma(R, C, step, q);
+      mma(R, C, half, q);
       __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int q = 0; q < NMM; ++q) pin(acc[q / TN][q % TN]);
   };
-  const Int<0> Step0;
-  const Int<1> Step1;
+  const Int<0> even;
+  const Int<1> odd;
 
-  // K % 128 != 0: scale rows are not dword-aligned; each lane keeps its slots' next dword in registers and writes it
-  // to the stage's LDS before the barrier that publishes the stage (bytes past K: 127)
-  uint32_t sreg[S::NSC];
-  auto fetch_scales = [&](int s) {
+  // Zeros in the activations' chunks past K of the last stage, once they have landed (E2M1 weights are finite, so the
+  // products are zeros; E4M3 ones may not be).
+  auto cut = [&](uint32_t base) {
+    if ((ns - 1) * KS + cx * (FP4A ? 32 : 16) >= K)
 #pragma unroll
-    for (int i = 0; i < S::NSC; ++i) {
-      const uint8_t* p = (sslot[i] < S::BM / 64 ? ast : wst) + soff[i] + s * 4;
-      uint32_t v = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) v |= (uint32_t)(s * 4 + b < nblk ? p[b] : 127) << (8 * b);
-      sreg[i] = v;
-    }
-  };
-  auto put_scales = [&](uint32_t base) {
-#pragma unroll
-    for (int i = 0; i < S::NSC; ++i)
-      *reinterpret_cast<__attribute__((address_space(3))) uint32_t*>(base + S::OFF_XS + sslot[i] * 256 + lane * 4) = sreg[i];
+      for (int i = 0; i < S::NX; ++i) lds_write(base + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
   };
 
+  fetch_scales(0);
+  put_scales(0);
 #pragma unroll
   for (int s = 0; s < NST; ++s)
     if (s < ns) issue(s, lds0 + s * S::STAGE);
-  if (TAIL) {
-    fetch_scales(0);
-    put_scales(lds0);
-    if (ns > 1) fetch_scales(1);
-  }
-  if (TAIL) wait_vm<0>();
-  else wait_stages<S::NV, NST>(min(ns - 1, NST - 1));
+  if (K > SCK) fetch_scales(1);
+  if (ns >= NST) wait_vm<S::NV * (NST - 1)>();                        // the first stage and its scales
+  else wait_vm<0>();
+  if (ragged && ns == 1) cut(lds0);
   lds_barrier();
   Regs R0, R1;
   Scales C, Cn;
 #pragma unroll
   for (int it = 0; it < NLD; ++it) load1(R0, lds0, 0, it);
-  load_scales(C, lds0);
+  load_scales(C, 0);
   shift_scales(C);
-  if (TAIL && ns == 1) cut_step(R0, 0, 0);
   uint32_t b0 = lds0;
-  // Stage s: step 0 while step 1's operands are read; then the next stage's data is waited for and published, this
-  // stage's buffer (read out by every wavefront) refilled, and step 1 multiplies while the next stage's are read.
-  auto stage = [&](int s, auto refill) {
-    const uint32_t b1 = b0 + S::STAGE == lds0 + NST * S::STAGE ? lds0 : b0 + S::STAGE;
-    step_with_loads(R0, C, Step0, R1, b0, 1);
-    if (TAIL) {
-      put_scales(b1);
-      wait_vm<0>();
-    } else if (decltype(refill)::value) {
-      wait_vm<S::NV * (NST - 2)>();
-    } else {
-      wait_stages<S::NV, NST>(min(ns - 2 - s, NST - 2));
+  // Steps of stage s but the last one: multiply while the next step's operands are read.
+  auto inner = [&](int s) {
+#pragma unroll
+    for (int ks = 0; ks + 1 < STEPS; ++ks) {
+      if (ks % 2) {
+        load_scales(Cn, s * (KS / 128) + (ks + 1) / 2);
+        step_with_loads(R1, C, odd, R0, b0, ks + 1);
+        shift_scales(Cn);
+        C = Cn;
+      } else {
+        step_with_loads(R0, C, even, R1, b0, ks + 1);
+      }
     }
+  };
+  // Then the next stage's data is waited for and published, this stage's buffer (read out by every wavefront)
+  // refilled, and the last step multiplies while the next stage's first operands are read.
+  for (int s = 0; s + 1 < ns; ++s) {
+    const uint32_t b1 = b0 + S::STAGE == lds0 + NST * S::STAGE ? lds0 : b0 + S::STAGE;
+    inner(s);
+    const bool chunk = (s + 1) % S::SPC == 0;                         // the next stage starts a scale chunk
+    if (chunk) put_scales((s + 1) / S::SPC);
+    if (NST > 2 && s + NST < ns) wait_vm<S::NV * (NST - 2)>();        // all but the stages after the next one
+    else wait_vm<0>();
+    if (ragged && s + 2 == ns) cut(b1);
     lds_barrier();
-    if (decltype(refill)::value) issue(s + NST, b0);
-    if (TAIL && s + 2 < ns) fetch_scales(s + 2);
-    load_scales(Cn, b1);
+    if (s + NST < ns) issue(s + NST, b0);
+    if (chunk && ((s + 1) / S::SPC + 1) * SCK < K) fetch_scales((s + 1) / S::SPC + 1);
+    load_scales(Cn, (s + 1) * (KS / 128));
     __builtin_amdgcn_sched_barrier(0);
-    step_with_loads(R1, C, Step1, R0, b1, 0);
-    if (TAIL && s + 1 == ns - 1) cut_step(R0, s + 1, 0);
+    step_with_loads(R1, C, odd, R0, b1, 0);
     shift_scales(Cn);
     C = Cn;
     b0 = b1;
-  };
-  int s = 0;
-  for (; s + NST < ns; ++s) stage(s, Step1);
-  for (; s + 1 < ns; ++s) stage(s, Step0);
+  }
+  inner(ns - 1);
 #pragma unroll
-  for (int it = 0; it < NLD; ++it) load1(R1, b0, 1, it);
-  if (TAIL) cut_step(R1, s, 1);
-#pragma unroll
-  for (int q = 0; q < NMM; ++q) mma(R0, C, Step0, q);
-#pragma unroll
-  for (int q = 0; q < NMM; ++q) mma(R1, C, Step1, q);
+  for (int q = 0; q < NMM; ++q) mma(R1, C, odd, q);
 
-  const bool quads = (N & 3) == 0;
+  // Results.  Where rows of y are whole 16-byte pieces (N % 8 == 0 in bf16, % 4 in fp32) each wavefront turns 32 rows
+  // at a time in its own part of LDS, so that a store instruction writes whole runs of a row.
+  const int esz = A.bf16_out ? 2 : 4;
+  uint8_t* const y = static_cast<uint8_t*>(A.y);
+  constexpr int WC = TN * 32;                                         // columns of a wavefront
+  if (N % (16 / esz) == 0) {
+    constexpr uint32_t PITCH = WC * 4 + 16;                           // + 16: rows start on different banks
+    static_assert(S::NW * 32 * PITCH <= S::OFF_S, "epilogue LDS");
+    lds_barrier();                                                    // every wavefront has read its operands
+    const uint32_t mine = lds0 + wave * 32 * PITCH;
+    const int nw = (int)min((int64_t)WC, N - n0 - wn * WC);           // this wavefront's columns
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int64_t m = m0 + wm * TM * 32 + i * 32 + lr;
-    if (m >= M) continue;
+    for (int i = 0; i < TM; ++i) {
+      if (A.bf16_out) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + wn * TN * 32 + j * 32 + 8 * q + 4 * g;
-        const float v0 = acc[i][j][4 * q], v1 = acc[i][j][4 * q + 1], v2 = acc[i][j][4 * q + 2], v3 = acc[i][j][4 * q + 3];
-        if (quads) {
-          if (n >= N) continue;
-          if (bf16_out) {
-            const u32x2_a4 d = {(uint32_t)f32_to_bf16_rne(v0) | ((uint32_t)f32_to_bf16_rne(v1) << 16),
-                                (uint32_t)f32_to_bf16_rne(v2) | ((uint32_t)f32_to_bf16_rne(v3) << 16)};
-            *reinterpret_cast<u32x2_a4*>(static_cast<uint16_t*>(y) + m * N + n) = d;
-          } else {
-            *reinterpret_cast<f32x4_a4*>(static_cast<float*>(y) + m * N + n) = f32x4_a4{v0, v1, v2, v3};
+          for (int q = 0; q < 4; ++q) {
+            const v16f& c = acc[i][j];
+            const u32x2 d = {(uint32_t)f32_to_bf16_rne(c[4 * q]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 1]) << 16),
+                                (uint32_t)f32_to_bf16_rne(c[4 * q + 2]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 3]) << 16)};
+            lds_write(mine + lr * PITCH + (j * 32 + 8 * q + 4 * g) * 2, d);
           }
-        } else {
-          const float v[4] = {v0, v1, v2, v3};
+      } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < N) {
-              if (bf16_out) static_cast<uint16_t*>(y)[m * N + n + e] = f32_to_bf16_rne(v[e]);
-              else static_cast<float*>(y)[m * N + n + e] = v[e];
-            }
-        }
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v16f& c = acc[i][j];
+            lds_write(mine + lr * PITCH + (j * 32 + 8 * q + 4 * g) * 4,
+                      u32x4{__float_as_uint(c[4 * q]), __float_as_uint(c[4 * q + 1]), __float_as_uint(c[4 * q + 2]),
+                            __float_as_uint(c[4 * q + 3])});
+          }
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");              // the wavefront's own writes, in order
+      const int lpr = WC * esz / 16;                                  // lanes per row
+      const int64_t mb = m0 + wm * TM * 32 + i * 32;
+      for (int r = lane / lpr; r < 32; r += 64 / lpr) {
+        const int c = (lane % lpr) * (16 / esz);
+        const u32x4 d = lds_read<u32x4>(mine + r * PITCH + c * esz);
+        if (mb + r < M && c < nw) *reinterpret_cast<u32x4_a4*>(y + ((mb + r) * N + n0 + wn * WC + c) * esz) = d;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int64_t m = m0 + wm * TM * 32 + i * 32 + lr;
+      if (m >= M) continue;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t n = n0 + wn * WC + j * 32 + 8 * (r / 4) + 4 * g + r % 4;
+          if (n < N) {
+            if (A.bf16_out) reinterpret_cast<uint16_t*>(y)[m * N + n] = f32_to_bf16_rne(acc[i][j][r]);
+            else reinterpret_cast<float*>(y)[m * N + n] = acc[i][j][r];
+          }
+        }
+    }
   }
 }
 
 constexpr int FP4_TILE_MIN_M = 64;
 
 template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
-static void launch_tile(const uint8_t* a, const uint8_t* a_sc, const uint8_t* w, const uint8_t* w_sc, int M, int N, int K,
-                        void* y, bool bf16_out, hipStream_t stream) {
+static void launch_tile(const TileArgs& a, hipStream_t stream) {
   using S = TileShape<FP4A, WM, WN, TM, TN, NST>;
-  const int64_t tiles = (int64_t)((M + S::BM - 1) / S::BM) * ((N + S::BN - 1) / S::BN);
+  const int64_t tiles = (int64_t)((a.M + S::BM - 1) / S::BM) * ((a.N + S::BN - 1) / S::BN);
   const dim3 grid((unsigned)((tiles + XCDS - 1) / XCDS * XCDS)), block(64 * S::NW);
-  if (K % KS) hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, NST, true>), grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
-  else hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, NST, false>), grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
+  hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, NST>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
                            int M, int N, int K, void* y, bool bf16_out, hipStream_t stream, const char** variant) {
-  if (M >= FP4_TILE_MIN_M) {
+  if (M >= FP4_TILE_MIN_M && K >= 128) {
     const int64_t big = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
+    const TileArgs t{a, a_sc, w, w_sc, M, N, K, y, bf16_out};
     if (big >= 192) {
-      if (fp4a) launch_tile<true, 2, 4, 4, 2, 4>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
-      else launch_tile<false, 4, 2, 2, 4, 3>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
+      if (fp4a) launch_tile<true, 2, 4, 4, 2, 2>(t, stream);
+      else launch_tile<false, 4, 2, 2, 4, 3>(t, stream);
       *variant = fp4a ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
     } else {
-      if (fp4a) launch_tile<true, 2, 2, 2, 2, 4>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
-      else launch_tile<false, 2, 2, 2, 2, 3>(a, a_sc, w, w_sc, M, N, K, y, bf16_out, stream);
+      if (fp4a) launch_tile<true, 2, 2, 2, 2, 2>(t, stream);
+      else launch_tile<false, 2, 2, 2, 2, 3>(t, stream);
       *variant = fp4a ? "fp4:tile128x128_a4" : "fp4:tile128x128_a8";
     }
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 15) / 16)), block(256);
+  const dim3 grid((unsigned)((int64_t)((N + 63) / 64) * ((M + 15) / 16))), block(256);   // < 2^30: M N < 2^40
   if (fp4a) hipLaunchKernelGGL(fp4_rows_kernel<true>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
   else hipLaunchKernelGGL(fp4_rows_kernel<false>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
   *variant = fp4a ? "fp4:rows16_a4" : "fp4:rows16_a8";
