@@ -96,12 +96,21 @@ __global__ __launch_bounds__(256) void fp4_rows_kernel(const uint8_t* __restrict
 // with bits of the row so that 8 (and 16) consecutive rows' reads of one
 // chunk fall on different banks (no conflicts counted).
 typedef float v16f __attribute__((ext_vector_type(16)));
+
+// dma16_to_lds if on is -1, nothing if it is 0 (in a wavefront whose lanes are all active): an instruction that may
+// have nothing to do, without a branch around it.
+__device__ __forceinline__ void dma16_to_lds_if(int on, const void* base, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+               "global_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
+               :: "v"(off), "s"(base), "s"(dst), "s"(__builtin_amdgcn_readfirstlane(on)) : "m0");
+}
+
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 
 __device__ __forceinline__ int swz4(int r) { return (((r >> 1) ^ (r >> 3)) & 1) | ((r >> 1) & 2); }
-__device__ __forceinline__ int swz8(int r) { return ((r >> 1) & 3) | (((r ^ (r >> 3)) & 1) << 2); }
+__device__ __forceinline__ int swz8(int r) { return (r & 6) | ((r >> 3) & 1); }
 
 template <typename V> __device__ __forceinline__ V lds_read(uint32_t addr) {
   return *reinterpret_cast<const __attribute__((address_space(3))) V*>(addr);
@@ -126,18 +135,20 @@ constexpr int XCDS = 8;
 constexpr int SCK = 512;                          // K whose scales (16 bytes a row) are fetched at a time
 
 // WM x WN wavefronts of TM x TN 32 x 32 tiles each.
-template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
+template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
 struct TileShape {
   static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
-  static constexpr int KS = FP4A ? 256 : 128, STEPS = KS / 64;
-  static constexpr int RA = 128, RW = KS / 2;     // bytes of an activation / a weight row per stage
-  static constexpr int CW = RW / 16;              // chunks of a weight row
+  static constexpr int RA = FP4A ? KS / 2 : KS, RW = KS / 2;     // bytes of an activation / a weight row per stage
+  static constexpr int CA = RA / 16, CW = RW / 16;               // their chunks
   static constexpr uint32_t OFF_W = BM * RA, STAGE = OFF_W + BN * RW;
   static constexpr uint32_t OFF_S = STAGE * NST, SCALES = (BM + BN) * 16, LDS = OFF_S + 2 * SCALES;
   static constexpr int NX = BM * RA / 1024 / NW, NWT = BN * RW / 1024 / NW;   // DMA instructions per wavefront and stage
   static constexpr int NV = NX + NWT;
   static constexpr int NSC = (BM + BN) / 64 / NW; // scale rows per lane
   static constexpr int SPC = SCK / KS;            // stages per scale chunk
+  static constexpr int STEPS = KS / 64;
+  // DMA instructions of stage s + NST that go out in the last step of stage s; the others go out in step 0 of stage s + 1
+  static constexpr int FIRST = NST == 2 ? NV : NV / 2;
   static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * RW && NSC * NW * 64 == BM + BN, "whole rows");
   static_assert(LDS <= 160 * 1024 && NV * (NST - 1) < 63, "LDS and vmcnt");
 };
@@ -149,10 +160,9 @@ struct TileArgs {
   void* y; bool bf16_out;                         // [M][N]
 };
 
-template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
+template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
-  using S = TileShape<FP4A, WM, WN, TM, TN, NST>;
-  constexpr int KS = S::KS, STEPS = S::STEPS;
+  using S = TileShape<FP4A, WM, WN, TM, TN, KS, NST>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -176,11 +186,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
 
   // this lane's DMA sources: byte offsets from the tile's first row
   uint32_t xoff[S::NX], woff[S::NWT];
-  const int cx = (lane % 8) ^ swz8(wave * 8 + lane / 8);              // its chunk of a row piece, the same for every i
-  const int cw = S::CW == 8 ? cx : (lane % 4) ^ swz4(lane / 4);
+  const int c8 = (lane % 8) ^ swz8(wave * 8 + lane / 8), c4 = (lane % 4) ^ swz4(lane / 4);
+  const int cx = S::CA == 8 ? c8 : c4, cw = S::CW == 8 ? c8 : c4;     // its chunk of a row piece, the same for every i
 #pragma unroll
   for (int i = 0; i < S::NX; ++i) {
-    const int r = (i * S::NW + wave) * 8 + lane / 8;                  // NW is 4 or 8: i * NW * 8 leaves the row's swizzle bits alone
+    const int r = (i * S::NW + wave) * (64 / S::CA) + lane / S::CA;   // NW is 4 or 8: i leaves the row's swizzle bits alone
     xoff[i] = (uint32_t)min(r, mlast) * (uint32_t)rowx + cx * 16;
   }
 #pragma unroll
@@ -195,25 +205,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
     srow[i] = r < S::BM ? A.x_sc + (m0 + min(r, mlast)) * nblk : A.w_sc + (n0 + min(r - S::BM, nlast)) * nblk;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  const bool ragged = K % KS != 0;                                    // the last stage runs past K
-  auto issue = [&](int s, uint32_t base) {
-    if (ragged && s == ns - 1) {                                      // chunks past K read the stage's first chunk
-#pragma unroll
-      for (int i = 0; i < S::NX; ++i)
-        dma16_to_lds(xt + (int64_t)s * S::RA, s * KS + cx * (FP4A ? 32 : 16) < K ? xoff[i] : xoff[i] - cx * 16,
-                     base + (i * S::NW + wave) * 1024);
-#pragma unroll
-      for (int i = 0; i < S::NWT; ++i)
-        dma16_to_lds(wt + (int64_t)s * S::RW, s * KS + cw * 32 < K ? woff[i] : woff[i] - cw * 16,
-                     base + S::OFF_W + (i * S::NW + wave) * 1024);
-    } else {
-#pragma unroll
-      for (int i = 0; i < S::NX; ++i)
-        dma16_to_lds(xt + (int64_t)s * S::RA, xoff[i], base + (i * S::NW + wave) * 1024);
-#pragma unroll
-      for (int i = 0; i < S::NWT; ++i)
-        dma16_to_lds(wt + (int64_t)s * S::RW, woff[i], base + S::OFF_W + (i * S::NW + wave) * 1024);
-    }
+  const bool ragged = K % KS != 0;                                    // the last stage runs past K:
+  const uint32_t xback = ragged && (ns - 1) * KS + cx * (FP4A ? 32 : 16) >= K ? cx * 16 : 0;   // chunks past K read the
+  const uint32_t wback = ragged && (ns - 1) * KS + cw * 32 >= K ? cw * 16 : 0;                 // stage's first chunk
+  // The i-th DMA instruction of stage s, activations then weights; none of the lanes take part in stages past the last.
+  auto issue1 = [&](int s, uint32_t base, int i) {
+    const int on = (s - ns) >> 31;
+    if (i < S::NX)
+      dma16_to_lds_if(on, xt + (int64_t)s * S::RA, xoff[i < S::NX ? i : 0] - (s == ns - 1 ? xback : 0),
+                      base + (i * S::NW + wave) * 1024);
+    else
+      dma16_to_lds_if(on, wt + (int64_t)s * S::RW, woff[i < S::NX ? 0 : i - S::NX] - (s == ns - 1 ? wback : 0),
+                      base + S::OFF_W + ((i - S::NX) * S::NW + wave) * 1024);
   };
   // Scales of K = 512 c + [0, 512) of this lane's rows, to the buffer c % 2: by DMA where the 16 bytes are the row's and
   // dword-aligned, else through registers, written to LDS when the chunk is published (put).  Blocks past K get 127;
@@ -245,12 +248,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
       lds_write(lds0 + S::OFF_S + (c & 1) * S::SCALES + ((i * S::NW + wave) * 64 + lane) * 16, sreg[i]);
   };
 
-  // Operands of one step, and the scale dwords of 128 of K shifted so that bytes 0 and 2 are the blocks of this lane's
+  // Operands of one step; the scale dwords of 256 of K (read from LDS in pairs: dword reads of rows 16 bytes apart meet on
+  // a quarter of the banks), and those of the current 128, shifted so that bytes 0 and 2 are the blocks of this lane's
   // half in their two steps.
   struct Regs { u32x4 xlo[TM], xhi[FP4A ? 1 : TM], w[TN]; };
+  struct Pairs { u32x2 x[TM], w[TN]; };
   struct Scales { uint32_t x[TM], w[TN]; };
   const uint32_t xrow = (uint32_t)(wm * TM * 32 + lr), wrow = (uint32_t)(wn * TN * 32 + lr);
-  const uint32_t xp = xrow * S::RA + (g ^ swz8(lr)) * 16, wp = S::OFF_W + wrow * S::RW + (g ^ (S::CW == 8 ? swz8(lr) : swz4(lr))) * 16;
+  const uint32_t xp = xrow * S::RA + (g ^ (S::CA == 8 ? swz8(lr) : swz4(lr))) * 16, wp = S::OFF_W + wrow * S::RW + (g ^ (S::CW == 8 ? swz8(lr) : swz4(lr))) * 16;
   const uint32_t sp = lds0 + S::OFF_S + xrow * 16, sw = lds0 + S::OFF_S + (S::BM + wrow) * 16;
   constexpr int NLD = TN + TM * (FP4A ? 1 : 2), NMM = TM * TN;       // LDS reads and matrix operations of a step
   // the it-th LDS read of step ks (weights first: every matrix operation row needs them); the step's chunk is an XOR
@@ -264,18 +269,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
       else R.xhi[FP4A ? 0 : i] = lds_read<u32x4>(base + (xp ^ (ks * 64 + 32)) + i * 32 * S::RA);
     }
   };
-  auto load_scales = [&](Scales& C, int k128) {                       // k128: K / 128
-    const uint32_t off = ((k128 >> 2) & 1) * S::SCALES + (k128 & 3) * 4;
+  auto load_pairs = [&](Pairs& H, int k256) {                         // of K = 256 k256 + [0, 256)
+    const uint32_t off = ((k256 >> 1) & 1) * S::SCALES + (k256 & 1) * 8;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) C.x[i] = lds_read<uint32_t>(sp + off + i * 32 * 16);
+    for (int i = 0; i < TM; ++i) H.x[i] = lds_read<u32x2>(sp + off + i * 32 * 16);
 #pragma unroll
-    for (int i = 0; i < TN; ++i) C.w[i] = lds_read<uint32_t>(sw + off + i * 32 * 16);
+    for (int i = 0; i < TN; ++i) H.w[i] = lds_read<u32x2>(sw + off + i * 32 * 16);
   };
-  auto shift_scales = [&](Scales& C) {
+  auto second = [&](Pairs& H) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) C.x[i] >>= 8 * g;
+    for (int i = 0; i < TM; ++i) H.x[i][0] = H.x[i][1];
 #pragma unroll
-    for (int i = 0; i < TN; ++i) C.w[i] >>= 8 * g;
+    for (int i = 0; i < TN; ++i) H.w[i][0] = H.w[i][1];
+  };
+  auto take = [&](Scales& C, const Pairs& H) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) C.x[i] = H.x[i][0] >> (8 * g);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) C.w[i] = H.w[i][0] >> (8 * g);
   };
   v16f acc[TM][TN];
 #pragma unroll
@@ -291,16 +302,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(R.w[j]), xv, acc[i][j], 4, FP4A ? 4 : 0, B,
                                                                 (int)C.w[j], B, (int)C.x[i]);
   };
-  // One step's matrix operations with the next step's LDS reads between them.  The order is held by scheduling
-  // barriers inside a block of code, and by the empty statements at the end (no instruction) beyond it: without them
-  // the compiler moves the matrix operations past the next branch, behind the wait for the next stage.
-  auto step_with_loads = [&](const Regs& R, const Scales& C, auto half, Regs& Rn, uint32_t base, int ks) {
+  // One step's matrix operations with the next step's LDS reads and DMA instructions [d0, d1) of stage sd between them:
+  // a wavefront stalls at a DMA instruction while the memory path is still taking its last ones, so they come one at a
+  // time.  The order is held by scheduling barriers inside a block of code, and by the empty statements at the end (no
+  // instruction) beyond it: without them the compiler moves the matrix operations past the next branch, behind the
+  // wait for the next stage.
+  auto step = [&](const Regs& R, const Scales& C, auto half, Regs& Rn, uint32_t base, int ks, int sd, uint32_t based,
+                  int d0, int d1) {
 #pragma unroll
     for (int q = 0; q < NMM; ++q) {
 #pragma unroll
       for (int it = q * NLD / NMM; it < (q + 1) * NLD / NMM; ++it) load1(Rn, base, ks, it);
       mma(R, C, half, q);
       __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int it = d0 + q * (d1 - d0) / NMM; it < d0 + (q + 1) * (d1 - d0) / NMM; ++it) issue1(sd, based, it);
     }
 #pragma unroll
     for (int q = 0; q < NMM; ++q) pin(acc[q / TN][q % TN]);
@@ -320,54 +336,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   put_scales(0);
 #pragma unroll
   for (int s = 0; s < NST; ++s)
-    if (s < ns) issue(s, lds0 + s * S::STAGE);
+#pragma unroll
+    for (int i = 0; i < (s + 1 < NST ? S::NV : S::FIRST); ++i) issue1(s, lds0 + s * S::STAGE, i);
   if (K > SCK) fetch_scales(1);
-  if (ns >= NST) wait_vm<S::NV * (NST - 1)>();                        // the first stage and its scales
+  if (ns >= NST) wait_vm<S::NV * (NST - 2) + S::FIRST>();             // the first stage and its scales
   else wait_vm<0>();
   if (ragged && ns == 1) cut(lds0);
   lds_barrier();
   Regs R0, R1;
-  Scales C, Cn;
+  Pairs H;
+  Scales C;
 #pragma unroll
   for (int it = 0; it < NLD; ++it) load1(R0, lds0, 0, it);
-  load_scales(C, 0);
-  shift_scales(C);
-  uint32_t b0 = lds0;
-  // Steps of stage s but the last one: multiply while the next step's operands are read.
+  load_pairs(H, 0);
+  take(C, H);
+  uint32_t bp = lds0 + (NST - 1) * S::STAGE, b0 = lds0;               // buffers of stages s - 1 and s
+  // steps 0 .. STEPS - 2 of stage s, with what is left of the DMA of stage s - 1 + NST into the buffer of stage s - 1
   auto inner = [&](int s) {
-#pragma unroll
-    for (int ks = 0; ks + 1 < STEPS; ++ks) {
-      if (ks % 2) {
-        load_scales(Cn, s * (KS / 128) + (ks + 1) / 2);
-        step_with_loads(R1, C, odd, R0, b0, ks + 1);
-        shift_scales(Cn);
-        C = Cn;
-      } else {
-        step_with_loads(R0, C, even, R1, b0, ks + 1);
-      }
+    step(R0, C, even, R1, b0, 1, s - 1 + NST, bp, S::FIRST, S::NV);
+    if (S::STEPS == 4) {
+      second(H);
+      step(R1, C, odd, R0, b0, 2, 0, 0, 0, 0);
+      take(C, H);
+      step(R0, C, even, R1, b0, 3, 0, 0, 0, 0);
     }
   };
-  // Then the next stage's data is waited for and published, this stage's buffer (read out by every wavefront)
-  // refilled, and the last step multiplies while the next stage's first operands are read.
   for (int s = 0; s + 1 < ns; ++s) {
     const uint32_t b1 = b0 + S::STAGE == lds0 + NST * S::STAGE ? lds0 : b0 + S::STAGE;
     inner(s);
+    // the next stage's data is waited for and published; this stage's buffer has been read out by every wavefront
     const bool chunk = (s + 1) % S::SPC == 0;                         // the next stage starts a scale chunk
     if (chunk) put_scales((s + 1) / S::SPC);
-    if (NST > 2 && s + NST < ns) wait_vm<S::NV * (NST - 2)>();        // all but the stages after the next one
+    if (NST > 2 && s + NST - 1 < ns) wait_vm<S::NV * (NST - 2)>();    // all but the stages after the next one
     else wait_vm<0>();
     if (ragged && s + 2 == ns) cut(b1);
     lds_barrier();
-    if (s + NST < ns) issue(s + NST, b0);
     if (chunk && ((s + 1) / S::SPC + 1) * SCK < K) fetch_scales((s + 1) / S::SPC + 1);
-    load_scales(Cn, (s + 1) * (KS / 128));
-    __builtin_amdgcn_sched_barrier(0);
-    step_with_loads(R1, C, odd, R0, b1, 0);
-    shift_scales(Cn);
-    C = Cn;
+    if (KS == 256) load_pairs(H, s + 1);
+    else if (s % 2) load_pairs(H, (s + 1) / 2);
+    else second(H);
+    step(R1, C, odd, R0, b1, 0, s + NST, b0, 0, S::FIRST);
+    take(C, H);
+    bp = b0;
     b0 = b1;
   }
-  inner(ns - 1);
+  inner(ns);                                                          // of stage ns - 1; no DMA is left
 #pragma unroll
   for (int q = 0; q < NMM; ++q) mma(R1, C, odd, q);
 
@@ -436,12 +449,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
 
 constexpr int FP4_TILE_MIN_M = 64;
 
-template <bool FP4A, int WM, int WN, int TM, int TN, int NST>
+template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
 static void launch_tile(const TileArgs& a, hipStream_t stream) {
-  using S = TileShape<FP4A, WM, WN, TM, TN, NST>;
+  using S = TileShape<FP4A, WM, WN, TM, TN, KS, NST>;
   const int64_t tiles = (int64_t)((a.M + S::BM - 1) / S::BM) * ((a.N + S::BN - 1) / S::BN);
   const dim3 grid((unsigned)((tiles + XCDS - 1) / XCDS * XCDS)), block(64 * S::NW);
-  hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, NST>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, KS, NST>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
@@ -450,12 +463,12 @@ hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, con
     const int64_t big = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
     const TileArgs t{a, a_sc, w, w_sc, M, N, K, y, bf16_out};
     if (big >= 192) {
-      if (fp4a) launch_tile<true, 2, 4, 4, 2, 2>(t, stream);
-      else launch_tile<false, 4, 2, 2, 4, 3>(t, stream);
+      if (fp4a) launch_tile<true, 2, 4, 4, 2, 256, 2>(t, stream);
+      else launch_tile<false, 4, 2, 2, 4, 128, 3>(t, stream);
       *variant = fp4a ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
     } else {
-      if (fp4a) launch_tile<true, 2, 2, 2, 2, 2>(t, stream);
-      else launch_tile<false, 2, 2, 2, 2, 3>(t, stream);
+      if (fp4a) launch_tile<true, 2, 2, 2, 2, 256, 2>(t, stream);
+      else launch_tile<false, 2, 2, 2, 2, 128, 3>(t, stream);
       *variant = fp4a ? "fp4:tile128x128_a4" : "fp4:tile128x128_a8";
     }
     return hipGetLastError();
