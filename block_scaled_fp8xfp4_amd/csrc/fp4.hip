@@ -20,49 +20,124 @@ __device__ __forceinline__ v4f mfma_fp4_fp4(const v8i& a, const v8i& b, v4f c, u
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// Few rows: one wavefront per 16 columns and 16 rows, operands straight to
-// registers.  Lane l serves row / column l % 16; lanes past M or N repeat the
-// last row / column, their results are not stored.  K past the end is zero
-// elements under scale 1.
+// Few rows: one wavefront per 16 x 16 tile, operands straight to registers,
+// RING pieces of K = 512 in flight per wavefront: with one wavefront per CU
+// (N = 4096) that is what it takes to keep HBM busy.  Wavefronts of one
+// workgroup are the row tiles of the same 16 columns; they meet at the
+// weights in L1.  Lane l serves row / column l % 16; lanes past M or N repeat
+// the last row / column, their results are not stored.  K past the last whole
+// piece is read with clamped addresses and zeroed, its scales past K are 127.
+typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
+
+constexpr int RPK = 512;                          // K per piece: four 16x16x128 steps
+
+template <bool FP4A> struct RowsPiece { u32x4 w[4], alo[4], ahi[FP4A ? 1 : 4], ws, as; };
+
 template <bool FP4A>
-__global__ __launch_bounds__(256) void fp4_rows_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_sc,
-                                                       const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_sc,
-                                                       int M, int N, int K, void* __restrict__ y, bool bf16_out) {
+__device__ __forceinline__ void rows_load(RowsPiece<FP4A>& P, const uint8_t* wp, const uint8_t* wsp, const uint8_t* ap,
+                                          const uint8_t* asp, int c, int g) {
+  P.as = *reinterpret_cast<const u32x4_a1*>(asp + c * 16);
+  P.ws = *reinterpret_cast<const u32x4_a1*>(wsp + c * 16);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if (FP4A) P.alo[s] = ldg16(ap + c * 256 + s * 64 + g * 16);
+    else {
+      P.alo[s] = ldg16(ap + c * 512 + s * 128 + g * 16);
+      P.ahi[FP4A ? 0 : s] = ldg16(ap + c * 512 + s * 128 + 64 + g * 16);
+    }
+    P.w[s] = ldg16(wp + c * 256 + s * 64 + g * 16);
+  }
+}
+
+// The piece that K ends in: blocks past K are read from the last block and replaced.
+template <bool FP4A>
+__device__ __forceinline__ void rows_load_tail(RowsPiece<FP4A>& P, const uint8_t* wp, const uint8_t* wsp,
+                                               const uint8_t* ap, const uint8_t* asp, int c, int g, int nblk) {
+  const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int b = c * 16 + s * 4 + g, bc = min(b, nblk - 1);
+    const u32x4 w = ldg16(wp + bc * 16);
+    P.w[s] = b < nblk ? w : zero;
+    P.ws[s] = (b < nblk ? (uint32_t)wsp[bc] : 127u) << (8 * g);
+    P.as[s] = (b < nblk ? (uint32_t)asp[bc] : 127u) << (8 * g);
+    if (FP4A) {
+      const u32x4 a = ldg16(ap + bc * 16);
+      P.alo[s] = b < nblk ? a : zero;
+    } else {                                                          // halves of 16: K = k0 + 16 g and k0 + 64 + 16 g
+      const int k = (c * 4 + s) * KSTEP + 16 * g, K = nblk * 32;
+      const u32x4 lo = ldg16(ap + min(k, K - 16)), hi = ldg16(ap + min(k + 64, K - 16));
+      P.alo[s] = k < K ? lo : zero;
+      P.ahi[FP4A ? 0 : s] = k + 64 < K ? hi : zero;
+    }
+  }
+}
+
+template <bool FP4A>
+__device__ __forceinline__ v4f rows_multiply(const RowsPiece<FP4A>& P, v4f acc, int g) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const v8i w = {(int)P.w[s][0], (int)P.w[s][1], (int)P.w[s][2], (int)P.w[s][3], 0, 0, 0, 0};
+    const u32x4 lo = P.alo[s], hi = FP4A ? u32x4{0, 0, 0, 0} : P.ahi[FP4A ? 0 : s];
+    const v8i a = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    const uint32_t sa = P.as[s] >> (8 * g), sb = P.ws[s] >> (8 * g);
+    acc = FP4A ? mfma_fp4_fp4(a, w, acc, sa, sb) : mfma_fp8_fp4(a, w, acc, sa, sb);
+  }
+  return acc;
+}
+
+// The 16 x 16 tile of rows ap (this lane's row) and columns wp (its column) over all of K.
+template <bool FP4A>
+__device__ __forceinline__ v4f rows_tile(const uint8_t* ap, const uint8_t* asp, const uint8_t* wp, const uint8_t* wsp,
+                                         int K, int g) {
+  constexpr int RING = FP4A ? 5 : 4;              // 40 and 56 registers each
+  const int nblk = K / 32, whole = K / RPK;
+  RowsPiece<FP4A> P[RING], T;
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  int c = 0;
+  if (whole >= RING) {
+#pragma unroll
+    for (int r = 0; r < RING; ++r) rows_load(P[r], wp, wsp, ap, asp, r, g);
+    for (; c + 2 * RING <= whole; c += RING)
+#pragma unroll
+      for (int r = 0; r < RING; ++r) {
+        acc = rows_multiply(P[r], acc, g);
+        rows_load(P[r], wp, wsp, ap, asp, c + RING + r, g);
+      }
+#pragma unroll
+    for (int r = 0; r < RING; ++r) {                                  // the last whole pieces but fewer than RING
+      acc = rows_multiply(P[r], acc, g);
+      if (c + RING + r < whole) rows_load(P[r], wp, wsp, ap, asp, c + RING + r, g);
+    }
+    c += RING;
+  } else {
+#pragma unroll
+    for (int r = 0; r + 1 < RING; ++r)
+      if (r < whole) rows_load(P[r], wp, wsp, ap, asp, r, g);
+  }
+  if (K % RPK) rows_load_tail(T, wp, wsp, ap, asp, whole, g, nblk);
+#pragma unroll
+  for (int r = 0; r + 1 < RING; ++r)
+    if (c + r < whole) acc = rows_multiply(P[r], acc, g);
+  if (K % RPK) acc = rows_multiply(T, acc, g);
+  return acc;
+}
+
+constexpr int ROWS_MAX = 64;                      // rows of one workgroup: 4 wavefronts
+
+template <bool FP4A>
+__global__ __launch_bounds__(256, 2) void fp4_rows_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_sc,
+                                                          const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_sc,
+                                                          int M, int N, int K, void* __restrict__ y, bool bf16_out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, g = lane >> 4;
-  const uint32_t nct = (N + 63) / 64;                            // workgroups per row tile
-  const int64_t n0 = ((int64_t)(blockIdx.x % nct) * 4 + wave) * 16;
-  const int64_t m0 = (int64_t)(blockIdx.x / nct) * 16;
-  if (n0 >= N) return;
-  const int64_t n = n0 + col < N ? n0 + col : N - 1, m = m0 + col < M ? m0 + col : M - 1;
+  const uint32_t nct = (N + 15) / 16;
+  const int64_t n0 = (int64_t)(blockIdx.x % nct) * 16;
+  const int64_t m0 = (int64_t)(blockIdx.x / nct) * ROWS_MAX + wave * 16;
+  if (m0 >= M) return;
+  const int64_t n = min(n0 + col, (int64_t)N - 1), m = min(m0 + col, (int64_t)M - 1);
   const int nblk = K / 32;
-  const uint8_t* wp = w + n * (K / 2);
-  const uint8_t* wsp = w_sc + n * nblk;
-  const uint8_t* ap = a + m * (FP4A ? K / 2 : K);
-  const uint8_t* asp = a_sc + m * nblk;
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < K; k += KSTEP) {
-    v8i av = {0, 0, 0, 0, 0, 0, 0, 0}, bv = {0, 0, 0, 0, 0, 0, 0, 0};
-    uint32_t sa = 127, sb = 127;
-    const int blk = k / 32 + g;
-    if (blk < nblk) {
-      const u32x4 d = ldg16(wp + blk * 16);
-      bv = v8i{(int)d[0], (int)d[1], (int)d[2], (int)d[3], 0, 0, 0, 0};
-      sb = wsp[blk];
-      sa = asp[blk];
-      if (FP4A) {
-        const u32x4 e = ldg16(ap + blk * 16);
-        av = v8i{(int)e[0], (int)e[1], (int)e[2], (int)e[3], 0, 0, 0, 0};
-      }
-    }
-    if (!FP4A) {
-      u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-      if (k + 16 * g < K) lo = ldg16(ap + k + 16 * g);
-      if (k + 64 + 16 * g < K) hi = ldg16(ap + k + 64 + 16 * g);
-      av = v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-    }
-    acc = FP4A ? mfma_fp4_fp4(av, bv, acc, sa, sb) : mfma_fp8_fp4(av, bv, acc, sa, sb);
-  }
+  const v4f acc = rows_tile<FP4A>(a + m * (FP4A ? K / 2 : K), a_sc + m * nblk, w + n * (K / 2), w_sc + n * nblk, K, g);
   if (n0 + col < N)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -102,7 +177,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void dma16_to_lds_if(int on, const void* base, uint32_t off, uint32_t dst) {
   asm volatile("s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
                "global_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
-               :: "v"(off), "s"(base), "s"(dst), "s"(__builtin_amdgcn_readfirstlane(on)) : "m0");
+               :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(dst)), "s"(__builtin_amdgcn_readfirstlane(on)) : "m0");
 }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -126,7 +201,12 @@ __device__ __forceinline__ v8i operand(const u32x4& lo, const u32x4& hi) {
 }
 
 // Holds the computation of v before what follows (no instruction).
-__device__ __forceinline__ void pin(v16f& v) { asm volatile("" : "+v"(v)); }
+// ACC: v lives in the accumulation registers, which the compiler uses for
+// kernels that LDS limits to one wavefront per SIMD (512 registers each).
+template <bool ACC> __device__ __forceinline__ void pin(v16f& v) {
+  if (ACC) asm volatile("" : "+a"(v));
+  else asm volatile("" : "+v"(v));
+}
 
 template <int V> struct Int { static constexpr int value = V; };
 template <int N> __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
@@ -140,16 +220,17 @@ struct TileShape {
   static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
   static constexpr int RA = FP4A ? KS / 2 : KS, RW = KS / 2;     // bytes of an activation / a weight row per stage
   static constexpr int CA = RA / 16, CW = RW / 16;               // their chunks
+  static constexpr int NSC = (BM + BN + 64 * NW - 1) / (64 * NW);     // scale rows per lane (surplus ones repeat the last)
   static constexpr uint32_t OFF_W = BM * RA, STAGE = OFF_W + BN * RW;
-  static constexpr uint32_t OFF_S = STAGE * NST, SCALES = (BM + BN) * 16, LDS = OFF_S + 2 * SCALES;
+  static constexpr uint32_t OFF_S = STAGE * NST, SCALES = NSC * NW * 1024, LDS = OFF_S + 2 * SCALES;
   static constexpr int NX = BM * RA / 1024 / NW, NWT = BN * RW / 1024 / NW;   // DMA instructions per wavefront and stage
   static constexpr int NV = NX + NWT;
-  static constexpr int NSC = (BM + BN) / 64 / NW; // scale rows per lane
   static constexpr int SPC = SCK / KS;            // stages per scale chunk
   static constexpr int STEPS = KS / 64;
+  static constexpr bool ACC = NW * (160 * 1024 / LDS) < 8;        // fewer than 2 wavefronts per SIMD
   // DMA instructions of stage s + NST that go out in the last step of stage s; the others go out in step 0 of stage s + 1
   static constexpr int FIRST = NST == 2 ? NV : NV / 2;
-  static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * RW && NSC * NW * 64 == BM + BN, "whole rows");
+  static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * RW, "whole rows");
   static_assert(LDS <= 160 * 1024 && NV * (NST - 1) < 63, "LDS and vmcnt");
 };
 
@@ -187,16 +268,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   // this lane's DMA sources: byte offsets from the tile's first row
   uint32_t xoff[S::NX], woff[S::NWT];
   const int c8 = (lane % 8) ^ swz8(wave * 8 + lane / 8), c4 = (lane % 4) ^ swz4(lane / 4);
-  const int cx = S::CA == 8 ? c8 : c4, cw = S::CW == 8 ? c8 : c4;     // its chunk of a row piece, the same for every i
+  auto cx = [&](int i) { return S::CA == 8 ? c8 ^ (S::NW & i & 1) : c4; };   // its chunk of a row piece in instruction i
+  auto cw = [&](int i) { return S::CW == 8 ? c8 ^ (S::NW & i & 1) : c4; };   // (an odd NW changes the row's bit 3 with i)
 #pragma unroll
   for (int i = 0; i < S::NX; ++i) {
-    const int r = (i * S::NW + wave) * (64 / S::CA) + lane / S::CA;   // NW is 4 or 8: i leaves the row's swizzle bits alone
-    xoff[i] = (uint32_t)min(r, mlast) * (uint32_t)rowx + cx * 16;
+    const int r = (i * S::NW + wave) * (64 / S::CA) + lane / S::CA;
+    xoff[i] = (uint32_t)min(r, mlast) * (uint32_t)rowx + cx(i) * 16;
   }
 #pragma unroll
   for (int i = 0; i < S::NWT; ++i) {
     const int r = (i * S::NW + wave) * (64 / S::CW) + lane / S::CW;
-    woff[i] = (uint32_t)min(r, nlast) * (uint32_t)roww + cw * 16;
+    woff[i] = (uint32_t)min(r, nlast) * (uint32_t)roww + cw(i) * 16;
   }
   const uint8_t* srow[S::NSC];                                        // this lane's scale rows: activations, then weights
 #pragma unroll
@@ -205,17 +287,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
     srow[i] = r < S::BM ? A.x_sc + (m0 + min(r, mlast)) * nblk : A.w_sc + (n0 + min(r - S::BM, nlast)) * nblk;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  const bool ragged = K % KS != 0;                                    // the last stage runs past K:
-  const uint32_t xback = ragged && (ns - 1) * KS + cx * (FP4A ? 32 : 16) >= K ? cx * 16 : 0;   // chunks past K read the
-  const uint32_t wback = ragged && (ns - 1) * KS + cw * 32 >= K ? cw * 16 : 0;                 // stage's first chunk
+  const bool ragged = K % KS != 0;                                    // the last stage runs past K: chunks past K
+  auto xpast = [&](int i) { return (ns - 1) * KS + cx(i) * (FP4A ? 32 : 16) >= K; };           // read the stage's first
+  auto wpast = [&](int i) { return (ns - 1) * KS + cw(i) * 32 >= K; };                         // chunk of their row
   // The i-th DMA instruction of stage s, activations then weights; none of the lanes take part in stages past the last.
   auto issue1 = [&](int s, uint32_t base, int i) {
     const int on = (s - ns) >> 31;
     if (i < S::NX)
-      dma16_to_lds_if(on, xt + (int64_t)s * S::RA, xoff[i < S::NX ? i : 0] - (s == ns - 1 ? xback : 0),
+      dma16_to_lds_if(on, xt + (int64_t)s * S::RA, xoff[i < S::NX ? i : 0] - (s == ns - 1 && xpast(i) ? cx(i) * 16 : 0),
                       base + (i * S::NW + wave) * 1024);
     else
-      dma16_to_lds_if(on, wt + (int64_t)s * S::RW, woff[i < S::NX ? 0 : i - S::NX] - (s == ns - 1 ? wback : 0),
+      dma16_to_lds_if(on, wt + (int64_t)s * S::RW, woff[i < S::NX ? 0 : i - S::NX] - (s == ns - 1 && wpast(i - S::NX) ? cw(i - S::NX) * 16 : 0),
                       base + S::OFF_W + ((i - S::NX) * S::NW + wave) * 1024);
   };
   // Scales of K = 512 c + [0, 512) of this lane's rows, to the buffer c % 2: by DMA where the 16 bytes are the row's and
@@ -319,7 +401,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
       for (int it = d0 + q * (d1 - d0) / NMM; it < d0 + (q + 1) * (d1 - d0) / NMM; ++it) issue1(sd, based, it);
     }
 #pragma unroll
-    for (int q = 0; q < NMM; ++q) pin(acc[q / TN][q % TN]);
+    for (int q = 0; q < NMM; ++q) pin<S::ACC>(acc[q / TN][q % TN]);
   };
   const Int<0> even;
   const Int<1> odd;
@@ -327,9 +409,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   // Zeros in the activations' chunks past K of the last stage, once they have landed (E2M1 weights are finite, so the
   // products are zeros; E4M3 ones may not be).
   auto cut = [&](uint32_t base) {
-    if ((ns - 1) * KS + cx * (FP4A ? 32 : 16) >= K)
 #pragma unroll
-      for (int i = 0; i < S::NX; ++i) lds_write(base + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
+    for (int i = 0; i < S::NX; ++i)
+      if (xpast(i)) lds_write(base + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
   };
 
   fetch_scales(0);
@@ -447,7 +529,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   }
 }
 
-constexpr int FP4_TILE_MIN_M = 64;
+constexpr int FP4_TILE_MIN_M = 65;
 
 template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
 static void launch_tile(const TileArgs& a, hipStream_t stream) {
@@ -460,8 +542,8 @@ static void launch_tile(const TileArgs& a, hipStream_t stream) {
 hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
                            int M, int N, int K, void* y, bool bf16_out, hipStream_t stream, const char** variant) {
   if (M >= FP4_TILE_MIN_M && K >= 128) {
-    const int64_t big = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
     const TileArgs t{a, a_sc, w, w_sc, M, N, K, y, bf16_out};
+    const int64_t big = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
     if (big >= 192) {
       if (fp4a) launch_tile<true, 2, 4, 4, 2, 256, 2>(t, stream);
       else launch_tile<false, 4, 2, 2, 4, 128, 3>(t, stream);
@@ -473,7 +555,8 @@ hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, con
     }
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)((int64_t)((N + 63) / 64) * ((M + 15) / 16))), block(256);   // < 2^30: M N < 2^40
+  const dim3 grid((unsigned)((int64_t)((N + 15) / 16) * ((M + ROWS_MAX - 1) / ROWS_MAX)));   // about M N / 2^10 < 2^31
+  const dim3 block(64 * (M < ROWS_MAX ? (M + 15) / 16 : 4));
   if (fp4a) hipLaunchKernelGGL(fp4_rows_kernel<true>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
   else hipLaunchKernelGGL(fp4_rows_kernel<false>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
   *variant = fp4a ? "fp4:rows16_a4" : "fp4:rows16_a8";
