@@ -90,7 +90,7 @@ __device__ __forceinline__ v4f rows_multiply(const RowsPiece<FP4A>& P, v4f acc, 
 template <bool FP4A>
 __device__ __forceinline__ v4f rows_tile(const uint8_t* ap, const uint8_t* asp, const uint8_t* wp, const uint8_t* wsp,
                                          int K, int g) {
-  constexpr int RING = FP4A ? 5 : 4;              // 40 and 56 registers each
+  constexpr int RING = FP4A ? 4 : 3;              // 40 and 56 registers each, and one more of them
   const int nblk = K / 32, whole = K / RPK;
   RowsPiece<FP4A> P[RING], T;
   v4f acc = {0.f, 0.f, 0.f, 0.f};
@@ -229,7 +229,8 @@ struct TileShape {
   static constexpr int STEPS = KS / 64;
   static constexpr bool ACC = NW * (160 * 1024 / LDS) < 8;        // fewer than 2 wavefronts per SIMD
   // DMA instructions of stage s + NST that go out in the last step of stage s; the others go out in step 0 of stage s + 1
-  static constexpr int FIRST = NST == 2 ? NV : NV / 2;
+  static constexpr bool WHOLE = TM * TN <= 2;     // small tiles: whole stages of operands in registers
+  static constexpr int FIRST = NST == 2 || WHOLE ? NV : NV / 2;
   static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * RW, "whole rows");
   static_assert(LDS <= 160 * 1024 && NV * (NST - 1) < 63, "LDS and vmcnt");
 };
@@ -291,14 +292,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   auto xpast = [&](int i) { return (ns - 1) * KS + cx(i) * (FP4A ? 32 : 16) >= K; };           // read the stage's first
   auto wpast = [&](int i) { return (ns - 1) * KS + cw(i) * 32 >= K; };                         // chunk of their row
   // The i-th DMA instruction of stage s, activations then weights; none of the lanes take part in stages past the last.
-  auto issue1 = [&](int s, uint32_t base, int i) {
+  auto issue1 = [&](int s, uint32_t buf, int i) {
     const int on = (s - ns) >> 31;
     if (i < S::NX)
       dma16_to_lds_if(on, xt + (int64_t)s * S::RA, xoff[i < S::NX ? i : 0] - (s == ns - 1 && xpast(i) ? cx(i) * 16 : 0),
-                      base + (i * S::NW + wave) * 1024);
+                      lds0 + buf + (i * S::NW + wave) * 1024);
     else
       dma16_to_lds_if(on, wt + (int64_t)s * S::RW, woff[i < S::NX ? 0 : i - S::NX] - (s == ns - 1 && wpast(i - S::NX) ? cw(i - S::NX) * 16 : 0),
-                      base + S::OFF_W + ((i - S::NX) * S::NW + wave) * 1024);
+                      lds0 + buf + S::OFF_W + ((i - S::NX) * S::NW + wave) * 1024);
   };
   // Scales of K = 512 c + [0, 512) of this lane's rows, to the buffer c % 2: by DMA where the 16 bytes are the row's and
   // dword-aligned, else through registers, written to LDS when the chunk is published (put).  Blocks past K get 127;
@@ -340,15 +341,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   const uint32_t xp = xrow * S::RA + (g ^ (S::CA == 8 ? swz8(lr) : swz4(lr))) * 16, wp = S::OFF_W + wrow * S::RW + (g ^ (S::CW == 8 ? swz8(lr) : swz4(lr))) * 16;
   const uint32_t sp = lds0 + S::OFF_S + xrow * 16, sw = lds0 + S::OFF_S + (S::BM + wrow) * 16;
   constexpr int NLD = TN + TM * (FP4A ? 1 : 2), NMM = TM * TN;       // LDS reads and matrix operations of a step
-  // the it-th LDS read of step ks (weights first: every matrix operation row needs them); the step's chunk is an XOR
-  // of bits that the row leaves zero
-  auto load1 = [&](Regs& R, uint32_t base, int ks, int it) {
-    if (it < TN) R.w[it] = lds_read<u32x4>(base + (wp ^ (ks * 32)) + it * 32 * S::RW);
-    else if (FP4A) R.xlo[it - TN] = lds_read<u32x4>(base + (xp ^ (ks * 32)) + (it - TN) * 32 * S::RA);
+  // LDS addresses of the steps' chunks in the first buffer; a step's chunk is an XOR of bits that the row leaves zero
+  uint32_t xa[2 * S::STEPS], wa[S::STEPS];
+#pragma unroll
+  for (int ks = 0; ks < S::STEPS; ++ks) {
+    wa[ks] = (lds0 + wp) ^ (ks * 32);
+    xa[2 * ks] = (lds0 + xp) ^ (ks * (FP4A ? 32 : 64));
+    xa[2 * ks + 1] = xa[2 * ks] ^ 32;                                 // E4M3: the second half's chunk
+  }
+  // the it-th LDS read of step ks from the buffer at offset buf (weights first: every matrix operation row needs them)
+  auto load1 = [&](Regs& R, uint32_t buf, int ks, int it) {
+    if (it < TN) R.w[it] = lds_read<u32x4>(wa[ks] + buf + it * 32 * S::RW);
+    else if (FP4A) R.xlo[it - TN] = lds_read<u32x4>(xa[2 * ks] + buf + (it - TN) * 32 * S::RA);
     else {
       const int i = (it - TN) / 2;
-      if ((it - TN) % 2 == 0) R.xlo[i] = lds_read<u32x4>(base + (xp ^ (ks * 64)) + i * 32 * S::RA);
-      else R.xhi[FP4A ? 0 : i] = lds_read<u32x4>(base + (xp ^ (ks * 64 + 32)) + i * 32 * S::RA);
+      if ((it - TN) % 2 == 0) R.xlo[i] = lds_read<u32x4>(xa[2 * ks] + buf + i * 32 * S::RA);
+      else R.xhi[FP4A ? 0 : i] = lds_read<u32x4>(xa[2 * ks + 1] + buf + i * 32 * S::RA);
     }
   };
   auto load_pairs = [&](Pairs& H, int k256) {                         // of K = 256 k256 + [0, 256)
@@ -408,70 +416,235 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
 
   // Zeros in the activations' chunks past K of the last stage, once they have landed (E2M1 weights are finite, so the
   // products are zeros; E4M3 ones may not be).
-  auto cut = [&](uint32_t base) {
+  auto cut = [&](uint32_t buf) {
 #pragma unroll
     for (int i = 0; i < S::NX; ++i)
-      if (xpast(i)) lds_write(base + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
+      if (xpast(i)) lds_write(lds0 + buf + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
   };
 
+  // Scale chunks are asked for before the stage that goes out with them, and are needed SPC stages later, when the
+  // waits leave NST - 2 later stages in flight at most.
+  static_assert(S::SPC >= NST - 2, "a chunk has landed when it is published");
   fetch_scales(0);
   put_scales(0);
+  if (K > SCK) fetch_scales(1);
 #pragma unroll
   for (int s = 0; s < NST; ++s)
 #pragma unroll
-    for (int i = 0; i < (s + 1 < NST ? S::NV : S::FIRST); ++i) issue1(s, lds0 + s * S::STAGE, i);
-  if (K > SCK) fetch_scales(1);
+    for (int i = 0; i < (s + 1 < NST ? S::NV : S::FIRST); ++i) issue1(s, s * S::STAGE, i);
   if (ns >= NST) wait_vm<S::NV * (NST - 2) + S::FIRST>();             // the first stage and its scales
   else wait_vm<0>();
-  if (ragged && ns == 1) cut(lds0);
+  if (ragged && ns == 1) cut(0);
   lds_barrier();
-  Regs R0, R1;
-  Pairs H;
-  Scales C;
+  if constexpr (S::WHOLE) {
+    // Small tiles: a stage's operands are read from LDS in one go, while the stage before multiplies, so that the LDS
+    // latency is met once per stage and not once per step.
+    struct Stage { Regs r[S::STEPS]; Scales c[KS / 128]; };
+    auto load_stage = [&](Stage& G, uint32_t buf, int s) {
 #pragma unroll
-  for (int it = 0; it < NLD; ++it) load1(R0, lds0, 0, it);
-  load_pairs(H, 0);
-  take(C, H);
-  uint32_t bp = lds0 + (NST - 1) * S::STAGE, b0 = lds0;               // buffers of stages s - 1 and s
-  // steps 0 .. STEPS - 2 of stage s, with what is left of the DMA of stage s - 1 + NST into the buffer of stage s - 1
-  auto inner = [&](int s) {
-    step(R0, C, even, R1, b0, 1, s - 1 + NST, bp, S::FIRST, S::NV);
-    if (S::STEPS == 4) {
-      second(H);
-      step(R1, C, odd, R0, b0, 2, 0, 0, 0, 0);
-      take(C, H);
-      step(R0, C, even, R1, b0, 3, 0, 0, 0, 0);
+      for (int ks = 0; ks < S::STEPS; ++ks)
+#pragma unroll
+        for (int it = 0; it < NLD; ++it) load1(G.r[ks], buf, ks, it);
+#pragma unroll
+      for (int d = 0; d < KS / 128; ++d) {
+        const int k128 = s * (KS / 128) + d;
+        const uint32_t off = ((k128 >> 2) & 1) * S::SCALES + (k128 & 3) * 4;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) G.c[d].x[i] = lds_read<uint32_t>(sp + off + i * 32 * 16);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) G.c[d].w[i] = lds_read<uint32_t>(sw + off + i * 32 * 16);
+      }
+    };
+    auto multiply = [&](Stage& G) {
+#pragma unroll
+      for (int d = 0; d < KS / 128; ++d) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) G.c[d].x[i] >>= 8 * g;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) G.c[d].w[i] >>= 8 * g;
+#pragma unroll
+        for (int q = 0; q < NMM; ++q) mma(G.r[2 * d], G.c[d], even, q);
+#pragma unroll
+        for (int q = 0; q < NMM; ++q) mma(G.r[2 * d + 1], G.c[d], odd, q);
+      }
+#pragma unroll
+      for (int q = 0; q < NMM; ++q) pin<S::ACC>(acc[q / TN][q % TN]);
+    };
+    Stage G0, G1;
+    load_stage(G0, 0, 0);
+    int s = 0;
+    // A lone wavefront per SIMD is bound by the instructions it issues, so the stages in the middle run without any of
+    // the choices below: four stages (the four buffers) at constant LDS offsets, whole scale chunks, whole rows.
+    static_assert(NST == 4, "four buffers");
+    const uint8_t* xs = xt + (int64_t)NST * S::RA;
+    const uint8_t* wst = wt + (int64_t)NST * S::RW;
+    auto quick = [&](auto u, Stage& G, Stage& Gn) {                   // stage s with s % 4 == u
+      constexpr int U = decltype(u)::value, V = (U + 1) % 4;
+      wait_vm<S::NV * (NST - 2)>();
+      lds_barrier();
+#pragma unroll
+      for (int ks = 0; ks < S::STEPS; ++ks)
+#pragma unroll
+        for (int it = 0; it < NLD; ++it) load1(Gn.r[ks], V * S::STAGE, ks, it);
+#pragma unroll
+      for (int d = 0; d < KS / 128; ++d) {
+        const uint32_t chunk = (FP4A ? (U + 1) >> 1 : (s + U + 1) >> 2) & 1, dword = FP4A ? 2 * ((U + 1) & 1) + d : (U + 1) & 3;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) Gn.c[d].x[i] = lds_read<uint32_t>(sp + chunk * S::SCALES + dword * 4 + i * 32 * 16);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) Gn.c[d].w[i] = lds_read<uint32_t>(sw + chunk * S::SCALES + dword * 4 + i * 32 * 16);
+      }
+      if ((U + 1) % S::SPC == 0) fetch_scales((s + U + 1) / S::SPC + 1);   // the next stage starts a chunk
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < S::NX; ++i) dma16_to_lds(xs, xoff[i], lds0 + U * S::STAGE + (i * S::NW + wave) * 1024);
+#pragma unroll
+      for (int i = 0; i < S::NWT; ++i) dma16_to_lds(wst, woff[i], lds0 + U * S::STAGE + S::OFF_W + (i * S::NW + wave) * 1024);
+      xs += S::RA;
+      wst += S::RW;
+      multiply(G);
+    };
+    const int last = ns - 1 - (ragged ? 1 : 0);                       // the last stage of whole rows
+    for (; s + 3 + NST <= last && by_dma((s + 4) / S::SPC + 1); s += 4) {
+      quick(Int<0>{}, G0, G1);
+      quick(Int<1>{}, G1, G0);
+      quick(Int<2>{}, G0, G1);
+      quick(Int<3>{}, G1, G0);
     }
-  };
-  for (int s = 0; s + 1 < ns; ++s) {
-    const uint32_t b1 = b0 + S::STAGE == lds0 + NST * S::STAGE ? lds0 : b0 + S::STAGE;
-    inner(s);
-    // the next stage's data is waited for and published; this stage's buffer has been read out by every wavefront
-    const bool chunk = (s + 1) % S::SPC == 0;                         // the next stage starts a scale chunk
-    if (chunk) put_scales((s + 1) / S::SPC);
-    if (NST > 2 && s + NST - 1 < ns) wait_vm<S::NV * (NST - 2)>();    // all but the stages after the next one
-    else wait_vm<0>();
-    if (ragged && s + 2 == ns) cut(b1);
-    lds_barrier();
-    if (chunk && ((s + 1) / S::SPC + 1) * SCK < K) fetch_scales((s + 1) / S::SPC + 1);
-    if (KS == 256) load_pairs(H, s + 1);
-    else if (s % 2) load_pairs(H, (s + 1) / 2);
-    else second(H);
-    step(R1, C, odd, R0, b1, 0, s + NST, b0, 0, S::FIRST);
-    take(C, H);
-    bp = b0;
-    b0 = b1;
-  }
-  inner(ns);                                                          // of stage ns - 1; no DMA is left
+    uint32_t b0 = 0;
+    auto stage = [&](int s, Stage& G, Stage& Gn) {
+      const uint32_t b1 = b0 + S::STAGE == NST * S::STAGE ? 0 : b0 + S::STAGE;
+      const bool chunk = (s + 1) % S::SPC == 0;
+      if (chunk) put_scales((s + 1) / S::SPC);
+      if (s + NST - 1 < ns) wait_vm<S::NV * (NST - 2)>();
+      else wait_vm<0>();
+      if (ragged && s + 2 == ns) cut(b1);
+      lds_barrier();                                                  // stage s has been read out by every wavefront
+      load_stage(Gn, b1, s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (chunk && ((s + 1) / S::SPC + 1) * SCK < K) fetch_scales((s + 1) / S::SPC + 1);
+      if (s + NST < ns) {
 #pragma unroll
-  for (int q = 0; q < NMM; ++q) mma(R1, C, odd, q);
+        for (int i = 0; i < S::NV; ++i) issue1(s + NST, b0, i);
+      }
+      multiply(G);
+      b0 = b1;
+    };
+    for (; s + 2 < ns; s += 2) {
+      stage(s, G0, G1);
+      stage(s + 1, G1, G0);
+    }
+    if (s + 1 < ns) {
+      stage(s, G0, G1);
+      multiply(G1);
+    } else {
+      multiply(G0);
+    }
+  } else {
+    Regs R0, R1;
+    Pairs H;
+    Scales C;
+#pragma unroll
+    for (int it = 0; it < NLD; ++it) load1(R0, 0, 0, it);
+    load_pairs(H, 0);
+    take(C, H);
+    int s = 0;
+    // One scale chunk of stages at a time while there is nothing to choose: whole rows and chunks, every stage that is
+    // asked for exists.
+    const uint8_t* xs = xt + (int64_t)(NST - 1) * S::RA;              // the stage whose DMA goes out next
+    const uint8_t* wst = wt + (int64_t)(NST - 1) * S::RW;
+    uint32_t bp = (NST - 1) * S::STAGE, b0 = 0;                       // buffers of stages s - 1 and s
+    auto quick_step = [&](const Regs& R, auto half, Regs& Rn, uint32_t buf, int ks, uint32_t bufd, int d0, int d1) {
+#pragma unroll
+      for (int q = 0; q < NMM; ++q) {
+#pragma unroll
+        for (int it = q * NLD / NMM; it < (q + 1) * NLD / NMM; ++it) load1(Rn, buf, ks, it);
+        mma(R, C, half, q);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int it = d0 + q * (d1 - d0) / NMM; it < d0 + (q + 1) * (d1 - d0) / NMM; ++it)
+          if (it < S::NX) dma16_to_lds(xs, xoff[it < S::NX ? it : 0], lds0 + bufd + (it * S::NW + wave) * 1024);
+          else dma16_to_lds(wst, woff[it < S::NX ? 0 : it - S::NX], lds0 + bufd + S::OFF_W + ((it - S::NX) * S::NW + wave) * 1024);
+      }
+#pragma unroll
+      for (int q = 0; q < NMM; ++q) pin<S::ACC>(acc[q / TN][q % TN]);
+    };
+    auto quick = [&](auto u) {                                        // stage s + U
+      constexpr int U = decltype(u)::value;
+      constexpr bool FIXED = S::SPC % NST == 0;                       // constant buffers
+      const uint32_t f0 = FIXED ? U % NST * S::STAGE : b0, fp = FIXED ? (U + NST - 1) % NST * S::STAGE : bp;
+      const uint32_t f1 = FIXED ? (U + 1) % NST * S::STAGE : b0 + S::STAGE == NST * S::STAGE ? 0 : b0 + S::STAGE;
+      quick_step(R0, even, R1, f0, 1, fp, S::FIRST, S::NV);
+      xs += S::RA;
+      wst += S::RW;
+      if (S::STEPS == 4) {
+        second(H);
+        quick_step(R1, odd, R0, f0, 2, 0, 0, 0);
+        take(C, H);
+        quick_step(R0, even, R1, f0, 3, 0, 0, 0);
+      }
+      wait_vm<S::NV * (NST - 2)>();
+      lds_barrier();
+      if (U + 1 == S::SPC) fetch_scales((s + U + 1) / S::SPC + 1);
+      if (KS == 256) load_pairs(H, s + U + 1);
+      else if (U % 2) load_pairs(H, (s + U + 1) / 2);
+      else second(H);
+      quick_step(R1, odd, R0, f1, 0, f0, 0, S::FIRST);
+      take(C, H);
+      if (!FIXED) {
+        bp = b0;
+        b0 = f1;
+      }
+    };
+    const int last = ns - 1 - (ragged ? 1 : 0);                       // the last stage of whole rows
+    for (; s + S::SPC - 1 + NST <= last && by_dma(s / S::SPC + 2); s += S::SPC) {
+      quick(Int<0>{});
+      quick(Int<1>{});
+      if constexpr (S::SPC == 4) {
+        quick(Int<2>{});
+        quick(Int<3>{});
+      }
+    }
+    // steps 0 .. STEPS - 2 of stage s, with what is left of the DMA of stage s - 1 + NST into the buffer of stage s - 1
+    auto inner = [&](int s) {
+      step(R0, C, even, R1, b0, 1, s - 1 + NST, bp, S::FIRST, S::NV);
+      if (S::STEPS == 4) {
+        second(H);
+        step(R1, C, odd, R0, b0, 2, 0, 0, 0, 0);
+        take(C, H);
+        step(R0, C, even, R1, b0, 3, 0, 0, 0, 0);
+      }
+    };
+    for (; s + 1 < ns; ++s) {
+      const uint32_t b1 = b0 + S::STAGE == NST * S::STAGE ? 0 : b0 + S::STAGE;
+      inner(s);
+      // the next stage's data is waited for and published; this stage's buffer has been read out by every wavefront
+      const bool chunk = (s + 1) % S::SPC == 0;                       // the next stage starts a scale chunk
+      if (chunk) put_scales((s + 1) / S::SPC);
+      if (NST > 2 && s + NST - 1 < ns) wait_vm<S::NV * (NST - 2)>();  // all but the stages after the next one
+      else wait_vm<0>();
+      if (ragged && s + 2 == ns) cut(b1);
+      lds_barrier();
+      if (chunk && ((s + 1) / S::SPC + 1) * SCK < K) fetch_scales((s + 1) / S::SPC + 1);
+      if (KS == 256) load_pairs(H, s + 1);
+      else if (s % 2) load_pairs(H, (s + 1) / 2);
+      else second(H);
+      step(R1, C, odd, R0, b1, 0, s + NST, b0, 0, S::FIRST);
+      take(C, H);
+      bp = b0;
+      b0 = b1;
+    }
+    inner(ns);                                                        // of stage ns - 1; no DMA is left
+#pragma unroll
+    for (int q = 0; q < NMM; ++q) mma(R1, C, odd, q);
+  }
 
-  // Results.  Where rows of y are whole 16-byte pieces (N % 8 == 0 in bf16, % 4 in fp32) each wavefront turns 32 rows
-  // at a time in its own part of LDS, so that a store instruction writes whole runs of a row.
+  // Results.  Where rows of y start on a dword each wavefront turns 32 rows at a time in its own part of LDS, so that a
+  // store instruction writes whole runs of a row (16 bytes a lane, the row's last piece by dwords).
   const int esz = A.bf16_out ? 2 : 4;
   uint8_t* const y = static_cast<uint8_t*>(A.y);
   constexpr int WC = TN * 32;                                         // columns of a wavefront
-  if (N % (16 / esz) == 0) {
+  if (N * esz % 4 == 0) {
     constexpr uint32_t PITCH = WC * 4 + 16;                           // + 16: rows start on different banks
     static_assert(S::NW * 32 * PITCH <= S::OFF_S, "epilogue LDS");
     lds_barrier();                                                    // every wavefront has read its operands
@@ -506,7 +679,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
       for (int r = lane / lpr; r < 32; r += 64 / lpr) {
         const int c = (lane % lpr) * (16 / esz);
         const u32x4 d = lds_read<u32x4>(mine + r * PITCH + c * esz);
-        if (mb + r < M && c < nw) *reinterpret_cast<u32x4_a4*>(y + ((mb + r) * N + n0 + wn * WC + c) * esz) = d;
+        uint8_t* const at = y + ((mb + r) * N + n0 + wn * WC + c) * esz;
+        if (mb + r < M && c + 16 / esz <= nw) *reinterpret_cast<u32x4_a4*>(at) = d;
+        else if (mb + r < M)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e * 4 / esz < nw) reinterpret_cast<uint32_t*>(at)[e] = d[e];
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -529,8 +707,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   }
 }
 
-constexpr int FP4_TILE_MIN_M = 65;
-
 template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
 static void launch_tile(const TileArgs& a, hipStream_t stream) {
   using S = TileShape<FP4A, WM, WN, TM, TN, KS, NST>;
@@ -539,27 +715,50 @@ static void launch_tile(const TileArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, KS, NST>), grid, block, 0, stream, a);
 }
 
+// Which kernel runs (M, N, K), by how many workgroups each shape gives.  Times at N = K = 4096, E2M1 / E4M3 activations:
+//   rows, a wavefront per 16 columns:     M = 1 4.2 / 4.9 us, 16 4.9 / 5.8, 32 7.1 / 8.7, 48 9.2 / 11.7 (every wavefront
+//                                         reads all of its rows, so its time grows with them)
+//   32 x 64 (2 wavefronts):               M = 32 6.8 / 8.5, 48 6.7 / 8.6, 128 7.0 / 8.8, 256 9.3 / 11.8
+//   64 x 64 (4, two workgroups per CU):   M = 48 7.4 / 9.2, 256 7.9 / 10.0, 512 10.6 / 15.2, 1024 20.3 / 26.9
+//   128 x 128 (4, two per CU):            M = 256 14.4 / 17.1, 512 13.0 / 17.8, 1024 16.6 / 20.8
+//   256 x 256 (8, one per CU):            M = 4096 38.6 / 56.2, about 1.6 times a full round of 128 x 128
+enum class Fp4Kernel { rows, t32x64, t64x64, t128x128, t256x256 };
+static int64_t tiles_of(int M, int N, int bm, int bn) { return ((int64_t)M + bm - 1) / bm * (((int64_t)N + bn - 1) / bn); }
+static Fp4Kernel pick_kernel(int M, int N, int K) {
+  if (M <= 16 || K < 128) return Fp4Kernel::rows;                     // the tiles' scale reads need four blocks a row
+  if (tiles_of(M, N, 32, 64) <= 256) return Fp4Kernel::t32x64;        // one per CU
+  if (tiles_of(M, N, 64, 64) <= 512) return Fp4Kernel::t64x64;        // two per CU
+  const int64_t r128 = (tiles_of(M, N, 128, 128) + 511) / 512, r256 = (tiles_of(M, N, 256, 256) + 255) / 256;
+  return r256 * 8 <= r128 * 5 ? Fp4Kernel::t256x256 : Fp4Kernel::t128x128;
+}
+
+template <bool FP4A>
+static const char* launch_product(const TileArgs& t, hipStream_t stream) {
+  switch (pick_kernel(t.M, t.N, t.K)) {
+    case Fp4Kernel::t32x64:
+      launch_tile<FP4A, 1, 2, 1, 1, FP4A ? 256 : 128, 4>(t, stream);
+      return FP4A ? "fp4:tile32x64_a4" : "fp4:tile32x64_a8";
+    case Fp4Kernel::t64x64:
+      launch_tile<FP4A, 2, 2, 1, 1, FP4A ? 256 : 128, 4>(t, stream);
+      return FP4A ? "fp4:tile64x64_a4" : "fp4:tile64x64_a8";
+    case Fp4Kernel::t128x128:
+      launch_tile<FP4A, 2, 2, 2, 2, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
+      return FP4A ? "fp4:tile128x128_a4" : "fp4:tile128x128_a8";
+    case Fp4Kernel::t256x256:
+      launch_tile<FP4A, FP4A ? 2 : 4, FP4A ? 4 : 2, FP4A ? 4 : 2, FP4A ? 2 : 4, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
+      return FP4A ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
+    default: break;
+  }
+  const dim3 grid((unsigned)((int64_t)((t.N + 15) / 16) * ((t.M + ROWS_MAX - 1) / ROWS_MAX)));   // about M N / 2^10 < 2^31
+  const dim3 block(64 * (t.M < ROWS_MAX ? (t.M + 15) / 16 : 4));
+  hipLaunchKernelGGL(fp4_rows_kernel<FP4A>, grid, block, 0, stream, t.x, t.x_sc, t.w, t.w_sc, t.M, t.N, t.K, t.y, t.bf16_out);
+  return FP4A ? "fp4:rows16_a4" : "fp4:rows16_a8";
+}
+
 hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
                            int M, int N, int K, void* y, bool bf16_out, hipStream_t stream, const char** variant) {
-  if (M >= FP4_TILE_MIN_M && K >= 128) {
-    const TileArgs t{a, a_sc, w, w_sc, M, N, K, y, bf16_out};
-    const int64_t big = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-    if (big >= 192) {
-      if (fp4a) launch_tile<true, 2, 4, 4, 2, 256, 2>(t, stream);
-      else launch_tile<false, 4, 2, 2, 4, 128, 3>(t, stream);
-      *variant = fp4a ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
-    } else {
-      if (fp4a) launch_tile<true, 2, 2, 2, 2, 256, 2>(t, stream);
-      else launch_tile<false, 2, 2, 2, 2, 128, 3>(t, stream);
-      *variant = fp4a ? "fp4:tile128x128_a4" : "fp4:tile128x128_a8";
-    }
-    return hipGetLastError();
-  }
-  const dim3 grid((unsigned)((int64_t)((N + 15) / 16) * ((M + ROWS_MAX - 1) / ROWS_MAX)));   // about M N / 2^10 < 2^31
-  const dim3 block(64 * (M < ROWS_MAX ? (M + 15) / 16 : 4));
-  if (fp4a) hipLaunchKernelGGL(fp4_rows_kernel<true>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
-  else hipLaunchKernelGGL(fp4_rows_kernel<false>, grid, block, 0, stream, a, a_sc, w, w_sc, M, N, K, y, bf16_out);
-  *variant = fp4a ? "fp4:rows16_a4" : "fp4:rows16_a8";
+  const TileArgs t{a, a_sc, w, w_sc, M, N, K, y, bf16_out};
+  *variant = fp4a ? launch_product<true>(t, stream) : launch_product<false>(t, stream);
   return hipGetLastError();
 }
 
