@@ -181,7 +181,6 @@ __device__ __forceinline__ void dma16_to_lds_if(int on, const void* base, uint32
 }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 
 __device__ __forceinline__ int swz4(int r) { return (((r >> 1) ^ (r >> 3)) & 1) | ((r >> 1) & 2); }
@@ -639,71 +638,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
     for (int q = 0; q < NMM; ++q) mma(R1, C, odd, q);
   }
 
-  // Results.  Where rows of y start on a dword each wavefront turns 32 rows at a time in its own part of LDS, so that a
-  // store instruction writes whole runs of a row (16 bytes a lane, the row's last piece by dwords).
+  // Results.  Each wavefront turns 32 rows at a time in its own part of LDS, so that a store instruction writes whole
+  // runs of a row: 16 bytes a lane, at whatever alignment the row has (2 bytes where N is odd), the row's last piece by
+  // elements.
   const int esz = A.bf16_out ? 2 : 4;
   uint8_t* const y = static_cast<uint8_t*>(A.y);
   constexpr int WC = TN * 32;                                         // columns of a wavefront
-  if (N * esz % 4 == 0) {
-    constexpr uint32_t PITCH = WC * 4 + 16;                           // + 16: rows start on different banks
-    static_assert(S::NW * 32 * PITCH <= S::OFF_S, "epilogue LDS");
-    lds_barrier();                                                    // every wavefront has read its operands
-    const uint32_t mine = lds0 + wave * 32 * PITCH;
-    const int nw = (int)min((int64_t)WC, N - n0 - wn * WC);           // this wavefront's columns
+  constexpr uint32_t PITCH = WC * 4 + 16;                             // + 16: rows start on different banks
+  static_assert(S::NW * 32 * PITCH <= S::OFF_S, "epilogue LDS");
+  lds_barrier();                                                      // every wavefront has read its operands
+  const uint32_t mine = lds0 + wave * 32 * PITCH;
+  const int nw = (int)min((int64_t)WC, N - n0 - wn * WC);             // this wavefront's columns
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      if (A.bf16_out) {
+  for (int i = 0; i < TM; ++i) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const v16f& c = acc[i][j];
-            const u32x2 d = {(uint32_t)f32_to_bf16_rne(c[4 * q]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 1]) << 16),
-                                (uint32_t)f32_to_bf16_rne(c[4 * q + 2]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 3]) << 16)};
-            lds_write(mine + lr * PITCH + (j * 32 + 8 * q + 4 * g) * 2, d);
-          }
-      } else {
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const v16f& c = acc[i][j];
-            lds_write(mine + lr * PITCH + (j * 32 + 8 * q + 4 * g) * 4,
-                      u32x4{__float_as_uint(c[4 * q]), __float_as_uint(c[4 * q + 1]), __float_as_uint(c[4 * q + 2]),
-                            __float_as_uint(c[4 * q + 3])});
-          }
+      for (int q = 0; q < 4; ++q) {
+        const v16f& c = acc[i][j];
+        const uint32_t at = mine + lr * PITCH + (j * 32 + 8 * q + 4 * g) * esz;
+        if (A.bf16_out)
+          lds_write(at, u32x2{(uint32_t)f32_to_bf16_rne(c[4 * q]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 1]) << 16),
+                              (uint32_t)f32_to_bf16_rne(c[4 * q + 2]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 3]) << 16)});
+        else
+          lds_write(at, u32x4{__float_as_uint(c[4 * q]), __float_as_uint(c[4 * q + 1]), __float_as_uint(c[4 * q + 2]),
+                              __float_as_uint(c[4 * q + 3])});
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");              // the wavefront's own writes, in order
-      const int lpr = WC * esz / 16;                                  // lanes per row
-      const int64_t mb = m0 + wm * TM * 32 + i * 32;
-      for (int r = lane / lpr; r < 32; r += 64 / lpr) {
-        const int c = (lane % lpr) * (16 / esz);
-        const u32x4 d = lds_read<u32x4>(mine + r * PITCH + c * esz);
-        uint8_t* const at = y + ((mb + r) * N + n0 + wn * WC + c) * esz;
-        if (mb + r < M && c + 16 / esz <= nw) *reinterpret_cast<u32x4_a4*>(at) = d;
-        else if (mb + r < M)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");                // the wavefront's own writes
+    const int lpr = WC * esz / 16, per = 16 / esz;                    // lanes per row, elements per lane
+    const int64_t mb = m0 + wm * TM * 32 + i * 32;
+    for (int r = lane / lpr; r < 32; r += 64 / lpr) {
+      const int c = (lane % lpr) * per;
+      const uint32_t from = mine + r * PITCH + c * esz;
+      uint8_t* const to = y + ((mb + r) * N + n0 + wn * WC + c) * esz;
+      const u32x4 d = lds_read<u32x4>(from);
+      if (mb + r >= M) continue;
+      if (c + per <= nw) *reinterpret_cast<u32x4_a1*>(to) = d;
+      else
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e * 4 / esz < nw) reinterpret_cast<uint32_t*>(at)[e] = d[e];
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int64_t m = m0 + wm * TM * 32 + i * 32 + lr;
-      if (m >= M) continue;
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t n = n0 + wn * WC + j * 32 + 8 * (r / 4) + 4 * g + r % 4;
-          if (n < N) {
-            if (A.bf16_out) reinterpret_cast<uint16_t*>(y)[m * N + n] = f32_to_bf16_rne(acc[i][j][r]);
-            else reinterpret_cast<float*>(y)[m * N + n] = acc[i][j][r];
-          }
+        for (int e = 0; e < 8; ++e) {
+          if (c + e >= nw) continue;
+          if (A.bf16_out) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(d[e / 2] >> (16 * (e % 2)));
+          else if (e < 4) reinterpret_cast<uint32_t*>(to)[e] = d[e < 4 ? e : 0];
         }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
