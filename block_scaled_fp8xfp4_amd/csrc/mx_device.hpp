@@ -269,26 +269,89 @@ __device__ __forceinline__ float quad_max(float m) {
   return m;
 }
 
+// Codes of N elements under scale code sc by the hardware conversions (round
+// to nearest even; E4M3 clamped to +-448 first, E2M1 saturates at +-6 by
+// itself): N / 4 dwords of E4M3 or N / 8 of E2M1.  Bit for bit encode_e4m3
+// and encode_e2m1 (every finite float compared).  f: 2^(127 - sc), possibly
+// times a number next to 1.
+template <bool FP4, int N>
+__device__ __forceinline__ void codes_scaled(const float* v, float f, uint32_t* out) {
+  if (FP4) {
+#pragma unroll
+    for (int w = 0; w < N / 8; ++w) {
+      uint32_t d = 0;
+      d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[8 * w] * f, v[8 * w + 1] * f, 1.0f, 0);
+      d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[8 * w + 2] * f, v[8 * w + 3] * f, 1.0f, 1);
+      d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[8 * w + 4] * f, v[8 * w + 5] * f, 1.0f, 2);
+      d = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(d, v[8 * w + 6] * f, v[8 * w + 7] * f, 1.0f, 3);
+      out[w] = d;
+    }
+  } else {
+    auto cl = [](float t) { return __builtin_amdgcn_fmed3f(t, -448.0f, 448.0f); };
+#pragma unroll
+    for (int w = 0; w < N / 4; ++w) {
+      int d = __builtin_amdgcn_cvt_pk_fp8_f32(cl(v[4 * w] * f), cl(v[4 * w + 1] * f), 0, false);
+      out[w] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(cl(v[4 * w + 2] * f), cl(v[4 * w + 3] * f), d, true);
+    }
+  }
+}
+
 // Codes of this lane's chunk of a block-32 row (all four lanes of its quad
 // active): chunk number `chunk` of the code array (8 or 4 bytes each), and
 // one scale byte per quad.
-__device__ __forceinline__ void store8_codes(bool fp4, const float* v, uint8_t* q, uint8_t* sc, int64_t chunk) {
+template <bool FP4>
+__device__ __forceinline__ void store8_codes(const float* v, uint8_t* q, uint8_t* sc, int64_t chunk) {
   float amax = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) amax = fmaxf(amax, __builtin_fabsf(v[j]));
-  const uint32_t s = e8m0_code_for_amax(quad_max(amax), fp4 ? 2 : 8);
-  if (fp4) {
-    uint32_t d = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) d |= encode_e2m1(v[j], s) << (4 * j);
-    *reinterpret_cast<uint32_t*>(q + chunk * 4) = d;
-  } else {
-    uint2 d;
-    d.x = requant2_e4m3(v[0], v[1], s) | (requant2_e4m3(v[2], v[3], s) << 16);
-    d.y = requant2_e4m3(v[4], v[5], s) | (requant2_e4m3(v[6], v[7], s) << 16);
-    *reinterpret_cast<uint2*>(q + chunk * 8) = d;
-  }
+  const uint32_t s = e8m0_code_for_amax(quad_max(amax), FP4 ? 2 : 8);
+  uint32_t d[2];
+  codes_scaled<FP4, 8>(v, __builtin_ldexpf(1.0f, 127 - (int)s), d);
+  if (FP4) *reinterpret_cast<uint32_t*>(q + chunk * 4) = d[0];
+  else *reinterpret_cast<uint2*>(q + chunk * 8) = uint2{d[0], d[1]};
   if ((chunk & 3) == 0) sc[chunk >> 2] = (uint8_t)s;
+}
+
+// ---------------------------------------------------------------------------
+// SwiGLU + codes without double arithmetic where the result cannot depend on
+// it.  The codes are defined by swiglu() (double, rounded once to fp32); an
+// fp32 value a within SWIGLU_EPS of that determines them too if a (1 - eps)
+// and a (1 + eps) have the same codes and the block's largest a has the same
+// exponent at both ends.  About one element in 2^15 fails that; then the
+// wavefront takes the double form.
+//
+// Error of swiglu_near for g > -60: the exponent's argument is carried in two
+// floats, v_exp_f32 and v_rcp_f32 are within 1 ulp, four more roundings; over
+// every float g the worst relative error of silu(g) measured 2^-21.9, and the
+// product with u adds 2^-24: under half of 2^-20.
+constexpr float SWIGLU_EPS = 9.5367431640625e-07f;               // 2^-20
+constexpr float SWIGLU_MIN_G = -60.0f;                           // below: 1 / (1 + e^-g) loses bits to small numbers
+
+__device__ __forceinline__ float swiglu_near(float g, float u) {
+  const float h = g * -1.44269504f;                              // -g log2 e = h + l
+  const float l = __builtin_fmaf(g, -1.44269504f, -h) - g * 1.92596303e-8f;
+  const float e = __builtin_amdgcn_exp2f(h);
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, l * 0.693147181f, e)) * u;
+}
+
+// Whether a block whose largest near value is amax can be cast from near
+// values: in a range where fp32 keeps its precision (zero is not), and with
+// one exponent at both ends.
+__device__ __forceinline__ bool near_block(float amax) {
+  return amax >= 7.9e-31f && amax <= 1.3e36f &&                  // 2^-100, 2^120
+         ((__float_as_uint(amax * (1.0f - SWIGLU_EPS)) ^ __float_as_uint(amax * (1.0f + SWIGLU_EPS))) >> 23) == 0;
+}
+
+// Codes of N near values; false if they depend on what near leaves open.
+template <bool FP4, int N>
+__device__ __forceinline__ bool codes_near(const float* v, uint32_t sc, uint32_t* out) {
+  const float f = __builtin_ldexpf(1.0f, 127 - (int)sc);
+  uint32_t other[FP4 ? N / 8 : N / 4], diff = 0;
+  codes_scaled<FP4, N>(v, f * (1.0f - SWIGLU_EPS), out);
+  codes_scaled<FP4, N>(v, f * (1.0f + SWIGLU_EPS), other);
+#pragma unroll
+  for (int i = 0; i < (FP4 ? N / 8 : N / 4); ++i) diff |= out[i] ^ other[i];
+  return diff == 0;
 }
 
 }  // namespace mx

@@ -65,7 +65,10 @@ __global__ __launch_bounds__(256) void add_rmsnorm_kernel(NormArgs A) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] = (float)((double)v[c][j] * r * (A.w ? (double)w[j] : 1.0));
       if (A.n) store8(A.n, true, t * A.H + ch * 8, v[c]);
-      if (A.q) store8_codes(A.fp4, v[c], A.q, A.sc, t * nch + ch);
+      if (A.q) {
+        if (A.fp4) store8_codes<true>(v[c], A.q, A.sc, t * nch + ch);
+        else store8_codes<false>(v[c], A.q, A.sc, t * nch + ch);
+      }
     }
   }
 }

@@ -118,7 +118,9 @@ hipError_t launch_dequantize(const uint8_t* q, const uint8_t* sc, bool fp4, int6
 // SwiGLU + block-32 codes of gate/up rows [T][2I] (gate, then up): what lies
 // between the two products of an FFN.  a = silu(gate) * up in double, rounded
 // once to fp32 (swiglu, as in every other kernel of the library), then the
-// block's codes.  One thread per 8 columns of one row.
+// block's codes: from fp32 values where those decide the codes (codes_near),
+// in double for the wavefronts that hold one that they do not.  One thread per
+// 8 columns of one row.
 template <bool BF16, bool FP4>
 __global__ __launch_bounds__(256) void swiglu_quantize_kernel(const void* __restrict__ gu, int64_t ld, int64_t nchunks,
                                                               int I, uint8_t* __restrict__ q, uint8_t* __restrict__ sc) {
@@ -129,9 +131,26 @@ __global__ __launch_bounds__(256) void swiglu_quantize_kernel(const void* __rest
   float g[8], u[8];
   load8(gu, BF16, t * ld + i, g);
   load8(gu, BF16, t * ld + I + i, u);
+  float a[8], amax = 0.0f, gmin = g[0];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    a[j] = swiglu_near(g[j], u[j]);
+    amax = fmaxf(amax, __builtin_fabsf(a[j]));
+    gmin = fminf(gmin, g[j]);
+  }
+  amax = quad_max(amax);
+  const uint32_t s = e8m0_code_for_amax(amax, FP4 ? 2 : 8);
+  uint32_t d[2];
+  const bool sure = gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 8>(a, s, d);
+  if (__all(sure)) {
+    if (FP4) *reinterpret_cast<uint32_t*>(q + c * 4) = d[0];
+    else *reinterpret_cast<uint2*>(q + c * 8) = uint2{d[0], d[1]};
+    if ((c & 3) == 0) sc[c >> 2] = (uint8_t)s;
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) g[j] = swiglu(g[j], u[j]);
-  store8_codes(FP4, g, q, sc, c);
+  store8_codes<FP4>(g, q, sc, c);
 }
 
 hipError_t launch_swiglu_quantize(const void* gu, bool bf16, int64_t ld, int64_t T, int I, bool fp4, uint8_t* q,
