@@ -236,12 +236,56 @@ struct TileShape {
 
 struct TileArgs {
   const uint8_t* x; const uint8_t* x_sc;          // activations [M][K]
-  const uint8_t* w; const uint8_t* w_sc;          // weights [N][K]
+  const uint8_t* w; const uint8_t* w_sc;          // weights [N][K]; SwiGLU: [2N][K], gate rows then up rows
   int M, N, K;
   void* y; bool bf16_out;                         // [M][N]
+  uint8_t* q; uint8_t* q_sc; bool fp4mid;         // SwiGLU: codes [M][N] instead
 };
 
-template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
+// SwiGLU + codes of one row's block of 32: gate and up of this lane's 16
+// columns 8 q + 4 g + [0, 4); its partner is 32 lanes away.  q, sc: the block's
+// codes and scale, written if ok (a block is whole or not there: N % 32 == 0).
+template <bool FP4>
+__device__ __forceinline__ void tile_codes(const v16f& gate, const v16f& up, int g, bool ok, uint8_t* q, uint8_t* sc) {
+  float a[16], amax = 0.0f, gmin = gate[0];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    a[r] = swiglu_near(gate[r], up[r]);
+    amax = fmaxf(amax, __builtin_fabsf(a[r]));
+    gmin = fminf(gmin, gate[r]);
+  }
+  amax = fmaxf(amax, __shfl_xor(amax, 32));
+  uint32_t s = e8m0_code_for_amax(amax, FP4 ? 2 : 8), d[4];
+  const bool sure = gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 16>(a, s, d);
+  if (!__all(sure || !ok)) {
+    amax = 0.0f;
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h)                                       // four at a time: the double form is long
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (r / 4 == h) {
+          a[r] = swiglu(gate[r], up[r]);
+          amax = fmaxf(amax, __builtin_fabsf(a[r]));
+        }
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    s = e8m0_code_for_amax(amax, FP4 ? 2 : 8);
+    codes_scaled<FP4, 16>(a, __builtin_ldexpf(1.0f, 127 - (int)s), d);
+  }
+  if (FP4) {                                                          // halves: q = 0 | q = 1, q = 2 | q = 3
+    const auto x = __builtin_amdgcn_permlane32_swap(d[0], d[1], false, false);
+    const uint32_t lo = __builtin_amdgcn_perm(x[1], x[0], 0x05040100), hi = __builtin_amdgcn_perm(x[1], x[0], 0x07060302);
+    if (ok) *reinterpret_cast<u32x2*>(q + g * 8) = u32x2{lo, hi};
+  } else {
+    const auto x = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+    if (ok) *reinterpret_cast<u32x4*>(q + g * 16) = u32x4{x[0], x[1], y[0], y[1]};
+  }
+  if (ok && g == 0) *sc = (uint8_t)s;
+}
+
+// What a product leaves: y, or the codes of silu(gate) * up (SWIGLU: a tile
+// holds 32 gate columns, then the 32 up columns they meet, and so on).
+template <bool FP4A, bool SWIGLU, int WM, int WN, int TM, int TN, int KS, int NST>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   using S = TileShape<FP4A, WM, WN, TM, TN, KS, NST>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
@@ -254,14 +298,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   const int rowx = FP4A ? K / 2 : K, roww = K / 2;
 
   // XCD-aware order: each XCD takes a run of consecutive tiles, which go down 8 row tiles before the next column tile
-  const int nrt = (M + S::BM - 1) / S::BM, nct = (N + S::BN - 1) / S::BN;
+  constexpr int CN = SWIGLU ? S::BN / 2 : S::BN;                      // result columns of a tile
+  const int nrt = (M + S::BM - 1) / S::BM, nct = (N + CN - 1) / CN;
   const uint32_t tiles = (uint32_t)nrt * nct, per = (tiles + XCDS - 1) / XCDS;   // M N < 2^40: fewer than 2^27 tiles
   const uint32_t t = blockIdx.x % XCDS * per + blockIdx.x / XCDS;
   if (t >= tiles) return;
   const uint32_t grp = t / (8u * nct), in = t - grp * 8u * nct, rows_in = min(8u, nrt - grp * 8u);
   const int rt = __builtin_amdgcn_readfirstlane(grp * 8 + in % rows_in), ct = __builtin_amdgcn_readfirstlane(in / rows_in);
-  const int64_t m0 = (int64_t)rt * S::BM, n0 = (int64_t)ct * S::BN;
-  const int mlast = (int)min((int64_t)S::BM, M - m0) - 1, nlast = (int)min((int64_t)S::BN, N - n0) - 1;   // rows past the end repeat the last one
+  const int64_t m0 = (int64_t)rt * S::BM, n0 = (int64_t)ct * CN;
+  const int mlast = (int)min((int64_t)S::BM, M - m0) - 1, nlast = (int)min((int64_t)CN, N - n0) - 1;   // rows past the end repeat the last one
+  // the weight row of the tile's r-th column, from row n0 on
+  auto wsrc = [&](int r) {
+    return SWIGLU ? (uint32_t)min(r / 64 * 32 + r % 32, nlast) + ((r & 32) ? (uint32_t)N : 0u) : (uint32_t)min(r, nlast);
+  };
   const uint8_t* xt = A.x + m0 * rowx;
   const uint8_t* wt = A.w + n0 * roww;
 
@@ -278,13 +327,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
 #pragma unroll
   for (int i = 0; i < S::NWT; ++i) {
     const int r = (i * S::NW + wave) * (64 / S::CW) + lane / S::CW;
-    woff[i] = (uint32_t)min(r, nlast) * (uint32_t)roww + cw(i) * 16;
+    woff[i] = wsrc(r) * (uint32_t)roww + cw(i) * 16;
   }
   const uint8_t* srow[S::NSC];                                        // this lane's scale rows: activations, then weights
 #pragma unroll
   for (int i = 0; i < S::NSC; ++i) {
     const int r = (i * S::NW + wave) * 64 + lane;
-    srow[i] = r < S::BM ? A.x_sc + (m0 + min(r, mlast)) * nblk : A.w_sc + (n0 + min(r - S::BM, nlast)) * nblk;
+    srow[i] = r < S::BM ? A.x_sc + (m0 + min(r, mlast)) * nblk : A.w_sc + (n0 + wsrc(min(r - S::BM, S::BN - 1))) * nblk;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   const bool ragged = K % KS != 0;                                    // the last stage runs past K: chunks past K
@@ -638,6 +687,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
     for (int q = 0; q < NMM; ++q) mma(R1, C, odd, q);
   }
 
+  if constexpr (SWIGLU) {
+    // Codes.  A lane and its partner 32 lanes away hold a block of 32 columns of one row, 16 each: four at 8 q + 4 g.
+    // Each pair of dwords (or halves) is exchanged so that a lane writes 16 neighbouring columns.
+    static_assert(TN % 2 == 0, "gate and up in one wavefront");
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; j += 2) {
+        const int64_t m = m0 + wm * TM * 32 + i * 32 + lr, n = n0 + wn * TN * 16 + j * 16;
+        if (A.fp4mid) tile_codes<true>(acc[i][j], acc[i][j + 1], g, m < M && n < N, A.q + m * (N / 2) + n / 2, A.q_sc + m * (N / 32) + n / 32);
+        else tile_codes<false>(acc[i][j], acc[i][j + 1], g, m < M && n < N, A.q + m * N + n, A.q_sc + m * (N / 32) + n / 32);
+      }
+    return;
+  }
   // Results.  Each wavefront turns 32 rows at a time in its own part of LDS, so that a store instruction writes whole
   // runs of a row: 16 bytes a lane, at whatever alignment the row has (2 bytes where N is odd), the row's last piece by
   // elements.
@@ -686,12 +749,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   }
 }
 
-template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
+template <bool FP4A, bool SWIGLU, int WM, int WN, int TM, int TN, int KS, int NST>
 static void launch_tile(const TileArgs& a, hipStream_t stream) {
   using S = TileShape<FP4A, WM, WN, TM, TN, KS, NST>;
-  const int64_t tiles = (int64_t)((a.M + S::BM - 1) / S::BM) * ((a.N + S::BN - 1) / S::BN);
+  constexpr int CN = SWIGLU ? S::BN / 2 : S::BN;
+  const int64_t tiles = (int64_t)((a.M + S::BM - 1) / S::BM) * ((a.N + CN - 1) / CN);
   const dim3 grid((unsigned)((tiles + XCDS - 1) / XCDS * XCDS)), block(64 * S::NW);
-  hipLaunchKernelGGL((fp4_tile_kernel<FP4A, WM, WN, TM, TN, KS, NST>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL((fp4_tile_kernel<FP4A, SWIGLU, WM, WN, TM, TN, KS, NST>), grid, block, 0, stream, a);
 }
 
 // Which kernel runs (M, N, K), by how many workgroups each shape gives.  Times at N = K = 4096, E2M1 / E4M3 activations:
@@ -715,16 +779,16 @@ template <bool FP4A>
 static const char* launch_product(const TileArgs& t, hipStream_t stream) {
   switch (pick_kernel(t.M, t.N, t.K)) {
     case Fp4Kernel::t32x64:
-      launch_tile<FP4A, 1, 2, 1, 1, FP4A ? 256 : 128, 4>(t, stream);
+      launch_tile<FP4A, false, 1, 2, 1, 1, FP4A ? 256 : 128, 4>(t, stream);
       return FP4A ? "fp4:tile32x64_a4" : "fp4:tile32x64_a8";
     case Fp4Kernel::t64x64:
-      launch_tile<FP4A, 2, 2, 1, 1, FP4A ? 256 : 128, 4>(t, stream);
+      launch_tile<FP4A, false, 2, 2, 1, 1, FP4A ? 256 : 128, 4>(t, stream);
       return FP4A ? "fp4:tile64x64_a4" : "fp4:tile64x64_a8";
     case Fp4Kernel::t128x128:
-      launch_tile<FP4A, 2, 2, 2, 2, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
+      launch_tile<FP4A, false, 2, 2, 2, 2, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
       return FP4A ? "fp4:tile128x128_a4" : "fp4:tile128x128_a8";
     case Fp4Kernel::t256x256:
-      launch_tile<FP4A, FP4A ? 2 : 4, FP4A ? 4 : 2, FP4A ? 4 : 2, FP4A ? 2 : 4, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
+      launch_tile<FP4A, false, FP4A ? 2 : 4, FP4A ? 4 : 2, FP4A ? 4 : 2, FP4A ? 2 : 4, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
       return FP4A ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
     default: break;
   }
@@ -736,31 +800,98 @@ static const char* launch_product(const TileArgs& t, hipStream_t stream) {
 
 hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
                            int M, int N, int K, void* y, bool bf16_out, hipStream_t stream, const char** variant) {
-  const TileArgs t{a, a_sc, w, w_sc, M, N, K, y, bf16_out};
+  const TileArgs t{a, a_sc, w, w_sc, M, N, K, y, bf16_out, nullptr, nullptr, false};
   *variant = fp4a ? launch_product<true>(t, stream) : launch_product<false>(t, stream);
   return hipGetLastError();
 }
 
 static size_t a256(size_t b) { return (b + 255) / 256 * 256; }
 
-// [gate/up T x 2I fp32][codes of the intermediate][its scales]
+// Gate/up of few rows: one workgroup per 16 rows and block of 32 intermediate
+// columns; its four wavefronts take 16 gate or 16 up columns each, meet in
+// LDS, and 16 lanes per row make the block's codes, two neighbouring columns
+// a lane.
+template <bool FP4A>
+__global__ __launch_bounds__(256, 2) void fp4_gate_up_rows_kernel(TileArgs A) {
+  __shared__ float h[16][4][17];                  // [row][gate, gate, up, up][column]; rows apart by 68: few conflicts
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = lane & 15, g = lane >> 4;
+  const int I = A.N, K = A.K, nblk = K / 32;
+  const uint32_t nb = I / 32;
+  const int64_t n0 = (int64_t)(blockIdx.x % nb) * 32, m0 = (int64_t)(blockIdx.x / nb) * 16;
+  const int64_t n = n0 + (wave & 1) * 16 + col + (wave >= 2 ? I : 0), m = min(m0 + col, (int64_t)A.M - 1);
+  const v4f acc = rows_tile<FP4A>(A.x + m * (FP4A ? K / 2 : K), A.x_sc + m * nblk, A.w + n * (K / 2), A.w_sc + n * nblk, K, g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[4 * g + i][wave][col] = acc[i];
+  __syncthreads();
+  const int row = threadIdx.x >> 4, c = (threadIdx.x & 15) * 2;       // a DPP row of 16 lanes holds one block
+  const int64_t r = m0 + row;
+  const float g0 = h[row][c >> 4][c & 15], g1 = h[row][c >> 4][(c & 15) + 1];
+  const float u0 = h[row][2 + (c >> 4)][c & 15], u1 = h[row][2 + (c >> 4)][(c & 15) + 1];
+  float a0 = swiglu_near(g0, u0), a1 = swiglu_near(g1, u1);
+  float amax = row16_max(fmaxf(__builtin_fabsf(a0), __builtin_fabsf(a1)));
+  const int emax = A.fp4mid ? 2 : 8;
+  uint32_t s = e8m0_code_for_amax(amax, emax), d;
+  auto codes = [&](float f) -> uint32_t {
+    if (A.fp4mid) return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a0 * f, a1 * f, 1.0f, 0) & 0xFFu;
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(a0 * f, -448.0f, 448.0f),
+                                                     __builtin_amdgcn_fmed3f(a1 * f, -448.0f, 448.0f), 0, false) & 0xFFFFu;
+  };
+  const float f = __builtin_ldexpf(1.0f, 127 - (int)s);
+  d = codes(f * (1.0f - SWIGLU_EPS));
+  const bool sure = fminf(g0, g1) > SWIGLU_MIN_G && near_block(amax) && d == codes(f * (1.0f + SWIGLU_EPS));
+  if (!__all(sure)) {
+    a0 = swiglu(g0, u0);
+    a1 = swiglu(g1, u1);
+    s = e8m0_code_for_amax(row16_max(fmaxf(__builtin_fabsf(a0), __builtin_fabsf(a1))), emax);
+    d = codes(__builtin_ldexpf(1.0f, 127 - (int)s));
+  }
+  if (r >= A.M) return;
+  if (A.fp4mid) A.q[r * (I / 2) + (n0 + c) / 2] = (uint8_t)d;
+  else *reinterpret_cast<uint16_t*>(A.q + r * I + n0 + c) = (uint16_t)d;
+  if (c == 0) A.q_sc[r * nb + n0 / 32] = (uint8_t)s;
+}
+
+// The kernel by the same counts as pick_kernel, of tiles that hold both halves of a block in one wavefront.
+template <bool FP4A>
+static const char* launch_gate_up(const TileArgs& t, hipStream_t stream) {
+  const int M = t.M, N = 2 * t.N;
+  constexpr int KS = FP4A ? 256 : 128, NB = FP4A ? 2 : 3;
+  if (M <= 16 || t.K < 128) {
+    const dim3 grid((unsigned)((int64_t)(t.N / 32) * ((M + 15) / 16)));
+    hipLaunchKernelGGL(fp4_gate_up_rows_kernel<FP4A>, grid, dim3(256), 0, stream, t);
+    return "fp4_ffn:rows16+";
+  }
+  if (tiles_of(M, N, 64, 128) <= 256) {
+    launch_tile<FP4A, true, 2, 2, 1, 2, KS, 4>(t, stream);
+    return "fp4_ffn:tile64x128+";
+  }
+  const int64_t r128 = (tiles_of(M, N, 128, 128) + 511) / 512, r256 = (tiles_of(M, N, 256, 256) + 255) / 256;
+  if (r256 * 8 <= r128 * 5) {
+    launch_tile<FP4A, true, FP4A ? 2 : 4, FP4A ? 4 : 2, FP4A ? 4 : 2, FP4A ? 2 : 4, KS, NB>(t, stream);
+    return "fp4_ffn:tile256x256+";
+  }
+  launch_tile<FP4A, true, 2, 2, 2, 2, KS, NB>(t, stream);
+  return "fp4_ffn:tile128x128+";
+}
+
+// [codes of the intermediate][its scales]
 size_t fp4_ffn_ws_bytes(int T, int H, int I, bool fp4mid) {
   (void)H;
-  return a256((size_t)T * 2 * I * 4) + a256((size_t)T * (fp4mid ? I / 2 : I)) + a256((size_t)T * (I / 32));
+  return a256((size_t)T * (fp4mid ? I / 2 : I)) + a256((size_t)T * (I / 32));
 }
 
 hipError_t launch_fp4_ffn(const uint8_t* x, const uint8_t* x_sc, bool fp4x, int T, int H, const uint8_t* w13,
                           const uint8_t* w13_sc, const uint8_t* w2, const uint8_t* w2_sc, int I, bool fp4mid, void* y,
                           bool bf16_out, void* ws, hipStream_t stream, const char** variant) {
-  float* h = static_cast<float*>(ws);
-  uint8_t* q = static_cast<uint8_t*>(ws) + a256((size_t)T * 2 * I * 4);
+  uint8_t* q = static_cast<uint8_t*>(ws);
   uint8_t* q_sc = q + a256((size_t)T * (fp4mid ? I / 2 : I));
-  hipError_t e = launch_fp4_gemm(x, x_sc, fp4x, w13, w13_sc, T, 2 * I, H, h, false, stream, variant);
-  if (e != hipSuccess) return e;
-  e = launch_swiglu_quantize(h, false, 2 * (int64_t)I, T, I, fp4mid, q, q_sc, stream);
+  const TileArgs t{x, x_sc, w13, w13_sc, T, I, H, nullptr, false, q, q_sc, fp4mid};
+  const char* v = fp4x ? launch_gate_up<true>(t, stream) : launch_gate_up<false>(t, stream);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   e = launch_fp4_gemm(q, q_sc, fp4mid, w2, w2_sc, T, H, I, y, bf16_out, stream, variant);
-  *variant = "fp4_ffn:product+swiglu_quantize+product";
+  *variant = v;
   return e;
 }
 
