@@ -297,81 +297,103 @@ def moe_shared_expert(x, x_sc, w13, w13_sc, w2, w2_sc, y, ws, stream=None):
 
 # ------------------------------------------- dense block in microscaled formats
 # These calls check their tensors here (type, shape, layout, device): a wrong
-# one raises ValueError before anything is launched.
+# one raises ValueError before anything is launched.  At decode sizes the
+# Python side of a call is longer than its kernel, so each call first asks one
+# question that holds for right tensors; only where it does not do the checks
+# below find out what is wrong, or read the strides of rows that lie apart.
+class _Torch:
+    """torch's names that the calls use (torch is imported with the first of them)."""
+
+    def __init__(self):
+        import torch
+        self.u8, self.f32, self.bf16 = torch.uint8, torch.float32, torch.bfloat16
+        self.ins = {torch.float32: MX_IN_F32, torch.bfloat16: MX_IN_BF16}
+        self.outs = {torch.bfloat16: MX_OUT_BF16, torch.float32: MX_OUT_F32}
+        self.current_device = torch.cuda.current_device
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+_torch = None
+
+
+def _tn():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
 def _rows(name, what, t, dtypes, rows, cols):
     """The row stride of t, a 2-D tensor [rows, cols] of one of dtypes with contiguous rows."""
     if t.dim() != 2 or t.dtype not in dtypes or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, expected ({rows}, {cols}) {dtypes}")
+        raise ValueError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, expected ({rows}, {cols}) {tuple(dtypes)}")
     if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
         raise ValueError(f"{name}: {what} must have contiguous rows")
-    return t.stride(0) if rows > 1 else _padded(cols)
-
-
-def _padded(cols):
-    return (cols + 7) // 8 * 8
+    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _packed(name, what, t, dtypes, shape):
     """t is contiguous, of one of dtypes and of this shape."""
     if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, expected contiguous {tuple(shape)} {dtypes}")
+        raise ValueError(f"{name}: {what} is {tuple(t.shape)} {t.dtype}, expected contiguous {tuple(shape)} {tuple(dtypes)}")
 
 
-def _on_current_device(name, *tensors):
-    import torch
-    d = torch.cuda.current_device()
+def _here(name, *tensors):
+    """Every tensor is on the current device."""
+    d = _tn().current_device()
     for t in tensors:
         if t is not None and t.get_device() != d:
             raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{d}")
 
 
-_types = None
-
-
-def _torch_types():
-    """(uint8 only, {fp32, bf16}, MX_IN_* by dtype, MX_OUT_* by dtype)"""
-    global _types
-    if _types is None:
-        import torch
-        _types = ((torch.uint8,), (torch.float32, torch.bfloat16), {torch.float32: MX_IN_F32, torch.bfloat16: MX_IN_BF16},
-                  {torch.bfloat16: MX_OUT_BF16, torch.float32: MX_OUT_F32}, (torch.bfloat16,))
-    return _types
+def _two(name, what, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: {what} must be 2-D")
+    return t.shape
 
 
 def _code_cols(name, fmt, cols):
     """Code bytes of a row of cols elements."""
-    if fmt not in (MX_FMT_E4M3, MX_FMT_E2M1):
-        raise ValueError(f"{name}: unknown format {fmt}")
-    return cols if fmt == MX_FMT_E4M3 else cols // 2
+    if fmt == MX_FMT_E4M3:
+        return cols
+    if fmt == MX_FMT_E2M1:
+        return cols // 2
+    raise ValueError(f"{name}: unknown format {fmt}")
 
 
 def mx_dequantize(q, sc, fmt, out, stream=None):
     """out [rows, cols] (fp32 or bf16) = the values of codes q and scales sc."""
-    name = "mx_dequantize"
-    u8, real, _, outs, _ = _torch_types()
-    if out.dim() != 2:
-        raise ValueError(f"{name}: out must be 2-D")
-    rows, cols = out.shape
-    _packed(name, "out", out, real, (rows, cols))
-    _packed(name, "q", q, u8, (rows, _code_cols(name, fmt, cols)))
-    _packed(name, "sc", sc, u8, (rows, cols // 32))
-    _on_current_device(name, q, sc, out)
-    _check(load().mx_dequantize(_ptr(q), _ptr(sc), fmt, rows, cols, _ptr(out), outs[out.dtype], _stream(stream)), name)
+    name, t = "mx_dequantize", _tn()
+    rows, cols = _two(name, "out", out)
+    qc, d = _code_cols(name, fmt, cols), out.get_device()
+    if not (q.dtype is t.u8 and sc.dtype is t.u8 and out.dtype in t.outs and q.shape == (rows, qc) and
+            sc.shape == (rows, cols // 32) and q.is_contiguous() and sc.is_contiguous() and out.is_contiguous() and
+            q.get_device() == d and sc.get_device() == d and t.current_device() == d):
+        _packed(name, "out", out, t.outs, (rows, cols))
+        _packed(name, "q", q, (t.u8,), (rows, qc))
+        _packed(name, "sc", sc, (t.u8,), (rows, cols // 32))
+        _here(name, q, sc, out)
+    _check(load().mx_dequantize(q.data_ptr(), sc.data_ptr(), fmt, rows, cols, out.data_ptr(), t.outs[out.dtype],
+                                t.raw_stream(d) if stream is None else stream), name)
 
 
 def mx_swiglu_quantize(gu, q, sc, fmt, stream=None):
     """q, sc = codes of silu(gate) * up; gu [T, 2I] (fp32 or bf16, any row stride that keeps rows 16-byte
     aligned), gate in the first I columns."""
-    name = "mx_swiglu_quantize"
-    u8, real, ins, _, _ = _torch_types()
-    if gu.dim() != 2:
-        raise ValueError(f"{name}: gu must be 2-D")
-    T, I = gu.shape[0], gu.shape[1] // 2
-    ld = _rows(name, "gu", gu, real, T, 2 * I)
-    _packed(name, "q", q, u8, (T, _code_cols(name, fmt, I)))
-    _packed(name, "sc", sc, u8, (T, I // 32))
-    _on_current_device(name, gu, q, sc)
-    _check(load().mx_swiglu_quantize(_ptr(gu), ins[gu.dtype], ld, T, I, fmt, _ptr(q), _ptr(sc), _stream(stream)), name)
+    name, t = "mx_swiglu_quantize", _tn()
+    T, two_i = _two(name, "gu", gu)
+    I = two_i // 2
+    qc, d, ld = _code_cols(name, fmt, I), gu.get_device(), two_i
+    if not (gu.dtype in t.ins and gu.is_contiguous() and two_i == 2 * I and q.dtype is t.u8 and sc.dtype is t.u8 and
+            q.shape == (T, qc) and sc.shape == (T, I // 32) and q.is_contiguous() and sc.is_contiguous() and
+            q.get_device() == d and sc.get_device() == d and t.current_device() == d):
+        ld = _rows(name, "gu", gu, t.ins, T, 2 * I)
+        _packed(name, "q", q, (t.u8,), (T, qc))
+        _packed(name, "sc", sc, (t.u8,), (T, I // 32))
+        _here(name, gu, q, sc)
+    _check(load().mx_swiglu_quantize(gu.data_ptr(), t.ins[gu.dtype], ld, T, I, fmt, q.data_ptr(), sc.data_ptr(),
+                                     t.raw_stream(d) if stream is None else stream), name)
 
 
 def mx_add_rmsnorm(x, weight, eps, residual=None, x2=None, h=None, n=None, q=None, sc=None, fmt=MX_FMT_E4M3,
@@ -380,51 +402,70 @@ def mx_add_rmsnorm(x, weight, eps, residual=None, x2=None, h=None, n=None, q=Non
     x, x2, residual, h [T, H] fp32 or bf16 (x and x2 of one type and row stride, residual and h too; h may be
     residual); weight [H] fp32 or bf16 or None; n [T, H] bf16; q, sc the codes of n in fmt.  The outputs that are
     given are written."""
-    name = "mx_add_rmsnorm"
-    u8, real, ins, _, bf16 = _torch_types()
-    if x.dim() != 2:
-        raise ValueError(f"{name}: x must be 2-D")
-    T, H = x.shape
-    x_ld = _rows(name, "x", x, real, T, H)
-    if x2 is not None and _rows(name, "x2", x2, (x.dtype,), T, H) != x_ld:
-        raise ValueError(f"{name}: x2 must have x's row stride")
+    name, t = "mx_add_rmsnorm", _tn()
+    shape = _two(name, "x", x)
+    T, H = shape
+    d, ins = x.get_device(), t.ins
     r = residual if residual is not None else h
-    r_ld, r_dtype = H, MX_IN_F32
-    if r is not None:
-        r_ld, r_dtype = _rows(name, "residual", r, real, T, H), ins[r.dtype]
-        if h is not None and h is not r and _rows(name, "h", h, (r.dtype,), T, H) != r_ld:
-            raise ValueError(f"{name}: h must have the residual's row stride")
-    if weight is not None:
-        _packed(name, "weight", weight, real, (H,))
-    if n is not None:
-        _packed(name, "n", n, bf16, (T, H))
-    if (q is None) != (sc is None):
-        raise ValueError(f"{name}: q and sc come together")
-    if q is not None:
-        _packed(name, "q", q, u8, (T, _code_cols(name, fmt, H)))
-        _packed(name, "sc", sc, u8, (T, H // 32))
-    _on_current_device(name, x, weight, residual, x2, h, n, q, sc)
-    _check(load().mx_add_rmsnorm(_ptr(x), _ptr(x2), ins[x.dtype], x_ld, _ptr(residual), _ptr(h), r_dtype, r_ld,
-                                 _ptr(weight), MX_IN_F32 if weight is None else ins[weight.dtype], T, H, eps, _ptr(n),
-                                 _ptr(q), _ptr(sc), fmt, _stream(stream)), name)
+    x_ld = r_ld = H
+    if not (x.dtype in ins and x.is_contiguous() and
+            (x2 is None or x2.dtype is x.dtype and x2.shape == shape and x2.is_contiguous() and x2.get_device() == d) and
+            (r is None or r.dtype in ins and r.shape == shape and r.is_contiguous() and r.get_device() == d) and
+            (h is None or h is r or h.dtype is r.dtype and h.shape == shape and h.is_contiguous() and
+             h.get_device() == d) and
+            (weight is None or weight.dtype in ins and weight.shape == (H,) and weight.is_contiguous() and
+             weight.get_device() == d) and
+            (n is None or n.dtype is t.bf16 and n.shape == shape and n.is_contiguous() and n.get_device() == d) and
+            (q is None and sc is None or q is not None and sc is not None and q.dtype is t.u8 and sc.dtype is t.u8 and
+             q.shape == (T, _code_cols(name, fmt, H)) and sc.shape == (T, H // 32) and q.is_contiguous() and
+             sc.is_contiguous() and q.get_device() == d and sc.get_device() == d) and t.current_device() == d):
+        x_ld = _rows(name, "x", x, ins, T, H)
+        if x2 is not None and _rows(name, "x2", x2, (x.dtype,), T, H) != x_ld:
+            raise ValueError(f"{name}: x2 must have x's row stride")
+        if r is not None:
+            r_ld = _rows(name, "residual", r, ins, T, H)
+            if h is not None and h is not r and _rows(name, "h", h, (r.dtype,), T, H) != r_ld:
+                raise ValueError(f"{name}: h must have the residual's row stride")
+        if weight is not None:
+            _packed(name, "weight", weight, ins, (H,))
+        if n is not None:
+            _packed(name, "n", n, (t.bf16,), (T, H))
+        if (q is None) != (sc is None):
+            raise ValueError(f"{name}: q and sc come together")
+        if q is not None:
+            _packed(name, "q", q, (t.u8,), (T, _code_cols(name, fmt, H)))
+            _packed(name, "sc", sc, (t.u8,), (T, H // 32))
+        _here(name, x, weight, residual, x2, h, n, q, sc)
+    _check(load().mx_add_rmsnorm(x.data_ptr(), None if x2 is None else x2.data_ptr(), ins[x.dtype], x_ld,
+                                 None if residual is None else residual.data_ptr(), None if h is None else h.data_ptr(),
+                                 MX_IN_F32 if r is None else ins[r.dtype], r_ld,
+                                 None if weight is None else weight.data_ptr(),
+                                 MX_IN_F32 if weight is None else ins[weight.dtype], T, H, eps,
+                                 None if n is None else n.data_ptr(), None if q is None else q.data_ptr(),
+                                 None if sc is None else sc.data_ptr(), fmt,
+                                 t.raw_stream(d) if stream is None else stream), name)
 
 
 def fp4_block_gemm(a, a_sc, a_fmt, w, w_sc, y, stream=None):
     """y [M, N] (bf16 or fp32) = a . w^T; a codes of K elements a row in a_fmt, w E2M1 [N, K/2], scales [., K/32]."""
-    name = "fp4_block_gemm"
-    u8, real, _, outs, _ = _torch_types()
-    if w.dim() != 2 or y.dim() != 2:
-        raise ValueError(f"{name}: w and y must be 2-D")
-    (N, K), M = w.shape, y.shape[0]
+    name, t = "fp4_block_gemm", _tn()
+    N, K = _two(name, "w", w)
+    M, yn = _two(name, "y", y)
     K *= 2
-    _packed(name, "w", w, u8, (N, K // 2))
-    _packed(name, "w_sc", w_sc, u8, (N, K // 32))
-    _packed(name, "a", a, u8, (M, _code_cols(name, a_fmt, K)))
-    _packed(name, "a_sc", a_sc, u8, (M, K // 32))
-    _packed(name, "y", y, real, (M, N))
-    _on_current_device(name, a, a_sc, w, w_sc, y)
-    _check(load().fp4_block_gemm(_ptr(a), _ptr(a_sc), a_fmt, _ptr(w), _ptr(w_sc), M, N, K, _ptr(y), outs[y.dtype],
-                                 _stream(stream)), name)
+    ac, nb, d, u8 = _code_cols(name, a_fmt, K), K // 32, y.get_device(), t.u8
+    if not (yn == N and y.dtype in t.outs and w.dtype is u8 and a.dtype is u8 and a_sc.dtype is u8 and w_sc.dtype is u8 and
+            a.shape == (M, ac) and a_sc.shape == (M, nb) and w_sc.shape == (N, nb) and w.is_contiguous() and
+            a.is_contiguous() and a_sc.is_contiguous() and w_sc.is_contiguous() and y.is_contiguous() and
+            a.get_device() == d and a_sc.get_device() == d and w.get_device() == d and w_sc.get_device() == d and
+            t.current_device() == d):
+        _packed(name, "w", w, (u8,), (N, K // 2))
+        _packed(name, "w_sc", w_sc, (u8,), (N, nb))
+        _packed(name, "a", a, (u8,), (M, ac))
+        _packed(name, "a_sc", a_sc, (u8,), (M, nb))
+        _packed(name, "y", y, t.outs, (M, N))
+        _here(name, a, a_sc, w, w_sc, y)
+    _check(load().fp4_block_gemm(a.data_ptr(), a_sc.data_ptr(), a_fmt, w.data_ptr(), w_sc.data_ptr(), M, N, K,
+                                 y.data_ptr(), t.outs[y.dtype], t.raw_stream(d) if stream is None else stream), name)
 
 
 def fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt):
@@ -433,24 +474,33 @@ def fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt):
 
 def fp4_dense_ffn(x, x_sc, x_fmt, w13, w13_sc, w2, w2_sc, mid_fmt, y, ws, stream=None):
     """y [T, H] (bf16 or fp32) = SwiGLU FFN of x (codes in x_fmt) with E2M1 weights w13 [2I, H/2] (gate, then up),
-    w2 [H, I/2]; the intermediate in mid_fmt; ws a uint8 tensor of fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt)."""
-    name = "fp4_dense_ffn"
-    u8, real, _, outs, _ = _torch_types()
-    if w2.dim() != 2 or y.dim() != 2:
-        raise ValueError(f"{name}: w2 and y must be 2-D")
-    T, H, I = y.shape[0], w2.shape[0], w2.shape[1] * 2
-    _packed(name, "x", x, u8, (T, _code_cols(name, x_fmt, H)))
-    _packed(name, "x_sc", x_sc, u8, (T, H // 32))
-    _packed(name, "w13", w13, u8, (2 * I, H // 2))
-    _packed(name, "w13_sc", w13_sc, u8, (2 * I, H // 32))
-    _packed(name, "w2", w2, u8, (H, I // 2))
-    _packed(name, "w2_sc", w2_sc, u8, (H, I // 32))
-    _packed(name, "y", y, real, (T, H))
-    if not ws.is_contiguous():
-        raise ValueError(f"{name}: ws must be contiguous")
-    _on_current_device(name, x, x_sc, w13, w13_sc, w2, w2_sc, y, ws)
-    _check(load().fp4_dense_ffn(_ptr(x), _ptr(x_sc), x_fmt, T, H, _ptr(w13), _ptr(w13_sc), _ptr(w2), _ptr(w2_sc), I,
-                                mid_fmt, _ptr(y), outs[y.dtype], _ptr(ws), ws.nbytes, _stream(stream)), name)
+    w2 [H, I/2]; the intermediate in mid_fmt; ws a tensor of fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt) bytes."""
+    name, t = "fp4_dense_ffn", _tn()
+    H, I = _two(name, "w2", w2)
+    T = _two(name, "y", y)[0]
+    I *= 2
+    xc, hb, ib, d, u8 = _code_cols(name, x_fmt, H), H // 32, I // 32, y.get_device(), t.u8
+    if not (y.dtype in t.outs and y.shape == (T, H) and x.dtype is u8 and x_sc.dtype is u8 and w13.dtype is u8 and
+            w13_sc.dtype is u8 and w2.dtype is u8 and w2_sc.dtype is u8 and x.shape == (T, xc) and
+            x_sc.shape == (T, hb) and w13.shape == (2 * I, H // 2) and w13_sc.shape == (2 * I, hb) and
+            w2_sc.shape == (H, ib) and x.is_contiguous() and x_sc.is_contiguous() and w13.is_contiguous() and
+            w13_sc.is_contiguous() and w2.is_contiguous() and w2_sc.is_contiguous() and y.is_contiguous() and
+            ws.is_contiguous() and x.get_device() == d and x_sc.get_device() == d and w13.get_device() == d and
+            w13_sc.get_device() == d and w2.get_device() == d and w2_sc.get_device() == d and ws.get_device() == d and
+            t.current_device() == d):
+        _packed(name, "x", x, (u8,), (T, xc))
+        _packed(name, "x_sc", x_sc, (u8,), (T, hb))
+        _packed(name, "w13", w13, (u8,), (2 * I, H // 2))
+        _packed(name, "w13_sc", w13_sc, (u8,), (2 * I, hb))
+        _packed(name, "w2", w2, (u8,), (H, I // 2))
+        _packed(name, "w2_sc", w2_sc, (u8,), (H, ib))
+        _packed(name, "y", y, t.outs, (T, H))
+        if not ws.is_contiguous():
+            raise ValueError(f"{name}: ws must be contiguous")
+        _here(name, x, x_sc, w13, w13_sc, w2, w2_sc, y, ws)
+    _check(load().fp4_dense_ffn(x.data_ptr(), x_sc.data_ptr(), x_fmt, T, H, w13.data_ptr(), w13_sc.data_ptr(),
+                                w2.data_ptr(), w2_sc.data_ptr(), I, mid_fmt, y.data_ptr(), t.outs[y.dtype],
+                                ws.data_ptr(), ws.nbytes, t.raw_stream(d) if stream is None else stream), name)
 
 
 def prefetch(t, chunk_bytes=0, stream=None, nbytes=None):
