@@ -395,7 +395,7 @@ mx_status mx_add_rmsnorm(const void* x, const void* x2, int x_dtype, int64_t x_l
       !aligned(n, 16) || !aligned(q, 16))
     return MX_EINVAL;
   const mx::NormArgs a{x, x2, x_ld, x_dtype == MX_IN_BF16, residual, h, res_ld, res && res_dtype == MX_IN_BF16,
-                       weight, w_dtype == MX_IN_BF16, n, q, sc, fmt == MX_FMT_E2M1, H, eps};
+                       weight, w_dtype == MX_IN_BF16, n, q, sc, fmt == MX_FMT_E2M1, H, eps, 1.0 / H};
   const hipError_t e = mx::launch_add_rmsnorm(a, T, static_cast<hipStream_t>(stream));
   if (e == hipSuccess) g_variant = "add_rmsnorm:row";
   return from_hip(e);

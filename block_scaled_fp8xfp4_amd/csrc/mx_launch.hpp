@@ -31,7 +31,7 @@ struct NormArgs {                                 // strides in elements; x2, re
   const void* residual; void* h; int64_t r_ld; bool r_bf16;
   const void* w; bool w_bf16;
   uint16_t* n; uint8_t* q; uint8_t* sc; bool fp4;
-  int H; float eps;
+  int H; float eps; double inv_h;                 // 1 / H
 };
 hipError_t launch_add_rmsnorm(const NormArgs& a, int T, hipStream_t stream);
 
