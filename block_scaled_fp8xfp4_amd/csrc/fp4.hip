@@ -20,21 +20,45 @@ __device__ __forceinline__ v4f mfma_fp4_fp4(const v8i& a, const v8i& b, v4f c, u
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// Few rows: one wavefront per 16 x 16 tile, operands straight to registers,
-// RING pieces of K = 512 in flight per wavefront: with one wavefront per CU
-// (N = 4096) that is what it takes to keep HBM busy.  Wavefronts of one
-// workgroup are the row tiles of the same 16 columns; they meet at the
-// weights in L1.  Lane l serves row / column l % 16; lanes past M or N repeat
-// the last row / column, their results are not stored.  K past the last whole
-// piece is read with clamped addresses and zeroed, its scales past K are 127.
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
 
-constexpr int RPK = 512;                          // K per piece: four 16x16x128 steps
+template <typename V> __device__ __forceinline__ V lds_read(uint32_t addr) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) V*>(addr);
+}
+template <typename V> __device__ __forceinline__ void lds_write(uint32_t addr, const V& v) {
+  *reinterpret_cast<__attribute__((address_space(3))) V*>(addr) = v;
+}
 
-template <bool FP4A> struct RowsPiece { u32x4 w[4], alo[4], ahi[FP4A ? 1 : 4], ws, as; };
+struct TileArgs {
+  const uint8_t* x; const uint8_t* x_sc;          // activations [M][K]
+  const uint8_t* w; const uint8_t* w_sc;          // weights [N][K]; SwiGLU: [2N][K], gate rows then up rows
+  int M, N, K;
+  void* y; bool bf16_out;                         // [M][N]
+  uint8_t* q; uint8_t* q_sc; bool fp4mid;         // SwiGLU: codes [M][N] instead
+};
+
+constexpr int RPK = 512;                          // K per piece of few rows: four 16x16x128 steps
+
+// This lane's column n of rows r0 .. r0 + 3.
+__device__ __forceinline__ void store_rows(const TileArgs& A, const v4f& acc, int64_t r0, int64_t n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (r0 + i >= A.M) continue;
+    if (A.bf16_out) static_cast<uint16_t*>(A.y)[(r0 + i) * A.N + n] = f32_to_bf16_rne(acc[i]);
+    else static_cast<float*>(A.y)[(r0 + i) * A.N + n] = acc[i];
+  }
+}
+
+// Up to 16 rows, 16 columns: one wavefront that reads both operands straight
+// to registers.  Lane l serves row / column l % 16; lanes past M or N repeat
+// the last row / column, their results are not stored.  K past the last whole
+// piece is read with clamped addresses and zeroed, its scales are 127.
+
+template <bool FP4A> struct LonePiece { u32x4 w[4], alo[4], ahi[FP4A ? 1 : 4], ws, as; };
 
 template <bool FP4A>
-__device__ __forceinline__ void rows_load(RowsPiece<FP4A>& P, const uint8_t* wp, const uint8_t* wsp, const uint8_t* ap,
+__device__ __forceinline__ void lone_load(LonePiece<FP4A>& P, const uint8_t* wp, const uint8_t* wsp, const uint8_t* ap,
                                           const uint8_t* asp, int c, int g) {
   P.as = *reinterpret_cast<const u32x4_a1*>(asp + c * 16);
   P.ws = *reinterpret_cast<const u32x4_a1*>(wsp + c * 16);
@@ -51,7 +75,7 @@ __device__ __forceinline__ void rows_load(RowsPiece<FP4A>& P, const uint8_t* wp,
 
 // The piece that K ends in: blocks past K are read from the last block and replaced.
 template <bool FP4A>
-__device__ __forceinline__ void rows_load_tail(RowsPiece<FP4A>& P, const uint8_t* wp, const uint8_t* wsp,
+__device__ __forceinline__ void lone_load_tail(LonePiece<FP4A>& P, const uint8_t* wp, const uint8_t* wsp,
                                                const uint8_t* ap, const uint8_t* asp, int c, int g, int nblk) {
   const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
@@ -74,7 +98,7 @@ __device__ __forceinline__ void rows_load_tail(RowsPiece<FP4A>& P, const uint8_t
 }
 
 template <bool FP4A>
-__device__ __forceinline__ v4f rows_multiply(const RowsPiece<FP4A>& P, v4f acc, int g) {
+__device__ __forceinline__ v4f lone_multiply(const LonePiece<FP4A>& P, v4f acc, int g) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const v8i w = {(int)P.w[s][0], (int)P.w[s][1], (int)P.w[s][2], (int)P.w[s][3], 0, 0, 0, 0};
@@ -88,65 +112,203 @@ __device__ __forceinline__ v4f rows_multiply(const RowsPiece<FP4A>& P, v4f acc, 
 
 // The 16 x 16 tile of rows ap (this lane's row) and columns wp (its column) over all of K.
 template <bool FP4A>
-__device__ __forceinline__ v4f rows_tile(const uint8_t* ap, const uint8_t* asp, const uint8_t* wp, const uint8_t* wsp,
+__device__ __forceinline__ v4f lone_tile(const uint8_t* ap, const uint8_t* asp, const uint8_t* wp, const uint8_t* wsp,
                                          int K, int g) {
   constexpr int RING = FP4A ? 4 : 3;              // 40 and 56 registers each, and one more of them
   const int nblk = K / 32, whole = K / RPK;
-  RowsPiece<FP4A> P[RING], T;
+  LonePiece<FP4A> P[RING], T;
   v4f acc = {0.f, 0.f, 0.f, 0.f};
   int c = 0;
   if (whole >= RING) {
 #pragma unroll
-    for (int r = 0; r < RING; ++r) rows_load(P[r], wp, wsp, ap, asp, r, g);
+    for (int r = 0; r < RING; ++r) lone_load(P[r], wp, wsp, ap, asp, r, g);
     for (; c + 2 * RING <= whole; c += RING)
 #pragma unroll
       for (int r = 0; r < RING; ++r) {
-        acc = rows_multiply(P[r], acc, g);
-        rows_load(P[r], wp, wsp, ap, asp, c + RING + r, g);
+        acc = lone_multiply(P[r], acc, g);
+        lone_load(P[r], wp, wsp, ap, asp, c + RING + r, g);
       }
 #pragma unroll
     for (int r = 0; r < RING; ++r) {                                  // the last whole pieces but fewer than RING
-      acc = rows_multiply(P[r], acc, g);
-      if (c + RING + r < whole) rows_load(P[r], wp, wsp, ap, asp, c + RING + r, g);
+      acc = lone_multiply(P[r], acc, g);
+      if (c + RING + r < whole) lone_load(P[r], wp, wsp, ap, asp, c + RING + r, g);
     }
     c += RING;
   } else {
 #pragma unroll
     for (int r = 0; r + 1 < RING; ++r)
-      if (r < whole) rows_load(P[r], wp, wsp, ap, asp, r, g);
+      if (r < whole) lone_load(P[r], wp, wsp, ap, asp, r, g);
   }
-  if (K % RPK) rows_load_tail(T, wp, wsp, ap, asp, whole, g, nblk);
+  if (K % RPK) lone_load_tail(T, wp, wsp, ap, asp, whole, g, nblk);
 #pragma unroll
   for (int r = 0; r + 1 < RING; ++r)
-    if (c + r < whole) acc = rows_multiply(P[r], acc, g);
-  if (K % RPK) acc = rows_multiply(T, acc, g);
+    if (c + r < whole) acc = lone_multiply(P[r], acc, g);
+  if (K % RPK) acc = lone_multiply(T, acc, g);
   return acc;
 }
 
-constexpr int ROWS_MAX = 64;                      // rows of one workgroup: 4 wavefronts
-
 template <bool FP4A>
-__global__ __launch_bounds__(256, 2) void fp4_rows_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_sc,
-                                                          const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_sc,
-                                                          int M, int N, int K, void* __restrict__ y, bool bf16_out) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = lane & 15, g = lane >> 4;
-  const uint32_t nct = (N + 15) / 16;
-  const int64_t n0 = (int64_t)(blockIdx.x % nct) * 16;
-  const int64_t m0 = (int64_t)(blockIdx.x / nct) * ROWS_MAX + wave * 16;
-  if (m0 >= M) return;
-  const int64_t n = min(n0 + col, (int64_t)N - 1), m = min(m0 + col, (int64_t)M - 1);
-  const int nblk = K / 32;
-  const v4f acc = rows_tile<FP4A>(a + m * (FP4A ? K / 2 : K), a_sc + m * nblk, w + n * (K / 2), w_sc + n * nblk, K, g);
-  if (n0 + col < N)
+__global__ __launch_bounds__(64, 2) void fp4_lone_kernel(TileArgs A) {
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const int M = A.M, N = A.N, K = A.K, nblk = K / 32;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n = min(n0 + col, (int64_t)N - 1), m = min(col, M - 1);
+  const v4f acc = lone_tile<FP4A>(A.x + m * (FP4A ? K / 2 : K), A.x_sc + m * nblk, A.w + n * (K / 2), A.w_sc + n * nblk, K, g);
+  if (n0 + col < N) store_rows(A, acc, 4 * g, n);
+}
+
+// The same for long rows or many columns: workgroups of four wavefronts, all
+// of which bring up to 16 rows and their scales to LDS by DMA; CW of them then
+// take 16 columns each, whose weights go straight to registers, eight pieces
+// of K = 512 in flight.  The weights are asked for behind the rows and before
+// the wait for them.  Read by every wavefront, the rows were two thirds of
+// what the CU's vector memory path moved.
+//
+// LDS: rows of a multiple of 128 bytes, the 16-byte chunks of each group of
+// eight XORed with the row's low bits; then rows of scales of a multiple of 16.
+constexpr int ROWS_WAVES = 4;
+constexpr uint32_t ROWS_LDS = 144 * 1024;         // most that a workgroup's rows and scales may take
+struct RowsShape { uint32_t row, sc; };           // bytes per row in LDS
+__host__ __device__ __forceinline__ RowsShape rows_shape(int K, bool fp4a) {
+  return {((uint32_t)(fp4a ? K / 2 : K) + 127) / 128 * 128, ((uint32_t)K / 32 + 15) / 16 * 16};
+}
+static uint32_t rows_lds(int M, int K, bool fp4a) {
+  const RowsShape s = rows_shape(K, fp4a);
+  return (uint32_t)(M < 16 ? M : 16) * (s.row + s.sc) + RPK;           // a row's last piece is read whole
+}
+
+struct RowsPiece { u32x4 w[4], ws; };             // five loads
+__device__ __forceinline__ void rows_load(RowsPiece& P, const uint8_t* wp, const uint8_t* wsp, int c, int g) {
+  P.ws = *reinterpret_cast<const u32x4_a1*>(wsp + c * 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = m0 + 4 * g + i;
-      if (r < M) {
-        if (bf16_out) static_cast<uint16_t*>(y)[r * N + n] = f32_to_bf16_rne(acc[i]);
-        else static_cast<float*>(y)[r * N + n] = acc[i];
-      }
+  for (int s = 0; s < 4; ++s) P.w[s] = ldg16(wp + c * 256 + s * 64 + g * 16);
+}
+// The piece that K ends in: blocks past K are read from the last block and replaced.
+__device__ __forceinline__ void rows_load_tail(RowsPiece& P, const uint8_t* wp, const uint8_t* wsp, int c, int g, int nblk) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int b = c * 16 + s * 4 + g, bc = min(b, nblk - 1);
+    const u32x4 w = ldg16(wp + bc * 16);
+    P.w[s] = b < nblk ? w : u32x4{0, 0, 0, 0};
+    P.ws[s] = (b < nblk ? (uint32_t)wsp[bc] : 127u) << (8 * g);
+  }
+}
+
+struct RowsLds { uint32_t row, sc; int r; };      // this lane's row and scales in LDS, and the row's number
+
+template <bool FP4A, bool TAIL>
+__device__ __forceinline__ v4f rows_multiply(const RowsPiece& P, const RowsLds& L, v4f acc, int c, int g, int nblk) {
+  const u32x4 as = lds_read<u32x4>(L.sc + c * 16);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const v8i w = {(int)P.w[s][0], (int)P.w[s][1], (int)P.w[s][2], (int)P.w[s][3], 0, 0, 0, 0};
+    // Chunks of 32 (E2M1) or 16 (E4M3: K = 128 s + 16 g and 64 further) elements; their places in LDS.
+    const int i = FP4A ? s * 4 + g : s * 8 + g, past = FP4A ? nblk - c * 16 : 2 * (nblk - c * 16);
+    auto chunk = [&](int i) {
+      return lds_read<u32x4>(L.row + c * (FP4A ? 256 : 512) + (uint32_t)(i / 8 * 8 + ((i ^ L.r) & 7)) * 16);
+    };
+    u32x4 lo = chunk(i), hi = {0, 0, 0, 0};
+    if (!FP4A) hi = chunk(i + 4);
+    uint32_t sa = as[s] >> (8 * g);
+    if (TAIL) {                                   // LDS past K holds anything
+      if (i >= past) lo = u32x4{0, 0, 0, 0};
+      if (i + 4 >= past) hi = u32x4{0, 0, 0, 0};
+      if (s * 4 + g >= nblk - c * 16) sa = 127;
     }
+    const v8i a = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    const uint32_t sb = P.ws[s] >> (8 * g);
+    acc = FP4A ? mfma_fp4_fp4(a, w, acc, sa, sb) : mfma_fp8_fp4(a, w, acc, sa, sb);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  return acc;
+}
+
+template <bool FP4A, int RING>
+__device__ __forceinline__ v4f rows_ring(const RowsLds& L, const uint8_t* wp, const uint8_t* wsp, int nblk, int g) {
+  const int whole = nblk / 16, tail = nblk % 16;
+  RowsPiece P[RING];
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int r = 0; r < RING; ++r) rows_load(P[r], wp, wsp, r, g);
+  __builtin_amdgcn_sched_barrier(0);              // the count below is of the loads above
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(RING * 5) : "memory");
+  lds_barrier();
+  int c = 0;
+  for (; c + 2 * RING <= whole; c += RING)
+#pragma unroll
+    for (int r = 0; r < RING; ++r) {
+      acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
+      rows_load(P[r], wp, wsp, c + RING + r, g);
+    }
+#pragma unroll
+  for (int r = 0; r < RING; ++r) {                                    // the last whole pieces but fewer than RING
+    acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
+    if (c + RING + r < whole) rows_load(P[r], wp, wsp, c + RING + r, g);
+  }
+  c += RING;
+  if (tail) rows_load_tail(P[RING - 1], wp, wsp, whole, g, nblk);
+#pragma unroll
+  for (int r = 0; r + 1 < RING; ++r)
+    if (c + r < whole) acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
+  if (tail) acc = rows_multiply<FP4A, true>(P[RING - 1], L, acc, whole, g, nblk);
+  return acc;
+}
+
+// The workgroup's rows (a, a_sc from its first row on) to LDS, and for the first CW wavefronts the 16 x 16 tile of this
+// lane's weight row wp, wsp over all of K.  Every wavefront passes one barrier.
+template <bool FP4A, int CW>
+__device__ __forceinline__ v4f rows_tile(uint32_t lds, const uint8_t* a, const uint8_t* a_sc, int rows, const uint8_t* wp,
+                                         const uint8_t* wsp, int K) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, nblk = K / 32, whole = K / RPK;
+  const uint32_t rowb = FP4A ? K / 2 : K;
+  const RowsShape sh = rows_shape(K, FP4A);
+  const uint32_t lsc = lds + rows * sh.row;
+  for (int r = wave; r < rows; r += ROWS_WAVES) {
+    const uint32_t swz = (lane ^ (r & 7)) * 16;
+    for (uint32_t c = 0; c < sh.row; c += 1024)
+      if (c + lane * 16 < sh.row) dma16_to_lds(a + (size_t)r * rowb, min(c + swz, rowb - 16), lds + r * sh.row + c);
+    if (K % 128 == 0) {
+      for (uint32_t c = 0; c < (uint32_t)nblk; c += 256)
+        if (c + lane * 4 < (uint32_t)nblk) dma4_to_lds(a_sc + r * nblk, c + lane * 4, lsc + r * sh.sc + c);
+    } else {                                      // rows of scales start at any byte
+      for (int c = lane; c < nblk; c += 64) lds_write<uint8_t>(lsc + r * sh.sc + c, a_sc[r * nblk + c]);
+    }
+  }
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  const int r = min(lane & 15, rows - 1);
+  const RowsLds L{lds + r * sh.row, lsc + r * sh.sc, r & 7};
+  asm volatile("" ::: "memory");
+  if (wave < CW && whole >= 8) return rows_ring<FP4A, 8>(L, wp, wsp, nblk, g);
+  if (wave < CW && whole >= 4) return rows_ring<FP4A, 4>(L, wp, wsp, nblk, g);
+  RowsPiece P[3], T;
+  if (wave < CW) {
+#pragma unroll
+    for (int r = 0; r < 3; ++r)
+      if (r < whole) rows_load(P[r], wp, wsp, r, g);
+    if (nblk % 16) rows_load_tail(T, wp, wsp, whole, g, nblk);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  lds_barrier();
+  if (wave >= CW) return acc;
+#pragma unroll
+  for (int r = 0; r < 3; ++r)
+    if (r < whole) acc = rows_multiply<FP4A, false>(P[r], L, acc, r, g, nblk);
+  if (nblk % 16) acc = rows_multiply<FP4A, true>(T, L, acc, whole, g, nblk);
+  return acc;
+}
+
+template <bool FP4A, int CW>
+__global__ __launch_bounds__(64 * ROWS_WAVES, 2) void fp4_rows_kernel(TileArgs A) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int M = A.M, N = A.N, K = A.K, col = lane & 15, nblk = K / 32;
+  const uint32_t nct = (N + 16 * CW - 1) / (16 * CW);
+  const int64_t n0 = ((int64_t)(blockIdx.x % nct) * CW + wave) * 16, m0 = (int64_t)(blockIdx.x / nct) * 16;
+  const int64_t n = min(n0 + col, (int64_t)N - 1);
+  const v4f acc = rows_tile<FP4A, CW>(__builtin_amdgcn_readfirstlane(lds_addr(lds)), A.x + m0 * (FP4A ? K / 2 : K), A.x_sc + m0 * nblk,
+                                      (int)min((int64_t)16, M - m0), A.w + n * (K / 2), A.w_sc + n * nblk, K);
+  if (wave < CW && n0 + col < N) store_rows(A, acc, m0 + 4 * (lane >> 4), n);
 }
 
 // Many rows: BM x BN output tiles staged through LDS.  A stage holds K = KS
@@ -181,17 +343,10 @@ __device__ __forceinline__ void dma16_to_lds_if(int on, const void* base, uint32
 }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32_a1 __attribute__((aligned(1)));
 
 __device__ __forceinline__ int swz4(int r) { return (((r >> 1) ^ (r >> 3)) & 1) | ((r >> 1) & 2); }
 __device__ __forceinline__ int swz8(int r) { return (r & 6) | ((r >> 3) & 1); }
 
-template <typename V> __device__ __forceinline__ V lds_read(uint32_t addr) {
-  return *reinterpret_cast<const __attribute__((address_space(3))) V*>(addr);
-}
-template <typename V> __device__ __forceinline__ void lds_write(uint32_t addr, const V& v) {
-  *reinterpret_cast<__attribute__((address_space(3))) V*>(addr) = v;
-}
 __device__ __forceinline__ v8i operand(const u32x4& lo) {
   return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], 0, 0, 0, 0};
 }
@@ -232,14 +387,6 @@ struct TileShape {
   static constexpr int FIRST = NST == 2 || WHOLE ? NV : NV / 2;
   static_assert(NX * NW * 1024 == BM * RA && NWT * NW * 1024 == BN * RW, "whole rows");
   static_assert(LDS <= 160 * 1024 && NV * (NST - 1) < 63, "LDS and vmcnt");
-};
-
-struct TileArgs {
-  const uint8_t* x; const uint8_t* x_sc;          // activations [M][K]
-  const uint8_t* w; const uint8_t* w_sc;          // weights [N][K]; SwiGLU: [2N][K], gate rows then up rows
-  int M, N, K;
-  void* y; bool bf16_out;                         // [M][N]
-  uint8_t* q; uint8_t* q_sc; bool fp4mid;         // SwiGLU: codes [M][N] instead
 };
 
 // SwiGLU + codes of one row's block of 32: gate and up of this lane's 16
@@ -758,17 +905,37 @@ static void launch_tile(const TileArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((fp4_tile_kernel<FP4A, SWIGLU, WM, WN, TM, TN, KS, NST>), grid, block, 0, stream, a);
 }
 
+static int64_t tiles_of(int M, int N, int bm, int bn) { return ((int64_t)M + bm - 1) / bm * (((int64_t)N + bn - 1) / bn); }
+template <bool FP4A, int CW> static void launch_rows_of(const TileArgs& t, hipStream_t stream) {
+  const dim3 grid((unsigned)(tiles_of(t.M, t.N, 16, 16 * CW)));       // CW = 4 past 512: about M N / 2^10 < 2^31
+  hipLaunchKernelGGL((fp4_rows_kernel<FP4A, CW>), grid, dim3(64 * ROWS_WAVES), rows_lds(t.M, t.K, FP4A), stream, t);
+}
+// By how many wavefronts of 16 columns there are and by what a row is long.  Alone / through LDS at M = 1 and 16, us:
+//   E2M1 4096 x 576 2.7 / 3.1, 3.0 / 4.0; 4096 x 4096 4.2 / 4.4, 4.9 / 5.3; 4096 x 8192 6.8 / 6.4, 7.9 / 7.7;
+//        16384 x 4096 8.9 / 8.9, 12.3 / 10.2
+//   E4M3 4096 x 2048 3.4 / 3.7, 4.0 / 4.6; 4096 x 4096 4.8 / 4.5, 5.8 / 5.8; 4096 x 8192 8.2 / 6.8, 9.9 / 8.7;
+//        16384 x 4096 10.5 / 9.1, 15.8 / 11.1
+template <bool FP4A> static const char* launch_rows(const TileArgs& t, hipStream_t stream) {
+  const int64_t n = tiles_of(t.M, t.N, 16, 16);
+  if (t.M <= 16 && n <= 256 && (FP4A ? t.K / 2 : t.K) <= 2048) {
+    hipLaunchKernelGGL(fp4_lone_kernel<FP4A>, dim3((unsigned)n), dim3(64), 0, stream, t);
+    return FP4A ? "fp4:lone16_a4" : "fp4:lone16_a8";
+  }
+  if (n <= 256) launch_rows_of<FP4A, 1>(t, stream);
+  else if (n <= 512) launch_rows_of<FP4A, 2>(t, stream);
+  else launch_rows_of<FP4A, 4>(t, stream);
+  return FP4A ? "fp4:rows16_a4" : "fp4:rows16_a8";
+}
+
 // Which kernel runs (M, N, K), by how many workgroups each shape gives.  Times at N = K = 4096, E2M1 / E4M3 activations:
-//   rows, a wavefront per 16 columns:     M = 1 4.2 / 4.9 us, 16 4.9 / 5.8, 32 7.1 / 8.7, 48 9.2 / 11.7 (every wavefront
-//                                         reads all of its rows, so its time grows with them)
+//   rows (16 at a time):                  M = 1 4.2 / 4.5 us, 16 4.9 / 5.8; a second wavefront for rows 17 to 32 7.1 / 8.7
 //   32 x 64 (2 wavefronts):               M = 32 6.8 / 8.5, 48 6.7 / 8.6, 128 7.0 / 8.8, 256 9.3 / 11.8
 //   64 x 64 (4, two workgroups per CU):   M = 48 7.4 / 9.2, 256 7.9 / 10.0, 512 10.6 / 15.2, 1024 20.3 / 26.9
 //   128 x 128 (4, two per CU):            M = 256 14.4 / 17.1, 512 13.0 / 17.8, 1024 16.6 / 20.8
 //   256 x 256 (8, one per CU):            M = 4096 38.6 / 56.2, about 1.6 times a full round of 128 x 128
 enum class Fp4Kernel { rows, t32x64, t64x64, t128x128, t256x256 };
-static int64_t tiles_of(int M, int N, int bm, int bn) { return ((int64_t)M + bm - 1) / bm * (((int64_t)N + bn - 1) / bn); }
-static Fp4Kernel pick_kernel(int M, int N, int K) {
-  if (M <= 16 || K < 128) return Fp4Kernel::rows;                     // the tiles' scale reads need four blocks a row
+static Fp4Kernel pick_kernel(int M, int N, int K, bool fp4a) {
+  if ((M <= 16 && rows_lds(M, K, fp4a) <= ROWS_LDS) || K < 128) return Fp4Kernel::rows;                     // the tiles' scale reads need four blocks a row
   if (tiles_of(M, N, 32, 64) <= 256) return Fp4Kernel::t32x64;        // one per CU
   if (tiles_of(M, N, 64, 64) <= 512) return Fp4Kernel::t64x64;        // two per CU
   const int64_t r128 = (tiles_of(M, N, 128, 128) + 511) / 512, r256 = (tiles_of(M, N, 256, 256) + 255) / 256;
@@ -777,7 +944,7 @@ static Fp4Kernel pick_kernel(int M, int N, int K) {
 
 template <bool FP4A>
 static const char* launch_product(const TileArgs& t, hipStream_t stream) {
-  switch (pick_kernel(t.M, t.N, t.K)) {
+  switch (pick_kernel(t.M, t.N, t.K, FP4A)) {
     case Fp4Kernel::t32x64:
       launch_tile<FP4A, false, 1, 2, 1, 1, FP4A ? 256 : 128, 4>(t, stream);
       return FP4A ? "fp4:tile32x64_a4" : "fp4:tile32x64_a8";
@@ -792,10 +959,7 @@ static const char* launch_product(const TileArgs& t, hipStream_t stream) {
       return FP4A ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
     default: break;
   }
-  const dim3 grid((unsigned)((int64_t)((t.N + 15) / 16) * ((t.M + ROWS_MAX - 1) / ROWS_MAX)));   // about M N / 2^10 < 2^31
-  const dim3 block(64 * (t.M < ROWS_MAX ? (t.M + 15) / 16 : 4));
-  hipLaunchKernelGGL(fp4_rows_kernel<FP4A>, grid, block, 0, stream, t.x, t.x_sc, t.w, t.w_sc, t.M, t.N, t.K, t.y, t.bf16_out);
-  return FP4A ? "fp4:rows16_a4" : "fp4:rows16_a8";
+  return launch_rows<FP4A>(t, stream);
 }
 
 hipError_t launch_fp4_gemm(const uint8_t* a, const uint8_t* a_sc, bool fp4a, const uint8_t* w, const uint8_t* w_sc,
@@ -813,14 +977,16 @@ static size_t a256(size_t b) { return (b + 255) / 256 * 256; }
 // a lane.
 template <bool FP4A>
 __global__ __launch_bounds__(256, 2) void fp4_gate_up_rows_kernel(TileArgs A) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   __shared__ float h[16][4][17];                  // [row][gate, gate, up, up][column]; rows apart by 68: few conflicts
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = lane & 15, g = lane >> 4;
   const int I = A.N, K = A.K, nblk = K / 32;
   const uint32_t nb = I / 32;
   const int64_t n0 = (int64_t)(blockIdx.x % nb) * 32, m0 = (int64_t)(blockIdx.x / nb) * 16;
-  const int64_t n = n0 + (wave & 1) * 16 + col + (wave >= 2 ? I : 0), m = min(m0 + col, (int64_t)A.M - 1);
-  const v4f acc = rows_tile<FP4A>(A.x + m * (FP4A ? K / 2 : K), A.x_sc + m * nblk, A.w + n * (K / 2), A.w_sc + n * nblk, K, g);
+  const int64_t n = n0 + (wave & 1) * 16 + col + (wave >= 2 ? I : 0);
+  const v4f acc = rows_tile<FP4A, 4>(__builtin_amdgcn_readfirstlane(lds_addr(lds)), A.x + m0 * (FP4A ? K / 2 : K), A.x_sc + m0 * nblk,
+                                     (int)min((int64_t)16, A.M - m0), A.w + n * (K / 2), A.w_sc + n * nblk, K);
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[4 * g + i][wave][col] = acc[i];
   __syncthreads();
@@ -857,9 +1023,9 @@ template <bool FP4A>
 static const char* launch_gate_up(const TileArgs& t, hipStream_t stream) {
   const int M = t.M, N = 2 * t.N;
   constexpr int KS = FP4A ? 256 : 128, NB = FP4A ? 2 : 3;
-  if (M <= 16 || t.K < 128) {
+  if ((M <= 16 && rows_lds(M, t.K, FP4A) <= ROWS_LDS) || t.K < 128) {
     const dim3 grid((unsigned)((int64_t)(t.N / 32) * ((M + 15) / 16)));
-    hipLaunchKernelGGL(fp4_gate_up_rows_kernel<FP4A>, grid, dim3(256), 0, stream, t);
+    hipLaunchKernelGGL(fp4_gate_up_rows_kernel<FP4A>, grid, dim3(64 * ROWS_WAVES), rows_lds(M, t.K, FP4A), stream, t);
     return "fp4_ffn:rows16+";
   }
   if (tiles_of(M, N, 64, 128) <= 256) {

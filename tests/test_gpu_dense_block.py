@@ -286,6 +286,62 @@ def test_fp4_block_gemm_rows_do_not_depend_on_M(N, K, a_fmt):
     say(f"N {N} K {K}: rows equal over {sorted(seen)}")
 
 
+def random_codes(rng, rows, K, fmt):
+    """Any codes and scales near 1, no NaN: (codes, scales) in numpy."""
+    q = rng.integers(0, 256, (rows, K if fmt == E4M3 else K // 2), dtype=np.uint8)
+    if fmt == E4M3:
+        q = np.where((q & 0x7F) == 0x7F, q & 0x87, q)
+    return q, rng.integers(120, 134, (rows, K // 32)).astype(np.uint8)
+
+
+@pytest.mark.parametrize("a_fmt", [E4M3, E2M1])
+@pytest.mark.parametrize("whole", [0, 1, 2, 3, 4, 5, 7, 8, 9, 12, 15, 16, 17, 24])
+def test_fp4_block_gemm_few_rows_at_every_end_of_K(whole, a_fmt):
+    """K around the pieces of 512 and the number of them that few rows keep in flight; rows and columns that end early."""
+    N = 40
+    for tail in (0, 32, 96, 128, 224, 480):
+        K = 512 * whole + tail
+        if K == 0:
+            continue
+        rng = np.random.default_rng(K)
+        a, a_sc = random_codes(rng, 16, K, a_fmt)
+        w, w_sc = random_codes(rng, N, K, E2M1)
+        want, room = ref.product(a, a_sc, a_fmt, w, w_sc)
+        a, a_sc, w, w_sc = (to_dev(t) for t in (a, a_sc, w, w_sc))
+        for M in (16, 1, 7, 9):
+            y32 = torch.full((M + 1, N), float("nan"), dtype=F32, device="cuda")
+            y16 = torch.full((M + 1, N), float("nan"), dtype=BF16, device="cuda")
+            mxmoe.fp4_block_gemm(a[16 - M:], a_sc[16 - M:], a_fmt, w, w_sc, y32[:M])
+            mxmoe.fp4_block_gemm(a[16 - M:], a_sc[16 - M:], a_fmt, w, w_sc, y16[:M])
+            check_product(y32[:M], y16[:M], want[16 - M:], room[16 - M:], K, a_fmt)
+            assert torch.isnan(y32[M]).all() and torch.isnan(y16[M]).all(), (K, M)
+
+
+@pytest.mark.parametrize("a_fmt", [E4M3, E2M1])
+@pytest.mark.parametrize("M,N", [(40, 100), (1040, 523), (1500, 1502), (2830, 2835)])
+def test_fp4_block_gemm_tiles_at_every_end_of_K(M, N, a_fmt):
+    """K around the stages and the K = 512 of scales of each tile: the bits of few rows, at the first, a middle and the last
+    rows, columns that end inside a tile at odd addresses, and nothing written behind."""
+    for K in (128, 160, 192, 256, 288, 384, 512, 544, 608, 640, 768, 896, 1024, 1056, 1280, 1536, 1632, 2048, 2080, 4096):
+        rng = np.random.default_rng(K + M)
+        a, a_sc, w, w_sc = (to_dev(t) for t in random_codes(rng, M, K, a_fmt) + random_codes(rng, N, K, E2M1))
+        for dtype in (F32, BF16):
+            buf = torch.full((M * N + 80,), float("nan"), dtype=dtype, device="cuda")
+            y = buf[16:16 + M * N].view(M, N)
+            mxmoe.fp4_block_gemm(a, a_sc, a_fmt, w, w_sc, y)
+            v = mxmoe.last_variant()
+            assert "tile" in v
+            for m0 in (0, M // 2 - 3, M - 16):
+                few = torch.empty((16, N), dtype=dtype, device="cuda")
+                mxmoe.fp4_block_gemm(a[m0:m0 + 16], a_sc[m0:m0 + 16], a_fmt, w, w_sc, few)
+                if 16 * K * (2 if a_fmt == E4M3 else 1) < 2 ** 17:
+                    assert "tile" not in mxmoe.last_variant()
+                assert torch.equal(y[m0:m0 + 16], few), (K, m0, dtype, v)
+            assert not torch.isnan(y).any(), (K, dtype, v)
+            assert torch.isnan(buf[:16]).all() and torch.isnan(buf[16 + M * N:]).all(), (K, dtype, v)
+    say(f"{v}: {M} x {N}")
+
+
 # -------------------------------------------------------------- dense FFN
 FFN_SIZES = [(1, 4096, 576), (1, 256, 64), (1, 128, 2048), (2, 32, 32), (3, 160, 96), (16, 512, 256), (17, 1056, 544),
              (48, 4096, 576), (100, 288, 1376), (129, 512, 160), (300, 640, 736), (600, 256, 512), (1, 16384, 32),
@@ -311,6 +367,34 @@ def test_fp4_dense_ffn_is_its_three_steps(T, H, I, x_fmt, mid_fmt):
         mxmoe.fp4_dense_ffn(x, x_sc, x_fmt, w13, w13_sc, w2, w2_sc, mid_fmt, y[:T], ws[:need])
         assert torch.equal(y[:T], want), mxmoe.last_variant()
         assert torch.isnan(y[T]).all() and torch.all(ws[need:] == 0xA5)
+    say(f"{mxmoe.last_variant()}: T {T} H {H} I {I}")
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E2M1])
+@pytest.mark.parametrize("T,H,I", [(5, 256, 96), (40, 256, 96), (600, 128, 1056), (1100, 160, 2080), (2100, 256, 4128)])
+def test_fp4_dense_ffn_blocks_that_need_double(T, H, I, fmt):
+    """Gates far below zero and products next to fp32's ends, whose codes fp32 does not decide, zero rows and gates whose
+    SwiGLU vanishes, in every kernel of the gate/up product: the codes of mx_swiglu_quantize on the product's own result."""
+    rng = np.random.default_rng(T + I)
+    x, x_sc = random_codes(rng, T, H, fmt)
+    w13, w13_sc = random_codes(rng, 2 * I, H, E2M1)
+    w2, w2_sc = random_codes(rng, H, I, E2M1)
+    x[T // 3] = 0                                                         # a row of zeros
+    x_sc[T // 2] = 141                                                    # gates in the thousands, both signs
+    x_sc[T - 1] = 20                                                      # subnormal blocks
+    w13_sc[3] = 100
+    x, x_sc, w13, w13_sc, w2, w2_sc = (to_dev(t) for t in (x, x_sc, w13, w13_sc, w2, w2_sc))
+    gu = torch.empty((T, 2 * I), dtype=F32, device="cuda")
+    mxmoe.fp4_block_gemm(x, x_sc, fmt, w13, w13_sc, gu)
+    assert float(gu[:, :I].min()) < -1000
+    q, sc = codes_like(T, I, fmt)
+    mxmoe.mx_swiglu_quantize(gu, q, sc, fmt)
+    want = torch.empty((T, H), dtype=F32, device="cuda")
+    mxmoe.fp4_block_gemm(q, sc, fmt, w2, w2_sc, want)
+    ws = torch.empty(mxmoe.fp4_dense_ffn_workspace_bytes(T, H, I, fmt), dtype=torch.uint8, device="cuda")
+    y = torch.empty((T, H), dtype=F32, device="cuda")
+    mxmoe.fp4_dense_ffn(x, x_sc, fmt, w13, w13_sc, w2, w2_sc, fmt, y, ws)
+    assert torch.equal(y.view(torch.int32), want.view(torch.int32)), mxmoe.last_variant()
     say(f"{mxmoe.last_variant()}: T {T} H {H} I {I}")
 
 
