@@ -1028,6 +1028,10 @@ static const char* launch_gate_up(const TileArgs& t, hipStream_t stream) {
     hipLaunchKernelGGL(fp4_gate_up_rows_kernel<FP4A>, grid, dim3(64 * ROWS_WAVES), rows_lds(M, t.K, FP4A), stream, t);
     return "fp4_ffn:rows16+";
   }
+  if (tiles_of(M, N, 64, 64) <= 256) {
+    launch_tile<FP4A, true, 2, 1, 1, 2, KS, 4>(t, stream);
+    return "fp4_ffn:tile64x64+";
+  }
   if (tiles_of(M, N, 64, 128) <= 256) {
     launch_tile<FP4A, true, 2, 2, 1, 2, KS, 4>(t, stream);
     return "fp4_ffn:tile64x128+";
