@@ -28,7 +28,11 @@ int row_unit(int in_dtype) { return in_dtype == MX_IN_BF16 ? 8 : 4; }
 // alignment of scale rows of K elements: dwords where every row is whole dwords, else bytes
 uintptr_t scale_unit(int K) { return K % 128 == 0 ? 4 : 1; }
 
-constexpr int64_t MAX_CHUNKS = int64_t(1) << 38;  // 8-element chunks of one call: 2^30 workgroups of 256 threads
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t MAX_CHUNKS = int64_t(1) << 31;  // 8-element chunks of one call, a thread each
+constexpr int NORM_MAX_T = (1 << 23) - 1;         // rows, up to 512 threads each
+// outputs of an FP4 product: tiles of at least 16 x 64, 256 threads each
+bool fp4_grid_fits(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 63) / 64) < int64_t(1) << 24; }
 
 mx_status from_hip(hipError_t e) { return e == hipSuccess ? MX_OK : MX_EHIP; }
 
@@ -387,7 +391,7 @@ mx_status mx_add_rmsnorm(const void* x, const void* x2, int x_dtype, int64_t x_l
   if (!(eps > 0.0f) || eps > 3.0e38f) return MX_EINVAL;                    // eps = 0 would make a zero row NaN
   if (x_ld < H || x_ld % row_unit(x_dtype) != 0) return MX_EINVAL;
   if (res && (res_ld < H || res_ld % row_unit(res_dtype) != 0)) return MX_EINVAL;
-  if (H > mx::NORM_MAX_H) return MX_EUNSUPPORTED;
+  if (H > mx::NORM_MAX_H || T > NORM_MAX_T) return MX_EUNSUPPORTED;
   if (T == 0) { g_variant = "add_rmsnorm:empty"; return MX_OK; }
   if (x_ld > (int64_t(1) << 60) / T || (res && res_ld > (int64_t(1) << 60) / T)) return MX_EUNSUPPORTED;
   if (!x || (!h && !n && !q) || (q == nullptr) != (sc == nullptr)) return MX_EINVAL;
@@ -406,7 +410,7 @@ mx_status fp4_block_gemm(const uint8_t* a, const uint8_t* a_sc, int a_fmt, const
   if (M < 0 || N < 1 || K < 32 || K % 32 != 0) return MX_EINVAL;
   if (a_fmt != MX_FMT_E4M3 && a_fmt != MX_FMT_E2M1) return MX_EINVAL;
   if (y_dtype != MX_OUT_BF16 && y_dtype != MX_OUT_F32) return MX_EINVAL;
-  if (K > mx::FP4_MAX_K || (int64_t)M * N >= (int64_t(1) << 40)) return MX_EUNSUPPORTED;
+  if (K > mx::FP4_MAX_K || !fp4_grid_fits(M, N)) return MX_EUNSUPPORTED;
   if (!w || !w_sc || (M > 0 && (!a || !a_sc || !y))) return MX_EINVAL;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 4)) return MX_EINVAL;
   if (!aligned(a_sc, scale_unit(K)) || !aligned(w_sc, scale_unit(K))) return MX_EINVAL;
@@ -434,9 +438,7 @@ mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T,
                         int y_dtype, void* ws, size_t ws_bytes, void* stream) {
   if (!fp4_ffn_shape(T, H, I, mid_fmt) || (x_fmt != MX_FMT_E4M3 && x_fmt != MX_FMT_E2M1)) return MX_EINVAL;
   if (y_dtype != MX_OUT_BF16 && y_dtype != MX_OUT_F32) return MX_EINVAL;
-  if (H > mx::FP4_MAX_K || I > mx::FP4_MAX_K || (int64_t)T * 2 * I >= (int64_t(1) << 40) ||
-      (int64_t)T * H >= (int64_t(1) << 40))
-    return MX_EUNSUPPORTED;
+  if (H > mx::FP4_MAX_K || I > mx::FP4_MAX_K || !fp4_grid_fits(T, 2 * I) || !fp4_grid_fits(T, H)) return MX_EUNSUPPORTED;
   if (!w13 || !w13_sc || !w2 || !w2_sc || (T > 0 && (!x || !x_sc || !y))) return MX_EINVAL;
   if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(y, 4) || !aligned(ws, 256)) return MX_EINVAL;
   if (!aligned(x_sc, scale_unit(H)) || !aligned(w13_sc, scale_unit(H)) || !aligned(w2_sc, scale_unit(I))) return MX_EINVAL;

@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   // XCD-aware order: each XCD takes a run of consecutive tiles, which go down 8 row tiles before the next column tile
   constexpr int CN = SWIGLU ? S::BN / 2 : S::BN;                      // result columns of a tile
   const int nrt = (M + S::BM - 1) / S::BM, nct = (N + CN - 1) / CN;
-  const uint32_t tiles = (uint32_t)nrt * nct, per = (tiles + XCDS - 1) / XCDS;   // M N < 2^40: fewer than 2^27 tiles
+  const uint32_t tiles = (uint32_t)nrt * nct, per = (tiles + XCDS - 1) / XCDS;   // fewer than 2^24
   const uint32_t t = blockIdx.x % XCDS * per + blockIdx.x / XCDS;
   if (t >= tiles) return;
   const uint32_t grp = t / (8u * nct), in = t - grp * 8u * nct, rows_in = min(8u, nrt - grp * 8u);
@@ -907,7 +907,7 @@ static void launch_tile(const TileArgs& a, hipStream_t stream) {
 
 static int64_t tiles_of(int M, int N, int bm, int bn) { return ((int64_t)M + bm - 1) / bm * (((int64_t)N + bn - 1) / bn); }
 template <bool FP4A, int CW> static void launch_rows_of(const TileArgs& t, hipStream_t stream) {
-  const dim3 grid((unsigned)(tiles_of(t.M, t.N, 16, 16 * CW)));       // CW = 4 past 512: about M N / 2^10 < 2^31
+  const dim3 grid((unsigned)(tiles_of(t.M, t.N, 16, 16 * CW)));       // CW = 4 past 512: fewer than 2^24
   hipLaunchKernelGGL((fp4_rows_kernel<FP4A, CW>), grid, dim3(64 * ROWS_WAVES), rows_lds(t.M, t.K, FP4A), stream, t);
 }
 // By how many wavefronts of 16 columns there are and by what a row is long.  Alone / through LDS at M = 1 and 16, us:

@@ -89,7 +89,7 @@ mx_status mx_quantize(const void* src, int src_dtype, int64_t rows, int64_t cols
  * rounded to nearest even (it holds every value of bf16's normal range).
  * E4M3's NaN codes (S.1111.111) give NaN.  cols % 32 == 0; rows or cols 0:
  * nothing to do.  q and out 16-byte aligned; sc needs no alignment.
- * Supported: rows * cols <= 2^41.
+ * Supported: rows * cols <= 2^34.
  */
 mx_status mx_dequantize(const uint8_t* q, const uint8_t* sc, int fmt, int64_t rows, int64_t cols, void* out,
                         int out_dtype, void* stream);
@@ -103,7 +103,7 @@ mx_status mx_dequantize(const uint8_t* q, const uint8_t* sc, int fmt, int64_t ro
  * gu: fp32 or bf16 (in_dtype) rows of gu_ld elements, gate in [0, I), up in
  * [I, 2I); gu_ld >= 2I, a multiple of 4 (fp32) or 8 (bf16).  q: E4M3 [T][I]
  * or E2M1 [T][I/2]; sc [T][I/32].  I % 32 == 0, T >= 0; gu, q 16-byte
- * aligned.  q and sc must not overlap gu.  Supported: T * I <= 2^41.
+ * aligned.  q and sc must not overlap gu.  Supported: T * I <= 2^34.
  */
 mx_status mx_swiglu_quantize(const void* gu, int in_dtype, int64_t gu_ld, int64_t T, int I, int fmt, uint8_t* q,
                              uint8_t* sc, void* stream);
@@ -127,7 +127,7 @@ mx_status mx_swiglu_quantize(const void* gu, int in_dtype, int64_t gu_ld, int64_
  * res_ld elements, or NULL.  weight: fp32 or bf16 [H], or NULL (ones).
  * x_ld, res_ld >= H, multiples of 4 (fp32) or 8 (bf16); res_ld and res_dtype
  * are ignored without residual and h, fmt without q, w_dtype without weight.
- * H % 32 == 0, 32 <= H <= 16384 (beyond: MX_EUNSUPPORTED), T >= 0, eps > 0.
+ * H % 32 == 0, 32 <= H <= 16384, 0 <= T < 2^23 (beyond: MX_EUNSUPPORTED), eps > 0.
  * All pointers but sc 16-byte aligned.
  */
 mx_status mx_add_rmsnorm(const void* x, const void* x2, int x_dtype, int64_t x_ld, const void* residual, void* h,
@@ -382,8 +382,8 @@ mx_status fp8_block_gemm(const uint8_t* a, const uint8_t* a_sc,
  * chain over K in order per element, the same for every M and kernel.
  * E2M1 x E2M1 sums are exact while they fit 24 bits; the matrix cores' sum of
  * E4M3 x E2M1 products is a few 1e-6 off relative to the result's norm.
- * Supported: M >= 0, any N >= 1, K % 32 == 0, 32 <= K <= 16384, M*N < 2^40;
- * beyond these MX_EUNSUPPORTED.  a, w 16-byte, y 4-byte aligned; a_sc, w_sc
+ * Supported: M >= 0, any N >= 1, K % 32 == 0, 32 <= K <= 16384, and
+ * ceil(M / 16) * ceil(N / 64) < 2^24 (M*N to about 2^34); beyond these MX_EUNSUPPORTED.  a, w 16-byte, y 4-byte aligned; a_sc, w_sc
  * 4-byte where K % 128 == 0, else at any byte.
  */
 mx_status fp4_block_gemm(const uint8_t* a, const uint8_t* a_sc, int a_fmt, const uint8_t* w, const uint8_t* w_sc,
@@ -398,10 +398,11 @@ mx_status fp4_block_gemm(const uint8_t* a, const uint8_t* a_sc, int a_fmt, const
  * + SC [H][I/32]; the intermediate is cast to mid_fmt; y [T][H] bf16 or fp32
  * (y_dtype).  Results, bit for bit, those of fp4_block_gemm (fp32 out),
  * mx_swiglu_quantize, fp4_block_gemm.  Supported: T >= 0; H, I % 32 == 0, at
- * most 16384; T*H, T*2I < 2^40.  x, w13, w2 16-byte, y 4-byte aligned;
- * scales as in fp4_block_gemm.  ws: fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt) bytes (0 for
- * an invalid shape), 256-byte aligned, contents ignored; calls that share a
- * workspace must not overlap.
+ * most 16384; T by 2I and T by H as M by N there.  x, w13, w2 16-byte, y
+ * 4-byte aligned; scales as in fp4_block_gemm.  ws:
+ * fp4_dense_ffn_workspace_bytes(T, H, I, mid_fmt) bytes (0 for an invalid
+ * shape), 256-byte aligned, contents ignored; calls that share a workspace
+ * must not overlap.
  */
 size_t    fp4_dense_ffn_workspace_bytes(int T, int H, int I, int mid_fmt);
 mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T, int H, const uint8_t* w13,

@@ -35,6 +35,7 @@ def test_add_rmsnorm_rejects_bad_arguments(lib):
         assert norm(lib, **bad) == MX_EINVAL, bad
     assert norm(lib, H=16416, x_ld=16416, r_ld=16416) == MX_EUNSUPPORTED
     assert norm(lib, x_ld=1 << 60) == MX_EUNSUPPORTED
+    assert norm(lib, T=1 << 23) == MX_EUNSUPPORTED
     assert norm(lib, T=0, x=None, r=None, h=None, n=None, q=None, sc=None) == MX_OK
 
 
@@ -45,6 +46,7 @@ def test_swiglu_quantize_rejects_bad_arguments(lib):
                 dict(dt=1, ld=132), dict(gu=None), dict(q=None), dict(sc=None), dict(gu=ODD), dict(q=ODD)):
         assert call(**bad) == MX_EINVAL, bad
     assert call(T=1 << 40, I=64) == MX_EUNSUPPORTED
+    assert call(T=(1 << 28) + 1, I=64) == MX_EUNSUPPORTED          # 2^32 threads and more do not fit one launch
     assert call(T=0, gu=None, q=None, sc=None) == MX_OK
 
 
@@ -55,6 +57,7 @@ def test_dequantize_rejects_bad_arguments(lib):
                 dict(out=None), dict(q=ODD), dict(out=ODD)):
         assert call(**bad) == MX_EINVAL, bad
     assert call(rows=1 << 40) == MX_EUNSUPPORTED
+    assert call(rows=(1 << 28) + 1) == MX_EUNSUPPORTED
     assert call(rows=0, q=None, sc=None, out=None) == MX_OK and call(cols=0) == MX_OK
 
 
@@ -67,6 +70,7 @@ def test_fp4_block_gemm_rejects_bad_arguments(lib):
         assert call(**bad) == MX_EINVAL, bad
     assert call(K=16416) == MX_EUNSUPPORTED
     assert call(M=1 << 20, N=1 << 20) == MX_EUNSUPPORTED
+    assert call(M=1 << 28, N=1) == MX_EUNSUPPORTED and call(M=16, N=(1 << 30) - 63) == MX_EUNSUPPORTED
     assert call(M=0, a=None, a_sc=None, y=None) == MX_OK
 
 
@@ -82,6 +86,7 @@ def test_fp4_dense_ffn_rejects_bad_arguments(lib):
                 dict(ws=ctypes.c_void_p((1 << 20) + 64))):
         assert call(**bad) == MX_EINVAL, bad
     assert call(H=16416) == MX_EUNSUPPORTED and call(I=16416) == MX_EUNSUPPORTED
+    assert call(T=1 << 27, I=128) == MX_EUNSUPPORTED and call(T=1 << 27, H=256, I=32) == MX_EUNSUPPORTED
     assert call(ws=None) == MX_EWORKSPACE
     need = mxmoe.fp4_dense_ffn_workspace_bytes(4, 128, 128, 0)
     assert need > 0 and call(n=need - 1) == MX_EWORKSPACE

@@ -326,8 +326,9 @@ def test_fp4_block_gemm_tiles_at_every_end_of_K(M, N, a_fmt):
         rng = np.random.default_rng(K + M)
         a, a_sc, w, w_sc = (to_dev(t) for t in random_codes(rng, M, K, a_fmt) + random_codes(rng, N, K, E2M1))
         for dtype in (F32, BF16):
-            buf = torch.full((M * N + 80,), float("nan"), dtype=dtype, device="cuda")
-            y = buf[16:16 + M * N].view(M, N)
+            off = 1 if dtype == F32 else 2                # four bytes: what y has to be aligned to
+            buf = torch.full((M * N + 64,), float("nan"), dtype=dtype, device="cuda")
+            y = buf[off:off + M * N].view(M, N)
             mxmoe.fp4_block_gemm(a, a_sc, a_fmt, w, w_sc, y)
             v = mxmoe.last_variant()
             assert "tile" in v
@@ -338,7 +339,7 @@ def test_fp4_block_gemm_tiles_at_every_end_of_K(M, N, a_fmt):
                     assert "tile" not in mxmoe.last_variant()
                 assert torch.equal(y[m0:m0 + 16], few), (K, m0, dtype, v)
             assert not torch.isnan(y).any(), (K, dtype, v)
-            assert torch.isnan(buf[:16]).all() and torch.isnan(buf[16 + M * N:]).all(), (K, dtype, v)
+            assert torch.isnan(buf[:off]).all() and torch.isnan(buf[off + M * N:]).all(), (K, dtype, v)
     say(f"{v}: {M} x {N}")
 
 
