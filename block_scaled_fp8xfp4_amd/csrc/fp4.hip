@@ -932,14 +932,21 @@ template <bool FP4A> static const char* launch_rows(const TileArgs& t, hipStream
 //   32 x 64 (2 wavefronts):               M = 32 6.8 / 8.5, 48 6.7 / 8.6, 128 7.0 / 8.8, 256 9.3 / 11.8
 //   64 x 64 (4, two workgroups per CU):   M = 48 7.4 / 9.2, 256 7.9 / 10.0, 512 10.6 / 15.2, 1024 20.3 / 26.9
 //   128 x 128 (4, two per CU):            M = 256 14.4 / 17.1, 512 13.0 / 17.8, 1024 16.6 / 20.8
+//   128 x 256 (8, one per CU):            M = 1024 20.0 / 26.5, 1500 21.9 / 28.5 (128 x 128: 23.7 / 32.1), 2048 24.7 / 34.2
+//                                         (26.6 / 37.2), 4096 46.8 / 66.8
 //   256 x 256 (8, one per CU):            M = 4096 38.6 / 56.2, about 1.6 times a full round of 128 x 128
-enum class Fp4Kernel { rows, t32x64, t64x64, t128x128, t256x256 };
+enum class Fp4Kernel { rows, t32x64, t64x64, t128x128, t128x256, t256x256 };
+// Past 512 tiles of 64 x 64.
+static Fp4Kernel pick_large(int M, int N) {
+  const int64_t t128 = tiles_of(M, N, 128, 128), t256 = tiles_of(M, N, 256, 256);
+  if (t128 > 256 && tiles_of(M, N, 128, 256) <= 256) return Fp4Kernel::t128x256;
+  return (t256 + 255) / 256 * 8 <= (t128 + 511) / 512 * 5 ? Fp4Kernel::t256x256 : Fp4Kernel::t128x128;
+}
 static Fp4Kernel pick_kernel(int M, int N, int K, bool fp4a) {
   if ((M <= 16 && rows_lds(M, K, fp4a) <= ROWS_LDS) || K < 128) return Fp4Kernel::rows;                     // the tiles' scale reads need four blocks a row
   if (tiles_of(M, N, 32, 64) <= 256) return Fp4Kernel::t32x64;        // one per CU
   if (tiles_of(M, N, 64, 64) <= 512) return Fp4Kernel::t64x64;        // two per CU
-  const int64_t r128 = (tiles_of(M, N, 128, 128) + 511) / 512, r256 = (tiles_of(M, N, 256, 256) + 255) / 256;
-  return r256 * 8 <= r128 * 5 ? Fp4Kernel::t256x256 : Fp4Kernel::t128x128;
+  return pick_large(M, N);
 }
 
 template <bool FP4A>
@@ -954,6 +961,9 @@ static const char* launch_product(const TileArgs& t, hipStream_t stream) {
     case Fp4Kernel::t128x128:
       launch_tile<FP4A, false, 2, 2, 2, 2, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
       return FP4A ? "fp4:tile128x128_a4" : "fp4:tile128x128_a8";
+    case Fp4Kernel::t128x256:
+      launch_tile<FP4A, false, 2, 4, 2, 2, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
+      return FP4A ? "fp4:tile128x256_a4" : "fp4:tile128x256_a8";
     case Fp4Kernel::t256x256:
       launch_tile<FP4A, false, FP4A ? 2 : 4, FP4A ? 4 : 2, FP4A ? 4 : 2, FP4A ? 2 : 4, FP4A ? 256 : 128, FP4A ? 2 : 3>(t, stream);
       return FP4A ? "fp4:tile256x256_a4" : "fp4:tile256x256_a8";
@@ -1036,10 +1046,14 @@ static const char* launch_gate_up(const TileArgs& t, hipStream_t stream) {
     launch_tile<FP4A, true, 2, 2, 1, 2, KS, 4>(t, stream);
     return "fp4_ffn:tile64x128+";
   }
-  const int64_t r128 = (tiles_of(M, N, 128, 128) + 511) / 512, r256 = (tiles_of(M, N, 256, 256) + 255) / 256;
-  if (r256 * 8 <= r128 * 5) {
-    launch_tile<FP4A, true, FP4A ? 2 : 4, FP4A ? 4 : 2, FP4A ? 4 : 2, FP4A ? 2 : 4, KS, NB>(t, stream);
-    return "fp4_ffn:tile256x256+";
+  switch (pick_large(M, N)) {
+    case Fp4Kernel::t128x256:
+      launch_tile<FP4A, true, 2, 4, 2, 2, KS, NB>(t, stream);
+      return "fp4_ffn:tile128x256+";
+    case Fp4Kernel::t256x256:
+      launch_tile<FP4A, true, FP4A ? 2 : 4, FP4A ? 4 : 2, FP4A ? 4 : 2, FP4A ? 2 : 4, KS, NB>(t, stream);
+      return "fp4_ffn:tile256x256+";
+    default: break;
   }
   launch_tile<FP4A, true, 2, 2, 2, 2, KS, NB>(t, stream);
   return "fp4_ffn:tile128x128+";

@@ -318,7 +318,7 @@ def test_fp4_block_gemm_few_rows_at_every_end_of_K(whole, a_fmt):
 
 
 @pytest.mark.parametrize("a_fmt", [E4M3, E2M1])
-@pytest.mark.parametrize("M,N", [(40, 100), (1040, 523), (1500, 1502), (2830, 2835)])
+@pytest.mark.parametrize("M,N", [(40, 100), (1040, 523), (1500, 1502), (2100, 2835), (2830, 2835)])
 def test_fp4_block_gemm_tiles_at_every_end_of_K(M, N, a_fmt):
     """K around the stages and the K = 512 of scales of each tile: the bits of few rows, at the first, a middle and the last
     rows, columns that end inside a tile at odd addresses, and nothing written behind."""
@@ -372,7 +372,7 @@ def test_fp4_dense_ffn_is_its_three_steps(T, H, I, x_fmt, mid_fmt):
 
 
 @pytest.mark.parametrize("fmt", [E4M3, E2M1])
-@pytest.mark.parametrize("T,H,I", [(5, 256, 96), (40, 256, 96), (600, 128, 1056), (1100, 160, 2080), (2100, 256, 4128)])
+@pytest.mark.parametrize("T,H,I", [(5, 256, 96), (40, 256, 96), (600, 128, 1056), (1100, 160, 2080), (1500, 128, 2080), (2100, 256, 4128)])
 def test_fp4_dense_ffn_blocks_that_need_double(T, H, I, fmt):
     """Gates far below zero and products next to fp32's ends, whose codes fp32 does not decide, zero rows and gates whose
     SwiGLU vanishes, in every kernel of the gate/up product: the codes of mx_swiglu_quantize on the product's own result."""
