@@ -368,15 +368,17 @@ template <int N> __device__ __forceinline__ void wait_vm() { asm volatile("s_wai
 constexpr int XCDS = 8;
 constexpr int SCK = 512;                          // K whose scales (16 bytes a row) are fetched at a time
 
-// WM x WN wavefronts of TM x TN 32 x 32 tiles each.
-template <bool FP4A, int WM, int WN, int TM, int TN, int KS, int NST>
+// WM x WN wavefronts of TM x TN 32 x 32 tiles each.  ODD: K % 128 != 0, rows
+// of scales start at any byte (small tiles; larger ones take the scales of
+// such K through registers, at a wait for all of memory per 512 of K).
+template <bool FP4A, bool ODD, int WM, int WN, int TM, int TN, int KS, int NST>
 struct TileShape {
   static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
   static constexpr int RA = FP4A ? KS / 2 : KS, RW = KS / 2;     // bytes of an activation / a weight row per stage
   static constexpr int CA = RA / 16, CW = RW / 16;               // their chunks
   static constexpr int NSC = (BM + BN + 64 * NW - 1) / (64 * NW);     // scale rows per lane (surplus ones repeat the last)
   static constexpr uint32_t OFF_W = BM * RA, STAGE = OFF_W + BN * RW;
-  static constexpr uint32_t OFF_S = STAGE * NST, SCALES = NSC * NW * 1024, LDS = OFF_S + 2 * SCALES;
+  static constexpr uint32_t OFF_S = STAGE * NST, SCALES = NSC * NW * (ODD ? 1280 : 1024), LDS = OFF_S + 2 * SCALES;
   static constexpr int NX = BM * RA / 1024 / NW, NWT = BN * RW / 1024 / NW;   // DMA instructions per wavefront and stage
   static constexpr int NV = NX + NWT;
   static constexpr int SPC = SCK / KS;            // stages per scale chunk
@@ -432,9 +434,10 @@ __device__ __forceinline__ void tile_codes(const v16f& gate, const v16f& up, int
 
 // What a product leaves: y, or the codes of silu(gate) * up (SWIGLU: a tile
 // holds 32 gate columns, then the 32 up columns they meet, and so on).
-template <bool FP4A, bool SWIGLU, int WM, int WN, int TM, int TN, int KS, int NST>
+template <bool FP4A, bool SWIGLU, bool ODD, int WM, int WN, int TM, int TN, int KS, int NST>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
-  using S = TileShape<FP4A, WM, WN, TM, TN, KS, NST>;
+  using S = TileShape<FP4A, ODD, WM, WN, TM, TN, KS, NST>;
+  static_assert(S::WHOLE || !ODD, "ODD: small tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -499,15 +502,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   // Scales of K = 512 c + [0, 512) of this lane's rows, to the buffer c % 2: by DMA where the 16 bytes are the row's and
   // dword-aligned, else through registers, written to LDS when the chunk is published (put).  Blocks past K get 127;
   // the dword that holds a row's last blocks is read from the row's last four bytes (K >= 128), so no read leaves the
-  // row.  Rows start at any byte where K % 128 != 0.
+  // row.  Rows start at any byte where K % 128 != 0: with ODD the DMA brings the five dwords that the 16 bytes lie in (the
+  // fifth, where they fill four, is the fourth again; a dword with one of the row's bytes in it is readable), the fifth
+  // behind the buffer's rows of 16, and a reader shifts by its row's offset.
   u32x4 sreg[S::NSC];
-  auto by_dma = [&](int c) { return K % 128 == 0 && c * 16 + 16 <= nblk; };
+  auto by_dma = [&](int c) { return (ODD || K % 128 == 0) && c * 16 + 16 <= nblk; };
   auto fetch_scales = [&](int c) {
     const int b0 = c * 16;
     if (by_dma(c)) {
 #pragma unroll
-      for (int i = 0; i < S::NSC; ++i)
-        dma16_to_lds(srow[i] + b0, lds + S::OFF_S + (c & 1) * S::SCALES + (i * S::NW + wave) * 1024);
+      for (int i = 0; i < S::NSC; ++i) {
+        uint8_t* const to = lds + S::OFF_S + (c & 1) * S::SCALES + (i * S::NW + wave) * 1024;
+        const uint32_t o = ODD ? (uint32_t)(uintptr_t)srow[i] & 3 : 0;
+        dma16_to_lds(srow[i] - o + b0, to);
+        if (ODD) dma4_to_lds(srow[i] - o + b0 + (o ? 16 : 12), lds + S::OFF_S + (c & 1) * S::SCALES + S::NSC * S::NW * 1024 + (i * S::NW + wave) * 256);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < S::NSC; ++i)
@@ -635,6 +644,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
     // Small tiles: a stage's operands are read from LDS in one go, while the stage before multiplies, so that the LDS
     // latency is met once per stage and not once per step.
     struct Stage { Regs r[S::STEPS]; Scales c[KS / 128]; };
+    Scales off = {};                                                  // ODD: where rows of scales start in their dword
+    if (ODD) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) off.x[i] = (uint32_t)(uintptr_t)(A.x_sc + (m0 + min((int)xrow + i * 32, mlast)) * nblk) & 3;
+#pragma unroll
+      for (int i = 0; i < TN; ++i) off.w[i] = (uint32_t)(uintptr_t)(A.w_sc + (n0 + wsrc(wrow + i * 32)) * nblk) & 3;
+    }
+    // The scales of 128 of K: dword d of the buffer at offset at; whole: the buffer was filled by DMA.
+    auto load_scales = [&](Scales& C, uint32_t at, int d, bool whole) {
+      const uint32_t fifth = lds0 + S::OFF_S + S::NSC * S::NW * 1024 + at;
+#pragma unroll
+      for (int i = 0; i < TM + TN; ++i) {
+        const uint32_t row = (i < TM ? sp + i * 32 * 16 : sw + (i - TM) * 32 * 16) + at;
+        uint32_t v = lds_read<uint32_t>(row + d * 4);
+        if (ODD) {
+          const uint32_t o = i < TM ? off.x[i < TM ? i : 0] : off.w[i < TM ? 0 : i - TM];
+          const uint32_t n = i < TM ? xrow + i * 32 : S::BM + wrow + (i - TM) * 32;
+          const uint32_t next = lds_read<uint32_t>(d < 3 ? row + d * 4 + 4 : fifth + n * 4);
+          v = __builtin_amdgcn_alignbyte(next, v, whole ? o : 0);
+        }
+        if (i < TM) C.x[i < TM ? i : 0] = v;
+        else C.w[i < TM ? 0 : i - TM] = v;
+      }
+    };
     auto load_stage = [&](Stage& G, uint32_t buf, int s) {
 #pragma unroll
       for (int ks = 0; ks < S::STEPS; ++ks)
@@ -643,11 +676,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
 #pragma unroll
       for (int d = 0; d < KS / 128; ++d) {
         const int k128 = s * (KS / 128) + d;
-        const uint32_t off = ((k128 >> 2) & 1) * S::SCALES + (k128 & 3) * 4;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) G.c[d].x[i] = lds_read<uint32_t>(sp + off + i * 32 * 16);
-#pragma unroll
-        for (int i = 0; i < TN; ++i) G.c[d].w[i] = lds_read<uint32_t>(sw + off + i * 32 * 16);
+        load_scales(G.c[d], ((k128 >> 2) & 1) * S::SCALES, k128 & 3, by_dma(k128 >> 2));
       }
     };
     auto multiply = [&](Stage& G) {
@@ -684,10 +713,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
 #pragma unroll
       for (int d = 0; d < KS / 128; ++d) {
         const uint32_t chunk = (FP4A ? (U + 1) >> 1 : (s + U + 1) >> 2) & 1, dword = FP4A ? 2 * ((U + 1) & 1) + d : (U + 1) & 3;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) Gn.c[d].x[i] = lds_read<uint32_t>(sp + chunk * S::SCALES + dword * 4 + i * 32 * 16);
-#pragma unroll
-        for (int i = 0; i < TN; ++i) Gn.c[d].w[i] = lds_read<uint32_t>(sw + chunk * S::SCALES + dword * 4 + i * 32 * 16);
+        load_scales(Gn.c[d], chunk * S::SCALES, dword, true);
       }
       if ((U + 1) % S::SPC == 0) fetch_scales((s + U + 1) / S::SPC + 1);   // the next stage starts a chunk
       __builtin_amdgcn_sched_barrier(0);
@@ -896,13 +922,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   }
 }
 
-template <bool FP4A, bool SWIGLU, int WM, int WN, int TM, int TN, int KS, int NST>
-static void launch_tile(const TileArgs& a, hipStream_t stream) {
-  using S = TileShape<FP4A, WM, WN, TM, TN, KS, NST>;
+template <bool FP4A, bool SWIGLU, bool ODD, int WM, int WN, int TM, int TN, int KS, int NST>
+static void launch_tile_of(const TileArgs& a, hipStream_t stream) {
+  using S = TileShape<FP4A, ODD, WM, WN, TM, TN, KS, NST>;
   constexpr int CN = SWIGLU ? S::BN / 2 : S::BN;
   const int64_t tiles = (int64_t)((a.M + S::BM - 1) / S::BM) * ((a.N + CN - 1) / CN);
   const dim3 grid((unsigned)((tiles + XCDS - 1) / XCDS * XCDS)), block(64 * S::NW);
-  hipLaunchKernelGGL((fp4_tile_kernel<FP4A, SWIGLU, WM, WN, TM, TN, KS, NST>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL((fp4_tile_kernel<FP4A, SWIGLU, ODD, WM, WN, TM, TN, KS, NST>), grid, block, 0, stream, a);
+}
+template <bool FP4A, bool SWIGLU, int WM, int WN, int TM, int TN, int KS, int NST>
+static void launch_tile(const TileArgs& a, hipStream_t stream) {
+  if constexpr (TileShape<FP4A, false, WM, WN, TM, TN, KS, NST>::WHOLE) {
+    if (a.K % 128 != 0) return launch_tile_of<FP4A, SWIGLU, true, WM, WN, TM, TN, KS, NST>(a, stream);
+  }
+  launch_tile_of<FP4A, SWIGLU, false, WM, WN, TM, TN, KS, NST>(a, stream);
 }
 
 static int64_t tiles_of(int M, int N, int bm, int bn) { return ((int64_t)M + bm - 1) / bm * (((int64_t)N + bn - 1) / bn); }
