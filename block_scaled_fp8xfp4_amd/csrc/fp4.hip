@@ -877,7 +877,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   // Results.  Each wavefront turns 32 rows at a time in its own part of LDS, so that a store instruction writes whole
   // runs of a row: 16 bytes a lane, at whatever alignment the row has (2 bytes where N is odd), the row's last piece by
   // elements.
-  const int esz = A.bf16_out ? 2 : 4;
   uint8_t* const y = static_cast<uint8_t*>(A.y);
   constexpr int WC = TN * 32;                                         // columns of a wavefront
   constexpr uint32_t PITCH = WC * 4 + 16;                             // + 16: rows start on different banks
@@ -885,41 +884,56 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   lds_barrier();                                                      // every wavefront has read its operands
   const uint32_t mine = lds0 + wave * 32 * PITCH;
   const int nw = (int)min((int64_t)WC, N - n0 - wn * WC);             // this wavefront's columns
+  auto store = [&](auto esize) {                                      // bytes of a result
+    constexpr int ESZ = decltype(esize)::value, LPR = WC * ESZ / 16, PER = 16 / ESZ;   // lanes per row, elements per lane
+    constexpr int RPP = 64 / LPR, PASSES = 32 / RPP, GROUP = PASSES < 4 ? PASSES : 4;  // rows at a time; LDS reads in flight
+    const int r0 = lane / LPR, c0 = lane % LPR * PER;
+    const uint32_t from = mine + r0 * PITCH + c0 * ESZ;
+    const int64_t step = (int64_t)RPP * N * ESZ;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+      for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v16f& c = acc[i][j];
-        const uint32_t at = mine + lr * PITCH + (j * 32 + 8 * q + 4 * g) * esz;
-        if (A.bf16_out)
-          lds_write(at, u32x2{(uint32_t)f32_to_bf16_rne(c[4 * q]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 1]) << 16),
-                              (uint32_t)f32_to_bf16_rne(c[4 * q + 2]) | ((uint32_t)f32_to_bf16_rne(c[4 * q + 3]) << 16)});
-        else
-          lds_write(at, u32x4{__float_as_uint(c[4 * q]), __float_as_uint(c[4 * q + 1]), __float_as_uint(c[4 * q + 2]),
-                              __float_as_uint(c[4 * q + 3])});
-      }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");                // the wavefront's own writes
-    const int lpr = WC * esz / 16, per = 16 / esz;                    // lanes per row, elements per lane
-    const int64_t mb = m0 + wm * TM * 32 + i * 32;
-    for (int r = lane / lpr; r < 32; r += 64 / lpr) {
-      const int c = (lane % lpr) * per;
-      const uint32_t from = mine + r * PITCH + c * esz;
-      uint8_t* const to = y + ((mb + r) * N + n0 + wn * WC + c) * esz;
-      const u32x4 d = lds_read<u32x4>(from);
-      if (mb + r >= M) continue;
-      if (c + per <= nw) *reinterpret_cast<u32x4_a1*>(to) = d;
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (c + e >= nw) continue;
-          if (A.bf16_out) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(d[e / 2] >> (16 * (e % 2)));
-          else if (e < 4) reinterpret_cast<uint32_t*>(to)[e] = d[e < 4 ? e : 0];
+        for (int q = 0; q < 4; ++q) {
+          const v16f& c = acc[i][j];
+          const uint32_t at = mine + lr * PITCH + (j * 32 + 8 * q + 4 * g) * ESZ;
+          if (ESZ == 2) lds_write(at, u32x2{bf16_pair(c[4 * q], c[4 * q + 1]), bf16_pair(c[4 * q + 2], c[4 * q + 3])});
+          else
+            lds_write(at, u32x4{__float_as_uint(c[4 * q]), __float_as_uint(c[4 * q + 1]), __float_as_uint(c[4 * q + 2]),
+                                __float_as_uint(c[4 * q + 3])});
         }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");              // the wavefront's own writes
+      const int64_t mb = m0 + wm * TM * 32 + i * 32;
+      const int64_t left = M - mb;                                    // rows
+      uint8_t* to = y + ((mb + r0) * N + n0 + wn * WC + c0) * ESZ;
+#pragma unroll
+      for (int p0 = 0; p0 < PASSES; p0 += GROUP) {
+        u32x4 d[GROUP];
+#pragma unroll
+        for (int p = 0; p < GROUP; ++p) d[p] = lds_read<u32x4>(from + (p0 + p) * RPP * PITCH);
+#pragma unroll
+        for (int p = 0; p < GROUP; ++p, to += step) {
+          if (left >= 32 && nw == WC) {
+            *reinterpret_cast<u32x4_a1*>(to) = d[p];
+            continue;
+          }
+          if (r0 + (p0 + p) * RPP >= left) continue;
+          if (c0 + PER <= nw) *reinterpret_cast<u32x4_a1*>(to) = d[p];
+          else
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+              if (c0 + e >= nw) continue;
+              if (ESZ == 2) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(d[p][e / (4 / ESZ)] >> (16 * (e % 2)));
+              else reinterpret_cast<uint32_t*>(to)[e] = d[p][e / (4 / ESZ)];
+            }
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  }
+  };
+  if (A.bf16_out) store(Int<2>{});
+  else store(Int<4>{});
 }
 
 template <bool FP4A, bool SWIGLU, bool ODD, int WM, int WN, int TM, int TN, int KS, int NST>

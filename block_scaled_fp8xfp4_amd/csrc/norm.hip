@@ -77,7 +77,11 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void add_rmsnorm_kern
     }
     if (R16 && (has_r || A.h)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = __uint_as_float((uint32_t)f32_to_bf16_rne(v[c][j]) << 16);
+      for (int j = 0; j < 8; j += 2) {
+        const uint32_t d = bf16_pair(v[c][j], v[c][j + 1]);
+        v[c][j] = __uint_as_float(d << 16);
+        v[c][j + 1] = __uint_as_float(d & 0xFFFF0000u);
+      }
     }
     if (c * LANES + tid < nch) {
 #pragma unroll
