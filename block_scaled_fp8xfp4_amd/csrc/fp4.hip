@@ -322,8 +322,14 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void fp4_rows_kernel(TileArgs A
 // Rows go to LDS in pieces of 128 bytes where they can: the vector memory
 // path takes a lookup per row piece, and with pieces of 64 bytes and a dword
 // of scales per row and stage the lookups, not the matrix cores, set the time
-// (109 us at 8192 x 4096 x 4096 in E2M1).  For the same reason a lane reads
-// 16 scale bytes of its row at a time (K = 512) and writes them to LDS.
+// (109 us at 8192 x 4096 x 4096 in E2M1).  For the same reason 16 scale bytes
+// of a row (K = 512) go to LDS at a time.
+//
+// 8192 x 4096 x 4096 takes 75 us in E2M1 (3.7 PFLOP/s) and 109 us in E4M3
+// (2.5): the matrix cores are busy for 41 and 59 % of the cycles, the rest
+// goes to the first loads and the last stores of each round of tiles and, in
+// E2M1, to LDS, whose reads and DMA writes of a stage take as many cycles as
+// its matrix operations.
 //
 // The weights take the instruction's A side and the activations its B side,
 // so a lane holds one row of y and four consecutive columns per register
@@ -331,7 +337,8 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void fp4_rows_kernel(TileArgs A
 //
 // LDS rows are 64 or 128 bytes in 16-byte chunks; the chunk index is XORed
 // with bits of the row so that 8 (and 16) consecutive rows' reads of one
-// chunk fall on different banks (no conflicts counted).
+// chunk fall on different banks.  The conflicts that are counted (14 to 19 %
+// of the LDS cycles of large tiles) are reads of scales, 16 bytes apart.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 // dma16_to_lds if on is -1, nothing if it is 0 (in a wavefront whose lanes are all active): an instruction that may
@@ -975,8 +982,9 @@ template <bool FP4A> static const char* launch_rows(const TileArgs& t, hipStream
 }
 
 // Which kernel runs (M, N, K), by how many workgroups each shape gives.  Times at N = K = 4096, E2M1 / E4M3 activations:
-//   rows (16 at a time):                  M = 1 4.2 / 4.5 us, 16 4.9 / 5.8; a second wavefront for rows 17 to 32 7.1 / 8.7
-//   32 x 64 (2 wavefronts):               M = 32 6.8 / 8.5, 48 6.7 / 8.6, 128 7.0 / 8.8, 256 9.3 / 11.8
+//   rows (16 at a time, 512 wavefronts):  M = 1 4.2 / 4.5 us, 16 4.8 / 6.0, 32 6.3 / 6.9, 48 8.5 / 9.2; N = 1024: M = 64
+//                                         5.1 / 5.8 (32 x 64: 6.3 / 8.0), 128 6.0 / 6.8 (6.3 / 8.0)
+//   32 x 64 (2 wavefronts):               M = 32 6.5 / 8.3, 48 6.4 / 8.3, 128 7.0 / 8.8, 256 9.3 / 11.8
 //   64 x 64 (4, two workgroups per CU):   M = 48 7.4 / 9.2, 256 7.9 / 10.0, 512 10.6 / 15.2, 1024 20.3 / 26.9
 //   128 x 128 (4, two per CU):            M = 256 14.4 / 17.1, 512 13.0 / 17.8, 1024 16.6 / 20.8
 //   128 x 256 (8, one per CU):            M = 1024 20.0 / 26.5, 1500 21.9 / 28.5 (128 x 128: 23.7 / 32.1), 2048 24.7 / 34.2
@@ -990,7 +998,7 @@ static Fp4Kernel pick_large(int M, int N) {
   return (t256 + 255) / 256 * 8 <= (t128 + 511) / 512 * 5 ? Fp4Kernel::t256x256 : Fp4Kernel::t128x128;
 }
 static Fp4Kernel pick_kernel(int M, int N, int K, bool fp4a) {
-  if ((M <= 16 && rows_lds(M, K, fp4a) <= ROWS_LDS) || K < 128) return Fp4Kernel::rows;                     // the tiles' scale reads need four blocks a row
+  if (((M <= 16 || tiles_of(M, N, 16, 16) <= 512) && rows_lds(M, K, fp4a) <= ROWS_LDS) || K < 128) return Fp4Kernel::rows;                     // the tiles' scale reads need four blocks a row
   if (tiles_of(M, N, 32, 64) <= 256) return Fp4Kernel::t32x64;        // one per CU
   if (tiles_of(M, N, 64, 64) <= 512) return Fp4Kernel::t64x64;        // two per CU
   return pick_large(M, N);
@@ -1031,7 +1039,8 @@ static size_t a256(size_t b) { return (b + 255) / 256 * 256; }
 // Gate/up of few rows: one workgroup per 16 rows and block of 32 intermediate
 // columns; its four wavefronts take 16 gate or 16 up columns each, meet in
 // LDS, and 16 lanes per row make the block's codes, two neighbouring columns
-// a lane.
+// a lane.  One row at H = 4096, I = 2048 takes 6.7 us: 64 workgroups are all
+// there is to spread, and a CU reads its 136 KB of weights in about 4 us.
 template <bool FP4A>
 __global__ __launch_bounds__(256, 2) void fp4_gate_up_rows_kernel(TileArgs A) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -1075,13 +1084,19 @@ __global__ __launch_bounds__(256, 2) void fp4_gate_up_rows_kernel(TileArgs A) {
   if (c == 0) A.q_sc[r * nb + n0 / 32] = (uint8_t)s;
 }
 
-// The kernel by the same counts as pick_kernel, of tiles that hold both halves of a block in one wavefront.
+// The kernel by the same counts as pick_kernel, of tiles that hold both halves of a block in one wavefront.  The whole FFN
+// at H = 4096, E2M1 / E4M3, us:
+//   rows (one workgroup per CU):          48 rows, I = 2048 14.1 / 15.9, 64 14.1 / 16.1, 96 18.4 / 20.4; 128, I = 576 13.7 / 14.5
+//   64 x 64 (2 wavefronts, one per CU):   48 rows, I = 2048 13.8 / 18.6, 64 14.6 / 18.9, 96 14.4 / 19.6; 128, I = 576 14.1 / 17.7
+//   64 x 128:                             48 rows, I = 2048 16.6 / 20.5, 256 18.2 / 22.1 (64 x 64: 16.2 / 21.2)
+//   128 x 256, one round:                 512 rows, I = 8192 46.1 / 66.6 (128 x 128: 47.1 / 68.6)
 template <bool FP4A>
 static const char* launch_gate_up(const TileArgs& t, hipStream_t stream) {
   const int M = t.M, N = 2 * t.N;
   constexpr int KS = FP4A ? 256 : 128, NB = FP4A ? 2 : 3;
-  if ((M <= 16 && rows_lds(M, t.K, FP4A) <= ROWS_LDS) || t.K < 128) {
-    const dim3 grid((unsigned)((int64_t)(t.N / 32) * ((M + 15) / 16)));
+  const int64_t rows = (int64_t)(t.N / 32) * ((M + 15) / 16);
+  if (((M <= 16 || rows <= 256) && rows_lds(M, t.K, FP4A) <= ROWS_LDS) || t.K < 128) {
+    const dim3 grid((unsigned)rows);
     hipLaunchKernelGGL(fp4_gate_up_rows_kernel<FP4A>, grid, dim3(64 * ROWS_WAVES), rows_lds(M, t.K, FP4A), stream, t);
     return "fp4_ffn:rows16+";
   }

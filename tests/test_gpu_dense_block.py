@@ -318,7 +318,7 @@ def test_fp4_block_gemm_few_rows_at_every_end_of_K(whole, a_fmt):
 
 
 @pytest.mark.parametrize("a_fmt", [E4M3, E2M1])
-@pytest.mark.parametrize("M,N", [(40, 100), (1040, 523), (1500, 1502), (2100, 2835), (2830, 2835)])
+@pytest.mark.parametrize("M,N", [(40, 2801), (1040, 523), (1500, 1502), (2100, 2835), (2830, 2835)])
 def test_fp4_block_gemm_tiles_at_every_end_of_K(M, N, a_fmt):
     """K around the stages and the K = 512 of scales of each tile: the bits of few rows, at the first, a middle and the last
     rows, columns that end inside a tile at odd addresses, and nothing written behind."""
@@ -372,7 +372,7 @@ def test_fp4_dense_ffn_is_its_three_steps(T, H, I, x_fmt, mid_fmt):
 
 
 @pytest.mark.parametrize("fmt", [E4M3, E2M1])
-@pytest.mark.parametrize("T,H,I", [(5, 256, 96), (40, 256, 96), (600, 128, 1056), (1100, 160, 2080), (1500, 128, 2080), (2100, 256, 4128)])
+@pytest.mark.parametrize("T,H,I", [(5, 256, 96), (40, 256, 96), (40, 128, 4128), (600, 128, 1056), (1100, 160, 2080), (1500, 128, 2080), (2040, 544, 4064), (2100, 256, 4128)])
 def test_fp4_dense_ffn_blocks_that_need_double(T, H, I, fmt):
     """Gates far below zero and products next to fp32's ends, whose codes fp32 does not decide, zero rows and gates whose
     SwiGLU vanishes, in every kernel of the gate/up product: the codes of mx_swiglu_quantize on the product's own result."""
@@ -501,6 +501,76 @@ def test_dense_block_in_a_graph_and_on_another_stream(T):
         block(rows[(k + 2) % 4], rows[(k + 3) % 4], eager)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, want[(k + 2) % 4])), k
+
+
+@pytest.mark.parametrize("T", [4, 70])
+def test_two_graphs_and_two_streams_at_once(T):
+    """Two captured blocks with workspaces of their own, replayed on two streams at the same time, over and over, while
+    eager calls run on the current stream; rows behind the last one stay as they were."""
+    H, I, K = 1056, 576, 5
+    rng = np.random.default_rng(T)
+    w = to_dev((1 + 0.1 * rng.standard_normal(H)).astype(np.float32))
+    wf = [to_dev(t) for t in ref.weights(rng, 2 * I, H) + ref.weights(rng, H, I)]
+    need = mxmoe.fp4_dense_ffn_workspace_bytes(T, H, I, E2M1)
+
+    class Block:
+        def __init__(self):
+            self.x, self.r = (typed(ref.activations(rng, T, H), BF16)[0] for _ in range(2))
+            self.h = torch.full((T + 1, H), 7.0, dtype=BF16, device="cuda")
+            self.q, self.sc = codes_like(T + 1, H, E4M3)
+            self.q.fill_(77)
+            self.sc.fill_(77)
+            self.y = torch.full((T + 1, H), 7.0, dtype=F32, device="cuda")
+            self.ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+        def run(self):
+            mxmoe.mx_add_rmsnorm(self.x, w, 1e-6, residual=self.r, h=self.h[:T], q=self.q[:T], sc=self.sc[:T], fmt=E4M3)
+            mxmoe.fp4_dense_ffn(self.q[:T], self.sc[:T], E4M3, *wf, E2M1, self.y[:T], self.ws)
+
+    blocks = [Block() for _ in range(3)]
+    want = []
+    for b in blocks:
+        b.run()
+        want.append((b.h.clone(), b.q.clone(), b.y.clone()))
+    graphs, streams = [torch.cuda.CUDAGraph() for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    for g, b in zip(graphs, blocks):
+        with torch.cuda.graph(g):
+            b.run()
+    for b in blocks:
+        b.h[:T].zero_()
+        b.q[:T].zero_()
+        b.y[:T].zero_()
+    torch.cuda.synchronize()
+    for k in range(K):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        blocks[2].run()
+    torch.cuda.synchronize()
+    for b, (h, q, y) in zip(blocks, want):
+        assert torch.equal(b.h, h) and torch.equal(b.q, q) and torch.equal(b.y, y)
+        assert torch.all(b.h[T] == 7) and torch.all(b.q[T] == 77) and torch.all(b.sc[T] == 77) and torch.all(b.y[T] == 7)
+
+
+@pytest.mark.parametrize("a_fmt", [E4M3, E2M1])
+@pytest.mark.parametrize("M,N,K", [(3, 48, 1056), (40, 2800, 1056), (300, 1040, 672)])
+def test_fp4_block_gemm_scales_at_every_byte(M, N, K, a_fmt):
+    """K % 128 != 0: scales that start at any byte, neighbours of other values around them."""
+    rng = np.random.default_rng(M)
+    a, a_sc, w, w_sc = random_codes(rng, M, K, a_fmt) + random_codes(rng, N, K, E2M1)
+    da, dw = to_dev(a), to_dev(w)
+    want = None
+    for oa, ow in ((0, 0), (1, 3), (2, 2), (3, 1)):
+        bufs = []
+        for sc, o in ((a_sc, oa), (w_sc, ow)):
+            b = torch.full((sc.size + 8,), 255, dtype=torch.uint8, device="cuda")
+            b[o:o + sc.size] = to_dev(sc.reshape(-1))
+            bufs.append(b[o:o + sc.size].view(sc.shape))
+        y = torch.empty((M, N), dtype=F32, device="cuda")
+        mxmoe.fp4_block_gemm(da, bufs[0], a_fmt, dw, bufs[1], y)
+        assert not torch.isnan(y).any()
+        want = y if want is None else want
+        assert torch.equal(y, want), (oa, ow, mxmoe.last_variant())
 
 
 def test_empty_batches():
