@@ -136,7 +136,8 @@ class FP4Linear:
 
 
 class DenseFFN:
-    """A dense SwiGLU FFN with MXFP4 weights (fp4_dense_ffn); owns the workspace of up to T rows."""
+    """A dense SwiGLU FFN with MXFP4 weights (fp4_dense_ffn); owns the workspace of up to T rows, which its calls and the
+    graphs captured of them share: they must not overlap."""
 
     def __init__(self, w13, w13_sc, w2, w2_sc, T, mid_fmt=mxmoe.MX_FMT_E4M3):
         self.weights, self.T, self.mid_fmt = (w13, w13_sc, w2, w2_sc), T, mid_fmt

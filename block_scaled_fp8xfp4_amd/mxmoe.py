@@ -353,6 +353,15 @@ def _two(name, what, t):
     return t.shape
 
 
+_INT_MAX = 2**31 - 1
+
+
+def _int(name, *sizes):
+    """Sizes the C-ABI takes as int (ctypes would cut larger ones)."""
+    if max(sizes) > _INT_MAX:
+        raise ValueError(f"{name}: a size of {max(sizes)}, at most {_INT_MAX} is supported")
+
+
 def _code_cols(name, fmt, cols):
     """Code bytes of a row of cols elements."""
     if fmt == MX_FMT_E4M3:
@@ -384,6 +393,7 @@ def mx_swiglu_quantize(gu, q, sc, fmt, stream=None):
     name, t = "mx_swiglu_quantize", _tn()
     T, two_i = _two(name, "gu", gu)
     I = two_i // 2
+    _int(name, I)
     qc, d, ld = _code_cols(name, fmt, I), gu.get_device(), two_i
     if not (gu.dtype in t.ins and gu.is_contiguous() and two_i == 2 * I and q.dtype is t.u8 and sc.dtype is t.u8 and
             q.shape == (T, qc) and sc.shape == (T, I // 32) and q.is_contiguous() and sc.is_contiguous() and
@@ -405,6 +415,7 @@ def mx_add_rmsnorm(x, weight, eps, residual=None, x2=None, h=None, n=None, q=Non
     name, t = "mx_add_rmsnorm", _tn()
     shape = _two(name, "x", x)
     T, H = shape
+    _int(name, T, H)
     d, ins = x.get_device(), t.ins
     r = residual if residual is not None else h
     x_ld = r_ld = H
@@ -452,6 +463,7 @@ def fp4_block_gemm(a, a_sc, a_fmt, w, w_sc, y, stream=None):
     N, K = _two(name, "w", w)
     M, yn = _two(name, "y", y)
     K *= 2
+    _int(name, M, N, K)
     ac, nb, d, u8 = _code_cols(name, a_fmt, K), K // 32, y.get_device(), t.u8
     if not (yn == N and y.dtype in t.outs and w.dtype is u8 and a.dtype is u8 and a_sc.dtype is u8 and w_sc.dtype is u8 and
             a.shape == (M, ac) and a_sc.shape == (M, nb) and w_sc.shape == (N, nb) and w.is_contiguous() and
@@ -479,6 +491,7 @@ def fp4_dense_ffn(x, x_sc, x_fmt, w13, w13_sc, w2, w2_sc, mid_fmt, y, ws, stream
     H, I = _two(name, "w2", w2)
     T = _two(name, "y", y)[0]
     I *= 2
+    _int(name, T, H, I)
     xc, hb, ib, d, u8 = _code_cols(name, x_fmt, H), H // 32, I // 32, y.get_device(), t.u8
     if not (y.dtype in t.outs and y.shape == (T, H) and x.dtype is u8 and x_sc.dtype is u8 and w13.dtype is u8 and
             w13_sc.dtype is u8 and w2.dtype is u8 and w2_sc.dtype is u8 and x.shape == (T, xc) and

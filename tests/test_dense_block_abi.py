@@ -138,3 +138,27 @@ def bf(*s):
 def test_binding_refuses_wrong_tensors(lib, call):
     with pytest.raises(ValueError):
         call()
+
+
+def meta(*s, dtype=torch.uint8):
+    return torch.empty(s, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("call", [
+    lambda n: mxmoe.mx_add_rmsnorm(meta(n, 32, dtype=torch.float32), None, 1e-6, n=meta(n, 32, dtype=torch.bfloat16)),
+    lambda n: mxmoe.mx_add_rmsnorm(meta(1, n, dtype=torch.float32), None, 1e-6, n=meta(1, n, dtype=torch.bfloat16)),
+    lambda n: mxmoe.mx_swiglu_quantize(meta(1, 2 * n, dtype=torch.float32), meta(1, n), meta(1, n // 32), mxmoe.MX_FMT_E4M3),
+    lambda n: mxmoe.fp4_block_gemm(meta(n, 32), meta(n, 1), mxmoe.MX_FMT_E4M3, meta(8, 16), meta(8, 1),
+                                   meta(n, 8, dtype=torch.float32)),
+    lambda n: mxmoe.fp4_block_gemm(meta(2, n), meta(2, n // 32), mxmoe.MX_FMT_E4M3, meta(8, n // 2), meta(8, n // 32),
+                                   meta(2, 8, dtype=torch.float32)),
+    lambda n: mxmoe.fp4_block_gemm(meta(2, 32), meta(2, 1), mxmoe.MX_FMT_E4M3, meta(n, 16), meta(n, 1),
+                                   meta(2, n, dtype=torch.float32)),
+    lambda n: mxmoe.fp4_dense_ffn(meta(n, 32), meta(n, 1), 0, meta(64, 16), meta(64, 1), meta(32, 16), meta(32, 1), 0,
+                                  meta(n, 32, dtype=torch.float32), meta(256)),
+])
+def test_binding_refuses_sizes_past_int(lib, call):
+    """A size that does not fit the C-ABI's int would arrive cut: 2^32 + 32 as 32."""
+    for n in (2**31, 2**32 + 32):
+        with pytest.raises(ValueError, match="at most 2147483647"):
+            call(n)

@@ -216,7 +216,8 @@ def check_product(y32, y16, want, room, K, a_fmt):
 PRODUCT_SIZES = [(1, 1, 32), (1, 16, 128), (1, 4096, 4096), (2, 100, 96), (3, 17, 160), (15, 33, 544), (16, 64, 1024),
                  (17, 48, 576), (33, 1152, 256), (48, 4096, 4096), (64, 130, 2080), (65, 300, 1056), (127, 129, 288),
                  (128, 128, 512), (130, 260, 4128), (255, 255, 640), (300, 520, 992), (513, 384, 256), (1000, 272, 1120),
-                 (2, 40, 16384), (129, 40, 16384)]
+                 (2, 40, 16384), (129, 40, 16384), (16, 8200, 96), (8192, 16, 160),
+                 (4100, 7, 544), (500, 250, 64)]
 
 
 @pytest.mark.parametrize("a_fmt", [E4M3, E2M1])
