@@ -20,6 +20,7 @@ __device__ __forceinline__ v4f mfma_fp4_fp4(const v8i& a, const v8i& b, v4f c, u
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
 
@@ -195,6 +196,10 @@ __device__ __forceinline__ void rows_load_tail(RowsPiece& P, const uint8_t* wp, 
 }
 
 struct RowsLds { uint32_t row, sc; int r; };      // this lane's row and scales in LDS, and the row's number
+__device__ __forceinline__ RowsLds rows_lane(uint32_t lds, const RowsShape& sh, int rows) {
+  const int r = min((int)threadIdx.x & 15, rows - 1);
+  return {lds + r * sh.row, lds + rows * sh.row + r * sh.sc, r & 7};
+}
 
 template <bool FP4A, bool TAIL>
 __device__ __forceinline__ v4f rows_multiply(const RowsPiece& P, const RowsLds& L, v4f acc, int c, int g, int nblk) {
@@ -223,35 +228,58 @@ __device__ __forceinline__ v4f rows_multiply(const RowsPiece& P, const RowsLds& 
   return acc;
 }
 
-template <bool FP4A, int RING>
-__device__ __forceinline__ v4f rows_ring(const RowsLds& L, const uint8_t* wp, const uint8_t* wsp, int nblk, int g) {
-  const int whole = nblk / 16, tail = nblk % 16;
-  RowsPiece P[RING];
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
+// The first RING pieces of a weight row (LONG: it has as many), or all of a shorter one.
+template <bool LONG, int RING>
+__device__ __forceinline__ void rows_prime(RowsPiece (&P)[RING], const uint8_t* wp, const uint8_t* wsp, int nblk, int g) {
+  const int whole = nblk / 16;
+  if (LONG) {
 #pragma unroll
-  for (int r = 0; r < RING; ++r) rows_load(P[r], wp, wsp, r, g);
-  __builtin_amdgcn_sched_barrier(0);              // the count below is of the loads above
-  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(RING * 5) : "memory");
-  lds_barrier();
-  int c = 0;
-  for (; c + 2 * RING <= whole; c += RING)
+    for (int r = 0; r < RING; ++r) rows_load(P[r], wp, wsp, r, g);
+  } else {
 #pragma unroll
-    for (int r = 0; r < RING; ++r) {
-      acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
-      rows_load(P[r], wp, wsp, c + RING + r, g);
-    }
-#pragma unroll
-  for (int r = 0; r < RING; ++r) {                                    // the last whole pieces but fewer than RING
-    acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
-    if (c + RING + r < whole) rows_load(P[r], wp, wsp, c + RING + r, g);
+    for (int r = 0; r + 1 < RING; ++r)
+      if (r < whole) rows_load(P[r], wp, wsp, r, g);
+    if (nblk % 16) rows_load_tail(P[RING - 1], wp, wsp, whole, g, nblk);
   }
-  c += RING;
-  if (tail) rows_load_tail(P[RING - 1], wp, wsp, whole, g, nblk);
+}
+// The tile over all of K, the rows in LDS and the pieces asked for by rows_prime.
+template <bool FP4A, bool LONG, int RING>
+__device__ __forceinline__ v4f rows_finish(RowsPiece (&P)[RING], const RowsLds& L, const uint8_t* wp, const uint8_t* wsp, int nblk,
+                                           int g) {
+  const int whole = nblk / 16, tail = nblk % 16;
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  int c = 0;
+  if (LONG) {
+    for (; c + 2 * RING <= whole; c += RING)
+#pragma unroll
+      for (int r = 0; r < RING; ++r) {
+        acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
+        rows_load(P[r], wp, wsp, c + RING + r, g);
+      }
+#pragma unroll
+    for (int r = 0; r < RING; ++r) {                                  // the last whole pieces but fewer than RING
+      acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
+      if (c + RING + r < whole) rows_load(P[r], wp, wsp, c + RING + r, g);
+    }
+    c += RING;
+    if (tail) rows_load_tail(P[RING - 1], wp, wsp, whole, g, nblk);
+  }
 #pragma unroll
   for (int r = 0; r + 1 < RING; ++r)
     if (c + r < whole) acc = rows_multiply<FP4A, false>(P[r], L, acc, c + r, g, nblk);
   if (tail) acc = rows_multiply<FP4A, true>(P[RING - 1], L, acc, whole, g, nblk);
   return acc;
+}
+// The same where the rows come by DMA that went out before: the loads of LONG rows (five a piece) may be on their way
+// while it is waited for.
+template <bool FP4A, bool LONG, int RING>
+__device__ __forceinline__ v4f rows_run(const RowsLds& L, const uint8_t* wp, const uint8_t* wsp, int nblk, int g) {
+  RowsPiece P[RING];
+  rows_prime<LONG>(P, wp, wsp, nblk, g);
+  __builtin_amdgcn_sched_barrier(0);              // the count is of the loads above
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LONG ? RING * 5 : 0) : "memory");
+  lds_barrier();
+  return rows_finish<FP4A, LONG>(P, L, wp, wsp, nblk, g);
 }
 
 // The workgroup's rows (a, a_sc from its first row on) to LDS, and for the first CW wavefronts the 16 x 16 tile of this
@@ -275,27 +303,16 @@ __device__ __forceinline__ v4f rows_tile(uint32_t lds, const uint8_t* a, const u
       for (int c = lane; c < nblk; c += 64) lds_write<uint8_t>(lsc + r * sh.sc + c, a_sc[r * nblk + c]);
     }
   }
-  v4f acc = {0.f, 0.f, 0.f, 0.f};
-  const int r = min(lane & 15, rows - 1);
-  const RowsLds L{lds + r * sh.row, lsc + r * sh.sc, r & 7};
+  const RowsLds L = rows_lane(lds, sh, rows);
   asm volatile("" ::: "memory");
-  if (wave < CW && whole >= 8) return rows_ring<FP4A, 8>(L, wp, wsp, nblk, g);
-  if (wave < CW && whole >= 4) return rows_ring<FP4A, 4>(L, wp, wsp, nblk, g);
-  RowsPiece P[3], T;
-  if (wave < CW) {
-#pragma unroll
-    for (int r = 0; r < 3; ++r)
-      if (r < whole) rows_load(P[r], wp, wsp, r, g);
-    if (nblk % 16) rows_load_tail(T, wp, wsp, whole, g, nblk);
+  if (wave >= CW) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();
+    return v4f{0.f, 0.f, 0.f, 0.f};
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  lds_barrier();
-  if (wave >= CW) return acc;
-#pragma unroll
-  for (int r = 0; r < 3; ++r)
-    if (r < whole) acc = rows_multiply<FP4A, false>(P[r], L, acc, r, g, nblk);
-  if (nblk % 16) acc = rows_multiply<FP4A, true>(T, L, acc, whole, g, nblk);
-  return acc;
+  if (whole >= 8) return rows_run<FP4A, true, 8>(L, wp, wsp, nblk, g);
+  if (whole >= 4) return rows_run<FP4A, true, 4>(L, wp, wsp, nblk, g);
+  return rows_run<FP4A, false, 4>(L, wp, wsp, nblk, g);
 }
 
 template <bool FP4A, int CW>
@@ -309,6 +326,59 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void fp4_rows_kernel(TileArgs A
   const v4f acc = rows_tile<FP4A, CW>(__builtin_amdgcn_readfirstlane(lds_addr(lds)), A.x + m0 * (FP4A ? K / 2 : K), A.x_sc + m0 * nblk,
                                       (int)min((int64_t)16, M - m0), A.w + n * (K / 2), A.w_sc + n * nblk, K);
   if (wave < CW && n0 + col < N) store_rows(A, acc, m0 + 4 * (lane >> 4), n);
+}
+
+// The down product of an FFN of very few rows, from its gate/up values in
+// fp32 (h: [M][2 K], gate, then up): every workgroup makes the codes of all
+// rows itself, 8 columns a lane, into the same places in LDS, while its
+// weights are on their way.  The gate/up product then spreads over all CUs,
+// where one that makes the codes has K / 32 workgroups.
+template <bool FP4A, int CW>
+__global__ __launch_bounds__(64 * ROWS_WAVES, 2) void fp4_down_rows_kernel(TileArgs A, const float* __restrict__ h) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds_[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int M = A.M, N = A.N, K = A.K, g = lane >> 4, nblk = K / 32;
+  const int64_t n0 = ((int64_t)blockIdx.x * CW + wave) * 16, n = min(n0 + (lane & 15), (int64_t)N - 1);
+  const uint8_t* const wp = A.w + n * (K / 2);
+  const uint8_t* const wsp = A.w_sc + n * nblk;
+  const uint32_t lds = __builtin_amdgcn_readfirstlane(lds_addr(lds_));
+  const RowsShape sh = rows_shape(K, FP4A);
+  const uint32_t per_row = K / 8, chunks = M * per_row;
+  float gt[8], up[8];
+  auto fetch = [&](uint32_t c) {
+    const uint32_t t = c / per_row, i = (c - t * per_row) * 8;
+    load8(h, false, (int64_t)t * 2 * K + i, gt);
+    load8(h, false, (int64_t)t * 2 * K + K + i, up);
+  };
+  // The wavefronts without columns make the codes; where all have some, all do (their values asked for before the weights,
+  // since loads arrive in order).
+  constexpr uint32_t MAKERS = 64 * (CW < ROWS_WAVES ? ROWS_WAVES - CW : ROWS_WAVES);
+  const uint32_t first = threadIdx.x - (64 * ROWS_WAVES - MAKERS);    // past the end in the others
+  if (first < chunks) fetch(first);
+  asm volatile("" ::: "memory");
+  RowsPiece P[4];
+  if (CW == ROWS_WAVES || wave < CW) {
+    if (nblk >= 64) rows_prime<true>(P, wp, wsp, nblk, g);
+    else rows_prime<false>(P, wp, wsp, nblk, g);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  for (uint32_t c = first; c < chunks;) {
+    uint32_t d[2];
+    const uint32_t s = swiglu_codes8<FP4A>(gt, up, d);
+    const uint32_t r = c / per_row, i = c - r * per_row;
+    const uint32_t at = i * (FP4A ? 4 : 8), chunk = at / 16;          // 16-byte chunks as rows_multiply reads them
+    const uint32_t to = lds + r * sh.row + ((chunk & ~7u) | ((chunk ^ r) & 7u)) * 16 + at % 16;
+    if (FP4A) lds_write<uint32_t>(to, d[0]);
+    else lds_write(to, u32x2{d[0], d[1]});
+    if (i % 4 == 0) lds_write<uint8_t>(lds + M * sh.row + r * sh.sc + i / 4, (uint8_t)s);
+    c += MAKERS;
+    if (c < chunks) fetch(c);
+  }
+  lds_barrier();
+  if (wave >= CW) return;
+  const RowsLds L = rows_lane(lds, sh, M);
+  const v4f acc = nblk >= 64 ? rows_finish<FP4A, true>(P, L, wp, wsp, nblk, g) : rows_finish<FP4A, false>(P, L, wp, wsp, nblk, g);
+  if (n0 + (lane & 15) < N) store_rows(A, acc, 4 * g, n);
 }
 
 // Many rows: BM x BN output tiles staged through LDS.  A stage holds K = KS
@@ -348,8 +418,6 @@ __device__ __forceinline__ void dma16_to_lds_if(int on, const void* base, uint32
                "global_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1"
                :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(dst)), "s"(__builtin_amdgcn_readfirstlane(on)) : "m0");
 }
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ int swz4(int r) { return (((r >> 1) ^ (r >> 3)) & 1) | ((r >> 1) & 2); }
 __device__ __forceinline__ int swz8(int r) { return (r & 6) | ((r >> 3) & 1); }
@@ -1122,14 +1190,40 @@ static const char* launch_gate_up(const TileArgs& t, hipStream_t stream) {
 }
 
 // [codes of the intermediate][its scales]
+// Up to this many rows the gate/up values go to the down product in fp32.  The FFN at H = 4096, E2M1 / E4M3, us, so and with
+// the codes made by the gate/up product: I = 576, 1 row 7.3 / 7.9, 10.4 / 10.7, 4 rows 8.5 / 9.3, 10.7 / 11.3; I = 2048, 1 row
+// 8.4 / 9.3, 10.6 / 11.3, 2 rows 9.5 / 10.3, 10.6 / 11.3, 4 rows 12.1 / 12.8, 11.2 / 11.9; I = 4096, 1 row 12.0 / 12.3, 11.9 / 12.6.
+// H = 1024, I = 1056, 3 rows 7.8 / 8.0, 7.0 / 7.2.  What the codes cost grows with T I, what they save with H.
+static int ffn_h_rows(int H, int I) { return H / I < 16 ? H / I : 16; }
+
+// Enough for fewer rows too.
 size_t fp4_ffn_ws_bytes(int T, int H, int I, bool fp4mid) {
-  (void)H;
-  return a256((size_t)T * (fp4mid ? I / 2 : I)) + a256((size_t)T * (I / 32));
+  const size_t codes = a256((size_t)T * (fp4mid ? I / 2 : I)) + a256((size_t)T * (I / 32));
+  const int rows = T < ffn_h_rows(H, I) ? T : ffn_h_rows(H, I);
+  const size_t h = a256((size_t)rows * 2 * I * 4);
+  return codes > h ? codes : h;
+}
+
+template <bool FP4A> static void launch_down_rows(const TileArgs& t, const float* h, hipStream_t stream) {
+  const uint32_t lds = rows_lds(t.M, t.K, FP4A);
+  const int64_t n = tiles_of(t.M, t.N, 16, 16);
+  if (n <= 256) hipLaunchKernelGGL((fp4_down_rows_kernel<FP4A, 1>), dim3((unsigned)n), dim3(64 * ROWS_WAVES), lds, stream, t, h);
+  else hipLaunchKernelGGL((fp4_down_rows_kernel<FP4A, 4>), dim3((unsigned)((t.N + 63) / 64)), dim3(64 * ROWS_WAVES), lds, stream, t, h);
 }
 
 hipError_t launch_fp4_ffn(const uint8_t* x, const uint8_t* x_sc, bool fp4x, int T, int H, const uint8_t* w13,
                           const uint8_t* w13_sc, const uint8_t* w2, const uint8_t* w2_sc, int I, bool fp4mid, void* y,
                           bool bf16_out, void* ws, hipStream_t stream, const char** variant) {
+  if (T <= ffn_h_rows(H, I)) {
+    float* const h = static_cast<float*>(ws);
+    const hipError_t e = launch_fp4_gemm(x, x_sc, fp4x, w13, w13_sc, T, 2 * I, H, h, false, stream, variant);
+    if (e != hipSuccess) return e;
+    const TileArgs t{nullptr, nullptr, w2, w2_sc, T, H, I, y, bf16_out, nullptr, nullptr, false};
+    if (fp4mid) launch_down_rows<true>(t, h, stream);
+    else launch_down_rows<false>(t, h, stream);
+    *variant = "fp4_ffn:h+";
+    return hipGetLastError();
+  }
   uint8_t* q = static_cast<uint8_t*>(ws);
   uint8_t* q_sc = q + a256((size_t)T * (fp4mid ? I / 2 : I));
   const TileArgs t{x, x_sc, w13, w13_sc, T, I, H, nullptr, false, q, q_sc, fp4mid};

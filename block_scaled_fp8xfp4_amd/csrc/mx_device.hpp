@@ -362,4 +362,30 @@ __device__ __forceinline__ bool codes_near(const float* v, uint32_t sc, uint32_t
   return diff == 0;
 }
 
+// Codes of silu(g) * u of this lane's 8 columns of a block (a quad of lanes): from fp32 values where those decide them in
+// the whole wavefront, else in double.  Returns the block's scale.
+template <bool FP4> __device__ __forceinline__ uint32_t swiglu_codes8(const float* g, const float* u, uint32_t* d) {
+  float a[8], amax = 0.0f, gmin = g[0];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    a[j] = swiglu_near(g[j], u[j]);
+    amax = fmaxf(amax, __builtin_fabsf(a[j]));
+    gmin = fminf(gmin, g[j]);
+  }
+  amax = quad_max(amax);
+  uint32_t s = e8m0_code_for_amax(amax, FP4 ? 2 : 8);
+  const bool sure = gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 8>(a, s, d);
+  if (!__all(sure)) {
+    amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = swiglu(g[j], u[j]);
+      amax = fmaxf(amax, __builtin_fabsf(a[j]));
+    }
+    s = e8m0_code_for_amax(quad_max(amax), FP4 ? 2 : 8);
+    codes_scaled<FP4, 8>(a, __builtin_ldexpf(1.0f, 127 - (int)s), d);
+  }
+  return s;
+}
+
 }  // namespace mx

@@ -131,26 +131,11 @@ __global__ __launch_bounds__(256) void swiglu_quantize_kernel(const void* __rest
   float g[8], u[8];
   load8(gu, BF16, t * ld + i, g);
   load8(gu, BF16, t * ld + I + i, u);
-  float a[8], amax = 0.0f, gmin = g[0];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    a[j] = swiglu_near(g[j], u[j]);
-    amax = fmaxf(amax, __builtin_fabsf(a[j]));
-    gmin = fminf(gmin, g[j]);
-  }
-  amax = quad_max(amax);
-  const uint32_t s = e8m0_code_for_amax(amax, FP4 ? 2 : 8);
   uint32_t d[2];
-  const bool sure = gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 8>(a, s, d);
-  if (__all(sure)) {
-    if (FP4) *reinterpret_cast<uint32_t*>(q + c * 4) = d[0];
-    else *reinterpret_cast<uint2*>(q + c * 8) = uint2{d[0], d[1]};
-    if ((c & 3) == 0) sc[c >> 2] = (uint8_t)s;
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) g[j] = swiglu(g[j], u[j]);
-  store8_codes<FP4>(g, q, sc, c);
+  const uint32_t s = swiglu_codes8<FP4>(g, u, d);
+  if (FP4) *reinterpret_cast<uint32_t*>(q + c * 4) = d[0];
+  else *reinterpret_cast<uint2*>(q + c * 8) = uint2{d[0], d[1]};
+  if ((c & 3) == 0) sc[c >> 2] = (uint8_t)s;
 }
 
 hipError_t launch_swiglu_quantize(const void* gu, bool bf16, int64_t ld, int64_t T, int I, bool fp4, uint8_t* q,

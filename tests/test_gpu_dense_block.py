@@ -347,7 +347,7 @@ def test_fp4_block_gemm_tiles_at_every_end_of_K(M, N, a_fmt):
 # -------------------------------------------------------------- dense FFN
 FFN_SIZES = [(1, 4096, 576), (1, 256, 64), (1, 128, 2048), (2, 32, 32), (3, 160, 96), (16, 512, 256), (17, 1056, 544),
              (48, 4096, 576), (100, 288, 1376), (129, 512, 160), (300, 640, 736), (600, 256, 512), (1, 16384, 32),
-             (5, 96, 16384)]
+             (5, 96, 16384), (7, 4096, 576), (2, 4096, 2048), (16, 4096, 160), (4, 8224, 2016)]
 
 
 @pytest.mark.parametrize("x_fmt,mid_fmt", [(E4M3, E4M3), (E2M1, E2M1), (E4M3, E2M1), (E2M1, E4M3)])
@@ -373,7 +373,8 @@ def test_fp4_dense_ffn_is_its_three_steps(T, H, I, x_fmt, mid_fmt):
 
 
 @pytest.mark.parametrize("fmt", [E4M3, E2M1])
-@pytest.mark.parametrize("T,H,I", [(5, 256, 96), (40, 256, 96), (40, 128, 4128), (600, 128, 1056), (1100, 160, 2080), (1500, 128, 2080), (2040, 544, 4064), (2100, 256, 4128)])
+@pytest.mark.parametrize("T,H,I", [(5, 256, 96), (40, 256, 96), (40, 128, 4128), (600, 128, 1056), (1100, 160, 2080), (1500, 128, 2080), (2040, 544, 4064), (2100, 256, 4128),
+                                   (8, 2048, 256), (16, 4096, 96), (3, 6240, 2080)])
 def test_fp4_dense_ffn_blocks_that_need_double(T, H, I, fmt):
     """Gates far below zero and products next to fp32's ends, whose codes fp32 does not decide, zero rows and gates whose
     SwiGLU vanishes, in every kernel of the gate/up product: the codes of mx_swiglu_quantize on the product's own result."""
