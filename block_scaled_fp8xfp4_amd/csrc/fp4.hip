@@ -1107,8 +1107,9 @@ static size_t a256(size_t b) { return (b + 255) / 256 * 256; }
 // Gate/up of few rows: one workgroup per 16 rows and block of 32 intermediate
 // columns; its four wavefronts take 16 gate or 16 up columns each, meet in
 // LDS, and 16 lanes per row make the block's codes, two neighbouring columns
-// a lane.  One row at H = 4096, I = 2048 takes 6.7 us: 64 workgroups are all
-// there is to spread, and a CU reads its 136 KB of weights in about 4 us.
+// a lane.  16 rows at H = 4096, I = 2048 take about 8.5 (E2M1) and 9.5 us: 64
+// workgroups are all there is to spread, and a CU reads its 136 KB of weights
+// in about 4 us.
 template <bool FP4A>
 __global__ __launch_bounds__(256, 2) void fp4_gate_up_rows_kernel(TileArgs A) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
