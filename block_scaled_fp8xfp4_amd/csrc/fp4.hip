@@ -55,7 +55,6 @@ __device__ __forceinline__ void store_rows(const TileArgs& A, const v4f& acc, in
 // to registers.  Lane l serves row / column l % 16; lanes past M or N repeat
 // the last row / column, their results are not stored.  K past the last whole
 // piece is read with clamped addresses and zeroed, its scales are 127.
-
 template <bool FP4A> struct LonePiece { u32x4 w[4], alo[4], ahi[FP4A ? 1 : 4], ws, as; };
 
 template <bool FP4A>
@@ -147,7 +146,6 @@ __device__ __forceinline__ v4f lone_tile(const uint8_t* ap, const uint8_t* asp, 
   if (K % RPK) acc = lone_multiply(T, acc, g);
   return acc;
 }
-
 template <bool FP4A>
 __global__ __launch_bounds__(64, 2) void fp4_lone_kernel(TileArgs A) {
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
