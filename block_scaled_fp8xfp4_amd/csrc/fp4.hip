@@ -442,8 +442,8 @@ constexpr int XCDS = 8;
 constexpr int SCK = 512;                          // K whose scales (16 bytes a row) are fetched at a time
 
 // WM x WN wavefronts of TM x TN 32 x 32 tiles each.  ODD: K % 128 != 0, rows
-// of scales start at any byte (small tiles; larger ones take the scales of
-// such K through registers, at a wait for all of memory per 512 of K).
+// of scales start at any byte (where LDS has the room; else such scales go
+// through registers, at a wait for all of memory per 512 of K).
 template <bool FP4A, bool ODD, int WM, int WN, int TM, int TN, int KS, int NST>
 struct TileShape {
   static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
@@ -510,7 +510,6 @@ __device__ __forceinline__ void tile_codes(const v16f& gate, const v16f& up, int
 template <bool FP4A, bool SWIGLU, bool ODD, int WM, int WN, int TM, int TN, int KS, int NST>
 __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
   using S = TileShape<FP4A, ODD, WM, WN, TM, TN, KS, NST>;
-  static_assert(S::WHOLE || !ODD, "ODD: small tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -636,12 +635,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
       else R.xhi[FP4A ? 0 : i] = lds_read<u32x4>(xa[2 * ks + 1] + buf + i * 32 * S::RA);
     }
   };
+  Scales off = {};                                                  // ODD: where rows of scales start in their dword
+  if (ODD) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) off.x[i] = (uint32_t)(uintptr_t)(A.x_sc + (m0 + min((int)xrow + i * 32, mlast)) * nblk) & 3;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) off.w[i] = (uint32_t)(uintptr_t)(A.w_sc + (n0 + wsrc(wrow + i * 32)) * nblk) & 3;
+  }
+  const uint32_t fifth = lds0 + S::OFF_S + S::NSC * S::NW * 1024;     // ODD: the fifth dwords
   auto load_pairs = [&](Pairs& H, int k256) {                         // of K = 256 k256 + [0, 256)
-    const uint32_t off = ((k256 >> 1) & 1) * S::SCALES + (k256 & 1) * 8;
+    const uint32_t at = ((k256 >> 1) & 1) * S::SCALES, d = (k256 & 1) * 8;
+    const bool whole = by_dma(k256 >> 1);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) H.x[i] = lds_read<u32x2>(sp + off + i * 32 * 16);
-#pragma unroll
-    for (int i = 0; i < TN; ++i) H.w[i] = lds_read<u32x2>(sw + off + i * 32 * 16);
+    for (int i = 0; i < TM + TN; ++i) {
+      const uint32_t row = (i < TM ? sp + i * 32 * 16 : sw + (i - TM) * 32 * 16) + at;
+      u32x2 v = lds_read<u32x2>(row + d);
+      if (ODD) {
+        const uint32_t o = whole ? (i < TM ? off.x[i < TM ? i : 0] : off.w[i < TM ? 0 : i - TM]) : 0;
+        const uint32_t n = i < TM ? xrow + i * 32 : S::BM + wrow + (i - TM) * 32;
+        const uint32_t next = lds_read<uint32_t>(d ? fifth + at + n * 4 : row + 8);
+        v = u32x2{__builtin_amdgcn_alignbyte(v[1], v[0], o), __builtin_amdgcn_alignbyte(next, v[1], o)};
+      }
+      if (i < TM) H.x[i < TM ? i : 0] = v;
+      else H.w[i < TM ? 0 : i - TM] = v;
+    }
   };
   auto second = [&](Pairs& H) {
 #pragma unroll
@@ -717,16 +734,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
     // Small tiles: a stage's operands are read from LDS in one go, while the stage before multiplies, so that the LDS
     // latency is met once per stage and not once per step.
     struct Stage { Regs r[S::STEPS]; Scales c[KS / 128]; };
-    Scales off = {};                                                  // ODD: where rows of scales start in their dword
-    if (ODD) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i) off.x[i] = (uint32_t)(uintptr_t)(A.x_sc + (m0 + min((int)xrow + i * 32, mlast)) * nblk) & 3;
-#pragma unroll
-      for (int i = 0; i < TN; ++i) off.w[i] = (uint32_t)(uintptr_t)(A.w_sc + (n0 + wsrc(wrow + i * 32)) * nblk) & 3;
-    }
     // The scales of 128 of K: dword d of the buffer at offset at; whole: the buffer was filled by DMA.
     auto load_scales = [&](Scales& C, uint32_t at, int d, bool whole) {
-      const uint32_t fifth = lds0 + S::OFF_S + S::NSC * S::NW * 1024 + at;
 #pragma unroll
       for (int i = 0; i < TM + TN; ++i) {
         const uint32_t row = (i < TM ? sp + i * 32 * 16 : sw + (i - TM) * 32 * 16) + at;
@@ -734,7 +743,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void fp4_tile_kernel(TileArgs A) {
         if (ODD) {
           const uint32_t o = i < TM ? off.x[i < TM ? i : 0] : off.w[i < TM ? 0 : i - TM];
           const uint32_t n = i < TM ? xrow + i * 32 : S::BM + wrow + (i - TM) * 32;
-          const uint32_t next = lds_read<uint32_t>(d < 3 ? row + d * 4 + 4 : fifth + n * 4);
+          const uint32_t next = lds_read<uint32_t>(d < 3 ? row + d * 4 + 4 : fifth + at + n * 4);
           v = __builtin_amdgcn_alignbyte(next, v, whole ? o : 0);
         }
         if (i < TM) C.x[i < TM ? i : 0] = v;
@@ -1019,7 +1028,9 @@ static void launch_tile_of(const TileArgs& a, hipStream_t stream) {
 }
 template <bool FP4A, bool SWIGLU, int WM, int WN, int TM, int TN, int KS, int NST>
 static void launch_tile(const TileArgs& a, hipStream_t stream) {
-  if constexpr (TileShape<FP4A, false, WM, WN, TM, TN, KS, NST>::WHOLE) {
+  using S = TileShape<FP4A, false, WM, WN, TM, TN, KS, NST>;
+  constexpr uint32_t CU = 160 * 1024;             // ODD where it leaves as many workgroups per CU
+  if constexpr (CU / (S::LDS + 2 * S::NSC * S::NW * 256) == CU / S::LDS) {
     if (a.K % 128 != 0) return launch_tile_of<FP4A, SWIGLU, true, WM, WN, TM, TN, KS, NST>(a, stream);
   }
   launch_tile_of<FP4A, SWIGLU, false, WM, WN, TM, TN, KS, NST>(a, stream);

@@ -555,7 +555,8 @@ def test_two_graphs_and_two_streams_at_once(T):
 
 
 @pytest.mark.parametrize("a_fmt", [E4M3, E2M1])
-@pytest.mark.parametrize("M,N,K", [(3, 48, 1056), (40, 2800, 1056), (300, 1040, 672)])
+@pytest.mark.parametrize("M,N,K", [(3, 48, 1056), (40, 2800, 1056), (300, 1040, 672), (1500, 1502, 1056), (2100, 2835, 1184),
+                                   (2830, 2835, 1056)])
 def test_fp4_block_gemm_scales_at_every_byte(M, N, K, a_fmt):
     """K % 128 != 0: scales that start at any byte, neighbours of other values around them."""
     rng = np.random.default_rng(M)
