@@ -473,12 +473,13 @@ __device__ __forceinline__ void tile_codes(const v16f& gate, const v16f& up, int
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     a[r] = swiglu_near(gate[r], up[r]);
-    amax = fmaxf(amax, __builtin_fabsf(a[r]));
+    amax = near_max(amax, a[r]);
     gmin = fminf(gmin, gate[r]);
   }
+  const bool whole = amax == amax;
   amax = fmaxf(amax, __shfl_xor(amax, 32));
   uint32_t s = e8m0_code_for_amax(amax, FP4 ? 2 : 8), d[4];
-  const bool sure = gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 16>(a, s, d);
+  const bool sure = whole && gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 16>(a, s, d);
   if (!__all(sure || !ok)) {
     amax = 0.0f;
 #pragma unroll 1
@@ -1139,7 +1140,9 @@ __global__ __launch_bounds__(256, 2) void fp4_gate_up_rows_kernel(TileArgs A) {
   const float g0 = h[row][c >> 4][c & 15], g1 = h[row][c >> 4][(c & 15) + 1];
   const float u0 = h[row][2 + (c >> 4)][c & 15], u1 = h[row][2 + (c >> 4)][(c & 15) + 1];
   float a0 = swiglu_near(g0, u0), a1 = swiglu_near(g1, u1);
-  float amax = row16_max(fmaxf(__builtin_fabsf(a0), __builtin_fabsf(a1)));
+  float amax = near_max(__builtin_fabsf(a0), a1);
+  const bool whole = amax == amax;
+  amax = row16_max(amax);
   const int emax = A.fp4mid ? 2 : 8;
   uint32_t s = e8m0_code_for_amax(amax, emax), d;
   auto codes = [&](float f) -> uint32_t {
@@ -1149,7 +1152,7 @@ __global__ __launch_bounds__(256, 2) void fp4_gate_up_rows_kernel(TileArgs A) {
   };
   const float f = __builtin_ldexpf(1.0f, 127 - (int)s);
   d = codes(f * (1.0f - SWIGLU_EPS));
-  const bool sure = fminf(g0, g1) > SWIGLU_MIN_G && near_block(amax) && d == codes(f * (1.0f + SWIGLU_EPS));
+  const bool sure = whole && fminf(g0, g1) > SWIGLU_MIN_G && near_block(amax) && d == codes(f * (1.0f + SWIGLU_EPS));
   if (!__all(sure)) {
     a0 = swiglu(g0, u0);
     a1 = swiglu(g1, u1);

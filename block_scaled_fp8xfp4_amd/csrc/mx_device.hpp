@@ -342,9 +342,15 @@ __device__ __forceinline__ float swiglu_near(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, l * 0.693147181f, e)) * u;
 }
 
+// The larger of m and |a|, NaN if either is one (fmaxf would drop it): a near
+// value is NaN where its gate's exponent argument overflows (2.36e38 and up),
+// and such a block's codes are the double form's.
+__device__ __forceinline__ float near_max(float m, float a) { return __builtin_elementwise_maximum(m, __builtin_fabsf(a)); }
+
 // Whether a block whose largest near value is amax can be cast from near
 // values: in a range where fp32 keeps its precision (zero is not), and with
-// one exponent at both ends.
+// one exponent at both ends.  False for NaN, which a maximum over lanes may
+// drop again: each lane asks for its own near_max too.
 __device__ __forceinline__ bool near_block(float amax) {
   return amax >= 7.9e-31f && amax <= 1.3e36f &&                  // 2^-100, 2^120
          ((__float_as_uint(amax * (1.0f - SWIGLU_EPS)) ^ __float_as_uint(amax * (1.0f + SWIGLU_EPS))) >> 23) == 0;
@@ -369,12 +375,13 @@ template <bool FP4> __device__ __forceinline__ uint32_t swiglu_codes8(const floa
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     a[j] = swiglu_near(g[j], u[j]);
-    amax = fmaxf(amax, __builtin_fabsf(a[j]));
+    amax = near_max(amax, a[j]);
     gmin = fminf(gmin, g[j]);
   }
+  const bool whole = amax == amax;
   amax = quad_max(amax);
   uint32_t s = e8m0_code_for_amax(amax, FP4 ? 2 : 8);
-  const bool sure = gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 8>(a, s, d);
+  const bool sure = whole && gmin > SWIGLU_MIN_G && near_block(amax) && codes_near<FP4, 8>(a, s, d);
   if (!__all(sure)) {
     amax = 0.0f;
 #pragma unroll
