@@ -329,9 +329,15 @@ __device__ __forceinline__ void store8_codes(const float* v, uint8_t* q, uint8_t
 // wavefront takes the double form.
 //
 // Error of swiglu_near for g > -60: the exponent's argument is carried in two
-// floats, v_exp_f32 and v_rcp_f32 are within 1 ulp, four more roundings; over
-// every float g the worst relative error of silu(g) measured 2^-21.9, and the
-// product with u adds 2^-24: under half of 2^-20.
+// floats, v_exp_f32 and v_rcp_f32 are within 1 ulp, five more roundings, the
+// last two those of the products: under half of 2^-20 while the results of
+// both products are normal (worst over every float g, with ups of 1 and at
+// random, 2^-21.75).  The sigmoid is multiplied by u first: the
+// product is subnormal only where u is under 2^-39 at most, and then either
+// the sigmoid is 1 (g > 16.7) and the product exact, or the result is under
+// 2^-120, which every block that near_block accepts rounds to zero (its codes'
+// smallest border is 2^-118).  g / 2 in place of it would lose bits of a
+// subnormal g that a large u brings back.
 constexpr float SWIGLU_EPS = 9.5367431640625e-07f;               // 2^-20
 constexpr float SWIGLU_MIN_G = -60.0f;                           // below: 1 / (1 + e^-g) loses bits to small numbers
 
@@ -339,7 +345,7 @@ __device__ __forceinline__ float swiglu_near(float g, float u) {
   const float h = g * -1.44269504f;                              // -g log2 e = h + l
   const float l = __builtin_fmaf(g, -1.44269504f, -h) - g * 1.92596303e-8f;
   const float e = __builtin_amdgcn_exp2f(h);
-  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, l * 0.693147181f, e)) * u;
+  return g * (__builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, l * 0.693147181f, e)) * u);
 }
 
 // The larger of m and |a|, NaN if either is one (fmaxf would drop it): a near

@@ -3,8 +3,8 @@ gate/up products of fp4_dense_ffn.
 
 Codes and scales are those of silu(gate) * up in 64 bits rounded once to fp32, bit for bit: no tolerance.  The kernels
 take them from a short fp32 evaluation where that decides them, so these inputs sit where fp32 leaves its range inside the
-evaluation: gates near the type's largest value (gate * log2 e overflows from 2.36e38 on), with ups that bring the product
-back to the size of ordinary neighbours."""
+evaluation: gates near the type's largest value (gate * log2 e overflows from 2.36e38 on) and under its smallest normal value
+(half of them loses bits), with ups that bring the product back to the size of ordinary neighbours."""
 import numpy as np
 import pytest
 import torch
@@ -52,6 +52,20 @@ def test_gates_near_the_largest_value(dtype, fmt):
 
 
 @pytest.mark.parametrize("fmt", [E4M3, E2M1])
+def test_gates_under_the_smallest_normal_value(fmt):
+    """Blocks of gates of a few units of 2^-149, and up to 2^-120, that large ups bring back."""
+    rng = np.random.default_rng(4)
+    g = (rng.integers(1, 16, (40, 32)) * 2.0 ** -149).astype(np.float32)
+    g[20:] = (rng.standard_normal((20, 32)) * 2.0 ** rng.integers(-140, -119, (20, 1))).astype(np.float32)
+    u = (rng.choice([-1.0, 1.0], (40, 32)) * rng.uniform(1, 2, (40, 32)) * 2.0 ** rng.integers(118, 124, (40, 32))).astype(np.float32)
+    gu = np.concatenate([g, u], -1)
+    q, sc = cast(to_dev(gu), fmt)
+    rq, rs = ref.quantize(ref.swiglu(gu), fmt)
+    same_bits(sc, rs, "scales")
+    same_bits(q, rq, "codes")
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E2M1])
 def test_a_row_alone_and_beside_one_that_needs_double(fmt):
     """A row with huge gates has the same codes alone and beside a row of gates far below zero, which sends the
     wavefront that both share to the evaluation in double."""
@@ -70,12 +84,12 @@ FFN_SIZES = [(1, 256, 64), (5, 256, 96), (40, 256, 96), (40, 128, 4128), (600, 1
              (1500, 128, 2080), (2040, 544, 4064), (2100, 256, 4128), (8, 2048, 256)]
 
 
-def check_ffn(T, H, I, fmt, scales, last_scale):
+def check_ffn(T, H, I, fmt, scales, last_scale, alone=False):
     """The FFN of rows with far columns (two or three in each block of the intermediate) among ordinary ones against the
     64-bit cast of its gate/up values and the product of that.  The far columns read one element of a row each: the first
     of its first block for the gate, of its second for the up; the ordinary columns read the row's other blocks.
     scales: exponents of the first block of the rows, and of the far gates (even, odd) and ups; last_scale: of the first
-    block of the last row.  Returns the gate/up values."""
+    block of the last row, whose ordinary columns are zeros with alone.  Returns the gate/up values."""
     rng = np.random.default_rng(T + I)
     half, one = (32, 0x38) if fmt == E4M3 else (16, 2)                 # bytes of a block, the code of 1.0
     x, x_sc = ref.quantize(ref.activations(rng, T, H), fmt)
@@ -83,6 +97,8 @@ def check_ffn(T, H, I, fmt, scales, last_scale):
     row, even, odd, up = scales
     x[:, :2 * half] = 0
     x[:, 0] = x[:, half] = one
+    if alone:
+        x[T - 1, 2 * half:] = 0
     x_sc[:, 0], x_sc[:, 1], x_sc[T - 1, 0] = 127 + row, 127, 127 + last_scale
     w13[:, :32] = 0
     far = np.arange(0, I, 11)
@@ -142,3 +158,19 @@ def test_every_normal_gate(fmt):
     """From 2^-120 to the largest float, and to -60 (below, the kernels use the double form)."""
     every_gate(fmt, 0, 0x03800000, 0x7F800000)
     every_gate(fmt, 1, 0x03800000, 0x42700000)
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E2M1])
+@pytest.mark.parametrize("T,H,I", FFN_SIZES)
+def test_ffn_gates_under_the_smallest_normal_value(T, H, I, fmt):
+    """A last row of gates of 3 and 6 units of 2^-149 alone, with ups of 1.5 * 2^120, in every kernel of the gate/up product:
+    half of 3 units is no float."""
+    v = check_ffn(T, H, I, fmt, (63, -76, -75, 120), -72, alone=True)
+    assert v[T - 1, 0] == np.float32(3 * 2.0 ** -149) and v[T - 1, I] == np.float32(1.5 * 2.0 ** 120)
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E2M1])
+def test_every_subnormal_gate(fmt):
+    """To 2^-120, both signs."""
+    every_gate(fmt, 0, 0, 0x03800000)
+    every_gate(fmt, 1, 0, 0x03800000)
