@@ -1,6 +1,8 @@
 """Device-side convenience wrapper around the C-ABI: uploads and quantizes a
 MoE layer on the GPU (with the library's own quantizer kernel) and owns the
 route / FFN workspaces.  Every computation is a libmxmoe.so call."""
+import contextlib
+
 import numpy as np
 import torch
 
@@ -97,8 +99,19 @@ class ExpertFFN:
         return q, sc, o
 
 
+def _under(stream):
+    """The context of a helper that makes tensors and launches on stream (a raw handle; None: torch's current stream, 0: the
+    default one).  What it makes then belongs to that stream, as under torch.cuda.stream: memory that the allocator hands
+    out or takes back is not in use by work elsewhere, and a copy is ordered before the kernel that reads it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    d = torch.cuda.current_device()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=d) if stream else torch.cuda.default_stream(d))
+
+
 class AddNorm:
-    """Residual addition + root-mean-square norm (mx_add_rmsnorm) with a weight [H]."""
+    """Residual addition + root-mean-square norm (mx_add_rmsnorm) with a weight [H].  A residual whose rows lie apart is
+    copied first, since h shares its layout."""
 
     def __init__(self, weight, eps=1e-6):
         self.weight, self.eps = weight, eps
@@ -107,19 +120,20 @@ class AddNorm:
         """(h, ...) with the codes and scales of the normed rows when fmt is given, then with the rows themselves in
         bf16 when hidden is set.  h is the new residual stream, in the residual's type (x's without one)."""
         T, H = x.shape
-        h = torch.empty((T, H), dtype=x.dtype if residual is None else residual.dtype, device=x.device)
-        if residual is not None and T > 1 and residual.stride(0) != H:
-            residual = residual.contiguous()
-        out, q, sc, n = [h], None, None, None
-        if fmt is not None:
-            q = torch.empty((T, H if fmt == mxmoe.MX_FMT_E4M3 else H // 2), dtype=torch.uint8, device=x.device)
-            sc = torch.empty((T, H // 32), dtype=torch.uint8, device=x.device)
-            out += [q, sc]
-        if hidden:
-            n = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-            out.append(n)
-        mxmoe.mx_add_rmsnorm(x, self.weight, self.eps, residual, x2, h, n, q, sc,
-                             mxmoe.MX_FMT_E4M3 if fmt is None else fmt, stream)
+        with _under(stream):
+            h = torch.empty((T, H), dtype=x.dtype if residual is None else residual.dtype, device=x.device)
+            if residual is not None and T > 1 and residual.stride(0) != H:
+                residual = residual.contiguous()
+            out, q, sc, n = [h], None, None, None
+            if fmt is not None:
+                q = torch.empty((T, H if fmt == mxmoe.MX_FMT_E4M3 else H // 2), dtype=torch.uint8, device=x.device)
+                sc = torch.empty((T, H // 32), dtype=torch.uint8, device=x.device)
+                out += [q, sc]
+            if hidden:
+                n = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+                out.append(n)
+            mxmoe.mx_add_rmsnorm(x, self.weight, self.eps, residual, x2, h, n, q, sc,
+                                 mxmoe.MX_FMT_E4M3 if fmt is None else fmt, stream)
         return tuple(out)
 
 
@@ -130,14 +144,16 @@ class FP4Linear:
         self.w, self.w_sc = w, w_sc
 
     def __call__(self, a, a_sc, a_fmt, dtype=torch.bfloat16, stream=None):
-        y = torch.empty((a.shape[0], self.w.shape[0]), dtype=dtype, device=a.device)
-        mxmoe.fp4_block_gemm(a, a_sc, a_fmt, self.w, self.w_sc, y, stream)
+        with _under(stream):
+            y = torch.empty((a.shape[0], self.w.shape[0]), dtype=dtype, device=a.device)
+            mxmoe.fp4_block_gemm(a, a_sc, a_fmt, self.w, self.w_sc, y, stream)
         return y
 
 
 class DenseFFN:
     """A dense SwiGLU FFN with MXFP4 weights (fp4_dense_ffn); owns the workspace of up to T rows, which its calls and the
-    graphs captured of them share: they must not overlap."""
+    graphs captured of them share: they must not overlap, and a call on another stream than the one that made the object
+    comes after that stream's work, the object's end after the call's."""
 
     def __init__(self, w13, w13_sc, w2, w2_sc, T, mid_fmt=mxmoe.MX_FMT_E4M3):
         self.weights, self.T, self.mid_fmt = (w13, w13_sc, w2, w2_sc), T, mid_fmt
@@ -148,6 +164,7 @@ class DenseFFN:
     def __call__(self, x, x_sc, x_fmt, dtype=torch.bfloat16, stream=None):
         if x.shape[0] > self.T:
             raise ValueError("DenseFFN: more rows than sized for")
-        y = torch.empty((x.shape[0], self.H), dtype=dtype, device=x.device)
-        mxmoe.fp4_dense_ffn(x, x_sc, x_fmt, *self.weights, self.mid_fmt, y, self.ws, stream)
+        with _under(stream):
+            y = torch.empty((x.shape[0], self.H), dtype=dtype, device=x.device)
+            mxmoe.fp4_dense_ffn(x, x_sc, x_fmt, *self.weights, self.mid_fmt, y, self.ws, stream)
         return y
