@@ -43,30 +43,41 @@ def log(msg):
     print(f"[bench] {msg}", file=sys.stderr, flush=True)
 
 
-def kernel_sources_hash():
-    """Hash of the library's code: every file under csrc/ with its comments
-    removed and its whitespace collapsed, so that a comment-only edit keeps
-    the profiles taken on the same code valid."""
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "block_scaled_fp8xfp4_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
+CSRC = os.path.join(ROOT, "block_scaled_fp8xfp4_amd", "csrc")
+
+
+def kernel_sources_hash(unit, csrc=CSRC):
+    """Hash of the code that the translation unit csrc/<unit> is built from:
+    the file and the headers of csrc/ that it includes, with their comments
+    removed and their whitespace collapsed, so that neither a comment nor a
+    kernel of another unit takes the profiles of this one away."""
+    texts, left = {}, [unit]
+    while left:
+        name = left.pop()
+        if name in texts or not os.path.isfile(os.path.join(csrc, name)):
+            continue                              # seen, or a header from elsewhere
         with open(os.path.join(csrc, name)) as f:
             text = f.read()
         text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
         text = re.sub(r"//[^\n]*", " ", text)
-        h.update(name.encode() + " ".join(text.split()).encode())
+        left += re.findall(r'#\s*include\s*"([^"]+)"', text)
+        texts[name] = " ".join(text.split())
+    h = hashlib.sha256()
+    for name in sorted(texts):
+        h.update(name.encode() + texts[name].encode())
     return h.hexdigest()[:16]
 
 
 def recorded_traffic(workload):
     """HBM bytes per launch of the dominant kernel from the committed rocprofv3
-    counter summary, if it was taken on the current kernel sources."""
+    counter summary, if it was taken on the current sources of that kernel."""
     path = os.path.join(ROOT, "profiles", f"traffic_{workload}.json")
     if not os.path.exists(path):
         return None
     with open(path) as f:
         rec = json.load(f)
-    if rec.get("kernel_sources_sha") != kernel_sources_hash():
+    unit = rec.get("translation_unit")
+    if unit is None or rec.get("kernel_sources_sha") != kernel_sources_hash(unit):
         return None
     return rec.get("hbm_bytes_per_launch")
 

@@ -18,7 +18,7 @@
 // and one more, and rounded to nearest even once per 64 of K.  E2M1 x E2M1
 // products fit those bits.  The cut is the instruction's; the routed experts'
 // products have it too.
-#include "mx_device.hpp"
+#include "mx_cast.hpp"
 #include "mx_launch.hpp"
 
 namespace mx {

@@ -18,7 +18,7 @@
 //
 // 8192 x 4096 bf16 with residual, to h and E4M3 codes: 50 us (303 MB, 6.0 TB/s, bound by memory); 48 x 5120 4.4 us, one
 // row of 4096 4.0 us (a launch, one round to memory, one reduction).
-#include "mx_device.hpp"
+#include "mx_cast.hpp"
 #include "mx_launch.hpp"
 
 namespace mx {

@@ -4,7 +4,7 @@
 // conversion rule is OCP MX v1.0's).  One thread per block of 32: a thread
 // reads 64-128 contiguous bytes and its neighbours the next ones, so a wave
 // streams a contiguous span of the row-major source.
-#include "mx_device.hpp"
+#include "mx_cast.hpp"
 #include "mx_launch.hpp"
 
 namespace mx {
