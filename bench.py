@@ -82,6 +82,55 @@ def recorded_traffic(workload):
     return rec.get("hbm_bytes_per_launch")
 
 
+def dense_block_calls(times):
+    """Each call of the dense block that its kernel profile lists, `times` times, on random data."""
+    import torch
+    from block_scaled_fp8xfp4_amd import mxmoe
+    from block_scaled_fp8xfp4_amd.layer import quantize
+    torch.manual_seed(0)
+    bf16 = torch.bfloat16
+
+    def randn(*shape, dtype=bf16):
+        return torch.randn(shape, device="cuda", dtype=torch.float32).to(dtype)
+
+    def empty(*shape, dtype=bf16):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+    def codes(rows, cols, fmt):
+        return quantize(torch.randn((rows, cols), device="cuda") * 0.05, fmt)
+
+    def repeat(name, call):
+        for _ in range(times):
+            call()
+        torch.cuda.synchronize()
+        log(f"{name}: {mxmoe.last_variant()}")
+
+    e4m3, e2m1 = mxmoe.MX_FMT_E4M3, mxmoe.MX_FMT_E2M1
+    for T, H, hidden in ((1, 4096, False), (48, 5120, False), (8192, 4096, False), (8192, 4096, True)):
+        x, r, w, h = randn(T, H), randn(T, H), torch.ones(H, dtype=bf16, device="cuda"), empty(T, H)
+        n = empty(T, H) if hidden else None
+        q, sc = codes(T, H, e4m3)
+        repeat(f"norm {T} x {H}{' with n' if hidden else ''}",
+               lambda: mxmoe.mx_add_rmsnorm(x, w, 1e-6, residual=r, h=h, n=n, q=q, sc=sc, fmt=e4m3))
+    for fmt in (e4m3, e2m1):
+        gu, values = randn(8192, 8192), empty(8192, 4096)
+        q, sc = codes(8192, 4096, fmt)
+        repeat(f"SwiGLU 8192 x 4096 to {fmt}", lambda: mxmoe.mx_swiglu_quantize(gu, q, sc, fmt))
+        repeat(f"dequantize 8192 x 4096 of {fmt}", lambda: mxmoe.mx_dequantize(q, sc, fmt, values))
+    for M, N, K in ((1, 4096, 4096), (48, 4096, 4096), (333, 4100, 4128), (512, 4096, 4096), (2048, 4096, 8192),
+                    (8192, 4096, 4096)):
+        for fmt in (e4m3, e2m1):
+            a, w, y = codes(M, K, fmt), codes(N, K, e2m1), empty(M, N)
+            repeat(f"product {M} x {N} x {K} of {fmt}", lambda: mxmoe.fp4_block_gemm(*a, fmt, *w, y))
+    for T, H, I in ((1, 4096, 576), (1, 4096, 2048), (48, 4096, 576), (48, 4096, 2048), (2048, 4096, 8192)):
+        for fmt in (e4m3, e2m1):
+            a, w13, w2, y = codes(T, H, fmt), codes(2 * I, H, e2m1), codes(H, I, e2m1), empty(T, H)
+            ws = empty(mxmoe.fp4_dense_ffn_workspace_bytes(T, H, I, fmt), dtype=torch.uint8)
+            repeat(f"FFN {T} x {H}, I = {I} of {fmt}",
+                   lambda: mxmoe.fp4_dense_ffn(*a, fmt, *w13, *w2, fmt, y, ws))
+    print(json.dumps({"dense_block_calls": times}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -103,7 +152,12 @@ def main():
                     help="decode step: prefetch the dense projection's weights on a side stream from the step's start")
     ap.add_argument("--copy-calibration", action="store_true",
                     help="only copy a 256 MiB buffer 5 times (reference kernel for the HBM byte counters)")
+    ap.add_argument("--dense-block-calls", type=int, default=0, metavar="N",
+                    help="only make each call of the dense block N times (for its kernel profile)")
     args = ap.parse_args()
+    if args.dense_block_calls > 0:
+        dense_block_calls(args.dense_block_calls)
+        return
     if args.copy_calibration:
         import torch
         src = torch.empty(256 << 20, dtype=torch.uint8, device="cuda").fill_(1)
