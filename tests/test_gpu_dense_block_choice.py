@@ -1,0 +1,40 @@
+"""Which form the dense FFN of few rows takes, by T, H and I: the gate/up values in fp32, or their codes from the gate/up
+product.  Both give the bits of the three steps."""
+import numpy as np
+import pytest
+import torch
+
+import dense_block_ref as ref
+from block_scaled_fp8xfp4_amd import mxmoe
+from dense_block_ref import E2M1, E4M3, codes_like, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E2M1])
+@pytest.mark.parametrize("T,H,I,values", [(1, 8192, 4096, True), (2, 8192, 4096, True), (1, 4096, 2048, True), (4, 4096, 2048, False),
+                                          (1, 8192, 4128, False), (1, 8192, 8192, False), (2, 16384, 8192, False),
+                                          (1, 4128, 4128, False)])
+def test_few_rows(T, H, I, values, fmt):
+    """Past I = 4096 the form with fp32 values is 2 to 7 us slower whatever H is."""
+    rng = np.random.default_rng(I)
+    x, x_sc = (to_dev(t) for t in ref.quantize(ref.activations(rng, T, H), fmt))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(I)
+
+    def weights(rows, cols):
+        q, sc = codes_like(rows, cols, E2M1)
+        mxmoe.mx_quantize(torch.randn((rows, cols), generator=g, device="cuda") * 0.02, q, sc, E2M1)
+        return q, sc
+
+    w13, w2 = weights(2 * I, H), weights(H, I)
+    gu = torch.empty((T, 2 * I), dtype=torch.float32, device="cuda")
+    mxmoe.fp4_block_gemm(x, x_sc, fmt, *w13, gu)
+    q, sc = codes_like(T, I, fmt)
+    mxmoe.mx_swiglu_quantize(gu, q, sc, fmt)
+    want, y = (torch.empty((T, H), dtype=torch.float32, device="cuda") for _ in range(2))
+    mxmoe.fp4_block_gemm(q, sc, fmt, *w2, want)
+    ws = torch.empty(max(256, mxmoe.fp4_dense_ffn_workspace_bytes(T, H, I, fmt)), dtype=torch.uint8, device="cuda")
+    mxmoe.fp4_dense_ffn(x, x_sc, fmt, *w13, *w2, fmt, y, ws)
+    assert torch.equal(y, want)
+    assert (mxmoe.last_variant() == "fp4_ffn:h+") == values, mxmoe.last_variant()
