@@ -1050,14 +1050,25 @@ template <bool FP4A, int CW> static void launch_rows_of(const TileArgs& t, hipSt
   const dim3 grid((unsigned)(tiles_of(t.M, t.N, 16, 16 * CW)));       // CW = 4 past 512: fewer than 2^24
   hipLaunchKernelGGL((fp4_rows_kernel<FP4A, CW>), grid, dim3(64 * ROWS_WAVES), rows_lds(t.M, t.K, FP4A), stream, t);
 }
-// By how many wavefronts of 16 columns there are and by what a row is long.  Alone / through LDS at M = 1 and 16, us:
-//   E2M1 4096 x 576 2.7 / 3.1, 3.0 / 4.0; 4096 x 4096 4.2 / 4.4, 4.9 / 5.3; 4096 x 8192 6.8 / 6.4, 7.9 / 7.7;
-//        16384 x 4096 8.9 / 8.9, 12.3 / 10.2
-//   E4M3 4096 x 2048 3.4 / 3.7, 4.0 / 4.6; 4096 x 4096 4.8 / 4.5, 5.8 / 5.8; 4096 x 8192 8.2 / 6.8, 9.9 / 8.7;
-//        16384 x 4096 10.5 / 9.1, 15.8 / 11.1
+// Up to 16 rows by a wavefront alone: n wavefronts of 16 columns, at most one per CU and short rows; more of them where the
+// rows are very short, since what LDS saves grows with both; and rows that LDS does not hold, against tiles.  Alone / through
+// LDS (tiles where marked t) at M = 1 and 16, us, weights from memory:
+//   E2M1 4096 x 576 2.6 / 3.2, 2.9 / 4.2; 4096 x 4096 3.8 / 4.3, 4.7 / 5.3; 4096 x 8192 7.3 / 7.2, 8.3 / 8.0;
+//        8192 x 576 3.1 / 3.7, 3.3 / 4.5; 8192 x 1536 3.5 / 3.9, 4.0 / 5.0; 16384 x 576 3.5 / 4.1, 3.8 / 5.0;
+//        16384 x 1536 5.2 / 5.5, 5.8 / 6.3; 16384 x 4096 9.7 / 9.6, 12.3 / 10.6
+//   E4M3 4096 x 2048 3.3 / 3.5, 3.8 / 4.6; 4096 x 4096 4.7 / 4.5, 5.8 / 5.8; 4096 x 8192 8.9 / 7.0, 10.3 / 8.9;
+//        8192 x 576 3.3 / 3.7, 3.6 / 4.6; 8192 x 1536 3.6 / 3.8, 4.4 / 5.1; 16384 x 576 3.7 / 4.0, 4.4 / 5.1;
+//        16384 x 1536 5.2 / 5.3, 6.9 / 6.6; 16384 x 4096 10.5 / 9.9, 15.7 / 11.2
+//        32768 x 256 4.6 / 4.2, 6.2 / 5.3; M = 16: 4096 x 10240 12.9 / t 21.1, 4096 x 16384 18.7 / t 29.9, 8192 x 16384 27.5 / t 29.7,
+//        12288 x 16384 39.2 / t 23.8
+static bool alone(int M, int64_t n, int K, bool fp4a) {
+  if (M > 16) return false;
+  if (rows_lds(M, K, fp4a) > ROWS_LDS) return n <= 512;
+  return (n <= 256 && (fp4a ? K / 2 : K) <= 2048) || (n <= 1024 && K <= 1536 && n * K <= 1 << 20);
+}
 template <bool FP4A> static const char* launch_rows(const TileArgs& t, hipStream_t stream) {
   const int64_t n = tiles_of(t.M, t.N, 16, 16);
-  if (t.M <= 16 && n <= 256 && (FP4A ? t.K / 2 : t.K) <= 2048) {
+  if (alone(t.M, n, t.K, FP4A)) {
     hipLaunchKernelGGL(fp4_lone_kernel<FP4A>, dim3((unsigned)n), dim3(64), 0, stream, t);
     return FP4A ? "fp4:lone16_a4" : "fp4:lone16_a8";
   }
@@ -1084,7 +1095,9 @@ static Fp4Kernel pick_large(int M, int N) {
   return (t256 + 255) / 256 * 8 <= (t128 + 511) / 512 * 5 ? Fp4Kernel::t256x256 : Fp4Kernel::t128x128;
 }
 static Fp4Kernel pick_kernel(int M, int N, int K, bool fp4a) {
-  if (((M <= 16 || tiles_of(M, N, 16, 16) <= 512) && rows_lds(M, K, fp4a) <= ROWS_LDS) || K < 128) return Fp4Kernel::rows;                     // the tiles' scale reads need four blocks a row
+  const int64_t n = tiles_of(M, N, 16, 16);
+  if (((M <= 16 || n <= 512) && rows_lds(M, K, fp4a) <= ROWS_LDS) || alone(M, n, K, fp4a)) return Fp4Kernel::rows;
+  if (K < 128) return Fp4Kernel::rows;                                // the tiles' scale reads need four blocks a row
   if (tiles_of(M, N, 32, 64) <= 256) return Fp4Kernel::t32x64;        // one per CU
   if (tiles_of(M, N, 64, 64) <= 512) return Fp4Kernel::t64x64;        // two per CU
   return pick_large(M, N);

@@ -1,5 +1,5 @@
-"""Which form the dense FFN of few rows takes, by T, H and I: the gate/up values in fp32, or their codes from the gate/up
-product.  Both give the bits of the three steps."""
+"""Which kernel runs few rows, by their sizes: of a product, a wavefront alone, through LDS or tiles (the same bits); of the
+dense FFN, the gate/up values in fp32 or their codes from the gate/up product (the bits of the three steps)."""
 import numpy as np
 import pytest
 import torch
@@ -9,6 +9,35 @@ from block_scaled_fp8xfp4_amd import mxmoe
 from dense_block_ref import E2M1, E4M3, codes_like, to_dev
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,N,K,fmt,kernel", [
+    (1, 4096, 2048, E4M3, "lone16_a8"), (16, 4096, 4096, E2M1, "lone16_a4"), (16, 4096, 4096, E4M3, "rows16_a8"),
+    (16, 8192, 576, E4M3, "lone16_a8"), (16, 8192, 1536, E2M1, "lone16_a4"), (9, 16384, 576, E2M1, "lone16_a4"),
+    (4, 8192, 1568, E4M3, "rows16_a8"), (16, 16384, 1056, E2M1, "rows16_a4"), (16, 40000, 576, E2M1, "rows16_a4"), (16, 32768, 256, E4M3, "rows16_a8"),
+    (8, 4096, 16384, E4M3, "rows16_a8"), (9, 4096, 16384, E4M3, "lone16_a8"), (16, 2055, 10240, E4M3, "lone16_a8"),
+    (16, 8192, 16384, E4M3, "lone16_a8"), (16, 8208, 16384, E4M3, "tile"), (16, 4096, 16384, E2M1, "rows16_a4"),
+    (17, 4096, 16384, E4M3, "tile")])
+def test_product_of_few_rows(M, N, K, fmt, kernel):
+    """Short rows are taken by wavefronts alone, and so are rows that do not fit LDS (E4M3 of 9 and more rows at K = 16384;
+    as tiles 16 x 4096 x 16384 takes 30 us against 19)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+
+    def codes(rows, fmt):
+        q, sc = codes_like(rows, K, fmt)
+        mxmoe.mx_quantize(torch.randn((rows, K), generator=g, device="cuda") * 0.1, q, sc, fmt)
+        return q, sc
+
+    a, w = codes(M, fmt), codes(N, E2M1)
+    y = torch.full((M + 1, N), float("nan"), device="cuda")
+    mxmoe.fp4_block_gemm(*a, fmt, *w, y[:M])
+    v = mxmoe.last_variant()
+    assert v.startswith("fp4:" + kernel), v
+    many = torch.empty((600, N), device="cuda")                       # the same rows in tiles
+    mxmoe.fp4_block_gemm(*(t.repeat(-(-600 // M), 1)[:600].contiguous() for t in a), fmt, *w, many)
+    assert "tile" in mxmoe.last_variant()
+    assert torch.equal(y[:M], many[:M]) and torch.isnan(y[M]).all()
 
 
 @pytest.mark.parametrize("fmt", [E4M3, E2M1])
