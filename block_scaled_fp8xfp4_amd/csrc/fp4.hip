@@ -1226,20 +1226,26 @@ static const char* launch_gate_up(const TileArgs& t, hipStream_t stream) {
 // [codes of the intermediate][its scales]
 // Up to this many rows the gate/up values go to the down product in fp32: what the codes cost every workgroup grows with
 // T I, what spreading the gate/up product over all CUs saves with H.  The FFN in E2M1 / E4M3, us, weights from memory, so and
-// with the codes made by the gate/up product:
-//   H = 1024:  I = 576, 1 row 5.2 / 5.4, 6.2 / 6.4; I = 256, 4 rows 5.0 / 5.2, 6.7 / 6.9
-//   H = 2048:  I = 2048, 1 row 7.2 / 7.9, 7.9 / 8.3, 2 rows 8.2 / 8.9, 8.1 / 8.4
-//   H = 4096:  I = 576, 1 row 6.4 / 7.2, 9.7 / 10.2, 4 rows 7.9 / 8.5, 10.1 / 10.8, 16 rows 11.6 / 13.0, 11.1 / 12.0;
+// with the codes made by the gate/up product (the border's last rows in, first out):
+//   H = 512:   I = 96, 16 rows 4.9 / 5.2, 6.4 / 6.5; I = 576, 2 rows 4.9 / 5.1, 5.5 / 5.6, 3 rows 5.9 / 6.0, 5.6 / 5.9
+//   H = 1024:  I = 576, 4 rows 6.4 / 6.7, 6.7 / 7.0; I = 1056, 2 rows 6.5 / 6.8, 6.7 / 6.9, 3 rows 7.4 / 7.8, 6.9 / 7.1
+//   H = 2048:  I = 576, 4 rows 7.0 / 7.5, 7.7 / 8.0, 8 rows 7.9 / 8.3, 8.0 / 8.2; I = 2048, 1 row 7.2 / 7.9, 7.9 / 8.3, 2 rows
+//              8.2 / 8.9, 8.1 / 8.4
+//   H = 4096:  I = 576, 1 row 6.4 / 7.2, 9.7 / 10.2, 8 rows 8.8 / 9.8, 10.4 / 11.2, 16 rows 11.6 / 13.0, 11.1 / 12.0;
 //              I = 2048, 1 row 8.7 / 9.2, 10.7 / 11.7, 2 rows 9.8 / 10.3, 11.0 / 11.6, 4 rows 12.3 / 13.1, 11.4 / 12.1;
 //              I = 4096, 1 row 12.5 / 13.1, 12.8 / 13.5
-//   H = 8192:  I = 2048, 4 rows 14.7 / 15.3, 17.3 / 17.8; I = 4096, 1 row 20.7 / 21.0, 20.0 / 20.3, 2 rows 22.3 / 22.9,
-//              20.6 / 21.4
-//   H = 16384: I = 4096, 4 rows 35.4 / 36.2, 35.7 / 37.1
-// The border is on the safe side of the crossing but for H of about 8192 with I next to 4096 (up to 1.7 us lost) and misses
-// up to 4.9 us (H = 8192, I = 576, 16 rows).  Past I = 4096 the gate/up product has more than 512 column tiles, which
-// launch_rows takes four to a workgroup: half of the CUs idle, 2 to 7 us lost (H = 8192, 1 row: I = 4608 25.5 / 25.6 against
-// 20.9 / 21.3, I = 8192 35.9 / 36.2 against 30.1 / 30.4).
-static int ffn_h_rows(int H, int I) { return I > 4096 ? 0 : H / I < 16 ? H / I : 16; }
+//   H = 8192:  I = 576, 16 rows 14.1 / 15.3, 18.9 / 19.8; I = 1056, 8 rows 14.4 / 15.2, 17.8 / 18.6; I = 2048, 4 rows
+//              14.7 / 15.3, 17.3 / 17.8, 8 rows 18.0 / 19.1, 17.9 / 18.7; I = 4096, 1 row 20.7 / 21.0, 20.0 / 20.3, 2 rows
+//              22.3 / 22.9, 20.6 / 21.4
+//   H = 16384: I = 2048, 8 rows 22.4 / 23.7, 29.2 / 30.2; I = 4096, 4 rows 35.4 / 36.2, 35.7 / 37.1
+// Between I = 2048 and 4096 the product has more than 256 column tiles and less is saved.  Past it they are more than 512,
+// which launch_rows takes four to a workgroup: half of the CUs idle, 2 to 7 us lost (H = 8192, 1 row: I = 4608 25.5 / 25.6
+// against 20.9 / 21.3, I = 8192 35.9 / 36.2 against 30.1 / 30.4).
+static int ffn_h_rows(int H, int I) {
+  if (I > 4096) return 0;
+  const int rows = (I > 2048 ? H : H + H / 4 + 1024) / I;
+  return rows < 16 ? rows : 16;
+}
 
 // Enough for fewer rows too.
 size_t fp4_ffn_ws_bytes(int T, int H, int I, bool fp4mid) {
