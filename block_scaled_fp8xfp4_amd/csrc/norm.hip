@@ -11,13 +11,15 @@
 // double operations per element that is far under the memory time.  The norm reads h as stored, so the fused call equals
 // the addition, then the norm of what it wrote.
 //
-// One wavefront per row up to H = 2048, four up to 4096, eight beyond, the row in registers (chunks of 8 elements per
+// One wavefront per row up to H = 1024, four up to 4096, eight beyond, the row in registers (chunks of 8 elements per
 // lane, all of a row's loads in flight at once, one pass over memory); four neighbouring lanes hold a block of 32, so its
 // amax is two quad exchanges.  The split depends on H alone, and with it the order of the sum: a row's bits never depend
-// on T.
+// on T.  One wavefront / four per row, us, bf16 rows and residual to h and E4M3 codes: 16 x 512 3.3 / 3.3, 8192 x 512 7.8 / 11.5;
+// 16 x 1024 4.0 / 3.4, 8192 x 1024 13.4 / 15.6; 16 x 2048 5.4 / 3.3, 8192 x 2048 24.1 / 21.8.
 //
-// 8192 x 4096 bf16 with residual, to h and E4M3 codes: 50 us (303 MB, 6.0 TB/s, bound by memory); 48 x 5120 4.4 us, one
-// row of 4096 4.0 us (a launch, one round to memory, one reduction).
+// 8192 x 4096 bf16 with residual, to h, n and E4M3 codes: 50 to 53 us (303 MB, 5.7 to 6.0 TB/s, bound by memory), to h and
+// codes alone 37 us (236 MB, 6.3 TB/s); 48 x 5120 4.4 us, one row of 4096 4.0 us (a launch, one round to memory, one
+// reduction).
 #include "mx_cast.hpp"
 #include "mx_launch.hpp"
 
@@ -132,7 +134,7 @@ static void launch_norm(const NormArgs& a, int T, hipStream_t stream) {
 hipError_t launch_add_rmsnorm(const NormArgs& a, int T, hipStream_t stream) {
   if (a.H <= 512) launch_norm<1, 1>(a, T, stream);
   else if (a.H <= 1024) launch_norm<1, 2>(a, T, stream);
-  else if (a.H <= 2048) launch_norm<1, 4>(a, T, stream);
+  else if (a.H <= 2048) launch_norm<4, 1>(a, T, stream);
   else if (a.H <= 4096) launch_norm<4, 2>(a, T, stream);
   else if (a.H <= 8192) launch_norm<8, 2>(a, T, stream);
   else launch_norm<8, 4>(a, T, stream);
