@@ -401,8 +401,8 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void fp4_down_rows_kernel(TileA
 // (109 us at 8192 x 4096 x 4096 in E2M1).  For the same reason 16 scale bytes
 // of a row (K = 512) go to LDS at a time.
 //
-// 8192 x 4096 x 4096 takes 75 us in E2M1 (3.7 PFLOP/s) and 109 us in E4M3
-// (2.5): the matrix cores are busy for 41 and 59 % of the cycles, the rest
+// 8192 x 4096 x 4096 takes 75 us in E2M1 (3.7 PFLOP/s) and 106 us in E4M3
+// (2.6): the matrix cores are busy for 43 and 62 % of the cycles, the rest
 // goes to the first loads and the last stores of each round of tiles and, in
 // E2M1, to LDS, whose reads and DMA writes of a stage take as many cycles as
 // its matrix operations.
