@@ -154,14 +154,19 @@ __device__ __forceinline__ v4f lone_tile(const uint8_t* ap, const uint8_t* asp, 
   if (K % RPK) acc = lone_multiply(T, acc, g);
   return acc;
 }
-template <bool FP4A>
-__global__ __launch_bounds__(64, 2) void fp4_lone_kernel(TileArgs A) {
+// WAVES such wavefronts to a workgroup, each 16 rows further down: one for up to 16 rows, four for more of K < 128, where a
+// tile is one piece and has nothing to share.
+template <bool FP4A, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void fp4_lone_kernel(TileArgs A) {
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int M = A.M, N = A.N, K = A.K, nblk = K / 32;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t n = min(n0 + col, (int64_t)N - 1), m = min(col, M - 1);
+  const uint32_t nct = (N + 15) / 16;
+  const int64_t n0 = (int64_t)(WAVES == 1 ? blockIdx.x : blockIdx.x % nct) * 16;
+  const int64_t m0 = WAVES == 1 ? 0 : ((int64_t)(blockIdx.x / nct) * WAVES + (threadIdx.x >> 6)) * 16;
+  if (m0 >= M) return;
+  const int64_t n = min(n0 + col, (int64_t)N - 1), m = min(m0 + col, (int64_t)M - 1);
   const v4f acc = lone_tile<FP4A>(A.x + m * (FP4A ? K / 2 : K), A.x_sc + m * nblk, A.w + n * (K / 2), A.w_sc + n * nblk, K, g);
-  if (n0 + col < N) store_rows(A, acc, 4 * g, n);
+  if (n0 + col < N) store_rows(A, acc, m0 + 4 * g, n);
 }
 
 // The same for long rows or many columns: workgroups of four wavefronts, all
@@ -1069,8 +1074,15 @@ static bool alone(int M, int64_t n, int K, bool fp4a) {
 template <bool FP4A> static const char* launch_rows(const TileArgs& t, hipStream_t stream) {
   const int64_t n = tiles_of(t.M, t.N, 16, 16);
   if (alone(t.M, n, t.K, FP4A)) {
-    hipLaunchKernelGGL(fp4_lone_kernel<FP4A>, dim3((unsigned)n), dim3(64), 0, stream, t);
+    hipLaunchKernelGGL((fp4_lone_kernel<FP4A, 1>), dim3((unsigned)n), dim3(64), 0, stream, t);
     return FP4A ? "fp4:lone16_a4" : "fp4:lone16_a8";
+  }
+  // K < 128, more than 16 rows (in fewer than 2^32 threads).  So / through LDS, us, E2M1 and E4M3: 17 x 1024 x 96 2.8 / 3.8,
+  // 2.9 / 3.9; 256 x 8192 x 96 9.3 / 13.1, 10.2 / 13.3; 4096 x 8192 x 96 111 / 199, 127 / 204; 4096 x 1024 x 32 16.5 / 24.9, 18.5 / 25.5
+  const int64_t n64 = tiles_of(t.M, t.N, 64, 16);
+  if (t.K < 128 && t.M > 16 && n64 < 1 << 24) {
+    hipLaunchKernelGGL((fp4_lone_kernel<FP4A, 4>), dim3((unsigned)n64), dim3(256), 0, stream, t);
+    return FP4A ? "fp4:lone64_a4" : "fp4:lone64_a8";
   }
   if (n <= 256) launch_rows_of<FP4A, 1>(t, stream);
   else if (n <= 512) launch_rows_of<FP4A, 2>(t, stream);

@@ -17,7 +17,8 @@ pytestmark = pytest.mark.gpu
     (4, 8192, 1568, E4M3, "rows16_a8"), (16, 16384, 1056, E2M1, "rows16_a4"), (16, 40000, 576, E2M1, "rows16_a4"),
     (16, 32768, 256, E4M3, "rows16_a8"), (8, 4096, 16384, E4M3, "rows16_a8"), (9, 4096, 16384, E4M3, "lone16_a8"),
     (16, 2055, 10240, E4M3, "lone16_a8"), (16, 8192, 16384, E4M3, "lone16_a8"), (16, 8208, 16384, E4M3, "tile"), (16, 4096, 16384, E2M1, "rows16_a4"),
-    (17, 4096, 16384, E4M3, "tile")])
+    (17, 4096, 16384, E4M3, "tile"), (17, 96, 64, E4M3, "lone64_a8"), (300, 1030, 96, E2M1, "lone64_a4"),
+    (64, 40, 32, E4M3, "lone64_a8"), (16, 1030, 96, E2M1, "lone16_a4")])
 def test_product_of_few_rows(M, N, K, fmt, kernel):
     """Short rows are taken by wavefronts alone, and so are rows that do not fit LDS (E4M3 of 9 and more rows at K = 16384;
     as tiles 16 x 4096 x 16384 takes 30 us against 19)."""
@@ -36,7 +37,7 @@ def test_product_of_few_rows(M, N, K, fmt, kernel):
     assert v.startswith("fp4:" + kernel), v
     many = torch.empty((600, N), device="cuda")                       # the same rows in tiles
     mxmoe.fp4_block_gemm(*(t.repeat(-(-600 // M), 1)[:600].contiguous() for t in a), fmt, *w, many)
-    assert "tile" in mxmoe.last_variant()
+    assert "tile" in mxmoe.last_variant() or K < 128
     assert torch.equal(y[:M], many[:M]) and torch.isnan(y[M]).all()
 
 
