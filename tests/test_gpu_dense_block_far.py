@@ -31,7 +31,8 @@ def give_back():
                                          (270000, 48, 16384, F32),           # 4.4 GB of E4M3 rows
                                          (3, 600000, 16384, F32),            # 4.9 GB of weights
                                          (300, 540000, 16384, BF16),
-                                         (16, 140000, 96, F32)])
+                                         (16, 140000, 96, F32),
+                                         (36000, 65001, 96, BF16)])
 @pytest.mark.parametrize("fmt", [E4M3, E2M1])
 def test_products(M, N, K, dtype, fmt):
     a, a_sc = codes(M, K, fmt, 1)
