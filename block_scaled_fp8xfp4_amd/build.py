@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmxmoe.so")
 SOURCES = ["quant.hip", "logits.hip", "route.hip", "ffn.hip", "gemm.hip", "shared.hip",
-           "norm.hip", "fp4.hip", "api.cpp"]
+           "norm.hip", "fp4.hip", "tokens.hip", "cast128.hip", "b128.hip", "api.cpp"]
 ARCH = "gfx950"
 
 

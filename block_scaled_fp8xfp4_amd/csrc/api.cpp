@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "b128_launch.hpp"
 #include "mxmoe.h"
 #include "mx_launch.hpp"
 
@@ -450,6 +451,158 @@ mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T,
                                           static_cast<hipStream_t>(stream), &v);
   if (e == hipSuccess) g_variant = v;
   return from_hip(e);
+}
+
+mx_status moe_permute(const void* x, int64_t x_ld, int64_t row_bytes, const void* x_sc, int64_t sc_bytes,
+                      const int32_t* slot_pos, int T, int k, void* out, void* out_sc, int64_t out_rows, void* stream) {
+  if (T < 0 || k < 1 || k > mx::MAX_K || row_bytes < 1 || sc_bytes < 0 || x_ld < row_bytes || out_rows < 0) return MX_EINVAL;
+  if (T == 0) { g_variant = "permute:empty"; return MX_OK; }
+  if (row_bytes > int64_t(1) << 40 || sc_bytes > int64_t(1) << 40 || x_ld > (int64_t(1) << 60) / T ||
+      mx::permute_chunks(row_bytes, sc_bytes) > mx::TOKEN_MAX_CHUNKS / T ||
+      (out_rows > 0 && (row_bytes > (int64_t(1) << 60) / out_rows || sc_bytes > (int64_t(1) << 60) / out_rows)))
+    return MX_EUNSUPPORTED;
+  if (!x || !slot_pos || !out || (sc_bytes > 0 && (!x_sc || !out_sc)) || !aligned(slot_pos, 4)) return MX_EINVAL;
+  const mx::PermuteArgs a{static_cast<const uint8_t*>(x), x_ld, row_bytes, static_cast<const uint8_t*>(x_sc), sc_bytes,
+                          slot_pos, T, k, static_cast<uint8_t*>(out), static_cast<uint8_t*>(out_sc), out_rows};
+  const hipError_t e = mx::launch_permute(a, static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = "permute:rows";
+  return from_hip(e);
+}
+
+namespace {
+// what moe_unpermute and its gradient ask of their sizes; 1: nothing to do
+int unpermute_sizes(int64_t o_rows, int T, int k, int H) {
+  if (T < 0 || k < 1 || k > mx::MAX_K || H < 1 || o_rows < 0) return MX_EINVAL;
+  if (T == 0) return 1;
+  if (H > mx::TOKEN_MAX_CHUNKS / T || k > (int64_t(1) << 24) / T || o_rows > (int64_t(1) << 60) / H) return MX_EUNSUPPORTED;
+  return MX_OK;
+}
+bool in_dtype(int d) { return d == MX_IN_F32 || d == MX_IN_BF16; }
+uintptr_t size_of_in(int d) { return d == MX_IN_BF16 ? 2 : 4; }
+uintptr_t size_of_out(int d) { return d == MX_OUT_BF16 ? 2 : 4; }
+}  // namespace
+
+mx_status moe_unpermute(const void* o, int o_dtype, int64_t o_rows, const float* w, const int32_t* slot_pos, int T, int k,
+                        int H, void* y, int y_dtype, void* stream) {
+  const int r = unpermute_sizes(o_rows, T, k, H);
+  if (!in_dtype(o_dtype) || (y_dtype != MX_OUT_BF16 && y_dtype != MX_OUT_F32) || r == MX_EINVAL) return MX_EINVAL;
+  if (r == 1) { g_variant = "unpermute:empty"; return MX_OK; }
+  if (r != MX_OK) return r;
+  if ((!o && o_rows > 0) || !slot_pos || !y) return MX_EINVAL;
+  if (!aligned(o, size_of_in(o_dtype)) || !aligned(w, 4) || !aligned(slot_pos, 4) || !aligned(y, size_of_out(y_dtype)))
+    return MX_EINVAL;
+  const mx::UnpermuteArgs a{o, o_dtype == MX_IN_BF16, o_rows, w, slot_pos, T, k, H, y, y_dtype == MX_OUT_BF16, nullptr, nullptr};
+  const hipError_t e = mx::launch_unpermute(a, static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = "unpermute:rows";
+  return from_hip(e);
+}
+
+mx_status moe_unpermute_grad(const void* dy, int dy_dtype, const void* o, int o_dtype, int64_t o_rows, const float* w,
+                             const int32_t* slot_pos, int T, int k, int H, void* d_o, float* dw, void* stream) {
+  const int r = unpermute_sizes(o_rows, T, k, H);
+  if (!in_dtype(o_dtype) || !in_dtype(dy_dtype) || r == MX_EINVAL) return MX_EINVAL;
+  if (r == 1) { g_variant = "unpermute_grad:empty"; return MX_OK; }
+  if (r != MX_OK) return r;
+  if (!dy || !slot_pos || (!d_o && !dw) || (dw && !o && o_rows > 0)) return MX_EINVAL;
+  if (!aligned(dy, size_of_in(dy_dtype)) || !aligned(o, size_of_in(o_dtype)) || !aligned(d_o, size_of_in(o_dtype)) ||
+      !aligned(w, 4) || !aligned(slot_pos, 4) || !aligned(dw, 4))
+    return MX_EINVAL;
+  const mx::UnpermuteArgs a{o, o_dtype == MX_IN_BF16, o_rows, w, slot_pos, T, k, H, const_cast<void*>(dy),
+                            dy_dtype == MX_IN_BF16, d_o, dw};
+  const hipError_t e = mx::launch_unpermute_grad(a, static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = "unpermute_grad:pairs";
+  return from_hip(e);
+}
+
+mx_status fp8_quantize128(const void* src, int src_dtype, int64_t src_ld, int64_t count, int64_t rows, int64_t cols,
+                          int block_rows, uint8_t* q, float* sc, void* stream) {
+  if (count < 0 || rows < 0 || cols < 16 || cols % 16 != 0 || !in_dtype(src_dtype)) return MX_EINVAL;
+  if (block_rows != 1 && block_rows != mx::B128) return MX_EINVAL;
+  if (src_ld < cols || src_ld % row_unit(src_dtype) != 0) return MX_EINVAL;
+  if (count == 0 || rows == 0) { g_variant = "quantize128:empty"; return MX_OK; }
+  if (count > (int64_t(1) << 40) / rows || cols > (int64_t(1) << 31) || src_ld > (int64_t(1) << 60) / (count * rows)) return MX_EUNSUPPORTED;
+  const int64_t nb = (cols + 127) / 128;
+  if (block_rows == 1 ? nb * 16 > MAX_CHUNKS / (count * rows) : nb * ((rows + 127) / 128) > ((int64_t(1) << 24) - 1) / count)
+    return MX_EUNSUPPORTED;
+  if (!src || !q || !sc || !aligned(src, 16) || !aligned(q, 16) || !aligned(sc, 4)) return MX_EINVAL;
+  const bool bf16 = src_dtype == MX_IN_BF16;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const hipError_t e = block_rows == 1 ? mx::launch_quantize128_rows(src, bf16, src_ld, count * rows, cols, false, q, sc, st)
+                                       : mx::launch_quantize128_tiles(src, bf16, src_ld, count, rows, cols, q, sc, st);
+  if (e == hipSuccess) g_variant = block_rows == 1 ? "quantize128:rows" : "quantize128:tiles";
+  return from_hip(e);
+}
+
+mx_status fp8_swiglu_quantize128(const void* gu, int in_dtype_, int64_t gu_ld, int64_t T, int I, uint8_t* q, float* sc,
+                                 void* stream) {
+  if (T < 0 || I < 16 || I % 16 != 0 || !in_dtype(in_dtype_)) return MX_EINVAL;
+  if (gu_ld < 2 * (int64_t)I || gu_ld % row_unit(in_dtype_) != 0) return MX_EINVAL;
+  if (T == 0) { g_variant = "swiglu_quantize128:empty"; return MX_OK; }
+  if (((int64_t)I + 127) / 128 * 16 > MAX_CHUNKS / T || gu_ld > (int64_t(1) << 60) / T) return MX_EUNSUPPORTED;
+  if (!gu || !q || !sc || !aligned(gu, 16) || !aligned(q, 16) || !aligned(sc, 4)) return MX_EINVAL;
+  const hipError_t e = mx::launch_quantize128_rows(gu, in_dtype_ == MX_IN_BF16, gu_ld, T, I, true, q, sc,
+                                                   static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = "swiglu_quantize128:rows";
+  return from_hip(e);
+}
+
+int64_t fp8_quantize128_t_cols(int64_t rows, int E) {
+  if (rows < 0 || E < 1 || rows > int64_t(1) << 40) return 0;
+  const int64_t groups = rows < E ? rows : E;
+  return (rows + 127 * groups) / 128 * 128;
+}
+
+mx_status fp8_quantize128_t(const void* src, int src_dtype, int64_t src_ld, int64_t rows, int cols, const int32_t* offsets,
+                            int E, uint8_t* q, float* sc, int64_t q_ld, void* stream) {
+  if (rows < 0 || cols < 1 || !in_dtype(src_dtype) || src_ld < cols) return MX_EINVAL;
+  if (E < 1 || E > mx::MAX_E || (!offsets && E != 1)) return MX_EINVAL;
+  if (q_ld < 0 || q_ld % 128 != 0 || rows >= int64_t(1) << 31 || q_ld < fp8_quantize128_t_cols(rows, E)) return MX_EINVAL;
+  if (rows == 0) { g_variant = "quantize128_t:empty"; return MX_OK; }
+  if (src_ld > (int64_t(1) << 60) / rows || q_ld / 128 > ((int64_t(1) << 24) - 1) / (((int64_t)cols + 63) / 64)) return MX_EUNSUPPORTED;
+  if (!src || !q || !sc || !aligned(src, size_of_in(src_dtype)) || !aligned(q, 16) || !aligned(sc, 4) || !aligned(offsets, 4))
+    return MX_EINVAL;
+  const hipError_t e = mx::launch_quantize128_t(src, src_dtype == MX_IN_BF16, src_ld, rows, cols, offsets, E, q, sc, q_ld,
+                                                static_cast<hipStream_t>(stream));
+  if (e == hipSuccess) g_variant = "quantize128_t:columns";
+  return from_hip(e);
+}
+
+namespace {
+mx_status b128(const mx::B128Args& a, mx::B128Mode mode, bool w_rows, void* stream) {
+  if (!mx::b128_fits(a, mode)) return MX_EUNSUPPORTED;
+  if (!a.a || !a.a_sc || !a.w || !a.w_sc || !a.y || (mode != mx::B128Mode::dense && !a.offsets)) return MX_EINVAL;
+  if (!aligned(a.a, 16) || !aligned(a.w, 16) || !aligned(a.a_sc, 4) || !aligned(a.w_sc, 4) || !aligned(a.offsets, 4) ||
+      !aligned(a.y, a.bf16_out ? 2 : 4))
+    return MX_EINVAL;
+  const char* v = "";
+  const hipError_t e = mx::launch_b128(a, mode, w_rows, static_cast<hipStream_t>(stream), &v);
+  if (e == hipSuccess) g_variant = v;
+  return from_hip(e);
+}
+bool out_dtype(int d) { return d == MX_OUT_BF16 || d == MX_OUT_F32; }
+}  // namespace
+
+mx_status fp8_block128_gemm(const uint8_t* a, const float* a_sc, const uint8_t* w, const float* w_sc, int w_rows, int M, int N,
+                            int K, void* y, int y_dtype, void* stream) {
+  if (M < 0 || N < 1 || K < 16 || K % 16 != 0 || !out_dtype(y_dtype) || (w_rows != 1 && w_rows != mx::B128)) return MX_EINVAL;
+  if (M == 0) { g_variant = "b128:empty"; return MX_OK; }
+  return b128(mx::B128Args{a, a_sc, w, w_sc, K, (K - 1) / 128 + 1, M, N, K, nullptr, 1, y, y_dtype == MX_OUT_BF16},
+              mx::B128Mode::dense, w_rows == 1, stream);
+}
+
+mx_status fp8_block128_grouped_gemm(const uint8_t* a, const float* a_sc, int R, const uint8_t* w, const float* w_sc,
+                                    const int32_t* offsets, int E, int N, int K, void* y, int y_dtype, void* stream) {
+  if (R < 0 || E < 1 || E > mx::MAX_E || N < 1 || K < 16 || K % 16 != 0 || !out_dtype(y_dtype)) return MX_EINVAL;
+  if (R == 0) { g_variant = "b128:empty"; return MX_OK; }
+  return b128(mx::B128Args{a, a_sc, w, w_sc, K, (K - 1) / 128 + 1, R, N, K, offsets, E, y, y_dtype == MX_OUT_BF16},
+              mx::B128Mode::grouped, false, stream);
+}
+
+mx_status fp8_block128_grouped_wgrad(const uint8_t* a, const float* a_sc, const uint8_t* b, const float* b_sc, int64_t ld,
+                                     const int32_t* offsets, int E, int N, int K, void* dw, int dw_dtype, void* stream) {
+  if (ld < 0 || ld % 128 != 0 || ld >= int64_t(1) << 31 || E < 1 || E > mx::MAX_E || N < 1 || K < 1 || !out_dtype(dw_dtype)) return MX_EINVAL;
+  return b128(mx::B128Args{a, a_sc, b, b_sc, ld, ld / 128, N, K, (int)ld, offsets, E, dw, dw_dtype == MX_OUT_BF16},
+              mx::B128Mode::wgrad, true, stream);
 }
 
 mx_status mx_prefetch(const void* p, uint64_t bytes, uint64_t chunk_bytes, void* stream) {

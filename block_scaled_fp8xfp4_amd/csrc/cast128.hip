@@ -1,0 +1,199 @@
+// Casts to E4M3 codes with an fp32 scale for each block of 128: along a row
+// (activations), of 128 x 128 (weights), along a column (sums over tokens,
+// transposed), and of SwiGLU between an FFN's products.
+//   scale = max(amax, 2^-60) / 448 (fp32 division), code = the E4M3 value nearest to x / scale, ties to even
+// A block that holds an infinity or a NaN has the scale NaN, so every sum over
+// it is NaN too.
+#include "b128_launch.hpp"
+#include "group_device.hpp"
+#include "lds_device.hpp"
+#include "mx_cast.hpp"
+
+namespace mx {
+
+constexpr uint32_t AMAX_FLOOR = 0x21800000u;      // 2^-60
+constexpr uint32_t INF_BITS = 0x7F800000u;
+
+struct Scale128 { float sc, inv; };
+// From the bits of a block's largest |x| (as whole numbers magnitudes are in order, infinities and NaN last).
+__device__ __forceinline__ Scale128 scale128(uint32_t amax) {
+  if (amax >= INF_BITS) return Scale128{__uint_as_float(0x7FC00000u), 0.0f};
+  const float sc = __uint_as_float(max(amax, AMAX_FLOOR)) / 448.0f;
+  return Scale128{sc, 1.0f / sc};
+}
+
+__device__ __forceinline__ uint32_t bits_max(uint32_t m, float x) { return max(m, __float_as_uint(x) & 0x7FFFFFFFu); }
+
+// x / sc rounded to odd: cut toward zero, the last bit set if anything was cut, so that rounding it again to fewer bits
+// gives the nearest of those to the quotient itself.  q is within an ulp of the quotient, and with sc >= 2^-69 the
+// remainder r of every element that is not far under the smallest code is exact.
+__device__ __forceinline__ float quotient_odd(float x, const Scale128& s) {
+  float q = x * s.inv;
+  q = __builtin_fmaf(__builtin_fmaf(-q, s.sc, x), s.inv, q);
+  const float r = __builtin_fmaf(-q, s.sc, x);
+  const uint32_t b = __float_as_uint(q);
+  // an even q: one up where the quotient is larger, one down where it is smaller
+  const int step = (int)((__float_as_uint(r) ^ b) & 0x80000000u) ? -1 : 1;
+  const float odd = __uint_as_float(r != 0.0f && (b & 1u) == 0u && q != 0.0f ? b + (uint32_t)step : b);
+  return __builtin_copysignf(odd, x);                                 // the remainder's step makes +0 of -0
+}
+
+__device__ __forceinline__ uint32_t code_pair(float a, float b, const Scale128& s) {
+  const float ta = __builtin_amdgcn_fmed3f(quotient_odd(a, s), -448.0f, 448.0f);
+  const float tb = __builtin_amdgcn_fmed3f(quotient_odd(b, s), -448.0f, 448.0f);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(ta, tb, 0, false) & 0xFFFFu;
+}
+__device__ __forceinline__ u32x2 codes8(const float* v, const Scale128& s) {
+  return u32x2{code_pair(v[0], v[1], s) | code_pair(v[2], v[3], s) << 16, code_pair(v[4], v[5], s) | code_pair(v[6], v[7], s) << 16};
+}
+
+// Maximum over the 16 lanes of a DPP row.
+__device__ __forceinline__ uint32_t row16_max_bits(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x124, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x128, 0xF, 0xF, false));
+  return m;
+}
+
+// Rows: 16 lanes hold a block, eight columns each; those past the row's end hold zeros and write nothing.
+template <bool BF16, bool SWIGLU>
+__global__ __launch_bounds__(256) void quantize128_rows_kernel(const void* __restrict__ src, int64_t ld, uint32_t n, uint32_t cols,
+                                                               uint32_t nb, uint8_t* __restrict__ q, float* __restrict__ sc) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n) return;                                                 // whole blocks are in or out
+  const uint32_t r = i / (nb * 16), c = (i - r * nb * 16) * 8;
+  const bool in = c < cols;
+  float v[8];
+  uint32_t amax = 0;
+  if (in) {
+    load8(src, BF16, (int64_t)r * ld + c, v);
+    if (SWIGLU) {
+      float u[8];
+      load8(src, BF16, (int64_t)r * ld + cols + c, u);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h)                                     // four at a time: the double form is long
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e / 4 == h) v[e] = swiglu(v[e], u[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = bits_max(amax, v[e]);
+  }
+  const Scale128 s = scale128(row16_max_bits(amax));
+  if (in) *reinterpret_cast<u32x2*>(q + (int64_t)r * cols + c) = codes8(v, s);
+  if ((i & 15) == 0) sc[i >> 4] = s.sc;
+}
+
+hipError_t launch_quantize128_rows(const void* src, bool bf16, int64_t ld, int64_t rows, int64_t cols, bool swiglu,
+                                   uint8_t* q, float* sc, hipStream_t stream) {
+  const int64_t nb = (cols + 127) / 128, n = rows * nb * 16;
+  if (n == 0) return hipSuccess;
+  const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+#define MX_Q(B, S) hipLaunchKernelGGL((quantize128_rows_kernel<B, S>), grid, block, 0, stream, src, ld, (uint32_t)n, (uint32_t)cols, (uint32_t)nb, q, sc)
+  if (bf16) { if (swiglu) MX_Q(true, true); else MX_Q(true, false); }
+  else { if (swiglu) MX_Q(false, true); else MX_Q(false, false); }
+#undef MX_Q
+  return hipGetLastError();
+}
+
+// 128 x 128 blocks, a workgroup each: 16 lanes per row, every 16th row.
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize128_tiles_kernel(const void* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
+                                                                uint32_t nbr, uint32_t nbc, uint8_t* __restrict__ q,
+                                                                float* __restrict__ sc) {
+  __shared__ uint32_t part[4];
+  const uint32_t per = nbr * nbc, mat = blockIdx.x / per, in = blockIdx.x - mat * per, br = in / nbc, bc = in - br * nbc;
+  const int64_t c = (int64_t)bc * 128 + (threadIdx.x & 15) * 8, r0 = (int64_t)br * 128 + (threadIdx.x >> 4);
+  const int64_t m0 = (int64_t)mat * rows;                             // matrices follow one another
+  float v[8][8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (c >= cols || r0 + i * 16 >= rows) continue;
+    load8(src, BF16, (m0 + r0 + i * 16) * ld + c, v[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = bits_max(amax, v[i][e]);
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = amax;
+  __syncthreads();
+  const Scale128 s = scale128(max(max(part[0], part[1]), max(part[2], part[3])));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (c >= cols || r0 + i * 16 >= rows) continue;
+    *reinterpret_cast<u32x2*>(q + (m0 + r0 + i * 16) * cols + c) = codes8(v[i], s);
+  }
+  if (threadIdx.x == 0) sc[blockIdx.x] = s.sc;
+}
+
+hipError_t launch_quantize128_tiles(const void* src, bool bf16, int64_t ld, int64_t count, int64_t rows, int64_t cols,
+                                    uint8_t* q, float* sc, hipStream_t stream) {
+  const int64_t nbr = (rows + 127) / 128, nbc = (cols + 127) / 128, n = count * nbr * nbc;
+  if (n == 0) return hipSuccess;
+  const dim3 grid((unsigned)n), block(256);
+  if (bf16) hipLaunchKernelGGL(quantize128_tiles_kernel<true>, grid, block, 0, stream, src, ld, rows, cols, (uint32_t)nbr, (uint32_t)nbc, q, sc);
+  else hipLaunchKernelGGL(quantize128_tiles_kernel<false>, grid, block, 0, stream, src, ld, rows, cols, (uint32_t)nbr, (uint32_t)nbc, q, sc);
+  return hipGetLastError();
+}
+
+// Columns: a workgroup takes 128 rows of one group and 64 columns, turns them in LDS, and four threads per column make
+// its 128 codes, 32 rows each.  A group's rows past its last are zeros.
+constexpr int TCOLS = 64;
+__device__ __forceinline__ float element(const void* p, bool bf16, int64_t i) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
+}
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize128_t_kernel(const void* __restrict__ src, int64_t ld, int64_t rows, int cols,
+                                                            const int32_t* __restrict__ offsets, int E, uint8_t* __restrict__ q,
+                                                            float* __restrict__ sc, int64_t q_ld, uint32_t nct) {
+  __shared__ float t[128][TCOLS + 1];
+  const uint32_t b = blockIdx.x / nct, ct = blockIdx.x - b * nct;
+  int64_t r0 = (int64_t)b * 128, n = rows - r0;
+  if (offsets) {
+    const GroupTile g = find_tile(offsets, E, rows, 128, b);
+    if (g.e < 0) return;
+    r0 = g.row0 + (int64_t)g.tile * 128;
+    n = g.rows - g.tile * 128;
+  }
+  n = min(n, (int64_t)128);
+  const int c0 = ct * TCOLS, c = threadIdx.x & 63;
+  for (int r = threadIdx.x >> 6; r < 128; r += 4) {
+    float v = 0.0f;
+    if (r < n && c0 + c < cols) v = element(src, BF16, (r0 + r) * ld + c0 + c);
+    t[r][c] = v;
+  }
+  __syncthreads();
+  const int col = threadIdx.x >> 2, part = threadIdx.x & 3;           // a quad of lanes per column
+  uint32_t amax = 0;
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = t[part * 32 + i][col];
+    amax = bits_max(amax, v[i]);
+  }
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xF, 0xF, false));
+  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x4E, 0xF, 0xF, false));
+  if (c0 + col >= cols) return;
+  const Scale128 s = scale128(amax);
+  uint8_t* const to = q + (int64_t)(c0 + col) * q_ld + (int64_t)b * 128 + part * 32;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const u32x2 lo = codes8(v + h * 16, s), hi = codes8(v + h * 16 + 8, s);
+    *reinterpret_cast<u32x4*>(to + h * 16) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+  }
+  if (part == 0) sc[(int64_t)(c0 + col) * (q_ld / 128) + b] = s.sc;
+}
+
+hipError_t launch_quantize128_t(const void* src, bool bf16, int64_t ld, int64_t rows, int cols, const int32_t* offsets,
+                                int E, uint8_t* q, float* sc, int64_t q_ld, hipStream_t stream) {
+  const int64_t nb = offsets ? q_ld / 128 : (rows + 127) / 128, nct = (cols + TCOLS - 1) / TCOLS;
+  if (nb * nct == 0) return hipSuccess;
+  const dim3 grid((unsigned)(nb * nct)), block(256);
+  if (bf16) hipLaunchKernelGGL(quantize128_t_kernel<true>, grid, block, 0, stream, src, ld, rows, cols, offsets, E, q, sc, q_ld, (uint32_t)nct);
+  else hipLaunchKernelGGL(quantize128_t_kernel<false>, grid, block, 0, stream, src, ld, rows, cols, offsets, E, q, sc, q_ld, (uint32_t)nct);
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -1,0 +1,81 @@
+// Which expert a tile of rows belongs to, from the experts' row offsets on the
+// device (moe_route's expert_offsets): found by every wavefront for itself,
+// with one load of the offsets and one sum over its lanes, so that the host
+// needs to know only a bound on the number of tiles.
+#pragma once
+#include "mx_device.hpp"
+
+namespace mx {
+
+struct GroupTile { int e, tile, first, row0, rows; };    // e < 0: no such tile
+
+// PER experts a lane (64 PER >= E).
+template <int PER>
+__device__ __forceinline__ GroupTile find_tile_of(const int32_t* offsets, int E, int64_t R, int unit, uint32_t t) {
+  const int lane = threadIdx.x & 63;
+  int o[PER + 1];
+  // what the offsets say is kept inside the R rows that there are
+#pragma unroll
+  for (int i = 0; i <= PER; ++i) o[i] = (int)max((int64_t)0, min((int64_t)offsets[min(lane * PER + i, E)], R));
+  uint32_t n[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    n[i] = o[i + 1] > o[i] ? (uint32_t)(o[i + 1] - o[i] + unit - 1) / (uint32_t)unit : 0u;
+    sum += n[i];
+  }
+  uint32_t upto = sum;                             // tiles up to and with this lane's
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t v = __shfl_up(upto, d);
+    upto += lane >= d ? v : 0u;
+  }
+  const uint64_t past = __ballot(upto > t);
+  if (past == 0) return GroupTile{-1, 0, 0, 0, 0};
+  uint32_t first = upto - sum;
+  GroupTile g{-1, 0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (g.e < 0 && t < first + n[i]) g = GroupTile{lane * PER + i, (int)(t - first), (int)first, o[i], o[i + 1] - o[i]};
+    first += n[i];
+  }
+  const int src = __builtin_ctzll(past);
+  g.e = __builtin_amdgcn_readlane(g.e, src);
+  g.tile = __builtin_amdgcn_readlane(g.tile, src);
+  g.first = __builtin_amdgcn_readlane(g.first, src);
+  g.row0 = __builtin_amdgcn_readlane(g.row0, src);
+  g.rows = __builtin_amdgcn_readlane(g.rows, src);
+  return g;
+}
+// The expert of tile t when each expert's rows are cut into tiles of `unit`; first is the expert's first tile.
+// All 64 lanes of the wavefront take part.
+__device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int E, int64_t R, int unit, uint32_t t) {
+  return E <= 256 ? find_tile_of<4>(offsets, E, R, unit, t) : find_tile_of<16>(offsets, E, R, unit, t);
+}
+
+// Tiles [first, first + n) of expert e when each expert's rows are cut into tiles of `unit`.
+struct GroupSpan { uint32_t first, n; };
+template <int PER>
+__device__ __forceinline__ GroupSpan find_span_of(const int32_t* offsets, int E, int64_t R, int unit, int e) {
+  const int lane = threadIdx.x & 63;
+  uint32_t before = 0, mine = 0;
+  int prev = (int)max((int64_t)0, min((int64_t)offsets[min(lane * PER, E)], R));
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int o = (int)max((int64_t)0, min((int64_t)offsets[min(lane * PER + i + 1, E)], R));
+    const uint32_t n = o > prev ? (uint32_t)(o - prev + unit - 1) / (uint32_t)unit : 0u;
+    before += lane * PER + i < e ? n : 0u;
+    mine += lane * PER + i == e ? n : 0u;
+    prev = o;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    before += __shfl_xor(before, d);
+    mine += __shfl_xor(mine, d);
+  }
+  return GroupSpan{(uint32_t)__builtin_amdgcn_readfirstlane((int)before), (uint32_t)__builtin_amdgcn_readfirstlane((int)mine)};
+}
+__device__ __forceinline__ GroupSpan find_span(const int32_t* offsets, int E, int64_t R, int unit, int e) {
+  return E <= 256 ? find_span_of<4>(offsets, E, R, unit, e) : find_span_of<16>(offsets, E, R, unit, e);
+}
+
+}  // namespace mx

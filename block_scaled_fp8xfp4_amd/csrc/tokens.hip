@@ -1,0 +1,187 @@
+// Tokens to the order of their experts and back (the buckets of moe_route):
+//   permute:        out[slot_pos[t][j]] = x[t]
+//   unpermute:      y[t] = sum_j w[t][j] * o[slot_pos[t][j]], fp32, in slot order
+//   unpermute_grad: d_o[slot_pos[t][j]] = w[t][j] * dy[t],  dw[t][j] = <dy[t], o[slot_pos[t][j]]>
+// A slot that is nowhere (slot_pos < 0 or past the rows there are) takes no
+// part.  All of it is memory traffic; every result has one writer and a fixed
+// order of addition, so nothing depends on timing.
+#include "b128_launch.hpp"
+#include "lds_device.hpp"
+#include "mx_cast.hpp"
+
+namespace mx {
+
+// ---------------------------------------------------------------------------
+// Rows of bytes: a thread holds 16 bytes of a token's row (or of its scales)
+// and writes them to the token's k places, so that each row is read once.  A
+// row's last piece reaches back to be whole (two threads then write the same
+// bytes); rows of less than 16 bytes go by bytes.
+int64_t permute_chunks(int64_t row, int64_t sc) { return (row + 15) / 16 + (sc + 15) / 16; }
+
+__global__ __launch_bounds__(256) void permute_kernel(PermuteArgs A, uint32_t chunks, uint32_t row_chunks, uint32_t n) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n) return;
+  const uint32_t t = i / chunks, c = i - t * chunks;
+  const bool scales = c >= row_chunks;
+  const uint8_t* src = scales ? A.x_sc + (int64_t)t * A.sc : A.x + (int64_t)t * A.x_ld;
+  uint8_t* const dst = scales ? A.out_sc : A.out;
+  const int64_t len = scales ? A.sc : A.row;
+  const int64_t at = (int64_t)(scales ? c - row_chunks : c) * 16;
+  const int32_t* pos = A.slot_pos + (int64_t)t * A.k;
+  if (len >= 16) {
+    const int64_t b = min(at, len - 16);
+    const u32x4 v = *reinterpret_cast<const u32x4_a1*>(src + b);
+    for (int j = 0; j < A.k; ++j) {
+      const int p = pos[j];
+      if (p >= 0 && p < A.out_rows) *reinterpret_cast<u32x4_a1*>(dst + (int64_t)p * len + b) = v;
+    }
+    return;
+  }
+  for (int j = 0; j < A.k; ++j) {
+    const int p = pos[j];
+    if (p < 0 || p >= A.out_rows) continue;
+    for (int64_t b = 0; b < len; ++b) dst[(int64_t)p * len + b] = src[b];
+  }
+}
+
+hipError_t launch_permute(const PermuteArgs& a, hipStream_t stream) {
+  const int64_t chunks = permute_chunks(a.row, a.sc), n = a.T * chunks;
+  if (n == 0 || a.k == 0) return hipSuccess;
+  hipLaunchKernelGGL(permute_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, a, (uint32_t)chunks,
+                     (uint32_t)((a.row + 15) / 16), (uint32_t)n);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// N elements from element i on, at any alignment that the type allows.
+template <int N> __device__ __forceinline__ void load_any(const void* p, bool bf16, int64_t i, float* v) {
+  if (N == 1) {
+    v[0] = bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
+  } else if (bf16) {
+    const u32x4 d = *reinterpret_cast<const u32x4_a1*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      v[2 * j] = __uint_as_float(d[j] << 16);
+      v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
+    }
+  } else {
+    const u32x4_a1* s = reinterpret_cast<const u32x4_a1*>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const u32x4 d = s[q];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * q + j] = __uint_as_float(d[j]);
+    }
+  }
+}
+template <int N> __device__ __forceinline__ void store_any(void* p, bool bf16, int64_t i, const float* v) {
+  if (N == 1) {
+    if (bf16) static_cast<uint16_t*>(p)[i] = (uint16_t)bf16_pair(v[0], 0.0f);
+    else static_cast<float*>(p)[i] = v[0];
+  } else if (bf16) {
+    u32x4 d;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) d[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<u32x4_a1*>(static_cast<uint16_t*>(p) + i) = d;
+  } else {
+    u32x4_a1* s = reinterpret_cast<u32x4_a1*>(static_cast<float*>(p) + i);
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q)
+      s[q] = u32x4{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                   __float_as_uint(v[4 * q + 3])};
+  }
+}
+
+// A thread per N columns of a token; a row's last piece reaches back to be whole (N = 1 for rows of less than 8).
+template <int N, bool OB, bool YB>
+__global__ __launch_bounds__(256) void unpermute_kernel(UnpermuteArgs A, uint32_t chunks, uint32_t n) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n) return;
+  const uint32_t t = i / chunks;
+  const int c = min((int)(i - t * chunks) * N, A.H - N);
+  const int32_t* pos = A.slot_pos + (int64_t)t * A.k;
+  const float* w = A.w + (int64_t)t * A.k;
+  float acc[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+  for (int j = 0; j < A.k; ++j) {
+    const int p = pos[j];
+    if (p < 0 || p >= A.o_rows) continue;
+    const float f = A.w ? w[j] : 1.0f;
+    float v[N];
+    load_any<N>(A.o, OB, (int64_t)p * A.H + c, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+  }
+  store_any<N>(A.y, YB, (int64_t)t * A.H + c, acc);
+}
+
+template <int N, bool OB> static void launch_unpermute_of(const UnpermuteArgs& a, hipStream_t stream) {
+  const int64_t chunks = (a.H + N - 1) / N, n = a.T * chunks;
+  const dim3 grid((unsigned)((n + 255) / 256));
+  if (a.y_bf16) hipLaunchKernelGGL((unpermute_kernel<N, OB, true>), grid, dim3(256), 0, stream, a, (uint32_t)chunks, (uint32_t)n);
+  else hipLaunchKernelGGL((unpermute_kernel<N, OB, false>), grid, dim3(256), 0, stream, a, (uint32_t)chunks, (uint32_t)n);
+}
+hipError_t launch_unpermute(const UnpermuteArgs& a, hipStream_t stream) {
+  if (a.H < 8) {
+    if (a.o_bf16) launch_unpermute_of<1, true>(a, stream);
+    else launch_unpermute_of<1, false>(a, stream);
+  } else {
+    if (a.o_bf16) launch_unpermute_of<8, true>(a, stream);
+    else launch_unpermute_of<8, false>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+// A wavefront per (token, slot): it scales the token's dy into the slot's row of d_o and sums dy * o on the way, eight
+// columns a lane.  d_o may be o itself: a lane has read a piece before it writes it.
+template <bool DYB, bool OB>
+__global__ __launch_bounds__(256) void unpermute_grad_kernel(UnpermuteArgs A) {
+  const int lane = threadIdx.x & 63;
+  const int64_t pair = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (pair >= (int64_t)A.T * A.k) return;
+  const int64_t t = pair / A.k;
+  const int p = A.slot_pos[pair];
+  if (p < 0 || p >= A.o_rows) {
+    if (A.dw && lane == 0) A.dw[pair] = 0.0f;
+    return;
+  }
+  const float f = A.w ? A.w[pair] : 1.0f;
+  const int64_t dy0 = t * A.H, o0 = (int64_t)p * A.H;
+  float sum = 0.0f;
+  auto piece = [&](auto size, int c) {
+    constexpr int N = decltype(size)::value;
+    float d[N], v[N];
+    load_any<N>(A.y, DYB, dy0 + c, d);
+    if (A.dw) {
+      load_any<N>(A.o, OB, o0 + c, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e) sum = __builtin_fmaf(d[e], v[e], sum);
+    }
+    if (!A.d_o) return;
+#pragma unroll
+    for (int e = 0; e < N; ++e) d[e] *= f;
+    store_any<N>(A.d_o, OB, o0 + c, d);
+  };
+  const int whole = A.H & ~7;
+  for (int c = lane * 8; c < whole; c += 512) piece(Int<8>{}, c);
+  if (whole + lane < A.H) piece(Int<1>{}, whole + lane);
+  if (!A.dw) return;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) sum += __shfl_xor(sum, d);
+  if (lane == 0) A.dw[pair] = sum;
+}
+
+hipError_t launch_unpermute_grad(const UnpermuteArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(((int64_t)a.T * a.k + 3) / 4)), block(256);
+  if (a.y_bf16) {
+    if (a.o_bf16) hipLaunchKernelGGL((unpermute_grad_kernel<true, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((unpermute_grad_kernel<true, false>), grid, block, 0, stream, a);
+  } else {
+    if (a.o_bf16) hipLaunchKernelGGL((unpermute_grad_kernel<false, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((unpermute_grad_kernel<false, false>), grid, block, 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mx

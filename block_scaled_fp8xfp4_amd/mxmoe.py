@@ -23,7 +23,10 @@ EXPORTS = ("mx_quantize", "moe_router_logits_workspace_bytes", "moe_router_logit
            "moe_layer_decode1", "mx_set_ffn_diag", "moe_expert_ffn_noalloc", "moe_expert_ffn_noalloc_max_bytes",
            "moe_layer_decode1_shared_workspace_bytes", "moe_layer_decode1_shared",
            "mx_dequantize", "mx_swiglu_quantize", "mx_add_rmsnorm", "fp4_block_gemm",
-           "fp4_dense_ffn_workspace_bytes", "fp4_dense_ffn")
+           "fp4_dense_ffn_workspace_bytes", "fp4_dense_ffn",
+           "moe_permute", "moe_unpermute", "moe_unpermute_grad",
+           "fp8_quantize128", "fp8_swiglu_quantize128", "fp8_quantize128_t_cols", "fp8_quantize128_t",
+           "fp8_block128_gemm", "fp8_block128_grouped_gemm", "fp8_block128_grouped_wgrad")
 
 _lib = None
 
@@ -92,6 +95,26 @@ def load():
     lib.fp4_dense_ffn_workspace_bytes.argtypes = [I32, I32, I32, I32]
     lib.fp4_dense_ffn.restype = I32
     lib.fp4_dense_ffn.argtypes = [P, P, I32, I32, I32, P, P, P, P, I32, I32, P, I32, P, SZ, P]
+    lib.moe_permute.restype = I32
+    lib.moe_permute.argtypes = [P, I64, I64, P, I64, P, I32, I32, P, P, I64, P]
+    lib.moe_unpermute.restype = I32
+    lib.moe_unpermute.argtypes = [P, I32, I64, P, P, I32, I32, I32, P, I32, P]
+    lib.moe_unpermute_grad.restype = I32
+    lib.moe_unpermute_grad.argtypes = [P, I32, P, I32, I64, P, P, I32, I32, I32, P, P, P]
+    lib.fp8_quantize128.restype = I32
+    lib.fp8_quantize128.argtypes = [P, I32, I64, I64, I64, I64, I32, P, P, P]
+    lib.fp8_swiglu_quantize128.restype = I32
+    lib.fp8_swiglu_quantize128.argtypes = [P, I32, I64, I64, I32, P, P, P]
+    lib.fp8_quantize128_t_cols.restype = I64
+    lib.fp8_quantize128_t_cols.argtypes = [I64, I32]
+    lib.fp8_quantize128_t.restype = I32
+    lib.fp8_quantize128_t.argtypes = [P, I32, I64, I64, I32, P, I32, P, P, I64, P]
+    lib.fp8_block128_gemm.restype = I32
+    lib.fp8_block128_gemm.argtypes = [P, P, P, P, I32, I32, I32, I32, P, I32, P]
+    lib.fp8_block128_grouped_gemm.restype = I32
+    lib.fp8_block128_grouped_gemm.argtypes = [P, P, I32, P, P, P, I32, I32, I32, P, I32, P]
+    lib.fp8_block128_grouped_wgrad.restype = I32
+    lib.fp8_block128_grouped_wgrad.argtypes = [P, P, P, P, I64, P, I32, I32, I32, P, I32, P]
     lib.mx_prefetch.restype = I32
     lib.mx_prefetch.argtypes = [P, ctypes.c_uint64, ctypes.c_uint64, P]
     lib.mx_status_string.restype = ctypes.c_char_p
@@ -306,7 +329,7 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.u8, self.f32, self.bf16 = torch.uint8, torch.float32, torch.bfloat16
+        self.u8, self.f32, self.bf16, self.i32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
         self.ins = {torch.float32: MX_IN_F32, torch.bfloat16: MX_IN_BF16}
         self.outs = {torch.bfloat16: MX_OUT_BF16, torch.float32: MX_OUT_F32}
         self.current_device = torch.cuda.current_device
@@ -514,6 +537,249 @@ def fp4_dense_ffn(x, x_sc, x_fmt, w13, w13_sc, w2, w2_sc, mid_fmt, y, ws, stream
     _check(load().fp4_dense_ffn(x.data_ptr(), x_sc.data_ptr(), x_fmt, T, H, w13.data_ptr(), w13_sc.data_ptr(),
                                 w2.data_ptr(), w2_sc.data_ptr(), I, mid_fmt, y.data_ptr(), t.outs[y.dtype],
                                 ws.data_ptr(), ws.nbytes, t.raw_stream(d) if stream is None else stream), name)
+
+
+# ------------------------------ experts' tokens, products with a scale for each block of 128
+# Checked as the dense block's calls are: one question that holds for right
+# tensors, and only where it does not the checks that find out what is wrong.
+def _plain(d, dtype, shape, *tensors):
+    """Every tensor is contiguous, of this type and shape, on device d."""
+    return all(t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == d for t in tensors)
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def moe_permute(x, slot_pos, out, x_sc=None, out_sc=None, stream=None):
+    """out[slot_pos[t, j]] = x[t]; x [T, H] of any type with contiguous rows, out [R, H] of the same type, slot_pos int32
+    [T, k]; rows that no slot names are left as they were.  x_sc [T, B] and out_sc [R, B]: the rows' scales, alike."""
+    name, t = "moe_permute", _tn()
+    T, H = _two(name, "x", x)
+    R = _two(name, "out", out)[0]
+    k = _two(name, "slot_pos", slot_pos)[1]
+    _int(name, T, k)
+    d, size, ld = x.get_device(), x.element_size(), H
+    if (x_sc is None) != (out_sc is None):
+        raise ValueError(f"{name}: x_sc and out_sc come together")
+    B = 0 if x_sc is None else _two(name, "x_sc", x_sc)[1]
+    if not (x.is_contiguous() and _plain(d, x.dtype, (R, H), out) and _plain(d, t.i32, (T, k), slot_pos) and
+            (x_sc is None or _plain(d, x_sc.dtype, (T, B), x_sc) and _plain(d, x_sc.dtype, (R, B), out_sc)) and
+            t.current_device() == d):
+        ld = _rows(name, "x", x, (x.dtype,), T, H) if T > 1 else H
+        if T == 1 and H > 1 and x.stride(1) != 1:
+            raise ValueError(f"{name}: x must have contiguous rows")
+        _packed(name, "out", out, (x.dtype,), (R, H))
+        _packed(name, "slot_pos", slot_pos, (t.i32,), (T, k))
+        if x_sc is not None:
+            _packed(name, "x_sc", x_sc, (x_sc.dtype,), (T, B))
+            _packed(name, "out_sc", out_sc, (x_sc.dtype,), (R, B))
+        _here(name, x, slot_pos, out, x_sc, out_sc)
+    if H == 0:
+        raise ValueError(f"{name}: x has no columns")
+    _check(load().moe_permute(x.data_ptr(), ld * size, H * size, None if not B else x_sc.data_ptr(),
+                              B * x_sc.element_size() if B else 0, slot_pos.data_ptr(), T, k, out.data_ptr(),
+                              None if not B else out_sc.data_ptr(), R, t.raw_stream(d) if stream is None else stream), name)
+
+
+def moe_unpermute(o, w, slot_pos, y, stream=None):
+    """y[t] = sum_j w[t, j] o[slot_pos[t, j]] (w None: ones); o [R, H] and y [T, H] fp32 or bf16, w fp32 [T, k], slot_pos
+    int32 [T, k]."""
+    name, t = "moe_unpermute", _tn()
+    R, H = _two(name, "o", o)
+    T = _two(name, "y", y)[0]
+    k = _two(name, "slot_pos", slot_pos)[1]
+    _int(name, T, k, H)
+    d = o.get_device()
+    if not (o.dtype in t.ins and y.dtype in t.outs and o.is_contiguous() and _plain(d, y.dtype, (T, H), y) and
+            _plain(d, t.i32, (T, k), slot_pos) and (w is None or _plain(d, t.f32, (T, k), w)) and t.current_device() == d):
+        _packed(name, "o", o, t.ins, (R, H))
+        _packed(name, "y", y, t.outs, (T, H))
+        _packed(name, "slot_pos", slot_pos, (t.i32,), (T, k))
+        if w is not None:
+            _packed(name, "w", w, (t.f32,), (T, k))
+        _here(name, o, w, slot_pos, y)
+    _check(load().moe_unpermute(o.data_ptr(), t.ins[o.dtype], R, None if w is None else w.data_ptr(), slot_pos.data_ptr(), T, k,
+                                H, y.data_ptr(), t.outs[y.dtype], t.raw_stream(d) if stream is None else stream), name)
+
+
+def moe_unpermute_grad(dy, o, w, slot_pos, d_o=None, dw=None, stream=None):
+    """The gradient of moe_unpermute: d_o[slot_pos[t, j]] = w[t, j] dy[t] (o's type; may be o itself), dw[t, j] =
+    <dy[t], o[slot_pos[t, j]]> (fp32).  The outputs that are given are written; o may be None without dw."""
+    name, t = "moe_unpermute_grad", _tn()
+    T, H = _two(name, "dy", dy)
+    k = _two(name, "slot_pos", slot_pos)[1]
+    rows = o if o is not None else d_o
+    if rows is None or d_o is None and dw is None or dw is not None and o is None:
+        raise ValueError(f"{name}: d_o or dw is needed, and o for dw")
+    R = _two(name, "o", rows)[0]
+    _int(name, T, k, H)
+    d = dy.get_device()
+    if not (dy.dtype in t.ins and rows.dtype in t.ins and dy.is_contiguous() and _plain(d, rows.dtype, (R, H), rows) and
+            (d_o is None or _plain(d, rows.dtype, (R, H), d_o)) and _plain(d, t.i32, (T, k), slot_pos) and
+            (w is None or _plain(d, t.f32, (T, k), w)) and (dw is None or _plain(d, t.f32, (T, k), dw)) and
+            t.current_device() == d):
+        _packed(name, "dy", dy, t.ins, (T, H))
+        _packed(name, "o", rows, t.ins, (R, H))
+        if d_o is not None:
+            _packed(name, "d_o", d_o, (rows.dtype,), (R, H))
+        _packed(name, "slot_pos", slot_pos, (t.i32,), (T, k))
+        for what, v in (("w", w), ("dw", dw)):
+            if v is not None:
+                _packed(name, what, v, (t.f32,), (T, k))
+        _here(name, dy, o, w, slot_pos, d_o, dw)
+    _check(load().moe_unpermute_grad(dy.data_ptr(), t.ins[dy.dtype], None if o is None else o.data_ptr(), t.ins[rows.dtype], R,
+                                     None if w is None else w.data_ptr(), slot_pos.data_ptr(), T, k, H,
+                                     None if d_o is None else d_o.data_ptr(), None if dw is None else dw.data_ptr(),
+                                     t.raw_stream(d) if stream is None else stream), name)
+
+
+def fp8_quantize128(src, q, sc, block_rows=1, stream=None):
+    """q, sc = E4M3 codes and fp32 scales of src, [rows, cols] or [count, rows, cols], fp32 or bf16, in blocks of 1 x 128
+    (block_rows 1: sc [..., rows, nb]) or 128 x 128 (sc [..., ceil(rows / 128), nb]).  Rows of a 2-D src may lie apart."""
+    name, t = "fp8_quantize128", _tn()
+    if src.dim() not in (2, 3):
+        raise ValueError(f"{name}: src must be 2-D or 3-D")
+    if block_rows not in (1, 128):
+        raise ValueError(f"{name}: block_rows is {block_rows}, expected 1 or 128")
+    head, (rows, cols) = tuple(src.shape[:-2]), src.shape[-2:]
+    count, d, ld = head[0] if head else 1, src.get_device(), cols
+    shape = head + (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
+    if not (src.dtype in t.ins and src.is_contiguous() and _plain(d, t.u8, src.shape, q) and _plain(d, t.f32, shape, sc) and
+            t.current_device() == d):
+        if head:
+            _packed(name, "src", src, t.ins, src.shape)
+        else:
+            ld = _rows(name, "src", src, t.ins, rows, cols)
+        _packed(name, "q", q, (t.u8,), src.shape)
+        _packed(name, "sc", sc, (t.f32,), shape)
+        _here(name, src, q, sc)
+    _check(load().fp8_quantize128(src.data_ptr(), t.ins[src.dtype], ld, count, rows, cols, block_rows, q.data_ptr(),
+                                  sc.data_ptr(), t.raw_stream(d) if stream is None else stream), name)
+
+
+def fp8_swiglu_quantize128(gu, q, sc, stream=None):
+    """q [T, I], sc [T, ceil(I / 128)] = codes and fp32 scales of silu(gate) * up; gu [T, 2I] (fp32 or bf16, any row stride
+    that keeps rows 16-byte aligned), gate in the first I columns."""
+    name, t = "fp8_swiglu_quantize128", _tn()
+    T, two_i = _two(name, "gu", gu)
+    I = two_i // 2
+    _int(name, I)
+    d, ld = gu.get_device(), two_i
+    if not (gu.dtype in t.ins and gu.is_contiguous() and two_i == 2 * I and _plain(d, t.u8, (T, I), q) and
+            _plain(d, t.f32, (T, _blocks(I)), sc) and t.current_device() == d):
+        ld = _rows(name, "gu", gu, t.ins, T, 2 * I)
+        _packed(name, "q", q, (t.u8,), (T, I))
+        _packed(name, "sc", sc, (t.f32,), (T, _blocks(I)))
+        _here(name, gu, q, sc)
+    _check(load().fp8_swiglu_quantize128(gu.data_ptr(), t.ins[gu.dtype], ld, T, I, q.data_ptr(), sc.data_ptr(),
+                                         t.raw_stream(d) if stream is None else stream), name)
+
+
+def fp8_quantize128_t_cols(rows, E=1):
+    """Columns of codes that hold any split of rows into E groups."""
+    return load().fp8_quantize128_t_cols(rows, E)
+
+
+def fp8_quantize128_t(src, q, sc, offsets=None, stream=None):
+    """q [cols, ld], sc [cols, ld / 128] = codes and scales of src [rows, cols] (fp32 or bf16) along its columns, transposed,
+    in blocks of 128 rows; offsets (int32 [E + 1]) cuts the rows into groups that start at multiples of 128.  ld at least
+    fp8_quantize128_t_cols(rows, E)."""
+    name, t = "fp8_quantize128_t", _tn()
+    rows, cols = _two(name, "src", src)
+    q_ld = _two(name, "q", q)[1]
+    _int(name, rows, cols)
+    E, d, ld = 1 if offsets is None else offsets.numel() - 1, src.get_device(), cols
+    if not (src.dtype in t.ins and src.is_contiguous() and q_ld % 128 == 0 and _plain(d, t.u8, (cols, q_ld), q) and
+            _plain(d, t.f32, (cols, q_ld // 128), sc) and (offsets is None or _plain(d, t.i32, (E + 1,), offsets)) and
+            t.current_device() == d):
+        if rows > 1:
+            ld = _rows(name, "src", src, t.ins, rows, cols)
+        else:
+            _packed(name, "src", src, t.ins, (rows, cols))
+        if q_ld % 128:
+            raise ValueError(f"{name}: q has {q_ld} columns, a multiple of 128 is expected")
+        _packed(name, "q", q, (t.u8,), (cols, q_ld))
+        _packed(name, "sc", sc, (t.f32,), (cols, q_ld // 128))
+        if offsets is not None:
+            _packed(name, "offsets", offsets, (t.i32,), (E + 1,))
+        _here(name, src, q, sc, offsets)
+    _check(load().fp8_quantize128_t(src.data_ptr(), t.ins[src.dtype], ld, rows, cols,
+                                    None if offsets is None else offsets.data_ptr(), E, q.data_ptr(), sc.data_ptr(), q_ld,
+                                    t.raw_stream(d) if stream is None else stream), name)
+
+
+def fp8_block128_gemm(a, a_sc, w, w_sc, y, stream=None):
+    """y [M, N] (bf16 or fp32) = a . w^T; E4M3 codes a [M, K], w [N, K], fp32 scales a_sc [M, nb] and w_sc [ceil(N / 128),
+    nb] (tiles) or [N, nb] (rows), nb = ceil(K / 128)."""
+    name, t = "fp8_block128_gemm", _tn()
+    N, K = _two(name, "w", w)
+    M = _two(name, "y", y)[0]
+    _int(name, M, N, K)
+    sn, nb, d = _two(name, "w_sc", w_sc)[0], _blocks(K), y.get_device()
+    if not (y.dtype in t.outs and _plain(d, y.dtype, (M, N), y) and _plain(d, t.u8, (M, K), a) and _plain(d, t.u8, (N, K), w) and
+            _plain(d, t.f32, (M, nb), a_sc) and (sn == N or sn == _blocks(N)) and _plain(d, t.f32, (sn, nb), w_sc) and
+            t.current_device() == d):
+        _packed(name, "a", a, (t.u8,), (M, K))
+        _packed(name, "w", w, (t.u8,), (N, K))
+        _packed(name, "a_sc", a_sc, (t.f32,), (M, nb))
+        _packed(name, "w_sc", w_sc, (t.f32,), (N if sn == N else _blocks(N), nb))
+        _packed(name, "y", y, t.outs, (M, N))
+        _here(name, a, a_sc, w, w_sc, y)
+    _check(load().fp8_block128_gemm(a.data_ptr(), a_sc.data_ptr(), w.data_ptr(), w_sc.data_ptr(), 1 if sn == N else 128, M, N, K,
+                                    y.data_ptr(), t.outs[y.dtype], t.raw_stream(d) if stream is None else stream), name)
+
+
+def fp8_block128_grouped_gemm(a, a_sc, w, w_sc, offsets, y, stream=None):
+    """y[r] = a[r] . w[e]^T for rows r in [offsets[e], offsets[e + 1]); a [R, K], a_sc [R, nb], w [E, N, K], w_sc [E,
+    ceil(N / 128), nb], offsets int32 [E + 1], y [R, N] bf16 or fp32.  Rows behind offsets[E] are left as they were."""
+    name, t = "fp8_block128_grouped_gemm", _tn()
+    if w.dim() != 3:
+        raise ValueError(f"{name}: w must be 3-D")
+    E, N, K = w.shape
+    R = _two(name, "y", y)[0]
+    _int(name, R, N, K)
+    nb, d = _blocks(K), y.get_device()
+    if not (y.dtype in t.outs and _plain(d, y.dtype, (R, N), y) and _plain(d, t.u8, (R, K), a) and _plain(d, t.u8, (E, N, K), w) and
+            _plain(d, t.f32, (R, nb), a_sc) and _plain(d, t.f32, (E, _blocks(N), nb), w_sc) and
+            _plain(d, t.i32, (E + 1,), offsets) and t.current_device() == d):
+        _packed(name, "a", a, (t.u8,), (R, K))
+        _packed(name, "w", w, (t.u8,), (E, N, K))
+        _packed(name, "a_sc", a_sc, (t.f32,), (R, nb))
+        _packed(name, "w_sc", w_sc, (t.f32,), (E, _blocks(N), nb))
+        _packed(name, "offsets", offsets, (t.i32,), (E + 1,))
+        _packed(name, "y", y, t.outs, (R, N))
+        _here(name, a, a_sc, w, w_sc, offsets, y)
+    _check(load().fp8_block128_grouped_gemm(a.data_ptr(), a_sc.data_ptr(), R, w.data_ptr(), w_sc.data_ptr(), offsets.data_ptr(), E,
+                                            N, K, y.data_ptr(), t.outs[y.dtype],
+                                            t.raw_stream(d) if stream is None else stream), name)
+
+
+def fp8_block128_grouped_wgrad(a, a_sc, b, b_sc, offsets, dw, stream=None):
+    """dw[e] = a . b^T over expert e's columns; a [N, ld] + a_sc [N, ld / 128] and b [K, ld] + b_sc as fp8_quantize128_t makes
+    them with these offsets (int32 [E + 1]); dw [E, N, K] bf16 or fp32."""
+    name, t = "fp8_block128_grouped_wgrad", _tn()
+    if dw.dim() != 3:
+        raise ValueError(f"{name}: dw must be 3-D")
+    E, N, K = dw.shape
+    ld = _two(name, "a", a)[1]
+    _int(name, N, K, ld)
+    nb, d = ld // 128, dw.get_device()
+    if not (dw.dtype in t.outs and ld % 128 == 0 and _plain(d, dw.dtype, (E, N, K), dw) and _plain(d, t.u8, (N, ld), a) and
+            _plain(d, t.u8, (K, ld), b) and _plain(d, t.f32, (N, nb), a_sc) and _plain(d, t.f32, (K, nb), b_sc) and
+            _plain(d, t.i32, (E + 1,), offsets) and t.current_device() == d):
+        if ld % 128:
+            raise ValueError(f"{name}: a has {ld} columns, a multiple of 128 is expected")
+        _packed(name, "a", a, (t.u8,), (N, ld))
+        _packed(name, "b", b, (t.u8,), (K, ld))
+        _packed(name, "a_sc", a_sc, (t.f32,), (N, nb))
+        _packed(name, "b_sc", b_sc, (t.f32,), (K, nb))
+        _packed(name, "offsets", offsets, (t.i32,), (E + 1,))
+        _packed(name, "dw", dw, t.outs, (E, N, K))
+        _here(name, a, a_sc, b, b_sc, offsets, dw)
+    _check(load().fp8_block128_grouped_wgrad(a.data_ptr(), a_sc.data_ptr(), b.data_ptr(), b_sc.data_ptr(), ld, offsets.data_ptr(),
+                                             E, N, K, dw.data_ptr(), t.outs[dw.dtype],
+                                             t.raw_stream(d) if stream is None else stream), name)
 
 
 def prefetch(t, chunk_bytes=0, stream=None, nbytes=None):

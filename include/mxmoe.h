@@ -420,6 +420,140 @@ mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T,
                         int y_dtype, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Tokens to the order of their experts (TP4 README, settings table, row
+ * "Experts": the route planner and the per-slot buffer; here as a step of its
+ * own, for experts whose products the caller chooses):
+ *   out[slot_pos[t][j]] = x[t]   for every slot with 0 <= slot_pos < out_rows
+ * slot_pos int32 [T][k] as moe_route writes it; slots that are nowhere (-1)
+ * or past out_rows are left out, and rows of out that no slot names are left
+ * as they were (no two slots may name one row).  x: T rows of row_bytes
+ * bytes, x_ld bytes apart (x_ld >= row_bytes); out: out_rows rows of
+ * row_bytes bytes without gaps.  With sc_bytes > 0 the rows' scales x_sc,
+ * rows of sc_bytes bytes without gaps, go the same way into out_sc.  Rows and
+ * scales are bytes of any type at any alignment (16-byte aligned rows are
+ * fastest); out must not overlap x.  Each row is read once.  1 <= k <= 16;
+ * T * (ceil(row_bytes / 16) + ceil(sc_bytes / 16)) <= 2^31.  The gradient of
+ * x is moe_unpermute of the gradient of out, without weights.
+ */
+mx_status moe_permute(const void* x, int64_t x_ld, int64_t row_bytes, const void* x_sc, int64_t sc_bytes,
+                      const int32_t* slot_pos, int T, int k, void* out, void* out_sc, int64_t out_rows, void* stream);
+
+/*
+ * The experts' rows back to their tokens, with the routing weights applied
+ * (the combine of moe_expert_ffn as a step of its own; TP4 README, row
+ * "Experts": a fixed-order sum instead of atomics):
+ *   y[t] = sum_{j = 0..k-1} w[t][j] * o[slot_pos[t][j]]
+ * fp32, acc = fma(w, o, acc) from zero in slot order, rounded once to y's
+ * type; slots that are nowhere or past o_rows add nothing (a row without any
+ * is +0).  o [o_rows][H] fp32 or bf16 (MX_IN_*), w fp32 [T][k] or NULL
+ * (ones), y [T][H] (MX_OUT_*), contiguous, at their types' alignment (16-byte
+ * aligned rows are fastest); y must not overlap o.  1 <= k <= 16, any
+ * H >= 1, T * H <= 2^31, T * k <= 2^24.
+ */
+mx_status moe_unpermute(const void* o, int o_dtype, int64_t o_rows, const float* w, const int32_t* slot_pos, int T, int k,
+                        int H, void* y, int y_dtype, void* stream);
+
+/*
+ * The gradient of moe_unpermute:
+ *   d_o[slot_pos[t][j]] = w[t][j] * dy[t],   dw[t][j] = sum_h dy[t][h] * o[slot_pos[t][j]][h]
+ * dy [T][H] (dy_dtype MX_IN_*), o and d_o [o_rows][H] of o_dtype, dw fp32
+ * [T][k].  d_o or dw may be NULL (not both), o too without dw; d_o may be o
+ * itself, otherwise outputs must not overlap inputs.  Products and sums are
+ * fp32 in one fixed order; d_o is rounded once.  Slots that are nowhere or
+ * past o_rows get dw = 0, and rows of d_o that no slot names are left as they
+ * were.  Sizes and alignment as moe_unpermute.
+ */
+mx_status moe_unpermute_grad(const void* dy, int dy_dtype, const void* o, int o_dtype, int64_t o_rows, const float* w,
+                             const int32_t* slot_pos, int T, int k, int H, void* d_o, float* dw, void* stream);
+
+/*
+ * Casts to E4M3 with an fp32 scale for each block of 128 (the format of FP8
+ * checkpoints with scales of 128 x 128 weights; post #6, "Why TileLang":
+ * per-block FP8 casts).  For each block, amax its largest magnitude:
+ *   scale = max(amax, 2^-60) / 448 (fp32),  code = E4M3 nearest to x / scale
+ * (ties to even, of the quotient itself, not of its fp32 value; saturating;
+ * the sign kept).  A block that holds an infinity or a NaN has the scale NaN.
+ * Value of an element = decode(code) * scale.
+ *
+ * fp8_quantize128: src [count][rows][cols] fp32 or bf16, rows src_ld elements
+ * apart (>= cols, a multiple of 4 (fp32) or 8 (bf16)), matrices following one
+ * another; q [count][rows][cols]; block_rows 1: sc [count * rows][ceil(cols /
+ * 128)] (activations); 128: sc [count][ceil(rows / 128)][ceil(cols / 128)]
+ * (weights).  Last blocks may be shorter.  cols % 16 == 0.
+ * fp8_swiglu_quantize128: the rows' cast of silu(gate) * up (as
+ * mx_swiglu_quantize: double, rounded once to fp32); gu rows of gu_ld
+ * elements, gate in [0, I), up in [I, 2I); I % 16 == 0.
+ * src, gu, q 16-byte, sc 4-byte aligned; outputs must not overlap inputs.
+ * rows: at most 2^31 / 16 blocks; tiles: fewer than 2^24 blocks.
+ */
+mx_status fp8_quantize128(const void* src, int src_dtype, int64_t src_ld, int64_t count, int64_t rows, int64_t cols,
+                          int block_rows, uint8_t* q, float* sc, void* stream);
+mx_status fp8_swiglu_quantize128(const void* gu, int in_dtype, int64_t gu_ld, int64_t T, int I, uint8_t* q, float* sc,
+                                 void* stream);
+
+/*
+ * The same cast along the columns, transposed: blocks of 128 rows of one
+ * column, for products whose sum runs over rows (the gradient of weights).
+ * src [rows][cols], rows src_ld elements apart, at the type's alignment.
+ * offsets int32 [E + 1] (device; moe_route's expert_offsets) cuts the rows
+ * into groups, each of which starts at a multiple of 128 columns of q:
+ * group e takes columns [c_e, c_e + ceil(n_e / 128) * 128), c_e the sum of
+ * the groups' before; its last block is filled up with zero codes.  Without
+ * offsets (E = 1) all rows are one group.  q [cols][q_ld], sc [cols][q_ld /
+ * 128], q_ld % 128 == 0 and at least fp8_quantize128_t_cols(rows, E), which
+ * holds any split; columns behind the last group are left as they were.
+ * Rows behind offsets[E] are not read.  E <= 1024, rows < 2^31, q 16-byte,
+ * sc 4-byte aligned, q_ld / 128 * ceil(cols / 64) < 2^24.
+ */
+int64_t   fp8_quantize128_t_cols(int64_t rows, int E);
+mx_status fp8_quantize128_t(const void* src, int src_dtype, int64_t src_ld, int64_t rows, int cols, const int32_t* offsets,
+                            int E, uint8_t* q, float* sc, int64_t q_ld, void* stream);
+
+/*
+ * Dense FP8 product with a scale for each block of 128, the sibling of
+ * fp8_block_gemm on the casts above:
+ *   y[m][n] = sum_b (a_sc[m][b] * w_sc[n'][b]) * sum_{k in block b} a[m][k] * w[n][k]
+ * a E4M3 [M][K], a_sc fp32 [M][ceil(K / 128)]; w E4M3 [N][K], w_sc fp32
+ * [ceil(N / 128)][ceil(K / 128)] with n' = n / 128 (w_rows 128), or
+ * [N][ceil(K / 128)] with n' = n (w_rows 1: e.g. the gradient of weights,
+ * both operands from fp8_quantize128_t).  y [M][N] bf16 (RNE of the fp32
+ * result) or fp32 (y_dtype MX_OUT_*).  A block's sum is one step of the matrix
+ * cores (which cut E4M3 products as fp4_block_gemm describes: a few 1e-6 of
+ * the result's norm); the blocks are added in order in fp32, one fma each, the
+ * same for every M and kernel.  The gradient of a is the product of dy with
+ * the transposed codes and scales of w (tiles of 128 x 128 are the same both
+ * ways).  Any M >= 0, N >= 1, K % 16 == 0, K >= 16; results of more tiles than
+ * one launch holds (about 2^36) return MX_EUNSUPPORTED.  a, w 16-byte
+ * aligned, scales 4-byte, y its type's.
+ */
+mx_status fp8_block128_gemm(const uint8_t* a, const float* a_sc, const uint8_t* w, const float* w_sc, int w_rows, int M, int N,
+                            int K, void* y, int y_dtype, void* stream);
+
+/*
+ * The experts' products in the same format: rows [offsets[e], offsets[e + 1])
+ * of a, which moe_permute has put together, with expert e's weights.
+ * a [R][K], a_sc [R][ceil(K / 128)], w [E][N][K], w_sc [E][ceil(N / 128)]
+ * [ceil(K / 128)], offsets int32 [E + 1] (device, ascending from 0, at most R),
+ * y [R][N].  Rows behind offsets[E] are neither read nor written.  Results of
+ * a row are, bit for bit, those of fp8_block128_gemm with its expert's
+ * weights.  E <= 1024; otherwise as fp8_block128_gemm.
+ */
+mx_status fp8_block128_grouped_gemm(const uint8_t* a, const float* a_sc, int R, const uint8_t* w, const float* w_sc,
+                                    const int32_t* offsets, int E, int N, int K, void* y, int y_dtype, void* stream);
+
+/*
+ * The gradient of the experts' weights:
+ *   dw[e][n][k] = sum over expert e's tokens t of a[n][t] * b[k][t]
+ * a [N][ld] + a_sc [N][ld / 128]: fp8_quantize128_t of the gradient of the
+ * products' rows; b [K][ld] + b_sc: of the rows that went in; both with the
+ * same offsets (int32 [E + 1], device).  dw [E][N][K] bf16 or fp32, written
+ * whole (experts without tokens: +0).  Any N, K >= 1; ld % 128 == 0,
+ * ld < 2^31; E <= 1024.
+ */
+mx_status fp8_block128_grouped_wgrad(const uint8_t* a, const float* a_sc, const uint8_t* b, const float* b_sc, int64_t ld,
+                                     const int32_t* offsets, int E, int N, int K, void* dw, int dw_dtype, void* stream);
+
+/*
  * Shared expert: a dense SwiGLU MLP on every row with block-32 FP8 operands
  * (post #6 "Kernel by kernel against B12X": the shared expert's two kernels
  * per call; TP4 README, settings table, row "Kernels", and its boot-log
