@@ -569,7 +569,8 @@ mx_status fp8_quantize128_t(const void* src, int src_dtype, int64_t src_ld, int6
 
 namespace {
 mx_status b128(const mx::B128Args& a, mx::B128Mode mode, bool w_rows, void* stream) {
-  if (!mx::b128_fits(a, mode)) return MX_EUNSUPPORTED;
+  // rows of a tile are addressed with 32-bit byte offsets
+  if (a.ld > mx::B128_MAX_LD || !mx::b128_fits(a, mode)) return MX_EUNSUPPORTED;
   if (!a.a || !a.a_sc || !a.w || !a.w_sc || !a.y || (mode != mx::B128Mode::dense && !a.offsets)) return MX_EINVAL;
   if (!aligned(a.a, 16) || !aligned(a.w, 16) || !aligned(a.a_sc, 4) || !aligned(a.w_sc, 4) || !aligned(a.offsets, 4) ||
       !aligned(a.y, a.bf16_out ? 2 : 4))

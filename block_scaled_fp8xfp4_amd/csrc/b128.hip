@@ -27,13 +27,6 @@ __device__ __forceinline__ v8i operand8(const u32x4& lo, const u32x4& hi) {
   return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// What a workgroup works on: a matrix of nrows x ncols results over blocks [0, nkb).
-struct B128Task {
-  const uint8_t* x; const float* x_sc; const uint8_t* w; const float* w_sc;
-  int rows, cols, nkb, K;                         // K: elements in the blocks (a multiple of 16)
-  int64_t y0;                                     // first result
-};
-
 // ---------------------------------------------------------------------------
 // Few rows: a workgroup per 16 columns and 16 MT rows.  Its four wavefronts
 // take every fourth block of K, both operands straight to registers, and leave
@@ -138,21 +131,33 @@ __global__ __launch_bounds__(256, 2) void b128_rows_kernel(B128Args A) {
 
 // ---------------------------------------------------------------------------
 // Many rows: BM x BN tiles staged through LDS.  A stage holds one block of K
-// of the tile's rows of both operands, brought by LDS DMA; WM x WN wavefronts
-// of TM x TN 16 x 16 products each.  LDS rows are 128 bytes in 16-byte chunks,
-// the chunk index XORed with the row's low bits, so that 8 rows' reads of one
-// chunk fall on different banks.
-template <int WM, int WN, int TM, int TN, int NST>
+// of the tile's rows of both operands and their scales, brought by LDS DMA;
+// WM x WN wavefronts of TM x TN 16 x 16 products each.  LDS rows are 128 bytes
+// in 16-byte chunks, the chunk index XORed with the row's low bits, so that 8
+// rows' reads of one chunk fall on different banks.
+//
+// A wavefront walks over its TN columns of products: while one column's TM
+// products are in the matrix cores, the column before is multiplied with its
+// scales and added, and the column after is read from LDS.  The stage's one
+// barrier comes before its last column, whose products cover the reads of the
+// next stage's first operands; behind it the stage's buffer is free for DMA.
+template <bool WROWS, int WM, int WN, int TM, int TN, int NST>
 struct B128Shape {
   static constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
-  static constexpr uint32_t OFF_W = BM * 128, STAGE = OFF_W + BN * 128, LDS = STAGE * NST;
-  static constexpr int NX = BM / 8 / NW, NWT = BN / 8 / NW, NV = NX + NWT;    // DMA instructions per wavefront and stage
+  static constexpr int NSR = BM + (WROWS ? BN : WN), NS = (NSR + 64 * NW - 1) / (64 * NW);   // rows of scales; surplus ones repeat the last
+  static constexpr uint32_t OFF_W = BM * 128, OFF_S = OFF_W + BN * 128, STAGE = OFF_S + NS * NW * 256, LDS = STAGE * NST;
+  static constexpr int NX = BM / 8 / NW, NWT = BN / 8 / NW, NV = NX + NWT + NS;    // DMA instructions per wavefront and stage
+  // DMA instructions go out one by one, two products apart, since a wavefront stalls at one while the memory path is still
+  // taking the last: FIRST of them in the column that follows the barrier, the others over SPREAD products of the next stage
+  static constexpr int FIRST = (TM + 1) / 2 < NV ? (TM + 1) / 2 : NV, REST = NV - FIRST;
+  static constexpr int SPREAD = REST * 2 < (TN - 1) * TM ? REST * 2 : (TN - 1) * TM;
   static_assert(NX * NW * 8 == BM && NWT * NW * 8 == BN && LDS <= 160 * 1024 && NV * (NST - 1) < 63, "shape");
+  static_assert(TN % 2 == 0 && (WROWS || 128 % (TN * 16) == 0), "pairs of columns; one tile of weights per wavefront");
 };
 
 template <bool WROWS, B128Mode MODE, int WM, int WN, int TM, int TN, int NST>
 __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) {
-  using S = B128Shape<WM, WN, TM, TN, NST>;
+  using S = B128Shape<WROWS, WM, WN, TM, TN, NST>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4, wm = wave / WN, wn = wave % WN;
@@ -195,53 +200,55 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
     n0 = (int)(in / rows_in) * S::BN;
     rows = (int)min((int64_t)S::BM, A.M - m0);
   }
+  rows = __builtin_amdgcn_readfirstlane(rows);
+  n0 = __builtin_amdgcn_readfirstlane(n0);
   const int cols = min(S::BN, A.N - n0);
   x += m0 * A.ld;
   w += (int64_t)n0 * A.ld;
   x_sc += m0 * A.ld_sc;
 
-  // this lane's DMA sources: rows past the last repeat it
-  const uint8_t* xrow[S::NX];
-  const uint8_t* wrow[S::NWT];
+  // this lane's DMA sources, from the tile's first row on: rows past the last repeat it
+  const uint32_t chunk = ((lane & 7) ^ (lane / 8)) * 16;              // (row % 8 is lane / 8 in every instruction)
+  uint32_t xoff[S::NX], woff[S::NWT];
+  const float* srow[S::NS];
 #pragma unroll
-  for (int i = 0; i < S::NX; ++i) xrow[i] = x + min((i * S::NW + wave) * 8 + lane / 8, rows - 1) * A.ld;
+  for (int i = 0; i < S::NX; ++i) xoff[i] = (uint32_t)min((i * S::NW + wave) * 8 + lane / 8, rows - 1) * (uint32_t)A.ld + chunk;
 #pragma unroll
-  for (int i = 0; i < S::NWT; ++i) wrow[i] = w + min((i * S::NW + wave) * 8 + lane / 8, cols - 1) * A.ld;
-  const int chunk = ((lane & 7) ^ (lane / 8)) * 16;                   // (row % 8 is lane / 8 in every instruction)
-  auto issue = [&](int s) {
-    uint8_t* const to = lds + (s % NST) * S::STAGE;
-    const int k = min(s * 128 + chunk, K - 16);                       // past K: the row's last 16 again, cut later
+  for (int i = 0; i < S::NWT; ++i) woff[i] = (uint32_t)min((i * S::NW + wave) * 8 + lane / 8, cols - 1) * (uint32_t)A.ld + chunk;
 #pragma unroll
-    for (int i = 0; i < S::NX; ++i) dma16_to_lds(xrow[i] + k, to + (i * S::NW + wave) * 1024);
-#pragma unroll
-    for (int i = 0; i < S::NWT; ++i) dma16_to_lds(wrow[i] + k, to + S::OFF_W + (i * S::NW + wave) * 1024);
-  };
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  // zeros in the chunks of x past K, by the lane that brought them
-  auto cut = [&](int s) {
-    if (s * 128 + chunk < K) return;
-#pragma unroll
-    for (int i = 0; i < S::NX; ++i)
-      lds_write(lds0 + (s % NST) * S::STAGE + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
-  };
-  const float* xs[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) xs[i] = x_sc + min((wm * TM + i) * 16 + col, rows - 1) * A.ld_sc;
-  const float* ws[WROWS ? TN * 4 : 1];
-  if (WROWS) {
-#pragma unroll
-    for (int j = 0; j < TN * 4; ++j) ws[WROWS ? j : 0] = w_sc + (int64_t)min(n0 + (wn * TN + j / 4) * 16 + 4 * g + j % 4, A.N - 1) * A.ld_sc;
-  } else {
-    static_assert(WROWS || 128 % (TN * 16) == 0, "one tile of weights per wavefront");
-    ws[0] = w_sc + (int64_t)min((n0 + wn * TN * 16) / 128, (A.N - 1) / 128) * A.ld_sc;
+  for (int i = 0; i < S::NS; ++i) {
+    const int r = (i * S::NW + wave) * 64 + lane, c = min(r - S::BM, WROWS ? S::BN - 1 : WN - 1);
+    const int64_t wr = WROWS ? (int64_t)n0 + min(c, cols - 1) : (n0 + min(c * TN * 16, cols - 1)) / 128;
+    srow[i] = r < S::BM ? x_sc + min(r, rows - 1) * A.ld_sc : w_sc + wr * A.ld_sc;
   }
-  float fx[TM], fw[WROWS ? TN * 4 : 1];
-  auto fetch_scales = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) fx[i] = xs[i][s];
-#pragma unroll
-    for (int j = 0; j < (WROWS ? TN * 4 : 1); ++j) fw[j] = ws[j][s];
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
+  // the d-th DMA instruction of stage s; past: what this lane's chunk reaches past K (the row's last 16 are read again,
+  // and cut when they have landed)
+  auto issue1 = [&](int s, uint32_t buf, int d, uint32_t past) {
+    const int ix = min(max(d - S::NS, 0), S::NX - 1), iw = max(d - S::NS - S::NX, 0);
+    if (d < S::NS) dma4_to_lds(srow[min(d, S::NS - 1)] + s, lds + buf + S::OFF_S + (d * S::NW + wave) * 256);
+    else if (d < S::NS + S::NX) dma16_to_lds(x + (int64_t)s * 128, xoff[ix] - past, lds0 + buf + (ix * S::NW + wave) * 1024);
+    else dma16_to_lds(w + (int64_t)s * 128, woff[iw] - past, lds0 + buf + S::OFF_W + (iw * S::NW + wave) * 1024);
   };
+  const uint32_t over = max((nkb - 1) * 128 + (int)chunk - (K - 16), 0);   // past K in the last stage
+  auto issue = [&](int s, uint32_t buf, int d0, int d1) {
+    const uint32_t past = s == nkb - 1 ? over : 0;
+#pragma unroll
+    for (int d = d0; d < d1; ++d) issue1(s, buf, d, past);
+  };
+  // Stage s has landed for this wavefront (later ones, as many as were asked for, may be on their way); zeros in the
+  // chunks of x past K, by the lane that brought them.
+  auto landed = [&](int s, uint32_t buf) {
+    if (NST > 2 && s + NST - 2 < nkb) wait_vm<S::NV * (NST > 2 ? NST - 2 : 0)>();
+    else wait_vm<0>();
+    if (s == nkb - 1 && over > 0) {
+#pragma unroll
+      for (int i = 0; i < S::NX; ++i) lds_write(lds0 + buf + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
+    }
+    lds_barrier();
+  };
+  auto before = [](uint32_t buf) { return buf == 0 ? S::LDS - S::STAGE : buf - S::STAGE; };
+  auto after = [](uint32_t buf) { return buf + S::STAGE == S::LDS ? 0u : buf + S::STAGE; };
 
   v4f acc[TM][TN];
 #pragma unroll
@@ -252,63 +259,168 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
   const uint32_t c0 = (uint32_t)(g ^ (col & 7)) * 16, c1 = c0 ^ 64;
 
   if (nkb > 0) {
-    fetch_scales(0);
 #pragma unroll
-    for (int s = 0; s < NST - 1; ++s)
-      if (s < nkb) issue(s);
-  }
-  for (int s = 0; s < nkb; ++s) {
-    if (NST > 2 && s + NST - 1 <= nkb) wait_vm<S::NV * (NST > 2 ? NST - 2 : 0)>();
+    for (int s = 0; s + 1 < NST; ++s)
+      if (s < nkb) issue(s, s * S::STAGE, 0, S::NV);
+    if (NST - 1 < nkb) issue(NST - 1, (NST - 1) * S::STAGE, 0, S::FIRST);
+    // the first stage: as landed(0), with part of one stage more on its way
+    if (nkb >= NST) wait_vm<S::NV * (NST - 2) + S::FIRST>();
     else wait_vm<0>();
-    if (s == nkb - 1 && K % 128 != 0) cut(s);
+    if (nkb == 1 && over > 0) {
+#pragma unroll
+      for (int i = 0; i < S::NX; ++i) lds_write(lds0 + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
+    }
     lds_barrier();
-    float sx[TM], sw[WROWS ? TN * 4 : 1];
+    if (wm * TM * 16 >= rows) {                   // nothing of this wavefront's is a result
+      uint32_t buf = 0;
+      if (NST - 1 < nkb) issue(NST - 1, (NST - 1) * S::STAGE, S::FIRST, S::NV);
+      for (int s = 0; s + 1 < nkb; ++s) {
+        landed(s + 1, after(buf));
+        if (s + NST < nkb) issue(s + NST, buf, 0, S::NV);
+        buf = after(buf);
+      }
+    } else {
+      v8i xf[TM], wf[2];                          // operands of a column of products: this one's and the next one's
+      v4f P[2][TM];                               // products on their way, and those of the column before
+      float f[TM], fn[TM], wn_ = 0.f;             // scales of the rows (times the tile's): the stage's, the next one's
+      v4f sw{}, sn{};                             // WROWS: scales of the column's weight rows, of the next one's
+      auto load_x = [&](int i, uint32_t buf) {
+        xf[i] = operand8(lds_read<u32x4>(xa + c0 + buf + i * 2048), lds_read<u32x4>(xa + c1 + buf + i * 2048));
+      };
+      auto load_w = [&](int j, uint32_t buf) {
+        wf[j & 1] = operand8(lds_read<u32x4>(wa + c0 + buf + j * 2048), lds_read<u32x4>(wa + c1 + buf + j * 2048));
+        if (WROWS) sn = lds_read<v4f>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + 4 * g) * 4);
+      };
+      auto load_scales = [&](uint32_t buf) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sx[i] = fx[i];
+        for (int i = 0; i < TM; ++i) fn[i] = lds_read<float>(lds0 + buf + S::OFF_S + ((wm * TM + i) * 16 + col) * 4);
+        if (!WROWS) wn_ = lds_read<float>(lds0 + buf + S::OFF_S + (S::BM + wn) * 4);
+      };
+      // Holds the sums before the branches that follow (no instruction): the compiler would move them behind.
+      auto pin = [&] {
 #pragma unroll
-    for (int j = 0; j < (WROWS ? TN * 4 : 1); ++j) sw[j] = fw[j];
-    if (s + 1 < nkb) fetch_scales(s + 1);
-    if (s + NST - 1 < nkb) issue(s + NST - 1);
-    const uint32_t buf = (s % NST) * S::STAGE;
-    v8i xf[TM];
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      xf[i] = operand8(lds_read<u32x4>(xa + buf + i * 2048 + c0), lds_read<u32x4>(xa + buf + i * 2048 + c1));
+          for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
+      };
+      // Stage s.  MORE 0: there is none after it; 1: there is, and maybe stages to ask for; 2: there are NST + 1 whole ones.
+      auto stage = [&](int s, uint32_t buf, auto more) {
+        constexpr int MORE = decltype(more)::value;
+        const uint32_t nbuf = after(buf);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const v8i wf = operand8(lds_read<u32x4>(wa + buf + j * 2048 + c0), lds_read<u32x4>(wa + buf + j * 2048 + c1));
+        for (int j = 0; j < TN; ++j) {
+          const bool end = j == TN - 1;
+          if (end && MORE == 1) {
+            pin();
+            landed(s + 1, nbuf);
+            if (s + NST < nkb) issue(s + NST, buf, 0, S::NV);
+          }
+          if (end && MORE == 2) {
+            wait_vm<S::NV * (NST - 2)>();
+            lds_barrier();
+          }
+          const v4f sp = sw;                      // of the column before
+          sw = sn;
+          if (!end) load_w(j + 1, buf);
+          else if (MORE) {
+            load_w(0, nbuf);
+            load_scales(nbuf);
+          }
+#pragma unroll
+          for (int i = 0; i < TM; ++i) {
+            P[j & 1][i] = block_product(wf[j & 1], xf[i]);
+            const int jp = j == 0 ? TN - 1 : j - 1;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[i][jp][r] = __builtin_fmaf(P[jp & 1][i][r], WROWS ? f[i] * sp[r] : f[i], acc[i][jp][r]);
+            if (end && MORE) load_x(i, nbuf);
+            if (end && MORE == 2 && i % 2 == 0 && i / 2 < S::FIRST) issue1(s + NST, buf, i / 2, 0);
+            if (!end && MORE == 2 && j * TM + i < S::SPREAD) {
+#pragma unroll
+              for (int d = (j * TM + i) * S::REST / S::SPREAD; d < (j * TM + i + 1) * S::REST / S::SPREAD; ++d)
+                issue1(s + NST - 1, before(buf), S::FIRST + d, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (j == 0) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) f[i] = WROWS ? fn[i] : fn[i] * wn_;
+          }
+        }
+      };
+      // before the first column: products of zero
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const v4f p = block_product(wf, xf[i]);
+        P[(TN - 1) & 1][i] = v4f{0.f, 0.f, 0.f, 0.f};
+        f[i] = 0.f;
+        load_x(i, 0);
+      }
+      load_w(0, 0);
+      load_scales(0);
+      uint32_t buf = 0;
+      int s = 0;
+      for (const int whole = K / 128; s + NST < whole; ++s) {
+        stage(s, buf, Int<2>{});
+        buf = after(buf);
+      }
+      if (s + NST - 1 < nkb) issue(s + NST - 1, before(buf), S::FIRST, S::NV);
+      for (; s + 1 < nkb; ++s) {
+        stage(s, buf, Int<1>{});
+        buf = after(buf);
+      }
+      stage(s, buf, Int<0>{});
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = __builtin_fmaf(p[r], sx[i] * sw[WROWS ? j * 4 + r : 0], acc[i][j][r]);
-      }
+          acc[i][TN - 1][r] = __builtin_fmaf(P[(TN - 1) & 1][i][r], WROWS ? f[i] * sw[r] : f[i], acc[i][TN - 1][r]);
     }
   }
 
+  // Results.  Each wavefront turns 16 rows at a time in its own part of LDS, so that a store instruction writes whole runs
+  // of a row: 16 bytes a lane, at whatever alignment the row has, the row's last piece by elements.
+  constexpr int WC = TN * 16;                                         // columns of a wavefront
+  constexpr uint32_t PITCH = WC * 4 + 16;                             // + 16: rows start on different banks
+  static_assert(S::NW * 16 * PITCH <= S::LDS, "results in LDS");
+  lds_barrier();                                                      // every wavefront has read its operands
+  const uint32_t mine = lds0 + wave * 16 * PITCH;
+  const int nw = min(WC, cols - wn * WC);                             // this wavefront's columns
+  auto store = [&](auto esize) {                                      // bytes of a result
+    constexpr int ESZ = decltype(esize)::value, LPR = WC * ESZ / 16, PER = 16 / ESZ;   // lanes per row, elements per lane
+    constexpr int RPP = 64 / LPR, PASSES = 16 / RPP;                  // rows at a time
+    const int r0 = lane / LPR, c = lane % LPR * PER;
+    const uint32_t from = mine + r0 * PITCH + c * ESZ;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int m = (wm * TM + i) * 16 + col;
-    if (m >= rows) continue;
+    for (int i = 0; i < TM; ++i) {
+      const int mb = (wm * TM + i) * 16;
+      if (mb >= rows) break;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int c = (wn * TN + j) * 16 + 4 * g;
-      const int64_t at = y0 + (m0 + m) * A.N + n0 + c;
-      const v4f& v = acc[i][j];
-      if (c + 4 <= cols) {
-        if (A.bf16_out) *reinterpret_cast<u32x2_a1*>(static_cast<uint16_t*>(A.y) + at) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-        else *reinterpret_cast<u32x4_a1*>(static_cast<float*>(A.y) + at) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (c + r >= cols) continue;
-          if (A.bf16_out) static_cast<uint16_t*>(A.y)[at + r] = (uint16_t)bf16_pair(v[r], 0.0f);
-          else static_cast<float*>(A.y)[at + r] = v[r];
-        }
+      for (int j = 0; j < TN; ++j) {
+        const v4f& v = acc[i][j];
+        const uint32_t at = mine + col * PITCH + (j * 16 + 4 * g) * ESZ;
+        if (ESZ == 2) lds_write(at, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
+        else lds_write(at, v);
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");              // the wavefront's own writes
+      uint8_t* to = static_cast<uint8_t*>(A.y) + (y0 + (m0 + mb + r0) * A.N + n0 + wn * WC + c) * ESZ;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p, to += (int64_t)RPP * A.N * ESZ) {
+        const u32x4 d = lds_read<u32x4>(from + p * RPP * PITCH);
+        if (mb + r0 + p * RPP >= rows) continue;
+        if (c + PER <= nw) *reinterpret_cast<u32x4_a1*>(to) = d;
+        else
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            if (c + e >= nw) continue;
+            if (ESZ == 2) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(d[e / (4 / ESZ)] >> (16 * (e % 2)));
+            else reinterpret_cast<uint32_t*>(to)[e] = d[e / (4 / ESZ)];
+          }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-  }
+  };
+  if (A.bf16_out) store(Int<2>{});
+  else store(Int<4>{});
 }
 
 // Row tiles of `unit` that M rows in E groups can make.
@@ -330,37 +442,36 @@ static int64_t tile_groups(const B128Args& a, B128Mode mode, int bm, int bn) {
 }
 template <bool WROWS, B128Mode MODE, int WM, int WN, int TM, int TN, int NST>
 static void launch_tile(const B128Args& a, hipStream_t stream) {
-  using S = B128Shape<WM, WN, TM, TN, NST>;
+  using S = B128Shape<WROWS, WM, WN, TM, TN, NST>;
   hipLaunchKernelGGL((b128_tile_kernel<WROWS, MODE, WM, WN, TM, TN, NST>), dim3((unsigned)tile_groups(a, MODE, S::BM, S::BN)),
                      dim3(64 * S::NW), 0, stream, a);
 }
 
-enum class B128Kernel { rows16, rows32, t64x64, t128x128 };
+enum class B128Kernel { rows16, rows32, t64x64, t128x128, t256x256 };
 static B128Kernel pick(const B128Args& a, B128Mode mode) {
-  if (mode != B128Mode::wgrad) {
-    const int64_t per = mode == B128Mode::grouped ? ((int64_t)a.M + a.E - 1) / a.E : a.M;   // rows of a matrix, about
-    if (per <= 16) return B128Kernel::rows16;
-    if (per <= 32) return B128Kernel::rows32;
-  }
-  if (mode == B128Mode::dense && tile_groups(a, mode, 128, 128) <= 256) return B128Kernel::t64x64;
-  return B128Kernel::t128x128;
+  if (mode == B128Mode::wgrad) return B128Kernel::t256x256;
+  const int64_t per = mode == B128Mode::grouped ? ((int64_t)a.M + a.E - 1) / a.E : a.M;   // rows of a matrix, about
+  if (per <= 16) return B128Kernel::rows16;
+  if (per <= 32) return B128Kernel::rows32;
+  if (tile_groups(a, mode, 64, 64) <= 512) return B128Kernel::t64x64;
+  if (mode == B128Mode::grouped) return per <= 96 ? B128Kernel::t128x128 : B128Kernel::t256x256;
+  // a round of 256 tiles of 256 x 256 takes about 1.6 times one of 512 of 128 x 128
+  return (tile_groups(a, mode, 256, 256) + 255) / 256 * 8 <= (tile_groups(a, mode, 128, 128) + 511) / 512 * 5 ? B128Kernel::t256x256
+                                                                                                              : B128Kernel::t128x128;
 }
 
 template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args& a, hipStream_t stream) {
-  switch (pick(a, MODE)) {
-    case B128Kernel::rows16:
-      if constexpr (MODE != B128Mode::wgrad) launch_rows<1, WROWS, MODE>(a, stream);
-      return "b128:rows16";
-    case B128Kernel::rows32:
-      if constexpr (MODE != B128Mode::wgrad) launch_rows<2, WROWS, MODE>(a, stream);
-      return "b128:rows32";
-    case B128Kernel::t64x64:
-      if constexpr (MODE == B128Mode::dense) launch_tile<WROWS, MODE, 2, 2, 2, 2, 4>(a, stream);
-      return "b128:tile64x64";
-    default: break;
+  if constexpr (MODE != B128Mode::wgrad) {
+    switch (pick(a, MODE)) {
+      case B128Kernel::rows16: launch_rows<1, WROWS, MODE>(a, stream); return "b128:rows16";
+      case B128Kernel::rows32: launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32";
+      case B128Kernel::t64x64: launch_tile<WROWS, MODE, 2, 2, 2, 2, 4>(a, stream); return "b128:tile64x64";
+      case B128Kernel::t128x128: launch_tile<WROWS, MODE, 2, 2, 4, 4, 2>(a, stream); return "b128:tile128x128";
+      default: break;
+    }
   }
-  launch_tile<WROWS, MODE, 2, 2, 4, 4, 2>(a, stream);
-  return "b128:tile128x128";
+  launch_tile<WROWS, MODE, 4, 2, 4, 8, 2>(a, stream);
+  return "b128:tile256x256";
 }
 
 // A launch holds fewer than 2^32 threads.
@@ -368,8 +479,9 @@ bool b128_fits(const B128Args& a, B128Mode mode) {
   switch (pick(a, mode)) {
     case B128Kernel::rows16: return row_tiles(a, mode, 16) * (((int64_t)a.N + 15) / 16) < int64_t(1) << 24;
     case B128Kernel::rows32: return row_tiles(a, mode, 32) * (((int64_t)a.N + 15) / 16) < int64_t(1) << 24;
-    case B128Kernel::t64x64: return tile_groups(a, mode, 64, 64) < int64_t(1) << 24;
-    default: return tile_groups(a, mode, 128, 128) < int64_t(1) << 24;
+    case B128Kernel::t64x64: return true;
+    case B128Kernel::t128x128: return tile_groups(a, mode, 128, 128) < int64_t(1) << 24;
+    default: return tile_groups(a, mode, 256, 256) < int64_t(1) << 23;
   }
 }
 

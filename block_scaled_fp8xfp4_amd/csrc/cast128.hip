@@ -4,10 +4,9 @@
 //   scale = max(amax, 2^-60) / 448 (fp32 division), code = the E4M3 value nearest to x / scale, ties to even
 // A block that holds an infinity or a NaN has the scale NaN, so every sum over
 // it is NaN too.
+#include "any_device.hpp"
 #include "b128_launch.hpp"
 #include "group_device.hpp"
-#include "lds_device.hpp"
-#include "mx_cast.hpp"
 
 namespace mx {
 
@@ -138,8 +137,9 @@ hipError_t launch_quantize128_tiles(const void* src, bool bf16, int64_t ld, int6
   return hipGetLastError();
 }
 
-// Columns: a workgroup takes 128 rows of one group and 64 columns, turns them in LDS, and four threads per column make
-// its 128 codes, 32 rows each.  A group's rows past its last are zeros.
+// Columns: a workgroup takes 128 rows of one group and 64 columns.  A thread holds four rows of eight columns; the columns'
+// largest values meet in LDS, where 64 threads make the scales; then each thread's codes go to LDS as dwords of four rows,
+// and come out as whole columns of 128 bytes.  A group's rows past its last are zeros.
 constexpr int TCOLS = 64;
 __device__ __forceinline__ float element(const void* p, bool bf16, int64_t i) {
   return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
@@ -148,7 +148,10 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void quantize128_t_kernel(const void* __restrict__ src, int64_t ld, int64_t rows, int cols,
                                                             const int32_t* __restrict__ offsets, int E, uint8_t* __restrict__ q,
                                                             float* __restrict__ sc, int64_t q_ld, uint32_t nct) {
-  __shared__ float t[128][TCOLS + 1];
+  constexpr int PITCH = 33;                                           // dwords per column: 8 columns' writes meet on no bank twice
+  __shared__ __attribute__((aligned(16))) uint32_t part[16][TCOLS];
+  __shared__ __attribute__((aligned(16))) float scale[TCOLS], inv[TCOLS];
+  __shared__ uint32_t code[TCOLS * PITCH];
   const uint32_t b = blockIdx.x / nct, ct = blockIdx.x - b * nct;
   int64_t r0 = (int64_t)b * 128, n = rows - r0;
   if (offsets) {
@@ -158,32 +161,57 @@ __global__ __launch_bounds__(256) void quantize128_t_kernel(const void* __restri
     n = g.rows - g.tile * 128;
   }
   n = min(n, (int64_t)128);
-  const int c0 = ct * TCOLS, c = threadIdx.x & 63;
-  for (int r = threadIdx.x >> 6; r < 128; r += 4) {
-    float v = 0.0f;
-    if (r < n && c0 + c < cols) v = element(src, BF16, (r0 + r) * ld + c0 + c);
-    t[r][c] = v;
+  const int c0 = ct * TCOLS, c = (threadIdx.x & 7) * 8, rq = threadIdx.x >> 3;   // columns c .. c + 7, rows 4 rq .. 4 rq + 3
+  float v[4][8];
+  uint32_t amax[8] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t at = (r0 + rq * 4 + i) * ld + c0 + c;
+    if (rq * 4 + i >= n) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+    } else if (c0 + c + 8 <= cols) {
+      load_any<8>(src, BF16, at, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = c0 + c + e < cols ? element(src, BF16, at + e) : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax[e] = bits_max(amax[e], v[i][e]);
+    amax[e] = max(amax[e], (uint32_t)__builtin_amdgcn_mov_dpp((int)amax[e], 0x128, 0xF, 0xF, false));   // the row's other half
+  }
+  if ((threadIdx.x & 8) == 0) {
+    u32x4* const to = reinterpret_cast<u32x4*>(&part[threadIdx.x >> 4][c]);
+    to[0] = u32x4{amax[0], amax[1], amax[2], amax[3]};
+    to[1] = u32x4{amax[4], amax[5], amax[6], amax[7]};
   }
   __syncthreads();
-  const int col = threadIdx.x >> 2, part = threadIdx.x & 3;           // a quad of lanes per column
-  uint32_t amax = 0;
-  float v[32];
+  if (threadIdx.x < TCOLS) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = t[part * 32 + i][col];
-    amax = bits_max(amax, v[i]);
+    for (int i = 0; i < 16; ++i) m = max(m, part[i][threadIdx.x]);
+    const Scale128 s = scale128(m);
+    scale[threadIdx.x] = s.sc;
+    inv[threadIdx.x] = s.inv;
+    if (c0 + (int)threadIdx.x < cols) sc[(int64_t)(c0 + threadIdx.x) * (q_ld / 128) + b] = s.sc;
   }
-  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xF, 0xF, false));
-  amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x4E, 0xF, 0xF, false));
-  if (c0 + col >= cols) return;
-  const Scale128 s = scale128(amax);
-  uint8_t* const to = q + (int64_t)(c0 + col) * q_ld + (int64_t)b * 128 + part * 32;
+  __syncthreads();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const u32x2 lo = codes8(v + h * 16, s), hi = codes8(v + h * 16 + 8, s);
-    *reinterpret_cast<u32x4*>(to + h * 16) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+  for (int e = 0; e < 8; ++e) {
+    const Scale128 s{scale[c + e], inv[c + e]};
+    code[(c + e) * PITCH + rq] = code_pair(v[0][e], v[1][e], s) | code_pair(v[2][e], v[3][e], s) << 16;
   }
-  if (part == 0) sc[(int64_t)(c0 + col) * (q_ld / 128) + b] = s.sc;
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {                                       // eight lanes write a column
+    const int col = p * 32 + rq, k = (threadIdx.x & 7) * 4;
+    if (c0 + col >= cols) continue;
+    const uint32_t* const from = &code[col * PITCH + k];
+    *reinterpret_cast<u32x4*>(q + (int64_t)(c0 + col) * q_ld + (int64_t)b * 128 + k * 4) = u32x4{from[0], from[1], from[2], from[3]};
+  }
 }
 
 hipError_t launch_quantize128_t(const void* src, bool bf16, int64_t ld, int64_t rows, int cols, const int32_t* offsets,

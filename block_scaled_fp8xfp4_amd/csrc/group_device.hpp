@@ -3,9 +3,23 @@
 // with one load of the offsets and one sum over its lanes, so that the host
 // needs to know only a bound on the number of tiles.
 #pragma once
-#include "mx_device.hpp"
+#include "lds_device.hpp"
 
 namespace mx {
+
+// Sum over the lanes up to and with this one, by DPP (rows of 16, then rows 1 and 3, then the upper half).
+__device__ __forceinline__ uint32_t lanes_upto(uint32_t v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+  };
+  add(Int<0x111>{}, Int<0xF>{});                  // row_shr:1
+  add(Int<0x112>{}, Int<0xF>{});                  // row_shr:2
+  add(Int<0x114>{}, Int<0xF>{});                  // row_shr:4
+  add(Int<0x118>{}, Int<0xF>{});                  // row_shr:8
+  add(Int<0x142>{}, Int<0xA>{});                  // row_bcast:15
+  add(Int<0x143>{}, Int<0xC>{});                  // row_bcast:31
+  return v;
+}
 
 struct GroupTile { int e, tile, first, row0, rows; };    // e < 0: no such tile
 
@@ -23,12 +37,7 @@ __device__ __forceinline__ GroupTile find_tile_of(const int32_t* offsets, int E,
     n[i] = o[i + 1] > o[i] ? (uint32_t)(o[i + 1] - o[i] + unit - 1) / (uint32_t)unit : 0u;
     sum += n[i];
   }
-  uint32_t upto = sum;                             // tiles up to and with this lane's
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint32_t v = __shfl_up(upto, d);
-    upto += lane >= d ? v : 0u;
-  }
+  const uint32_t upto = lanes_upto(sum);           // tiles up to and with this lane's
   const uint64_t past = __ballot(upto > t);
   if (past == 0) return GroupTile{-1, 0, 0, 0, 0};
   uint32_t first = upto - sum;
@@ -67,12 +76,8 @@ __device__ __forceinline__ GroupSpan find_span_of(const int32_t* offsets, int E,
     mine += lane * PER + i == e ? n : 0u;
     prev = o;
   }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    before += __shfl_xor(before, d);
-    mine += __shfl_xor(mine, d);
-  }
-  return GroupSpan{(uint32_t)__builtin_amdgcn_readfirstlane((int)before), (uint32_t)__builtin_amdgcn_readfirstlane((int)mine)};
+  return GroupSpan{(uint32_t)__builtin_amdgcn_readlane((int)lanes_upto(before), 63),
+                   (uint32_t)__builtin_amdgcn_readlane((int)lanes_upto(mine), 63)};
 }
 __device__ __forceinline__ GroupSpan find_span(const int32_t* offsets, int E, int64_t R, int unit, int e) {
   return E <= 256 ? find_span_of<4>(offsets, E, R, unit, e) : find_span_of<16>(offsets, E, R, unit, e);

@@ -5,9 +5,8 @@
 // A slot that is nowhere (slot_pos < 0 or past the rows there are) takes no
 // part.  All of it is memory traffic; every result has one writer and a fixed
 // order of addition, so nothing depends on timing.
+#include "any_device.hpp"
 #include "b128_launch.hpp"
-#include "lds_device.hpp"
-#include "mx_cast.hpp"
 
 namespace mx {
 
@@ -53,45 +52,6 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// N elements from element i on, at any alignment that the type allows.
-template <int N> __device__ __forceinline__ void load_any(const void* p, bool bf16, int64_t i, float* v) {
-  if (N == 1) {
-    v[0] = bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
-  } else if (bf16) {
-    const u32x4 d = *reinterpret_cast<const u32x4_a1*>(static_cast<const uint16_t*>(p) + i);
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      v[2 * j] = __uint_as_float(d[j] << 16);
-      v[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
-    }
-  } else {
-    const u32x4_a1* s = reinterpret_cast<const u32x4_a1*>(static_cast<const float*>(p) + i);
-#pragma unroll
-    for (int q = 0; q < N / 4; ++q) {
-      const u32x4 d = s[q];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * q + j] = __uint_as_float(d[j]);
-    }
-  }
-}
-template <int N> __device__ __forceinline__ void store_any(void* p, bool bf16, int64_t i, const float* v) {
-  if (N == 1) {
-    if (bf16) static_cast<uint16_t*>(p)[i] = (uint16_t)bf16_pair(v[0], 0.0f);
-    else static_cast<float*>(p)[i] = v[0];
-  } else if (bf16) {
-    u32x4 d;
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) d[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
-    *reinterpret_cast<u32x4_a1*>(static_cast<uint16_t*>(p) + i) = d;
-  } else {
-    u32x4_a1* s = reinterpret_cast<u32x4_a1*>(static_cast<float*>(p) + i);
-#pragma unroll
-    for (int q = 0; q < N / 4; ++q)
-      s[q] = u32x4{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                   __float_as_uint(v[4 * q + 3])};
-  }
-}
-
 // A thread per N columns of a token; a row's last piece reaches back to be whole (N = 1 for rows of less than 8).
 template <int N, bool OB, bool YB>
 __global__ __launch_bounds__(256) void unpermute_kernel(UnpermuteArgs A, uint32_t chunks, uint32_t n) {

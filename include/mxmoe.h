@@ -522,8 +522,9 @@ mx_status fp8_quantize128_t(const void* src, int src_dtype, int64_t src_ld, int6
  * the result's norm); the blocks are added in order in fp32, one fma each, the
  * same for every M and kernel.  The gradient of a is the product of dy with
  * the transposed codes and scales of w (tiles of 128 x 128 are the same both
- * ways).  Any M >= 0, N >= 1, K % 16 == 0, K >= 16; results of more tiles than
- * one launch holds (about 2^36) return MX_EUNSUPPORTED.  a, w 16-byte
+ * ways).  Any M >= 0, N >= 1, K % 16 == 0, 16 <= K <= 2^23; results of more
+ * tiles than one launch holds (about 2^32 to 2^39, by the tile) return
+ * MX_EUNSUPPORTED.  a, w 16-byte
  * aligned, scales 4-byte, y its type's.
  */
 mx_status fp8_block128_gemm(const uint8_t* a, const float* a_sc, const uint8_t* w, const float* w_sc, int w_rows, int M, int N,
@@ -548,7 +549,7 @@ mx_status fp8_block128_grouped_gemm(const uint8_t* a, const float* a_sc, int R, 
  * products' rows; b [K][ld] + b_sc: of the rows that went in; both with the
  * same offsets (int32 [E + 1], device).  dw [E][N][K] bf16 or fp32, written
  * whole (experts without tokens: +0).  Any N, K >= 1; ld % 128 == 0,
- * ld < 2^31; E <= 1024.
+ * ld <= 2^23; E <= 1024.
  */
 mx_status fp8_block128_grouped_wgrad(const uint8_t* a, const float* a_sc, const uint8_t* b, const float* b_sc, int64_t ld,
                                      const int32_t* offsets, int E, int N, int K, void* dw, int dw_dtype, void* stream);
