@@ -30,16 +30,17 @@ __device__ __forceinline__ v8i operand8(const u32x4& lo, const u32x4& hi) {
 // ---------------------------------------------------------------------------
 // Few rows: a workgroup per 16 columns and 16 MT rows.  Its four wavefronts
 // take every fourth block of K, both operands straight to registers, and leave
-// each block's products in LDS; then a thread per result adds them up in order.
-constexpr int ROWS_CHUNK = 64;                    // 16 x 16 products held in LDS at a time
-
+// each block's products in LDS; then a thread per result adds them up in
+// order.  What counts is bytes on their way: four workgroups per CU with RING
+// blocks per wavefront.
 template <int MT, bool WROWS, B128Mode MODE>
-__global__ __launch_bounds__(256, 2) void b128_rows_kernel(B128Args A) {
-  constexpr int CH = ROWS_CHUNK / MT;             // blocks of K per chunk
-  constexpr int RING = MT == 1 ? 8 : MT == 2 ? 4 : 2;
-  static_assert(CH / 4 >= RING, "a wavefront's ring is at most its blocks of a chunk");
+__global__ __launch_bounds__(256, 4) void b128_rows_kernel(B128Args A) {
+  constexpr int CH = 32 / MT;                     // blocks of K whose products LDS holds at a time
+  constexpr int RING = MT == 1 ? 4 : 2;
+  constexpr int NS = CH * 16 * MT / 256;          // scales per thread and chunk
+  static_assert(CH % (4 * RING) == 0 && NS * 256 == CH * 16 * MT, "chunks of whole rings, whole scales");
   __shared__ __attribute__((aligned(1024))) float prod[CH][MT][16][16];
-  __shared__ float sa[CH][MT * 16], sw[CH][16];
+  __shared__ float sa[CH][MT * 16], sw[WROWS ? CH : 1][16];           // rows' scales, times the tile's; WROWS: the columns'
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const uint32_t nct = (uint32_t)(((int64_t)A.N + 15) / 16), rt = blockIdx.x / nct;
@@ -63,6 +64,32 @@ __global__ __launch_bounds__(256, 2) void b128_rows_kernel(B128Args A) {
 #pragma unroll
   for (int i = 0; i < MT; ++i) xp[i] = A.a + (m0 + min(i * 16 + col, rows - 1)) * A.ld;
 
+  // scales of the chunk from block b0 on: thread's entries e = block, row (and column)
+  float ra[NS], rw[NS], rc[WROWS ? CH / 16 : 1];
+  auto fetch = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int e = i * 256 + threadIdx.x, b = min(b0 + e / (16 * MT), nkb - 1), m = e % (16 * MT);
+      ra[i] = A.a_sc[(m0 + min(m, rows - 1)) * A.ld_sc + b];
+      rw[i] = WROWS ? 1.0f : w_sc[(int64_t)(n0 / 128) * A.ld_sc + b];
+    }
+    if (WROWS) {
+#pragma unroll
+      for (int i = 0; i < CH / 16; ++i) {
+        const int e = i * 256 + threadIdx.x;
+        rc[WROWS ? i : 0] = w_sc[min(n0 + e % 16, A.N - 1) * A.ld_sc + min(b0 + e / 16, nkb - 1)];
+      }
+    }
+  };
+  auto put = [&] {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) (&sa[0][0])[i * 256 + threadIdx.x] = ra[i] * rw[i];
+    if (WROWS) {
+#pragma unroll
+      for (int i = 0; i < CH / 16; ++i) (&sw[0][0])[i * 256 + threadIdx.x] = rc[WROWS ? i : 0];
+    }
+  };
+
   struct Piece { u32x4 wlo, whi, xlo[MT], xhi[MT]; };
   auto load = [&](Piece& P, int b) {
     const int k = b * 128 + g * 16, k0 = min(k, A.K - 16), k1 = min(k + 64, A.K - 16);   // past K: the row's last 16 again
@@ -84,24 +111,21 @@ __global__ __launch_bounds__(256, 2) void b128_rows_kernel(B128Args A) {
       *reinterpret_cast<v4f*>(&prod[at][i][col][4 * g]) = p;
     }
   };
+  fetch(0);
+  __builtin_amdgcn_sched_barrier(0);              // the scales first: loads arrive in order
   Piece R[RING];
 #pragma unroll
   for (int r = 0; r < RING; ++r)
     if (wave + 4 * r < nkb) load(R[r], wave + 4 * r);
 
+  const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
   float acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = 0.0f;
   for (int b0 = 0; b0 < nkb; b0 += CH) {
     const int nb = min(CH, nkb - b0);
-    for (int e = threadIdx.x; e < nb * 16 * MT; e += 256) {
-      const int b = e / (16 * MT), m = e % (16 * MT);
-      sa[b][m] = A.a_sc[(m0 + min(m, rows - 1)) * A.ld_sc + b0 + b];
-    }
-    for (int e = threadIdx.x; e < nb * 16; e += 256) {
-      const int b = e / 16, c = e % 16;
-      sw[b][c] = w_sc[(WROWS ? (int64_t)min(n0 + c, A.N - 1) : n0 / 128) * A.ld_sc + b0 + b];
-    }
+    put();
+    if (b0 + CH < nkb) fetch(b0 + CH);
 #pragma unroll 1
     for (int at = wave; at < nb; at += 4 * RING) {
 #pragma unroll
@@ -112,14 +136,13 @@ __global__ __launch_bounds__(256, 2) void b128_rows_kernel(B128Args A) {
       }
     }
     lds_barrier();
-    const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
-#pragma unroll 4
+#pragma unroll 8
     for (int b = 0; b < nb; ++b)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i] = __builtin_fmaf(prod[b][i][m][c], sa[b][i * 16 + m] * sw[b][c], acc[i]);
+      for (int i = 0; i < MT; ++i)
+        acc[i] = __builtin_fmaf(prod[b][i][m][c], WROWS ? sa[b][i * 16 + m] * sw[WROWS ? b : 0][c] : sa[b][i * 16 + m], acc[i]);
     if (b0 + CH < nkb) lds_barrier();
   }
-  const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     if (i * 16 + m >= rows || n0 + c >= A.N) continue;

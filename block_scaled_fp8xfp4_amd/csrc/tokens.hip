@@ -64,14 +64,24 @@ __global__ __launch_bounds__(256) void unpermute_kernel(UnpermuteArgs A, uint32_
   float acc[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-  for (int j = 0; j < A.k; ++j) {
-    const int p = pos[j];
-    if (p < 0 || p >= A.o_rows) continue;
-    const float f = A.w ? w[j] : 1.0f;
-    float v[N];
-    load_any<N>(A.o, OB, (int64_t)p * A.H + c, v);
+  constexpr int AT = OB ? 8 : 4;                                      // slots whose rows are on their way at a time
+  for (int j0 = 0; j0 < A.k; j0 += AT) {
+    int p[AT];
+    float f[AT], v[AT][N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+    for (int j = 0; j < AT; ++j) {
+      p[j] = j0 + j < A.k ? pos[j0 + j] : -1;
+      f[j] = A.w && j0 + j < A.k ? w[j0 + j] : 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < AT; ++j)
+      if (p[j] >= 0 && p[j] < A.o_rows) load_any<N>(A.o, OB, (int64_t)p[j] * A.H + c, v[j]);
+#pragma unroll
+    for (int j = 0; j < AT; ++j) {
+      if (p[j] < 0 || p[j] >= A.o_rows) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] = __builtin_fmaf(f[j], v[j][e], acc[e]);
+    }
   }
   store_any<N>(A.y, YB, (int64_t)t * A.H + c, acc);
 }

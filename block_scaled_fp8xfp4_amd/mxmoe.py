@@ -542,9 +542,9 @@ def fp4_dense_ffn(x, x_sc, x_fmt, w13, w13_sc, w2, w2_sc, mid_fmt, y, ws, stream
 # ------------------------------ experts' tokens, products with a scale for each block of 128
 # Checked as the dense block's calls are: one question that holds for right
 # tensors, and only where it does not the checks that find out what is wrong.
-def _plain(d, dtype, shape, *tensors):
-    """Every tensor is contiguous, of this type and shape, on device d."""
-    return all(t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == d for t in tensors)
+def _is(t, d, dtype, shape):
+    """t is contiguous, of this type and shape, on device d."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == d
 
 
 def _blocks(n):
@@ -563,8 +563,8 @@ def moe_permute(x, slot_pos, out, x_sc=None, out_sc=None, stream=None):
     if (x_sc is None) != (out_sc is None):
         raise ValueError(f"{name}: x_sc and out_sc come together")
     B = 0 if x_sc is None else _two(name, "x_sc", x_sc)[1]
-    if not (x.is_contiguous() and _plain(d, x.dtype, (R, H), out) and _plain(d, t.i32, (T, k), slot_pos) and
-            (x_sc is None or _plain(d, x_sc.dtype, (T, B), x_sc) and _plain(d, x_sc.dtype, (R, B), out_sc)) and
+    if not (x.is_contiguous() and _is(out, d, x.dtype, (R, H)) and _is(slot_pos, d, t.i32, (T, k)) and
+            (x_sc is None or _is(x_sc, d, x_sc.dtype, (T, B)) and _is(out_sc, d, x_sc.dtype, (R, B))) and
             t.current_device() == d):
         ld = _rows(name, "x", x, (x.dtype,), T, H) if T > 1 else H
         if T == 1 and H > 1 and x.stride(1) != 1:
@@ -591,8 +591,8 @@ def moe_unpermute(o, w, slot_pos, y, stream=None):
     k = _two(name, "slot_pos", slot_pos)[1]
     _int(name, T, k, H)
     d = o.get_device()
-    if not (o.dtype in t.ins and y.dtype in t.outs and o.is_contiguous() and _plain(d, y.dtype, (T, H), y) and
-            _plain(d, t.i32, (T, k), slot_pos) and (w is None or _plain(d, t.f32, (T, k), w)) and t.current_device() == d):
+    if not (o.dtype in t.ins and y.dtype in t.outs and o.is_contiguous() and _is(y, d, y.dtype, (T, H)) and
+            _is(slot_pos, d, t.i32, (T, k)) and (w is None or _is(w, d, t.f32, (T, k))) and t.current_device() == d):
         _packed(name, "o", o, t.ins, (R, H))
         _packed(name, "y", y, t.outs, (T, H))
         _packed(name, "slot_pos", slot_pos, (t.i32,), (T, k))
@@ -615,9 +615,9 @@ def moe_unpermute_grad(dy, o, w, slot_pos, d_o=None, dw=None, stream=None):
     R = _two(name, "o", rows)[0]
     _int(name, T, k, H)
     d = dy.get_device()
-    if not (dy.dtype in t.ins and rows.dtype in t.ins and dy.is_contiguous() and _plain(d, rows.dtype, (R, H), rows) and
-            (d_o is None or _plain(d, rows.dtype, (R, H), d_o)) and _plain(d, t.i32, (T, k), slot_pos) and
-            (w is None or _plain(d, t.f32, (T, k), w)) and (dw is None or _plain(d, t.f32, (T, k), dw)) and
+    if not (dy.dtype in t.ins and rows.dtype in t.ins and dy.is_contiguous() and _is(rows, d, rows.dtype, (R, H)) and
+            (d_o is None or _is(d_o, d, rows.dtype, (R, H))) and _is(slot_pos, d, t.i32, (T, k)) and
+            (w is None or _is(w, d, t.f32, (T, k))) and (dw is None or _is(dw, d, t.f32, (T, k))) and
             t.current_device() == d):
         _packed(name, "dy", dy, t.ins, (T, H))
         _packed(name, "o", rows, t.ins, (R, H))
@@ -645,7 +645,7 @@ def fp8_quantize128(src, q, sc, block_rows=1, stream=None):
     head, (rows, cols) = tuple(src.shape[:-2]), src.shape[-2:]
     count, d, ld = head[0] if head else 1, src.get_device(), cols
     shape = head + (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
-    if not (src.dtype in t.ins and src.is_contiguous() and _plain(d, t.u8, src.shape, q) and _plain(d, t.f32, shape, sc) and
+    if not (src.dtype in t.ins and src.is_contiguous() and _is(q, d, t.u8, src.shape) and _is(sc, d, t.f32, shape) and
             t.current_device() == d):
         if head:
             _packed(name, "src", src, t.ins, src.shape)
@@ -666,8 +666,8 @@ def fp8_swiglu_quantize128(gu, q, sc, stream=None):
     I = two_i // 2
     _int(name, I)
     d, ld = gu.get_device(), two_i
-    if not (gu.dtype in t.ins and gu.is_contiguous() and two_i == 2 * I and _plain(d, t.u8, (T, I), q) and
-            _plain(d, t.f32, (T, _blocks(I)), sc) and t.current_device() == d):
+    if not (gu.dtype in t.ins and gu.is_contiguous() and two_i == 2 * I and _is(q, d, t.u8, (T, I)) and
+            _is(sc, d, t.f32, (T, _blocks(I))) and t.current_device() == d):
         ld = _rows(name, "gu", gu, t.ins, T, 2 * I)
         _packed(name, "q", q, (t.u8,), (T, I))
         _packed(name, "sc", sc, (t.f32,), (T, _blocks(I)))
@@ -690,8 +690,8 @@ def fp8_quantize128_t(src, q, sc, offsets=None, stream=None):
     q_ld = _two(name, "q", q)[1]
     _int(name, rows, cols)
     E, d, ld = 1 if offsets is None else offsets.numel() - 1, src.get_device(), cols
-    if not (src.dtype in t.ins and src.is_contiguous() and q_ld % 128 == 0 and _plain(d, t.u8, (cols, q_ld), q) and
-            _plain(d, t.f32, (cols, q_ld // 128), sc) and (offsets is None or _plain(d, t.i32, (E + 1,), offsets)) and
+    if not (src.dtype in t.ins and src.is_contiguous() and q_ld % 128 == 0 and _is(q, d, t.u8, (cols, q_ld)) and
+            _is(sc, d, t.f32, (cols, q_ld // 128)) and (offsets is None or _is(offsets, d, t.i32, (E + 1,))) and
             t.current_device() == d):
         if rows > 1:
             ld = _rows(name, "src", src, t.ins, rows, cols)
@@ -717,8 +717,8 @@ def fp8_block128_gemm(a, a_sc, w, w_sc, y, stream=None):
     M = _two(name, "y", y)[0]
     _int(name, M, N, K)
     sn, nb, d = _two(name, "w_sc", w_sc)[0], _blocks(K), y.get_device()
-    if not (y.dtype in t.outs and _plain(d, y.dtype, (M, N), y) and _plain(d, t.u8, (M, K), a) and _plain(d, t.u8, (N, K), w) and
-            _plain(d, t.f32, (M, nb), a_sc) and (sn == N or sn == _blocks(N)) and _plain(d, t.f32, (sn, nb), w_sc) and
+    if not (y.dtype in t.outs and _is(y, d, y.dtype, (M, N)) and _is(a, d, t.u8, (M, K)) and _is(w, d, t.u8, (N, K)) and
+            _is(a_sc, d, t.f32, (M, nb)) and (sn == N or sn == _blocks(N)) and _is(w_sc, d, t.f32, (sn, nb)) and
             t.current_device() == d):
         _packed(name, "a", a, (t.u8,), (M, K))
         _packed(name, "w", w, (t.u8,), (N, K))
@@ -740,9 +740,9 @@ def fp8_block128_grouped_gemm(a, a_sc, w, w_sc, offsets, y, stream=None):
     R = _two(name, "y", y)[0]
     _int(name, R, N, K)
     nb, d = _blocks(K), y.get_device()
-    if not (y.dtype in t.outs and _plain(d, y.dtype, (R, N), y) and _plain(d, t.u8, (R, K), a) and _plain(d, t.u8, (E, N, K), w) and
-            _plain(d, t.f32, (R, nb), a_sc) and _plain(d, t.f32, (E, _blocks(N), nb), w_sc) and
-            _plain(d, t.i32, (E + 1,), offsets) and t.current_device() == d):
+    if not (y.dtype in t.outs and _is(y, d, y.dtype, (R, N)) and _is(a, d, t.u8, (R, K)) and _is(w, d, t.u8, (E, N, K)) and
+            _is(a_sc, d, t.f32, (R, nb)) and _is(w_sc, d, t.f32, (E, _blocks(N), nb)) and
+            _is(offsets, d, t.i32, (E + 1,)) and t.current_device() == d):
         _packed(name, "a", a, (t.u8,), (R, K))
         _packed(name, "w", w, (t.u8,), (E, N, K))
         _packed(name, "a_sc", a_sc, (t.f32,), (R, nb))
@@ -765,9 +765,9 @@ def fp8_block128_grouped_wgrad(a, a_sc, b, b_sc, offsets, dw, stream=None):
     ld = _two(name, "a", a)[1]
     _int(name, N, K, ld)
     nb, d = ld // 128, dw.get_device()
-    if not (dw.dtype in t.outs and ld % 128 == 0 and _plain(d, dw.dtype, (E, N, K), dw) and _plain(d, t.u8, (N, ld), a) and
-            _plain(d, t.u8, (K, ld), b) and _plain(d, t.f32, (N, nb), a_sc) and _plain(d, t.f32, (K, nb), b_sc) and
-            _plain(d, t.i32, (E + 1,), offsets) and t.current_device() == d):
+    if not (dw.dtype in t.outs and ld % 128 == 0 and _is(dw, d, dw.dtype, (E, N, K)) and _is(a, d, t.u8, (N, ld)) and
+            _is(b, d, t.u8, (K, ld)) and _is(a_sc, d, t.f32, (N, nb)) and _is(b_sc, d, t.f32, (K, nb)) and
+            _is(offsets, d, t.i32, (E + 1,)) and t.current_device() == d):
         if ld % 128:
             raise ValueError(f"{name}: a has {ld} columns, a multiple of 128 is expected")
         _packed(name, "a", a, (t.u8,), (N, ld))
