@@ -37,8 +37,8 @@ template <int MT, bool WROWS, B128Mode MODE>
 __global__ __launch_bounds__(256, 4) void b128_rows_kernel(B128Args A) {
   constexpr int CH = 32 / MT;                     // blocks of K whose products LDS holds at a time
   constexpr int RING = MT == 1 ? 4 : 2;
-  constexpr int NS = CH * 16 * MT / 256;          // scales per thread and chunk
-  static_assert(CH % (4 * RING) == 0 && NS * 256 == CH * 16 * MT, "chunks of whole rings, whole scales");
+  constexpr int NS = CH * 16 * MT / 256, NC = CH * 16 / 256;  // rows' and columns' scales per thread and chunk
+  static_assert(CH % (4 * RING) == 0 && NS * 256 == CH * 16 * MT && NC > 0, "chunks of whole rings, whole scales");
   __shared__ __attribute__((aligned(1024))) float prod[CH][MT][16][16];
   __shared__ float sa[CH][MT * 16], sw[WROWS ? CH : 1][16];           // rows' scales, times the tile's; WROWS: the columns'
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256, 4) void b128_rows_kernel(B128Args A) {
   for (int i = 0; i < MT; ++i) xp[i] = A.a + (m0 + min(i * 16 + col, rows - 1)) * A.ld;
 
   // scales of the chunk from block b0 on: thread's entries e = block, row (and column)
-  float ra[NS], rw[NS], rc[WROWS ? CH / 16 : 1];
+  float ra[NS], rw[NS], rc[WROWS ? NC : 1];
   auto fetch = [&](int b0) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256, 4) void b128_rows_kernel(B128Args A) {
     }
     if (WROWS) {
 #pragma unroll
-      for (int i = 0; i < CH / 16; ++i) {
+      for (int i = 0; i < NC; ++i) {
         const int e = i * 256 + threadIdx.x;
         rc[WROWS ? i : 0] = w_sc[min(n0 + e % 16, A.N - 1) * A.ld_sc + min(b0 + e / 16, nkb - 1)];
       }
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(256, 4) void b128_rows_kernel(B128Args A) {
     for (int i = 0; i < NS; ++i) (&sa[0][0])[i * 256 + threadIdx.x] = ra[i] * rw[i];
     if (WROWS) {
 #pragma unroll
-      for (int i = 0; i < CH / 16; ++i) (&sw[0][0])[i * 256 + threadIdx.x] = rc[WROWS ? i : 0];
+      for (int i = 0; i < NC; ++i) (&sw[0][0])[i * 256 + threadIdx.x] = rc[WROWS ? i : 0];
     }
   };
 
@@ -470,26 +470,51 @@ static void launch_tile(const B128Args& a, hipStream_t stream) {
                      dim3(64 * S::NW), 0, stream, a);
 }
 
-enum class B128Kernel { rows16, rows32, t64x64, t128x128, t256x256 };
+// Which kernel, by how many workgroups each shape gives and what a round of them takes.  us, weights from memory:
+//   rows of 4096 x 4096:    1 rows16 8.2, 64 x 64 11.4; 32 rows32 9.8, 64 x 64 12.0; 48 64 x 64 13.5, rows32 13.7
+//           16384 x 4096:   1 rows16 18.8, 64 x 64 12.9 (DMA keeps more bytes on their way than registers)
+//           1152 x 4096:    48 rows16 7.1, 64 x 64 10.2; 96 rows32 8.7, 64 x 64 10.3
+//           4096 x 4096:    256 64 x 64 14.9, 64 x 128 20.5; 512 64 x 128 20.6, 64 x 64 23.3; 1024 64 x 256 29.9, 64 x 128 32.2,
+//                           128 x 256 36.9; 2048 128 x 256 41.2, 256 x 256 59.6; 4096 256 x 256 68.0, 128 x 256 79.5
+//   256 experts' 1152 x 4096, rows each: 4 64 x 64 209, 64 x 128 225, rows16 248; 32 64 x 128 248, 64 x 64 254, 128 x 256 259;
+//                           64 128 x 256 275, 64 x 128 295; 256 256 x 256 492, 128 x 256 510; one row of all: 12.7 rows16 and 64 x 64
+//   256 experts' 4096 x 576, 48 rows of all: 64 x 128 95, 64 x 64 126, rows16 187 (few blocks of K: what a workgroup begins
+//                           and ends with counts)
+enum class B128Kernel { rows16, rows32, t64x64, t64x128, t64x256, t128x256, t256x256 };
+static int64_t row_groups(const B128Args& a, B128Mode mode, int rows) { return row_tiles(a, mode, rows) * (((int64_t)a.N + 15) / 16); }
 static B128Kernel pick(const B128Args& a, B128Mode mode) {
   if (mode == B128Mode::wgrad) return B128Kernel::t256x256;
-  const int64_t per = mode == B128Mode::grouped ? ((int64_t)a.M + a.E - 1) / a.E : a.M;   // rows of a matrix, about
-  if (per <= 16) return B128Kernel::rows16;
-  if (per <= 32) return B128Kernel::rows32;
-  if (tile_groups(a, mode, 64, 64) <= 512) return B128Kernel::t64x64;
-  if (mode == B128Mode::grouped) return per <= 96 ? B128Kernel::t128x128 : B128Kernel::t256x256;
-  // a round of 256 tiles of 256 x 256 takes about 1.6 times one of 512 of 128 x 128
-  return (tile_groups(a, mode, 256, 256) + 255) / 256 * 8 <= (tile_groups(a, mode, 128, 128) + 511) / 512 * 5 ? B128Kernel::t256x256
-                                                                                                              : B128Kernel::t128x128;
+  if (row_groups(a, mode, 16) <= 256) return B128Kernel::rows16;
+  if (mode == B128Mode::grouped) {
+    if (row_groups(a, mode, 16) <= 512) return B128Kernel::rows16;
+    const int64_t per = ((int64_t)a.M + a.E - 1) / a.E;               // rows of an expert, about; most fit one tile
+    if (per <= 44) return per <= 24 && (a.K > 2048 || a.N <= 64) ? B128Kernel::t64x64 : B128Kernel::t64x128;
+    return per <= 96 ? B128Kernel::t128x256 : B128Kernel::t256x256;
+  }
+  if (a.M > 16 && row_groups(a, mode, 32) <= 256) return B128Kernel::rows32;
+  if (a.M <= 16 && row_groups(a, mode, 16) <= 512) return B128Kernel::rows16;
+  // the smallest tiles that are one round; past them rounds of the largest two, at 5 to 3
+  if (tile_groups(a, mode, 64, 64) <= 256) return B128Kernel::t64x64;
+  if (tile_groups(a, mode, 64, 128) <= 256) return B128Kernel::t64x128;
+  if (tile_groups(a, mode, 64, 256) <= 256) return B128Kernel::t64x256;
+  return (tile_groups(a, mode, 256, 256) + 255) / 256 * 5 <= (tile_groups(a, mode, 128, 256) + 255) / 256 * 3 ? B128Kernel::t256x256
+                                                                                                              : B128Kernel::t128x256;
 }
 
 template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args& a, hipStream_t stream) {
   if constexpr (MODE != B128Mode::wgrad) {
     switch (pick(a, MODE)) {
       case B128Kernel::rows16: launch_rows<1, WROWS, MODE>(a, stream); return "b128:rows16";
-      case B128Kernel::rows32: launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32";
       case B128Kernel::t64x64: launch_tile<WROWS, MODE, 2, 2, 2, 2, 4>(a, stream); return "b128:tile64x64";
-      case B128Kernel::t128x128: launch_tile<WROWS, MODE, 2, 2, 4, 4, 2>(a, stream); return "b128:tile128x128";
+      case B128Kernel::t64x128: launch_tile<WROWS, MODE, 2, 4, 2, 2, 3>(a, stream); return "b128:tile64x128";
+      case B128Kernel::t128x256: launch_tile<WROWS, MODE, 2, 4, 4, 4, 3>(a, stream); return "b128:tile128x256";
+      default: break;
+    }
+  }
+  if constexpr (MODE == B128Mode::dense) {
+    switch (pick(a, MODE)) {
+      case B128Kernel::rows32: launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32";
+      case B128Kernel::t64x256: launch_tile<WROWS, MODE, 1, 4, 4, 4, 3>(a, stream); return "b128:tile64x256";
       default: break;
     }
   }
@@ -497,14 +522,15 @@ template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args
   return "b128:tile256x256";
 }
 
-// A launch holds fewer than 2^32 threads.
+// A launch holds fewer than 2^32 threads (at most 512 a workgroup).
 bool b128_fits(const B128Args& a, B128Mode mode) {
+  constexpr int64_t MOST = int64_t(1) << 23;
   switch (pick(a, mode)) {
-    case B128Kernel::rows16: return row_tiles(a, mode, 16) * (((int64_t)a.N + 15) / 16) < int64_t(1) << 24;
-    case B128Kernel::rows32: return row_tiles(a, mode, 32) * (((int64_t)a.N + 15) / 16) < int64_t(1) << 24;
-    case B128Kernel::t64x64: return true;
-    case B128Kernel::t128x128: return tile_groups(a, mode, 128, 128) < int64_t(1) << 24;
-    default: return tile_groups(a, mode, 256, 256) < int64_t(1) << 23;
+    case B128Kernel::t64x64: return tile_groups(a, mode, 64, 64) < MOST;
+    case B128Kernel::t64x128: return tile_groups(a, mode, 64, 128) < MOST;
+    case B128Kernel::t128x256: return tile_groups(a, mode, 128, 256) < MOST;
+    case B128Kernel::t256x256: return tile_groups(a, mode, 256, 256) < MOST;
+    default: return true;                                             // few
   }
 }
 

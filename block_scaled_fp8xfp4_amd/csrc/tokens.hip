@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void unpermute_kernel(UnpermuteArgs A, uint32_
   float acc[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-  constexpr int AT = OB ? 8 : 4;                                      // slots whose rows are on their way at a time
+  constexpr int AT = 4;                                      // slots whose rows are on their way at a time
   for (int j0 = 0; j0 < A.k; j0 += AT) {
     int p[AT];
     float f[AT], v[AT][N];

@@ -168,3 +168,120 @@ class DenseFFN:
             y = torch.empty((x.shape[0], self.H), dtype=dtype, device=x.device)
             mxmoe.fp4_dense_ffn(x, x_sc, x_fmt, *self.weights, self.mid_fmt, y, self.ws, stream)
         return y
+
+
+def quantize128(v, block_rows=1, stream=None):
+    """fp32/bf16 device tensor [rows, cols] or [count, rows, cols] -> (E4M3 codes, fp32 scales of blocks block_rows x 128)."""
+    with _under(stream):
+        rows, cols = v.shape[-2:]
+        q = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
+        sc = torch.empty(v.shape[:-2] + (rows if block_rows == 1 else -(-rows // 128), -(-cols // 128)), dtype=torch.float32,
+                         device=v.device)
+        mxmoe.fp8_quantize128(v, q, sc, block_rows, stream)
+    return q, sc
+
+
+def quantize128_t(v, offsets=None, stream=None):
+    """fp32/bf16 device tensor [rows, cols] -> (E4M3 codes [cols, ld], fp32 scales [cols, ld / 128]) of its columns in blocks
+    of 128 rows; offsets: int32 [E + 1], groups of rows that start at multiples of 128."""
+    with _under(stream):
+        rows, cols = v.shape
+        ld = mxmoe.fp8_quantize128_t_cols(rows, 1 if offsets is None else offsets.numel() - 1)
+        q = torch.empty((cols, ld), dtype=torch.uint8, device=v.device)
+        sc = torch.empty((cols, ld // 128), dtype=torch.float32, device=v.device)
+        mxmoe.fp8_quantize128_t(v, q, sc, offsets, stream)
+    return q, sc
+
+
+class FP8Linear128:
+    """A dense projection with FP8 weights [N, K] + scales [ceil(N / 128), ceil(K / 128)] (fp8_block128_gemm), and its
+    gradients.  Rows come and go in bf16 or fp32 and are cast here; train: the transposed weights are laid out too."""
+
+    def __init__(self, w, w_sc, train=False):
+        self.w, self.w_sc = w, w_sc
+        self.w_t, self.w_t_sc = (w.t().contiguous(), w_sc.t().contiguous()) if train else (None, None)
+
+    def _product(self, x, w, w_sc, dtype, stream):
+        with _under(stream):
+            q, sc = quantize128(x, stream=stream)
+            y = torch.empty((x.shape[0], w.shape[0]), dtype=dtype, device=x.device)
+            mxmoe.fp8_block128_gemm(q, sc, w, w_sc, y, stream)
+        return y
+
+    def __call__(self, x, dtype=torch.bfloat16, stream=None):
+        return self._product(x, self.w, self.w_sc, dtype, stream)
+
+    def input_grad(self, dy, dtype=torch.bfloat16, stream=None):
+        if self.w_t is None:
+            raise ValueError("FP8Linear128: made without train")
+        return self._product(dy, self.w_t, self.w_t_sc, dtype, stream)
+
+    def weight_grad(self, dy, x, dtype=torch.float32, stream=None):
+        """dy^T x [N, K], both cast along their rows."""
+        with _under(stream):
+            a, a_sc = quantize128_t(dy, stream=stream)
+            b, b_sc = quantize128_t(x, stream=stream)
+            dw = torch.empty((dy.shape[1], x.shape[1]), dtype=dtype, device=x.device)
+            if x.shape[0] == 0:
+                return dw.zero_()
+            mxmoe.fp8_block128_gemm(a, a_sc, b, b_sc, dw, stream)
+        return dw
+
+
+class ExpertLinear128:
+    """The experts' projections [E, N, K] + scales [E, ceil(N / 128), ceil(K / 128)] of rows sorted by expert (offsets: a
+    Route's), and their gradients; rows in bf16 or fp32, cast here.  Rows behind offsets[E] are undefined in what comes out."""
+
+    def __init__(self, w, w_sc, train=False):
+        self.w, self.w_sc = w, w_sc
+        self.w_t, self.w_t_sc = (w.transpose(1, 2).contiguous(), w_sc.transpose(1, 2).contiguous()) if train else (None, None)
+
+    def _product(self, x, w, w_sc, offsets, dtype, stream):
+        with _under(stream):
+            q, sc = quantize128(x, stream=stream)
+            y = torch.empty((x.shape[0], w.shape[1]), dtype=dtype, device=x.device)
+            mxmoe.fp8_block128_grouped_gemm(q, sc, w, w_sc, offsets, y, stream)
+        return y
+
+    def __call__(self, x, offsets, dtype=torch.bfloat16, stream=None):
+        return self._product(x, self.w, self.w_sc, offsets, dtype, stream)
+
+    def input_grad(self, dy, offsets, dtype=torch.bfloat16, stream=None):
+        if self.w_t is None:
+            raise ValueError("ExpertLinear128: made without train")
+        return self._product(dy, self.w_t, self.w_t_sc, offsets, dtype, stream)
+
+    def weight_grad(self, dy, x, offsets, dtype=torch.float32, stream=None):
+        with _under(stream):
+            a, a_sc = quantize128_t(dy, offsets, stream)
+            b, b_sc = quantize128_t(x, offsets, stream)
+            dw = torch.empty(self.w.shape, dtype=dtype, device=x.device)
+            mxmoe.fp8_block128_grouped_wgrad(a, a_sc, b, b_sc, offsets, dw, stream)
+        return dw
+
+
+class ExpertFFN128:
+    """The routed experts' SwiGLU FFN with FP8 weights, w13 [E, 2I, H] (gate, then up) and w2 [E, H, I] with scales of 128 x
+    128: rows cast and sorted by expert (moe_permute), gate/up, SwiGLU, down, and back with the routing weights
+    (moe_unpermute).  The gate/up values and the experts' outputs are kept in bf16 between the launches."""
+
+    def __init__(self, w13, w13_sc, w2, w2_sc):
+        self.w13, self.w13_sc, self.w2, self.w2_sc = w13, w13_sc, w2, w2_sc
+
+    def __call__(self, x, route, dtype=torch.float32, stream=None):
+        T, H = x.shape
+        R, I = T * route.slot_pos.shape[1], self.w2.shape[2]
+        with _under(stream):
+            def new(*shape, dtype=torch.uint8):
+                return torch.empty(shape, dtype=dtype, device=x.device)
+            q, sc = quantize128(x, stream=stream)
+            xs, xs_sc = new(R, H), new(R, sc.shape[1], dtype=torch.float32)
+            mxmoe.moe_permute(q, route.slot_pos, xs, sc, xs_sc, stream)
+            gu = new(R, 2 * I, dtype=torch.bfloat16)
+            mxmoe.fp8_block128_grouped_gemm(xs, xs_sc, self.w13, self.w13_sc, route.offsets, gu, stream)
+            a, a_sc = new(R, I), new(R, -(-I // 128), dtype=torch.float32)
+            mxmoe.fp8_swiglu_quantize128(gu, a, a_sc, stream)
+            o, y = new(R, H, dtype=torch.bfloat16), new(T, H, dtype=dtype)
+            mxmoe.fp8_block128_grouped_gemm(a, a_sc, self.w2, self.w2_sc, route.offsets, o, stream)
+            mxmoe.moe_unpermute(o, route.w, route.slot_pos, y, stream)
+        return y

@@ -163,6 +163,21 @@ def test_product_in_order(M, N, K, w_rows):
     assert np.array_equal(gemm(*args, BF16).float().cpu().numpy(), ref.bf16(want))
 
 
+@pytest.mark.parametrize("w_rows", [128, 1])
+@pytest.mark.parametrize("M,N,K,variant", [(9, 4100, 400, "rows16"), (31, 4080, 272, "rows32"), (300, 1030, 656, "tile64x64"),
+                                           (1030, 1100, 400, "tile64x128"), (2000, 1300, 272, "tile64x256"),
+                                           (3001, 1500, 528, "tile128x256"), (6001, 1502, 400, "tile256x256"),
+                                           (6000, 1500, 128, "tile256x256"), (6000, 1500, 16, "tile256x256")])
+def test_every_kernel_in_order(M, N, K, variant, w_rows):
+    rng = np.random.default_rng(M + N + K)
+    a, w = ref.whole_codes(rng, M, K), ref.whole_codes(rng, N, K)
+    a_sc, w_sc = ref.short_scales(rng, M, blocks(K)), ref.short_scales(rng, -(-N // w_rows), blocks(K))
+    want = ref.in_order(a, a_sc, w, w_sc, w_rows)
+    args = [dev(v) for v in (a, a_sc, w, w_sc)]
+    assert np.array_equal(gemm(*args, F32).cpu().numpy(), want) and mxmoe.last_variant() == "b128:" + variant
+    assert np.array_equal(gemm(*args, BF16).float().cpu().numpy(), ref.bf16(want))
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_product_long(M):
     rng = np.random.default_rng(M)
@@ -194,16 +209,17 @@ def test_product_of_cast_values(M, N, K):
 def test_a_row_does_not_depend_on_the_others():
     """The same bits alone, in few rows and in many: every kernel adds in the same order."""
     rng = np.random.default_rng(8)
-    N, K = 520, 1168
+    N, K = 1100, 1168
     a, a_sc = [dev(v) for v in ref.cast(loud(rng, 700, K), 1, B)]
+    a, a_sc = a.repeat(25, 1), a_sc.repeat(25, 1)
     w, w_sc = [dev(v) for v in ref.cast(rng.standard_normal((N, K)), B, B)]
     variants, full = set(), gemm(a, a_sc, w, w_sc, F32)
-    for M in (1, 2, 15, 16, 17, 31, 33, 48, 64, 65, 100, 129, 200, 257, 400, 700):
+    for M in (1, 2, 15, 16, 17, 31, 33, 48, 64, 65, 100, 129, 200, 257, 400, 700, 1200, 2500, 4000, 9000, 17000):
         y = gemm(a[-M:].contiguous(), a_sc[-M:].contiguous(), w, w_sc, F32)
         variants.add(mxmoe.last_variant())
         assert torch.equal(y, full[-M:]), M
     print(sorted(variants), flush=True)
-    assert len(variants) >= 3
+    assert len(variants) == 7
 
 
 def test_nan_scales_reach_their_rows_only():
@@ -230,7 +246,8 @@ def ragged(rng, E, R):
 
 @pytest.mark.parametrize("E,R,more,N,K", [(1, 1, 0, 16, 128), (1, 300, 7, 130, 272), (3, 5, 2, 20, 48), (8, 8, 0, 200, 1040),
                                           (5, 70, 3, 65, 400), (16, 400, 9, 100, 256), (16, 3000, 100, 144, 272), (257, 1, 0, 33, 144),
-                                          (257, 900, 5, 20, 144), (1024, 40, 0, 16, 16), (7, 0, 12, 40, 144), (4, 900, 0, 300, 656)])
+                                          (257, 900, 5, 20, 144), (1024, 40, 0, 16, 16), (7, 0, 12, 40, 144), (4, 900, 0, 300, 656),
+                                          (16, 1000, 30, 300, 400), (16, 300, 5, 520, 2064), (64, 1100, 0, 130, 528)])
 def test_grouped_product_in_order(E, R, more, N, K):
     rng = np.random.default_rng(E + R)
     bounds = ragged(rng, E, R)
@@ -243,6 +260,7 @@ def test_grouped_product_in_order(E, R, more, N, K):
             want[i:j] = ref.in_order(a[i:j], a_sc[i:j], w[e], w_sc[e], B)
     args = [dev(v) for v in (a, a_sc, w, w_sc)]
     assert np.array_equal(grouped(*args, bounds, F32).cpu().numpy(), want)
+    print(mxmoe.last_variant(), flush=True)
     assert np.array_equal(grouped(*args, bounds, BF16).float().cpu().numpy(), ref.bf16(want))
 
 
