@@ -587,7 +587,7 @@ mx_status fp8_block128_gemm(const uint8_t* a, const float* a_sc, const uint8_t* 
                             int K, void* y, int y_dtype, void* stream) {
   if (M < 0 || N < 1 || K < 16 || K % 16 != 0 || !out_dtype(y_dtype) || (w_rows != 1 && w_rows != mx::B128)) return MX_EINVAL;
   if (M == 0) { g_variant = "b128:empty"; return MX_OK; }
-  return b128(mx::B128Args{a, a_sc, w, w_sc, K, (K - 1) / 128 + 1, M, N, K, nullptr, 1, y, y_dtype == MX_OUT_BF16},
+  return b128(mx::B128Args{a, a_sc, w, w_sc, K, (K - 1) / 128 + 1, M, N, K, nullptr, 1, y, y_dtype == MX_OUT_BF16, false},
               mx::B128Mode::dense, w_rows == 1, stream);
 }
 
@@ -595,14 +595,14 @@ mx_status fp8_block128_grouped_gemm(const uint8_t* a, const float* a_sc, int R, 
                                     const int32_t* offsets, int E, int N, int K, void* y, int y_dtype, void* stream) {
   if (R < 0 || E < 1 || E > mx::MAX_E || N < 1 || K < 16 || K % 16 != 0 || !out_dtype(y_dtype)) return MX_EINVAL;
   if (R == 0) { g_variant = "b128:empty"; return MX_OK; }
-  return b128(mx::B128Args{a, a_sc, w, w_sc, K, (K - 1) / 128 + 1, R, N, K, offsets, E, y, y_dtype == MX_OUT_BF16},
+  return b128(mx::B128Args{a, a_sc, w, w_sc, K, (K - 1) / 128 + 1, R, N, K, offsets, E, y, y_dtype == MX_OUT_BF16, false},
               mx::B128Mode::grouped, false, stream);
 }
 
 mx_status fp8_block128_grouped_wgrad(const uint8_t* a, const float* a_sc, const uint8_t* b, const float* b_sc, int64_t ld,
                                      const int32_t* offsets, int E, int N, int K, void* dw, int dw_dtype, void* stream) {
   if (ld < 0 || ld % 128 != 0 || ld >= int64_t(1) << 31 || E < 1 || E > mx::MAX_E || N < 1 || K < 1 || !out_dtype(dw_dtype)) return MX_EINVAL;
-  return b128(mx::B128Args{a, a_sc, b, b_sc, ld, ld / 128, N, K, (int)ld, offsets, E, dw, dw_dtype == MX_OUT_BF16},
+  return b128(mx::B128Args{a, a_sc, b, b_sc, ld, ld / 128, N, K, (int)ld, offsets, E, dw, dw_dtype == MX_OUT_BF16, false},
               mx::B128Mode::wgrad, true, stream);
 }
 

@@ -164,11 +164,13 @@ __global__ __launch_bounds__(256, 4) void b128_rows_kernel(B128Args A) {
 // scales and added, and the column after is read from LDS.  The stage's one
 // barrier comes before its last column, whose products cover the reads of the
 // next stage's first operands; behind it the stage's buffer is free for DMA.
+
 template <bool WROWS, int WM, int WN, int TM, int TN, int NST>
 struct B128Shape {
   static constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
   static constexpr int NSR = BM + (WROWS ? BN : WN), NS = (NSR + 64 * NW - 1) / (64 * NW);   // rows of scales; surplus ones repeat the last
-  static constexpr uint32_t OFF_W = BM * 128, OFF_S = OFF_W + BN * 128, STAGE = OFF_S + NS * NW * 256, LDS = STAGE * NST;
+  static constexpr uint32_t OFF_W = BM * 128, OFF_S = OFF_W + BN * 128, STAGE = OFF_S + NS * NW * 256;
+  static constexpr uint32_t LDS = STAGE * NST;
   static constexpr int NX = BM / 8 / NW, NWT = BN / 8 / NW, NV = NX + NWT + NS;    // DMA instructions per wavefront and stage
   // DMA instructions go out one by one, two products apart, since a wavefront stalls at one while the memory path is still
   // taking the last: FIRST of them in the column that follows the barrier, the others over SPREAD products of the next stage
@@ -185,26 +187,38 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4, wm = wave / WN, wn = wave % WN;
   const int nct = (int)(((int64_t)A.N + S::BN - 1) / S::BN);
+
+  // The tile that the workgroup is at.
   int64_t m0, y0 = 0;                             // first row of the operand; first result of the matrix
-  int n0, rows, nkb = (A.K - 1) / 128 + 1, K = A.K;
-  const uint8_t *x = A.a, *w = A.w;
-  const float *x_sc = A.a_sc, *w_sc = A.w_sc;
+  int n0, rows, cols, nkb, K;
+  const uint8_t *x, *w;
+  const float *xs, *ws;
+  // this lane's DMA sources, from the tile's first row on: rows past the last repeat it
+  uint32_t xoff[S::NX], woff[S::NWT], soff[S::NS];
+  const int chunk = ((lane & 7) ^ (lane / 8)) * 16;                   // (row % 8 is lane / 8 in every instruction)
+  const uint32_t seq = blockIdx.x / XCDS;         // of this XCD's tiles
+  xs = A.a_sc;
+  ws = A.w_sc;
+  x = A.a;
+  w = A.w;
+  K = A.K;
+  nkb = (K - 1) / 128 + 1;
   if (MODE == B128Mode::grouped) {
     // an XCD takes a row tile with all of its column tiles: its rows stay in that L2
-    const uint32_t seq = blockIdx.x / XCDS, rt = seq / nct * XCDS + blockIdx.x % XCDS;
+    const uint32_t rt = seq / nct * XCDS + blockIdx.x % XCDS;
     const GroupTile t = find_tile(A.offsets, A.E, A.M, S::BM, rt);
     if (t.e < 0) return;
     m0 = t.row0 + (int64_t)t.tile * S::BM;
     rows = min(S::BM, t.rows - t.tile * S::BM);
     n0 = (int)(seq % nct) * S::BN;
     w += (int64_t)t.e * A.N * A.K;
-    w_sc += (int64_t)t.e * ((A.N - 1) / 128 + 1) * nkb;
+    ws += (int64_t)t.e * ((A.N - 1) / 128 + 1) * nkb;
   } else {
     // XCD-aware order: each XCD takes a run of consecutive tiles, which go down 8 row tiles before the next column tile
     const int nrt = (int)(((int64_t)A.M + S::BM - 1) / S::BM);
     const uint32_t per_e = (uint32_t)nrt * nct, tiles = per_e * (MODE == B128Mode::wgrad ? A.E : 1), per = (tiles + XCDS - 1) / XCDS;
-    uint32_t t = blockIdx.x % XCDS * per + blockIdx.x / XCDS;
-    if (blockIdx.x / XCDS >= per || t >= tiles) return;
+    uint32_t t = blockIdx.x % XCDS * per + seq;
+    if (seq >= per || t >= tiles) return;
     if (MODE == B128Mode::wgrad) {
       const int e = (int)(t / per_e);
       t -= e * per_e;
@@ -214,8 +228,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       K = nkb * 128;
       x += (int64_t)first * 128;
       w += (int64_t)first * 128;
-      x_sc += first;
-      w_sc += first;
+      xs += first;
+      ws += first;
       y0 = (int64_t)e * A.M * A.N;
     }
     const uint32_t grp = t / (8u * nct), in = t - grp * 8u * nct, rows_in = min(8u, nrt - grp * 8u);
@@ -225,62 +239,64 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
   }
   rows = __builtin_amdgcn_readfirstlane(rows);
   n0 = __builtin_amdgcn_readfirstlane(n0);
-  const int cols = min(S::BN, A.N - n0);
+  cols = min(S::BN, A.N - n0);
   x += m0 * A.ld;
   w += (int64_t)n0 * A.ld;
-  x_sc += m0 * A.ld_sc;
-
-  // this lane's DMA sources, from the tile's first row on: rows past the last repeat it
-  const uint32_t chunk = ((lane & 7) ^ (lane / 8)) * 16;              // (row % 8 is lane / 8 in every instruction)
-  uint32_t xoff[S::NX], woff[S::NWT];
-  const float* srow[S::NS];
+  xs += m0 * A.ld_sc;
+  ws += (int64_t)(WROWS ? n0 : n0 / 128) * A.ld_sc;
 #pragma unroll
-  for (int i = 0; i < S::NX; ++i) xoff[i] = (uint32_t)min((i * S::NW + wave) * 8 + lane / 8, rows - 1) * (uint32_t)A.ld + chunk;
+  for (int i = 0; i < S::NX; ++i) xoff[i] = (uint32_t)min((i * S::NW + wave) * 8 + lane / 8, rows - 1) * (uint32_t)A.ld + (uint32_t)chunk;
 #pragma unroll
-  for (int i = 0; i < S::NWT; ++i) woff[i] = (uint32_t)min((i * S::NW + wave) * 8 + lane / 8, cols - 1) * (uint32_t)A.ld + chunk;
+  for (int i = 0; i < S::NWT; ++i) woff[i] = (uint32_t)min((i * S::NW + wave) * 8 + lane / 8, cols - 1) * (uint32_t)A.ld + (uint32_t)chunk;
 #pragma unroll
   for (int i = 0; i < S::NS; ++i) {
     const int r = (i * S::NW + wave) * 64 + lane, c = min(r - S::BM, WROWS ? S::BN - 1 : WN - 1);
-    const int64_t wr = WROWS ? (int64_t)n0 + min(c, cols - 1) : (n0 + min(c * TN * 16, cols - 1)) / 128;
-    srow[i] = r < S::BM ? x_sc + min(r, rows - 1) * A.ld_sc : w_sc + wr * A.ld_sc;
+    const int wr = WROWS ? min(c, cols - 1) : (n0 % 128 + min(c * TN * 16, cols - 1)) / 128;
+    soff[i] = (uint32_t)(r < S::BM ? min(r, rows - 1) : wr) * (uint32_t)A.ld_sc * 4;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
-  // the d-th DMA instruction of stage s; past: what this lane's chunk reaches past K (the row's last 16 are read again,
-  // and cut when they have landed)
+  // the d-th DMA instruction of stage s; past: what this lane's chunk reaches past K (the row's last 16 are read again, and
+  // cut when they have landed)
   auto issue1 = [&](int s, uint32_t buf, int d, uint32_t past) {
     const int ix = min(max(d - S::NS, 0), S::NX - 1), iw = max(d - S::NS - S::NX, 0);
-    if (d < S::NS) dma4_to_lds(srow[min(d, S::NS - 1)] + s, lds + buf + S::OFF_S + (d * S::NW + wave) * 256);
+    if (d < S::NS)                                // 64 rows of scales are all x's or all w's
+      dma4_to_lds(((d * S::NW + wave) * 64 < S::BM ? xs : ws) + s, soff[min(d, S::NS - 1)], lds0 + buf + S::OFF_S + (d * S::NW + wave) * 256);
     else if (d < S::NS + S::NX) dma16_to_lds(x + (int64_t)s * 128, xoff[ix] - past, lds0 + buf + (ix * S::NW + wave) * 1024);
     else dma16_to_lds(w + (int64_t)s * 128, woff[iw] - past, lds0 + buf + S::OFF_W + (iw * S::NW + wave) * 1024);
   };
-  const uint32_t over = max((nkb - 1) * 128 + (int)chunk - (K - 16), 0);   // past K in the last stage
+  auto reach = [&] {                              // past K in the last stage
+    const int lane = fresh(threadIdx.x) & 63;
+    return max((nkb - 1) * 128 + ((lane & 7) ^ (lane / 8)) * 16 - (K - 16), 0);
+  };
   auto issue = [&](int s, uint32_t buf, int d0, int d1) {
-    const uint32_t past = s == nkb - 1 ? over : 0;
+    const uint32_t past = s == nkb - 1 ? reach() : 0;
 #pragma unroll
     for (int d = d0; d < d1; ++d) issue1(s, buf, d, past);
   };
-  // Stage s has landed for this wavefront (later ones, as many as were asked for, may be on their way); zeros in the
-  // chunks of x past K, by the lane that brought them.
+  // zeros in the chunks of x past K, by the lane that brought them
+  auto cut = [&](int s, uint32_t buf) {
+    if (s != nkb - 1 || K % 128 == 0 || reach() == 0) return;
+#pragma unroll
+    for (int i = 0; i < S::NX; ++i) lds_write(lds0 + buf + (i * S::NW + wave) * 1024 + (fresh(threadIdx.x) & 63) * 16, u32x4{0, 0, 0, 0});
+  };
+  // Stage s has landed for this wavefront (later ones, as many as were asked for, may be on their way).
   auto landed = [&](int s, uint32_t buf) {
     if (NST > 2 && s + NST - 2 < nkb) wait_vm<S::NV * (NST > 2 ? NST - 2 : 0)>();
     else wait_vm<0>();
-    if (s == nkb - 1 && over > 0) {
-#pragma unroll
-      for (int i = 0; i < S::NX; ++i) lds_write(lds0 + buf + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
-    }
+    cut(s, buf);
     lds_barrier();
   };
-  auto before = [](uint32_t buf) { return buf == 0 ? S::LDS - S::STAGE : buf - S::STAGE; };
-  auto after = [](uint32_t buf) { return buf + S::STAGE == S::LDS ? 0u : buf + S::STAGE; };
+  auto before = [](uint32_t buf) { return buf == 0 ? (NST - 1) * S::STAGE : buf - S::STAGE; };
+  auto after = [](uint32_t buf) { return buf + S::STAGE == NST * S::STAGE ? 0u : buf + S::STAGE; };
+
+  const uint32_t xa = lds0 + (wm * TM * 16 + col) * 128, wa = lds0 + S::OFF_W + (wn * TN * 16 + col) * 128;
+  const uint32_t c0 = (uint32_t)(g ^ (col & 7)) * 16, c1 = c0 ^ 64;
 
   v4f acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  const uint32_t xa = lds0 + (wm * TM * 16 + col) * 128, wa = lds0 + S::OFF_W + (wn * TN * 16 + col) * 128;
-  const uint32_t c0 = (uint32_t)(g ^ (col & 7)) * 16, c1 = c0 ^ 64;
-
   if (nkb > 0) {
 #pragma unroll
     for (int s = 0; s + 1 < NST; ++s)
@@ -289,10 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
     // the first stage: as landed(0), with part of one stage more on its way
     if (nkb >= NST) wait_vm<S::NV * (NST - 2) + S::FIRST>();
     else wait_vm<0>();
-    if (nkb == 1 && over > 0) {
-#pragma unroll
-      for (int i = 0; i < S::NX; ++i) lds_write(lds0 + (i * S::NW + wave) * 1024 + lane * 16, u32x4{0, 0, 0, 0});
-    }
+    cut(0, 0);
     lds_barrier();
     if (wm * TM * 16 >= rows) {                   // nothing of this wavefront's is a result
       uint32_t buf = 0;
@@ -306,13 +319,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       v8i xf[TM], wf[2];                          // operands of a column of products: this one's and the next one's
       v4f P[2][TM];                               // products on their way, and those of the column before
       float f[TM], fn[TM], wn_ = 0.f;             // scales of the rows (times the tile's): the stage's, the next one's
-      v4f sw{}, sn{};                             // WROWS: scales of the column's weight rows, of the next one's
+      v4f sn{};                                   // WROWS: scales of the column's weight rows
       auto load_x = [&](int i, uint32_t buf) {
         xf[i] = operand8(lds_read<u32x4>(xa + c0 + buf + i * 2048), lds_read<u32x4>(xa + c1 + buf + i * 2048));
       };
       auto load_w = [&](int j, uint32_t buf) {
         wf[j & 1] = operand8(lds_read<u32x4>(wa + c0 + buf + j * 2048), lds_read<u32x4>(wa + c1 + buf + j * 2048));
-        if (WROWS) sn = lds_read<v4f>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + 4 * g) * 4);
       };
       auto load_scales = [&](uint32_t buf) {
 #pragma unroll
@@ -333,6 +345,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           const bool end = j == TN - 1;
+          const v4f sp = sn;                      // of the column before
+          if (WROWS) sn = lds_read<v4f>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + 4 * g) * 4);
           if (end && MORE == 1) {
             pin();
             landed(s + 1, nbuf);
@@ -342,8 +356,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
             wait_vm<S::NV * (NST - 2)>();
             lds_barrier();
           }
-          const v4f sp = sw;                      // of the column before
-          sw = sn;
           if (!end) load_w(j + 1, buf);
           else if (MORE) {
             load_w(0, nbuf);
@@ -396,50 +408,57 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][TN - 1][r] = __builtin_fmaf(P[(TN - 1) & 1][i][r], WROWS ? f[i] * sw[r] : f[i], acc[i][TN - 1][r]);
+          acc[i][TN - 1][r] = __builtin_fmaf(P[(TN - 1) & 1][i][r], WROWS ? f[i] * sn[r] : f[i], acc[i][TN - 1][r]);
     }
   }
 
-  // Results.  Each wavefront turns 16 rows at a time in its own part of LDS, so that a store instruction writes whole runs
-  // of a row: 16 bytes a lane, at whatever alignment the row has, the row's last piece by elements.
-  constexpr int WC = TN * 16;                                         // columns of a wavefront
-  constexpr uint32_t PITCH = WC * 4 + 16;                             // + 16: rows start on different banks
-  static_assert(S::NW * 16 * PITCH <= S::LDS, "results in LDS");
+  // Results.  Each wavefront turns 16 rows of 128 bytes at a time in its own part of LDS, so that a store instruction writes
+  // whole runs of a row: 16 bytes a lane, at whatever alignment the row has, the row's last piece by elements.
   lds_barrier();                                                      // every wavefront has read its operands
+  const int nw = min(TN * 16, cols - wn * TN * 16);                   // this wavefront's columns
+  const int64_t y_ = y0 + m0 * A.N + n0 + wn * TN * 16;
+  constexpr uint32_t PITCH = 128 + 16;                                // + 16: rows start on different banks
+  const int lane_ = fresh(threadIdx.x) & 63, col_ = lane_ & 15, g_ = lane_ >> 4;
   const uint32_t mine = lds0 + wave * 16 * PITCH;
-  const int nw = min(WC, cols - wn * WC);                             // this wavefront's columns
+  static_assert(S::NW * 16 * PITCH <= S::LDS, "results in LDS");
   auto store = [&](auto esize) {                                      // bytes of a result
-    constexpr int ESZ = decltype(esize)::value, LPR = WC * ESZ / 16, PER = 16 / ESZ;   // lanes per row, elements per lane
+    constexpr int ESZ = decltype(esize)::value, PER = 16 / ESZ;       // elements per lane
+    constexpr int JS = TN * 16 * ESZ < 128 ? TN : 128 / ESZ / 16, LPR = JS * 16 * ESZ / 16;   // products and lanes per run
     constexpr int RPP = 64 / LPR, PASSES = 16 / RPP;                  // rows at a time
-    const int r0 = lane / LPR, c = lane % LPR * PER;
+    const int r0 = lane_ / LPR, c = lane_ % LPR * PER;
     const uint32_t from = mine + r0 * PITCH + c * ESZ;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int mb = (wm * TM + i) * 16;
       if (mb >= rows) break;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const v4f& v = acc[i][j];
-        const uint32_t at = mine + col * PITCH + (j * 16 + 4 * g) * ESZ;
-        if (ESZ == 2) lds_write(at, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
-        else lds_write(at, v);
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");              // the wavefront's own writes
-      uint8_t* to = static_cast<uint8_t*>(A.y) + (y0 + (m0 + mb + r0) * A.N + n0 + wn * WC + c) * ESZ;
+      for (int j0 = 0; j0 < TN; j0 += JS) {
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p, to += (int64_t)RPP * A.N * ESZ) {
-        const u32x4 d = lds_read<u32x4>(from + p * RPP * PITCH);
-        if (mb + r0 + p * RPP >= rows) continue;
-        if (c + PER <= nw) *reinterpret_cast<u32x4_a1*>(to) = d;
-        else
+        for (int j = j0; j < j0 + JS; ++j) {
+          const v4f& v = acc[i][j];
+          const uint32_t at = mine + col_ * PITCH + ((j - j0) * 16 + 4 * g_) * ESZ;
+          if (ESZ == 2) lds_write(at, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
+          else lds_write(at, v);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");            // the wavefront's own writes
+        uint8_t* to = static_cast<uint8_t*>(A.y) + (y_ + (int64_t)(mb + r0) * A.N + j0 * 16 + c) * ESZ;
 #pragma unroll
-          for (int e = 0; e < PER; ++e) {
-            if (c + e >= nw) continue;
-            if (ESZ == 2) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(d[e / (4 / ESZ)] >> (16 * (e % 2)));
-            else reinterpret_cast<uint32_t*>(to)[e] = d[e / (4 / ESZ)];
-          }
+        for (int p = 0; p < PASSES; ++p, to += (int64_t)RPP * A.N * ESZ) {
+          const u32x4 d = lds_read<u32x4>(from + p * RPP * PITCH);
+          if (mb + r0 + p * RPP >= rows) continue;
+          if (j0 * 16 + c + PER <= nw) {
+            if (A.far) __builtin_nontemporal_store(d, reinterpret_cast<u32x4_a1*>(to));
+            else *reinterpret_cast<u32x4_a1*>(to) = d;
+          } else
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+              if (j0 * 16 + c + e >= nw) continue;
+              if (ESZ == 2) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(d[e / (4 / ESZ)] >> (16 * (e % 2)));
+              else reinterpret_cast<uint32_t*>(to)[e] = d[e / (4 / ESZ)];
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
   };
   if (A.bf16_out) store(Int<2>{});
@@ -466,8 +485,8 @@ static int64_t tile_groups(const B128Args& a, B128Mode mode, int bm, int bn) {
 template <bool WROWS, B128Mode MODE, int WM, int WN, int TM, int TN, int NST>
 static void launch_tile(const B128Args& a, hipStream_t stream) {
   using S = B128Shape<WROWS, WM, WN, TM, TN, NST>;
-  hipLaunchKernelGGL((b128_tile_kernel<WROWS, MODE, WM, WN, TM, TN, NST>), dim3((unsigned)tile_groups(a, MODE, S::BM, S::BN)),
-                     dim3(64 * S::NW), 0, stream, a);
+  const int64_t n = tile_groups(a, MODE, S::BM, S::BN);
+  hipLaunchKernelGGL((b128_tile_kernel<WROWS, MODE, WM, WN, TM, TN, NST>), dim3((unsigned)n), dim3(64 * S::NW), 0, stream, a);
 }
 
 // Which kernel, by how many workgroups each shape gives and what a round of them takes.  us, weights from memory:
@@ -534,7 +553,15 @@ bool b128_fits(const B128Args& a, B128Mode mode) {
   }
 }
 
-hipError_t launch_b128(const B128Args& a, B128Mode mode, bool w_rows, hipStream_t stream, const char** variant) {
+// Results of more than 64 MB go past the caches: nothing finds them there, and what they would push out is read again
+// (64 experts' 1152 x 2048 gradients of 512 tokens each 172 us from 199, 256 experts' rows of 8192 x 8 by 1152 x 4096 504
+// from 515).
+static bool far_results(const B128Args& a, B128Mode mode) {
+  return (int64_t)a.M * a.N * (mode == B128Mode::wgrad ? a.E : 1) * (a.bf16_out ? 2 : 4) > int64_t(64) << 20;
+}
+
+hipError_t launch_b128(B128Args a, B128Mode mode, bool w_rows, hipStream_t stream, const char** variant) {
+  a.far = far_results(a, mode);
   if (mode == B128Mode::grouped) *variant = launch_of<false, B128Mode::grouped>(a, stream);
   else if (mode == B128Mode::wgrad) *variant = launch_of<true, B128Mode::wgrad>(a, stream);
   else if (w_rows) *variant = launch_of<true, B128Mode::dense>(a, stream);

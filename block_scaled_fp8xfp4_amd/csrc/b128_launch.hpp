@@ -47,10 +47,11 @@ struct B128Args {
   int M, N, K;                                    // M: rows in all (grouped), or one matrix's
   const int32_t* offsets; int E;                  // groups: of rows, or of K (weight gradient); NULL: none
   void* y; bool bf16_out;
+  bool far;                                       // set by launch_b128: results go past the caches
 };
 constexpr int64_t B128_MAX_LD = int64_t(1) << 23;
 enum class B128Mode { dense, grouped, wgrad };
 bool b128_fits(const B128Args& a, B128Mode mode);   // whether one launch holds it
-hipError_t launch_b128(const B128Args& a, B128Mode mode, bool w_rows, hipStream_t stream, const char** variant);
+hipError_t launch_b128(B128Args a, B128Mode mode, bool w_rows, hipStream_t stream, const char** variant);
 
 }  // namespace mx

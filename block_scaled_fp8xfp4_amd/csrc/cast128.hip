@@ -55,6 +55,44 @@ __device__ __forceinline__ uint32_t row16_max_bits(uint32_t m) {
   return m;
 }
 
+// SwiGLU without double arithmetic where the result cannot depend on it.  Near values (fp32) are within 2^-20 of the values
+// that the cast is defined on, so a block's largest value is one of those whose near value is within 2^-19 of the largest
+// near one: one evaluation in double, in the lanes that hold such a one, gives the scale.  A code is that of a near value
+// times the reciprocal of the scale if it does not change within NEAR_EPS of it (2^-20 and the roundings of the reciprocal
+// and the product).  About one wavefront in 50 holds a code that does, or two such values in one lane, or a block out of
+// the range in which near values are good; it takes the double form.
+constexpr float NEAR_EPS = 1.25f * 9.5367431640625e-07f;
+struct Near128 { bool sure; Scale128 s; u32x2 codes; };
+__device__ __forceinline__ u32x2 codes8_of(const float* v, float f) {
+  uint32_t d[2];
+  codes_scaled<false, 8>(v, f, d);
+  return u32x2{d[0], d[1]};
+}
+__device__ __forceinline__ Near128 swiglu_near128(const float* g, const float* u, bool in) {
+  float a[8], amax = 0.0f, gmin = 0.0f, gbest = 0.0f, ubest = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    a[e] = in ? swiglu_near(g[e], u[e]) : 0.0f;
+    const bool more = __builtin_fabsf(a[e]) > amax;
+    gbest = more ? g[e] : gbest;
+    ubest = more ? u[e] : ubest;
+    amax = near_max(amax, a[e]);
+    gmin = in ? fminf(gmin, g[e]) : gmin;
+  }
+  const uint32_t top = row16_max_bits(__float_as_uint(amax) & 0x7FFFFFFFu);        // NaN is the largest
+  const float most = __uint_as_float(top), edge = most * (1.0f - 1.9073486328125e-06f);
+  int n = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) n += __builtin_fabsf(a[e]) >= edge;
+  bool sure = gmin > SWIGLU_MIN_G && most >= 3.5e-18f && most <= 1.3e36f && n <= 1;   // 2^-58, 2^120
+  uint32_t exact = 0;
+  if (n == 1) exact = __float_as_uint(swiglu(gbest, ubest)) & 0x7FFFFFFFu;
+  const Scale128 s = scale128(row16_max_bits(exact));
+  const u32x2 lo = codes8_of(a, s.inv * (1.0f - NEAR_EPS)), hi = codes8_of(a, s.inv * (1.0f + NEAR_EPS));
+  sure = sure && lo[0] == hi[0] && lo[1] == hi[1];
+  return Near128{sure, s, lo};
+}
+
 // Rows: 16 lanes hold a block, eight columns each; those past the row's end hold zeros and write nothing.
 template <bool BF16, bool SWIGLU>
 __global__ __launch_bounds__(256) void quantize128_rows_kernel(const void* __restrict__ src, int64_t ld, uint32_t n, uint32_t cols,
@@ -63,22 +101,26 @@ __global__ __launch_bounds__(256) void quantize128_rows_kernel(const void* __res
   if (i >= n) return;                                                 // whole blocks are in or out
   const uint32_t r = i / (nb * 16), c = (i - r * nb * 16) * 8;
   const bool in = c < cols;
-  float v[8];
-  uint32_t amax = 0;
-  if (in) {
-    load8(src, BF16, (int64_t)r * ld + c, v);
-    if (SWIGLU) {
-      float u[8];
-      load8(src, BF16, (int64_t)r * ld + cols + c, u);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h)                                     // four at a time: the double form is long
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e / 4 == h) v[e] = swiglu(v[e], u[e]);
+  float v[8] = {};
+  if (in) load8(src, BF16, (int64_t)r * ld + c, v);
+  if (SWIGLU) {
+    float u[8] = {};
+    if (in) load8(src, BF16, (int64_t)r * ld + cols + c, u);
+    const Near128 near = swiglu_near128(v, u, in);
+    if (__all(near.sure)) {
+      if (in) *reinterpret_cast<u32x2*>(q + (int64_t)r * cols + c) = near.codes;
+      if ((i & 15) == 0) sc[i >> 4] = near.s.sc;
+      return;
     }
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h)                                       // four at a time: the double form is long
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = bits_max(amax, v[e]);
+      for (int e = 0; e < 8; ++e)
+        if (e / 4 == h) v[e] = in ? swiglu(v[e], u[e]) : 0.0f;
   }
+  uint32_t amax = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = bits_max(amax, v[e]);
   const Scale128 s = scale128(row16_max_bits(amax));
   if (in) *reinterpret_cast<u32x2*>(q + (int64_t)r * cols + c) = codes8(v, s);
   if ((i & 15) == 0) sc[i >> 4] = s.sc;

@@ -26,7 +26,7 @@ struct GroupTile { int e, tile, first, row0, rows; };    // e < 0: no such tile
 // PER experts a lane (64 PER >= E).
 template <int PER>
 __device__ __forceinline__ GroupTile find_tile_of(const int32_t* offsets, int E, int64_t R, int unit, uint32_t t) {
-  const int lane = threadIdx.x & 63;
+  const int lane = fresh(threadIdx.x) & 63;
   int o[PER + 1];
   // what the offsets say is kept inside the R rows that there are
 #pragma unroll
@@ -65,7 +65,7 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int E, in
 struct GroupSpan { uint32_t first, n; };
 template <int PER>
 __device__ __forceinline__ GroupSpan find_span_of(const int32_t* offsets, int E, int64_t R, int unit, int e) {
-  const int lane = threadIdx.x & 63;
+  const int lane = fresh(threadIdx.x) & 63;
   uint32_t before = 0, mine = 0;
   int prev = (int)max((int64_t)0, min((int64_t)offsets[min(lane * PER, E)], R));
 #pragma unroll

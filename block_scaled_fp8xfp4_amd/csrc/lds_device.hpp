@@ -20,6 +20,12 @@ template <typename V> __device__ __forceinline__ void lds_write(uint32_t addr, c
 template <int V> struct Int { static constexpr int value = V; };
 template <int N> __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
 
+// v, of which the compiler knows nothing: what is made from it inside a loop is not kept in registers outside of it.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 constexpr int XCDS = 8;
 
 }  // namespace mx

@@ -119,23 +119,32 @@ __global__ __launch_bounds__(256) void unpermute_grad_kernel(UnpermuteArgs A) {
   const float f = A.w ? A.w[pair] : 1.0f;
   const int64_t dy0 = t * A.H, o0 = (int64_t)p * A.H;
   float sum = 0.0f;
-  auto piece = [&](auto size, int c) {
-    constexpr int N = decltype(size)::value;
-    float d[N], v[N];
-    load_any<N>(A.y, DYB, dy0 + c, d);
-    if (A.dw) {
-      load_any<N>(A.o, OB, o0 + c, v);
+  // B pieces of N columns, `apart` columns apart, those before the row's end, all on their way at a time
+  auto pieces = [&](auto size, auto batch, int c, int apart, int end) {
+    constexpr int N = decltype(size)::value, B = decltype(batch)::value;
+    float d[B][N], v[B][N];
 #pragma unroll
-      for (int e = 0; e < N; ++e) sum = __builtin_fmaf(d[e], v[e], sum);
+    for (int b = 0; b < B; ++b) {
+      if (c + b * apart >= end) continue;
+      load_any<N>(A.y, DYB, dy0 + c + b * apart, d[b]);
+      if (A.dw) load_any<N>(A.o, OB, o0 + c + b * apart, v[b]);
     }
-    if (!A.d_o) return;
 #pragma unroll
-    for (int e = 0; e < N; ++e) d[e] *= f;
-    store_any<N>(A.d_o, OB, o0 + c, d);
+    for (int b = 0; b < B; ++b) {
+      if (c + b * apart >= end) continue;
+      if (A.dw) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum = __builtin_fmaf(d[b][e], v[b][e], sum);
+      }
+      if (!A.d_o) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) d[b][e] *= f;
+      store_any<N>(A.d_o, OB, o0 + c + b * apart, d[b]);
+    }
   };
   const int whole = A.H & ~7;
-  for (int c = lane * 8; c < whole; c += 512) piece(Int<8>{}, c);
-  if (whole + lane < A.H) piece(Int<1>{}, whole + lane);
+  for (int c = lane * 8; c < whole; c += 1024) pieces(Int<8>{}, Int<2>{}, c, 512, whole);
+  pieces(Int<1>{}, Int<1>{}, whole + lane, 1, A.H);
   if (!A.dw) return;
 #pragma unroll
   for (int d = 32; d >= 1; d /= 2) sum += __shfl_xor(sum, d);
