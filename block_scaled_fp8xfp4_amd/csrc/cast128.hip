@@ -23,28 +23,25 @@ __device__ __forceinline__ Scale128 scale128(uint32_t amax) {
 
 __device__ __forceinline__ uint32_t bits_max(uint32_t m, float x) { return max(m, __float_as_uint(x) & 0x7FFFFFFFu); }
 
-// x / sc rounded to odd: cut toward zero, the last bit set if anything was cut, so that rounding it again to fewer bits
-// gives the nearest of those to the quotient itself.  q is within an ulp of the quotient, and with sc >= 2^-69 the
-// remainder r of every element that is not far under the smallest code is exact.
-__device__ __forceinline__ float quotient_odd(float x, const Scale128& s) {
-  float q = x * s.inv;
-  q = __builtin_fmaf(__builtin_fmaf(-q, s.sc, x), s.inv, q);
-  const float r = __builtin_fmaf(-q, s.sc, x);
-  const uint32_t b = __float_as_uint(q);
-  // an even q: one up where the quotient is larger, one down where it is smaller
-  const int step = (int)((__float_as_uint(r) ^ b) & 0x80000000u) ? -1 : 1;
-  const float odd = __uint_as_float(r != 0.0f && (b & 1u) == 0u && q != 0.0f ? b + (uint32_t)step : b);
-  return __builtin_copysignf(odd, x);                                 // the remainder's step makes +0 of -0
+// A number that rounds to the code of x / sc: the product with the reciprocal, which is within 2^-23 of the quotient,
+// rounded to 16 bits, and moved by one of its last bits toward the side that the remainder says the quotient is on.  Borders
+// between codes have few bits, so the quotient is on the same side of every one of them; it is on one where the remainder is
+// zero.  With sc >= 2^-69 no remainder that counts falls under fp32's smallest numbers.  Codes from the product alone, with a
+// check for borders nearby, are slower: rows in bf16 meet borders in most wavefronts, since both x and the scale come from 8
+// bits (8192 x 4096 27.5 us).
+__device__ __forceinline__ float quotient_side(float x, const Scale128& s) {
+  const float a = __builtin_fabsf(x);
+  const uint32_t b = (__float_as_uint(a * s.inv) + 0x80u) & 0xFFFFFF00u;
+  const int r = __float_as_int(__builtin_fmaf(-__uint_as_float(b), s.sc, a));      // an exact zero is +0
+  const float q = __uint_as_float(b + (uint32_t)min(max(r, -1), 1));
+  return __builtin_copysignf(fminf(q, 448.0f), x);
 }
 
-__device__ __forceinline__ uint32_t code_pair(float a, float b, const Scale128& s) {
-  const float ta = __builtin_amdgcn_fmed3f(quotient_odd(a, s), -448.0f, 448.0f);
-  const float tb = __builtin_amdgcn_fmed3f(quotient_odd(b, s), -448.0f, 448.0f);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(ta, tb, 0, false) & 0xFFFFu;
+__device__ __forceinline__ uint32_t code_quad(const float* v, const Scale128& s) {
+  const int d = __builtin_amdgcn_cvt_pk_fp8_f32(quotient_side(v[0], s), quotient_side(v[1], s), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient_side(v[2], s), quotient_side(v[3], s), d, true);
 }
-__device__ __forceinline__ u32x2 codes8(const float* v, const Scale128& s) {
-  return u32x2{code_pair(v[0], v[1], s) | code_pair(v[2], v[3], s) << 16, code_pair(v[4], v[5], s) | code_pair(v[6], v[7], s) << 16};
-}
+__device__ __forceinline__ u32x2 codes8(const float* v, const Scale128& s) { return u32x2{code_quad(v, s), code_quad(v + 4, s)}; }
 
 // Maximum over the 16 lanes of a DPP row.
 __device__ __forceinline__ uint32_t row16_max_bits(uint32_t m) {
@@ -63,7 +60,7 @@ __device__ __forceinline__ uint32_t row16_max_bits(uint32_t m) {
 // the range in which near values are good; it takes the double form.
 constexpr float NEAR_EPS = 1.25f * 9.5367431640625e-07f;
 struct Near128 { bool sure; Scale128 s; u32x2 codes; };
-__device__ __forceinline__ u32x2 codes8_of(const float* v, float f) {
+__device__ __forceinline__ u32x2 codes8_times(const float* v, float f) {
   uint32_t d[2];
   codes_scaled<false, 8>(v, f, d);
   return u32x2{d[0], d[1]};
@@ -88,7 +85,7 @@ __device__ __forceinline__ Near128 swiglu_near128(const float* g, const float* u
   uint32_t exact = 0;
   if (n == 1) exact = __float_as_uint(swiglu(gbest, ubest)) & 0x7FFFFFFFu;
   const Scale128 s = scale128(row16_max_bits(exact));
-  const u32x2 lo = codes8_of(a, s.inv * (1.0f - NEAR_EPS)), hi = codes8_of(a, s.inv * (1.0f + NEAR_EPS));
+  const u32x2 lo = codes8_times(a, s.inv * (1.0f - NEAR_EPS)), hi = codes8_times(a, s.inv * (1.0f + NEAR_EPS));
   sure = sure && lo[0] == hi[0] && lo[1] == hi[1];
   return Near128{sure, s, lo};
 }
@@ -179,7 +176,7 @@ hipError_t launch_quantize128_tiles(const void* src, bool bf16, int64_t ld, int6
   return hipGetLastError();
 }
 
-// Columns: a workgroup takes 128 rows of one group and 64 columns.  A thread holds four rows of eight columns; the columns'
+// Columns: a workgroup takes 128 rows of one group and 64 columns at a time.  A thread holds four rows of eight columns; the columns'
 // largest values meet in LDS, where 64 threads make the scales; then each thread's codes go to LDS as dwords of four rows,
 // and come out as whole columns of 128 bytes.  A group's rows past its last are zeros.
 constexpr int TCOLS = 64;
@@ -189,12 +186,12 @@ __device__ __forceinline__ float element(const void* p, bool bf16, int64_t i) {
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize128_t_kernel(const void* __restrict__ src, int64_t ld, int64_t rows, int cols,
                                                             const int32_t* __restrict__ offsets, int E, uint8_t* __restrict__ q,
-                                                            float* __restrict__ sc, int64_t q_ld, uint32_t nct) {
+                                                            float* __restrict__ sc, int64_t q_ld, uint32_t ncg, int per) {
   constexpr int PITCH = 33;                                           // dwords per column: 8 columns' writes meet on no bank twice
   __shared__ __attribute__((aligned(16))) uint32_t part[16][TCOLS];
   __shared__ __attribute__((aligned(16))) float scale[TCOLS], inv[TCOLS];
   __shared__ uint32_t code[TCOLS * PITCH];
-  const uint32_t b = blockIdx.x / nct, ct = blockIdx.x - b * nct;
+  const uint32_t b = blockIdx.x / ncg, cg = blockIdx.x - b * ncg;
   int64_t r0 = (int64_t)b * 128, n = rows - r0;
   if (offsets) {
     const GroupTile g = find_tile(offsets, E, rows, 128, b);
@@ -203,66 +200,73 @@ __global__ __launch_bounds__(256) void quantize128_t_kernel(const void* __restri
     n = g.rows - g.tile * 128;
   }
   n = min(n, (int64_t)128);
-  const int c0 = ct * TCOLS, c = (threadIdx.x & 7) * 8, rq = threadIdx.x >> 3;   // columns c .. c + 7, rows 4 rq .. 4 rq + 3
-  float v[4][8];
-  uint32_t amax[8] = {};
+  const int c = (threadIdx.x & 7) * 8, rq = threadIdx.x >> 3;         // columns c .. c + 7, rows 4 rq .. 4 rq + 3
+  for (int t = 0; t < per; ++t) {
+    const int c0 = (int)(cg * per + t) * TCOLS;
+    if (c0 >= cols) break;
+    float v[4][8];
+    uint32_t amax[8] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t at = (r0 + rq * 4 + i) * ld + c0 + c;
-    if (rq * 4 + i >= n) {
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = (r0 + rq * 4 + i) * ld + c0 + c;
+      if (rq * 4 + i >= n) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-    } else if (c0 + c + 8 <= cols) {
-      load_any<8>(src, BF16, at, v[i]);
-    } else {
+        for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+      } else if (c0 + c + 8 <= cols) {
+        load_any<8>(src, BF16, at, v[i]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = c0 + c + e < cols ? element(src, BF16, at + e) : 0.0f;
+        for (int e = 0; e < 8; ++e) v[i][e] = c0 + c + e < cols ? element(src, BF16, at + e) : 0.0f;
+      }
     }
-  }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 8; ++e) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) amax[e] = bits_max(amax[e], v[i][e]);
-    amax[e] = max(amax[e], (uint32_t)__builtin_amdgcn_mov_dpp((int)amax[e], 0x128, 0xF, 0xF, false));   // the row's other half
-  }
-  if ((threadIdx.x & 8) == 0) {
-    u32x4* const to = reinterpret_cast<u32x4*>(&part[threadIdx.x >> 4][c]);
-    to[0] = u32x4{amax[0], amax[1], amax[2], amax[3]};
-    to[1] = u32x4{amax[4], amax[5], amax[6], amax[7]};
-  }
-  __syncthreads();
-  if (threadIdx.x < TCOLS) {
-    uint32_t m = 0;
+      for (int i = 0; i < 4; ++i) amax[e] = bits_max(amax[e], v[i][e]);
+      amax[e] = max(amax[e], (uint32_t)__builtin_amdgcn_mov_dpp((int)amax[e], 0x128, 0xF, 0xF, false));   // the row's other half
+    }
+    if ((threadIdx.x & 8) == 0) {
+      u32x4* const to = reinterpret_cast<u32x4*>(&part[threadIdx.x >> 4][c]);
+      to[0] = u32x4{amax[0], amax[1], amax[2], amax[3]};
+      to[1] = u32x4{amax[4], amax[5], amax[6], amax[7]};
+    }
+    __syncthreads();
+    if (threadIdx.x < TCOLS) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, part[i][threadIdx.x]);
-    const Scale128 s = scale128(m);
-    scale[threadIdx.x] = s.sc;
-    inv[threadIdx.x] = s.inv;
-    if (c0 + (int)threadIdx.x < cols) sc[(int64_t)(c0 + threadIdx.x) * (q_ld / 128) + b] = s.sc;
-  }
-  __syncthreads();
+      for (int i = 0; i < 16; ++i) m = max(m, part[i][threadIdx.x]);
+      const Scale128 s = scale128(m);
+      scale[threadIdx.x] = s.sc;
+      inv[threadIdx.x] = s.inv;
+      if (c0 + (int)threadIdx.x < cols) sc[(int64_t)(c0 + threadIdx.x) * (q_ld / 128) + b] = s.sc;
+    }
+    __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const Scale128 s{scale[c + e], inv[c + e]};
-    code[(c + e) * PITCH + rq] = code_pair(v[0][e], v[1][e], s) | code_pair(v[2][e], v[3][e], s) << 16;
-  }
-  __syncthreads();
+    for (int e = 0; e < 8; ++e) {
+      const float col4[4] = {v[0][e], v[1][e], v[2][e], v[3][e]};
+      code[(c + e) * PITCH + rq] = code_quad(col4, Scale128{scale[c + e], inv[c + e]});
+    }
+    __syncthreads();
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {                                       // eight lanes write a column
-    const int col = p * 32 + rq, k = (threadIdx.x & 7) * 4;
-    if (c0 + col >= cols) continue;
-    const uint32_t* const from = &code[col * PITCH + k];
-    *reinterpret_cast<u32x4*>(q + (int64_t)(c0 + col) * q_ld + (int64_t)b * 128 + k * 4) = u32x4{from[0], from[1], from[2], from[3]};
+    for (int p = 0; p < 2; ++p) {                                       // eight lanes write a column
+      const int col = p * 32 + rq, k = (threadIdx.x & 7) * 4;
+      if (c0 + col >= cols) continue;
+      const uint32_t* const from = &code[col * PITCH + k];
+      *reinterpret_cast<u32x4*>(q + (int64_t)(c0 + col) * q_ld + (int64_t)b * 128 + k * 4) = u32x4{from[0], from[1], from[2], from[3]};
+    }
   }
 }
 
 hipError_t launch_quantize128_t(const void* src, bool bf16, int64_t ld, int64_t rows, int cols, const int32_t* offsets,
                                 int E, uint8_t* q, float* sc, int64_t q_ld, hipStream_t stream) {
   const int64_t nb = offsets ? q_ld / 128 : (rows + 127) / 128, nct = (cols + TCOLS - 1) / TCOLS;
-  if (nb * nct == 0) return hipSuccess;
-  const dim3 grid((unsigned)(nb * nct)), block(256);
-  if (bf16) hipLaunchKernelGGL(quantize128_t_kernel<true>, grid, block, 0, stream, src, ld, rows, cols, offsets, E, q, sc, q_ld, (uint32_t)nct);
-  else hipLaunchKernelGGL(quantize128_t_kernel<false>, grid, block, 0, stream, src, ld, rows, cols, offsets, E, q, sc, q_ld, (uint32_t)nct);
+  // a workgroup finds its group once for four column tiles where there are many
+  const int per = nb * nct > 4096 ? 4 : 1;
+  const int64_t ncg = (nct + per - 1) / per;
+  if (nb * ncg == 0) return hipSuccess;
+  const dim3 grid((unsigned)(nb * ncg)), block(256);
+  if (bf16) hipLaunchKernelGGL(quantize128_t_kernel<true>, grid, block, 0, stream, src, ld, rows, cols, offsets, E, q, sc, q_ld, (uint32_t)ncg, per);
+  else hipLaunchKernelGGL(quantize128_t_kernel<false>, grid, block, 0, stream, src, ld, rows, cols, offsets, E, q, sc, q_ld, (uint32_t)ncg, per);
   return hipGetLastError();
 }
 
