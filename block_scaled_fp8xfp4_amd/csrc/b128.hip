@@ -421,7 +421,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
   const int lane_ = fresh(threadIdx.x) & 63, col_ = lane_ & 15, g_ = lane_ >> 4;
   const uint32_t mine = lds0 + wave * 16 * PITCH;
   static_assert(S::NW * 16 * PITCH <= S::LDS, "results in LDS");
-  auto store = [&](auto esize) {                                      // bytes of a result
+  auto store = [&](auto esize, auto far) {                            // bytes of a result; past the caches
     constexpr int ESZ = decltype(esize)::value, PER = 16 / ESZ;       // elements per lane
     constexpr int JS = TN * 16 * ESZ < 128 ? TN : 128 / ESZ / 16, LPR = JS * 16 * ESZ / 16;   // products and lanes per run
     constexpr int RPP = 64 / LPR, PASSES = 16 / RPP;                  // rows at a time
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
           const u32x4 d = lds_read<u32x4>(from + p * RPP * PITCH);
           if (mb + r0 + p * RPP >= rows) continue;
           if (j0 * 16 + c + PER <= nw) {
-            if (A.far) __builtin_nontemporal_store(d, reinterpret_cast<u32x4_a1*>(to));
+            if constexpr (decltype(far)::value) __builtin_nontemporal_store(d, reinterpret_cast<u32x4_a1*>(to));
             else *reinterpret_cast<u32x4_a1*>(to) = d;
           } else
 #pragma unroll
@@ -461,8 +461,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       }
     }
   };
-  if (A.bf16_out) store(Int<2>{});
-  else store(Int<4>{});
+  if (A.far) {
+    if (A.bf16_out) store(Int<2>{}, Int<1>{});
+    else store(Int<4>{}, Int<1>{});
+  } else {
+    if (A.bf16_out) store(Int<2>{}, Int<0>{});
+    else store(Int<4>{}, Int<0>{});
+  }
 }
 
 // Row tiles of `unit` that M rows in E groups can make.
