@@ -260,8 +260,8 @@ __global__ __launch_bounds__(256) void quantize128_t_kernel(const void* __restri
 hipError_t launch_quantize128_t(const void* src, bool bf16, int64_t ld, int64_t rows, int cols, const int32_t* offsets,
                                 int E, uint8_t* q, float* sc, int64_t q_ld, hipStream_t stream) {
   const int64_t nb = offsets ? q_ld / 128 : (rows + 127) / 128, nct = (cols + TCOLS - 1) / TCOLS;
-  // a workgroup finds its group once for four column tiles where there are many
-  const int per = nb * nct > 4096 ? 4 : 1;
+  // a workgroup finds its group once for two column tiles where there are many (32768 x 2048 in 64 groups 58 us, for one 63)
+  const int per = nb * nct > 4096 ? 2 : 1;
   const int64_t ncg = (nct + per - 1) / per;
   if (nb * ncg == 0) return hipSuccess;
   const dim3 grid((unsigned)(nb * ncg)), block(256);

@@ -542,11 +542,6 @@ def fp4_dense_ffn(x, x_sc, x_fmt, w13, w13_sc, w2, w2_sc, mid_fmt, y, ws, stream
 # ------------------------------ experts' tokens, products with a scale for each block of 128
 # Checked as the dense block's calls are: one question that holds for right
 # tensors, and only where it does not the checks that find out what is wrong.
-def _is(t, d, dtype, shape):
-    """t is contiguous, of this type and shape, on device d."""
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == d
-
-
 def _blocks(n):
     return -(-n // 128)
 
@@ -556,30 +551,35 @@ def moe_permute(x, slot_pos, out, x_sc=None, out_sc=None, stream=None):
     [T, k]; rows that no slot names are left as they were.  x_sc [T, B] and out_sc [R, B]: the rows' scales, alike."""
     name, t = "moe_permute", _tn()
     T, H = _two(name, "x", x)
-    R = _two(name, "out", out)[0]
-    k = _two(name, "slot_pos", slot_pos)[1]
-    _int(name, T, k)
-    d, size, ld = x.get_device(), x.element_size(), H
-    if (x_sc is None) != (out_sc is None):
-        raise ValueError(f"{name}: x_sc and out_sc come together")
-    B = 0 if x_sc is None else _two(name, "x_sc", x_sc)[1]
-    if not (x.is_contiguous() and _is(out, d, x.dtype, (R, H)) and _is(slot_pos, d, t.i32, (T, k)) and
-            (x_sc is None or _is(x_sc, d, x_sc.dtype, (T, B)) and _is(out_sc, d, x_sc.dtype, (R, B))) and
-            t.current_device() == d):
-        ld = _rows(name, "x", x, (x.dtype,), T, H) if T > 1 else H
-        if T == 1 and H > 1 and x.stride(1) != 1:
+    R, k = _two(name, "out", out)[0], _two(name, "slot_pos", slot_pos)[1]
+    d, size, dtype, B = x.get_device(), x.element_size(), x.dtype, 0
+    ld = H
+    if x_sc is not None and out_sc is not None:
+        B = _two(name, "x_sc", x_sc)[1]
+    if not (x.is_contiguous() and out.dtype is dtype and out.shape == (R, H) and out.is_contiguous() and
+            out.get_device() == d and slot_pos.dtype is t.i32 and slot_pos.shape == (T, k) and slot_pos.is_contiguous() and
+            slot_pos.get_device() == d and H > 0 and T <= _INT_MAX and
+            (x_sc is None and out_sc is None or
+             out_sc is not None and x_sc is not None and x_sc.shape == (T, B) and x_sc.is_contiguous() and
+             x_sc.get_device() == d and out_sc.dtype is x_sc.dtype and out_sc.shape == (R, B) and out_sc.is_contiguous() and
+             out_sc.get_device() == d) and t.current_device() == d):
+        if (x_sc is None) != (out_sc is None):
+            raise ValueError(f"{name}: x_sc and out_sc come together")
+        if H == 0:
+            raise ValueError(f"{name}: x has no columns")
+        _int(name, T, k)
+        ld = _rows(name, "x", x, (dtype,), T, H) if T > 1 else H
+        if H > 1 and x.stride(1) != 1:
             raise ValueError(f"{name}: x must have contiguous rows")
-        _packed(name, "out", out, (x.dtype,), (R, H))
+        _packed(name, "out", out, (dtype,), (R, H))
         _packed(name, "slot_pos", slot_pos, (t.i32,), (T, k))
         if x_sc is not None:
             _packed(name, "x_sc", x_sc, (x_sc.dtype,), (T, B))
             _packed(name, "out_sc", out_sc, (x_sc.dtype,), (R, B))
         _here(name, x, slot_pos, out, x_sc, out_sc)
-    if H == 0:
-        raise ValueError(f"{name}: x has no columns")
-    _check(load().moe_permute(x.data_ptr(), ld * size, H * size, None if not B else x_sc.data_ptr(),
+    _check(load().moe_permute(x.data_ptr(), ld * size, H * size, x_sc.data_ptr() if B else None,
                               B * x_sc.element_size() if B else 0, slot_pos.data_ptr(), T, k, out.data_ptr(),
-                              None if not B else out_sc.data_ptr(), R, t.raw_stream(d) if stream is None else stream), name)
+                              out_sc.data_ptr() if B else None, R, t.raw_stream(d) if stream is None else stream), name)
 
 
 def moe_unpermute(o, w, slot_pos, y, stream=None):
@@ -587,12 +587,13 @@ def moe_unpermute(o, w, slot_pos, y, stream=None):
     int32 [T, k]."""
     name, t = "moe_unpermute", _tn()
     R, H = _two(name, "o", o)
-    T = _two(name, "y", y)[0]
-    k = _two(name, "slot_pos", slot_pos)[1]
-    _int(name, T, k, H)
+    T, k = _two(name, "slot_pos", slot_pos)
     d = o.get_device()
-    if not (o.dtype in t.ins and y.dtype in t.outs and o.is_contiguous() and _is(y, d, y.dtype, (T, H)) and
-            _is(slot_pos, d, t.i32, (T, k)) and (w is None or _is(w, d, t.f32, (T, k))) and t.current_device() == d):
+    if not (o.dtype in t.ins and o.is_contiguous() and y.dtype in t.outs and y.shape == (T, H) and y.is_contiguous() and
+            y.get_device() == d and slot_pos.dtype is t.i32 and slot_pos.is_contiguous() and slot_pos.get_device() == d and
+            (w is None or w.dtype is t.f32 and w.shape == (T, k) and w.is_contiguous() and w.get_device() == d) and
+            (T | H) <= _INT_MAX and t.current_device() == d):
+        _int(name, T, k, H)
         _packed(name, "o", o, t.ins, (R, H))
         _packed(name, "y", y, t.outs, (T, H))
         _packed(name, "slot_pos", slot_pos, (t.i32,), (T, k))
@@ -612,23 +613,25 @@ def moe_unpermute_grad(dy, o, w, slot_pos, d_o=None, dw=None, stream=None):
     rows = o if o is not None else d_o
     if rows is None or d_o is None and dw is None or dw is not None and o is None:
         raise ValueError(f"{name}: d_o or dw is needed, and o for dw")
-    R = _two(name, "o", rows)[0]
-    _int(name, T, k, H)
-    d = dy.get_device()
-    if not (dy.dtype in t.ins and rows.dtype in t.ins and dy.is_contiguous() and _is(rows, d, rows.dtype, (R, H)) and
-            (d_o is None or _is(d_o, d, rows.dtype, (R, H))) and _is(slot_pos, d, t.i32, (T, k)) and
-            (w is None or _is(w, d, t.f32, (T, k))) and (dw is None or _is(dw, d, t.f32, (T, k))) and
-            t.current_device() == d):
+    R, d, f32, dtype = _two(name, "o", rows)[0], dy.get_device(), t.f32, rows.dtype
+    if not (dy.dtype in t.ins and dy.is_contiguous() and dtype in t.ins and rows.shape == (R, H) and rows.is_contiguous() and
+            rows.get_device() == d and
+            (d_o is None or d_o.dtype is dtype and d_o.shape == (R, H) and d_o.is_contiguous() and d_o.get_device() == d) and
+            slot_pos.dtype is t.i32 and slot_pos.shape == (T, k) and slot_pos.is_contiguous() and slot_pos.get_device() == d and
+            (w is None or w.dtype is f32 and w.shape == (T, k) and w.is_contiguous() and w.get_device() == d) and
+            (dw is None or dw.dtype is f32 and dw.shape == (T, k) and dw.is_contiguous() and dw.get_device() == d) and
+            (T | H) <= _INT_MAX and t.current_device() == d):
+        _int(name, T, k, H)
         _packed(name, "dy", dy, t.ins, (T, H))
         _packed(name, "o", rows, t.ins, (R, H))
         if d_o is not None:
-            _packed(name, "d_o", d_o, (rows.dtype,), (R, H))
+            _packed(name, "d_o", d_o, (dtype,), (R, H))
         _packed(name, "slot_pos", slot_pos, (t.i32,), (T, k))
         for what, v in (("w", w), ("dw", dw)):
             if v is not None:
-                _packed(name, what, v, (t.f32,), (T, k))
+                _packed(name, what, v, (f32,), (T, k))
         _here(name, dy, o, w, slot_pos, d_o, dw)
-    _check(load().moe_unpermute_grad(dy.data_ptr(), t.ins[dy.dtype], None if o is None else o.data_ptr(), t.ins[rows.dtype], R,
+    _check(load().moe_unpermute_grad(dy.data_ptr(), t.ins[dy.dtype], None if o is None else o.data_ptr(), t.ins[dtype], R,
                                      None if w is None else w.data_ptr(), slot_pos.data_ptr(), T, k, H,
                                      None if d_o is None else d_o.data_ptr(), None if dw is None else dw.data_ptr(),
                                      t.raw_stream(d) if stream is None else stream), name)
@@ -638,21 +641,23 @@ def fp8_quantize128(src, q, sc, block_rows=1, stream=None):
     """q, sc = E4M3 codes and fp32 scales of src, [rows, cols] or [count, rows, cols], fp32 or bf16, in blocks of 1 x 128
     (block_rows 1: sc [..., rows, nb]) or 128 x 128 (sc [..., ceil(rows / 128), nb]).  Rows of a 2-D src may lie apart."""
     name, t = "fp8_quantize128", _tn()
-    if src.dim() not in (2, 3):
+    shape = src.shape
+    if len(shape) not in (2, 3):
         raise ValueError(f"{name}: src must be 2-D or 3-D")
     if block_rows not in (1, 128):
         raise ValueError(f"{name}: block_rows is {block_rows}, expected 1 or 128")
-    head, (rows, cols) = tuple(src.shape[:-2]), src.shape[-2:]
-    count, d, ld = head[0] if head else 1, src.get_device(), cols
-    shape = head + (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
-    if not (src.dtype in t.ins and src.is_contiguous() and _is(q, d, t.u8, src.shape) and _is(sc, d, t.f32, shape) and
-            t.current_device() == d):
-        if head:
-            _packed(name, "src", src, t.ins, src.shape)
+    rows, cols = shape[-2:]
+    count, d, ld = shape[0] if len(shape) == 3 else 1, src.get_device(), cols
+    sc_shape = tuple(shape[:-2]) + (rows if block_rows == 1 else _blocks(rows), _blocks(cols))
+    if not (src.dtype in t.ins and src.is_contiguous() and q.dtype is t.u8 and q.shape == shape and q.is_contiguous() and
+            q.get_device() == d and sc.dtype is t.f32 and sc.shape == sc_shape and sc.is_contiguous() and
+            sc.get_device() == d and t.current_device() == d):
+        if len(shape) == 3:
+            _packed(name, "src", src, t.ins, shape)
         else:
             ld = _rows(name, "src", src, t.ins, rows, cols)
-        _packed(name, "q", q, (t.u8,), src.shape)
-        _packed(name, "sc", sc, (t.f32,), shape)
+        _packed(name, "q", q, (t.u8,), shape)
+        _packed(name, "sc", sc, (t.f32,), sc_shape)
         _here(name, src, q, sc)
     _check(load().fp8_quantize128(src.data_ptr(), t.ins[src.dtype], ld, count, rows, cols, block_rows, q.data_ptr(),
                                   sc.data_ptr(), t.raw_stream(d) if stream is None else stream), name)
@@ -664,10 +669,11 @@ def fp8_swiglu_quantize128(gu, q, sc, stream=None):
     name, t = "fp8_swiglu_quantize128", _tn()
     T, two_i = _two(name, "gu", gu)
     I = two_i // 2
-    _int(name, I)
     d, ld = gu.get_device(), two_i
-    if not (gu.dtype in t.ins and gu.is_contiguous() and two_i == 2 * I and _is(q, d, t.u8, (T, I)) and
-            _is(sc, d, t.f32, (T, _blocks(I))) and t.current_device() == d):
+    if not (gu.dtype in t.ins and gu.is_contiguous() and two_i == 2 * I and q.dtype is t.u8 and q.shape == (T, I) and
+            q.is_contiguous() and q.get_device() == d and sc.dtype is t.f32 and sc.shape == (T, _blocks(I)) and
+            sc.is_contiguous() and sc.get_device() == d and I <= _INT_MAX and t.current_device() == d):
+        _int(name, I)
         ld = _rows(name, "gu", gu, t.ins, T, 2 * I)
         _packed(name, "q", q, (t.u8,), (T, I))
         _packed(name, "sc", sc, (t.f32,), (T, _blocks(I)))
@@ -688,11 +694,13 @@ def fp8_quantize128_t(src, q, sc, offsets=None, stream=None):
     name, t = "fp8_quantize128_t", _tn()
     rows, cols = _two(name, "src", src)
     q_ld = _two(name, "q", q)[1]
-    _int(name, rows, cols)
     E, d, ld = 1 if offsets is None else offsets.numel() - 1, src.get_device(), cols
-    if not (src.dtype in t.ins and src.is_contiguous() and q_ld % 128 == 0 and _is(q, d, t.u8, (cols, q_ld)) and
-            _is(sc, d, t.f32, (cols, q_ld // 128)) and (offsets is None or _is(offsets, d, t.i32, (E + 1,))) and
-            t.current_device() == d):
+    if not (src.dtype in t.ins and src.is_contiguous() and q_ld % 128 == 0 and q.dtype is t.u8 and q.shape == (cols, q_ld) and
+            q.is_contiguous() and q.get_device() == d and sc.dtype is t.f32 and sc.shape == (cols, q_ld // 128) and
+            sc.is_contiguous() and sc.get_device() == d and
+            (offsets is None or offsets.dtype is t.i32 and offsets.shape == (E + 1,) and offsets.is_contiguous() and
+             offsets.get_device() == d) and (rows | cols) <= _INT_MAX and t.current_device() == d):
+        _int(name, rows, cols)
         if rows > 1:
             ld = _rows(name, "src", src, t.ins, rows, cols)
         else:
@@ -714,16 +722,18 @@ def fp8_block128_gemm(a, a_sc, w, w_sc, y, stream=None):
     nb] (tiles) or [N, nb] (rows), nb = ceil(K / 128)."""
     name, t = "fp8_block128_gemm", _tn()
     N, K = _two(name, "w", w)
-    M = _two(name, "y", y)[0]
-    _int(name, M, N, K)
-    sn, nb, d = _two(name, "w_sc", w_sc)[0], _blocks(K), y.get_device()
-    if not (y.dtype in t.outs and _is(y, d, y.dtype, (M, N)) and _is(a, d, t.u8, (M, K)) and _is(w, d, t.u8, (N, K)) and
-            _is(a_sc, d, t.f32, (M, nb)) and (sn == N or sn == _blocks(N)) and _is(w_sc, d, t.f32, (sn, nb)) and
-            t.current_device() == d):
-        _packed(name, "a", a, (t.u8,), (M, K))
-        _packed(name, "w", w, (t.u8,), (N, K))
-        _packed(name, "a_sc", a_sc, (t.f32,), (M, nb))
-        _packed(name, "w_sc", w_sc, (t.f32,), (N if sn == N else _blocks(N), nb))
+    M, sn = _two(name, "y", y)[0], _two(name, "w_sc", w_sc)[0]
+    nb, d, u8, f32 = -(-K // 128), y.get_device(), t.u8, t.f32
+    if not (y.dtype in t.outs and y.shape == (M, N) and y.is_contiguous() and a.dtype is u8 and a.shape == (M, K) and
+            a.is_contiguous() and a.get_device() == d and w.dtype is u8 and w.is_contiguous() and w.get_device() == d and
+            a_sc.dtype is f32 and a_sc.shape == (M, nb) and a_sc.is_contiguous() and a_sc.get_device() == d and
+            w_sc.dtype is f32 and (sn == N or sn == -(-N // 128)) and w_sc.shape == (sn, nb) and w_sc.is_contiguous() and
+            w_sc.get_device() == d and (M | N | K) <= _INT_MAX and t.current_device() == d):
+        _int(name, M, N, K)
+        _packed(name, "a", a, (u8,), (M, K))
+        _packed(name, "w", w, (u8,), (N, K))
+        _packed(name, "a_sc", a_sc, (f32,), (M, nb))
+        _packed(name, "w_sc", w_sc, (f32,), (N if sn == N else _blocks(N), nb))
         _packed(name, "y", y, t.outs, (M, N))
         _here(name, a, a_sc, w, w_sc, y)
     _check(load().fp8_block128_gemm(a.data_ptr(), a_sc.data_ptr(), w.data_ptr(), w_sc.data_ptr(), 1 if sn == N else 128, M, N, K,
@@ -738,15 +748,18 @@ def fp8_block128_grouped_gemm(a, a_sc, w, w_sc, offsets, y, stream=None):
         raise ValueError(f"{name}: w must be 3-D")
     E, N, K = w.shape
     R = _two(name, "y", y)[0]
-    _int(name, R, N, K)
-    nb, d = _blocks(K), y.get_device()
-    if not (y.dtype in t.outs and _is(y, d, y.dtype, (R, N)) and _is(a, d, t.u8, (R, K)) and _is(w, d, t.u8, (E, N, K)) and
-            _is(a_sc, d, t.f32, (R, nb)) and _is(w_sc, d, t.f32, (E, _blocks(N), nb)) and
-            _is(offsets, d, t.i32, (E + 1,)) and t.current_device() == d):
-        _packed(name, "a", a, (t.u8,), (R, K))
-        _packed(name, "w", w, (t.u8,), (E, N, K))
-        _packed(name, "a_sc", a_sc, (t.f32,), (R, nb))
-        _packed(name, "w_sc", w_sc, (t.f32,), (E, _blocks(N), nb))
+    nb, d, u8, f32 = -(-K // 128), y.get_device(), t.u8, t.f32
+    if not (y.dtype in t.outs and y.shape == (R, N) and y.is_contiguous() and a.dtype is u8 and a.shape == (R, K) and
+            a.is_contiguous() and a.get_device() == d and w.dtype is u8 and w.is_contiguous() and w.get_device() == d and
+            a_sc.dtype is f32 and a_sc.shape == (R, nb) and a_sc.is_contiguous() and a_sc.get_device() == d and
+            w_sc.dtype is f32 and w_sc.shape == (E, -(-N // 128), nb) and w_sc.is_contiguous() and w_sc.get_device() == d and
+            offsets.dtype is t.i32 and offsets.shape == (E + 1,) and offsets.is_contiguous() and offsets.get_device() == d and
+            (R | N | K) <= _INT_MAX and t.current_device() == d):
+        _int(name, R, N, K)
+        _packed(name, "a", a, (u8,), (R, K))
+        _packed(name, "w", w, (u8,), (E, N, K))
+        _packed(name, "a_sc", a_sc, (f32,), (R, nb))
+        _packed(name, "w_sc", w_sc, (f32,), (E, _blocks(N), nb))
         _packed(name, "offsets", offsets, (t.i32,), (E + 1,))
         _packed(name, "y", y, t.outs, (R, N))
         _here(name, a, a_sc, w, w_sc, offsets, y)
@@ -763,17 +776,20 @@ def fp8_block128_grouped_wgrad(a, a_sc, b, b_sc, offsets, dw, stream=None):
         raise ValueError(f"{name}: dw must be 3-D")
     E, N, K = dw.shape
     ld = _two(name, "a", a)[1]
-    _int(name, N, K, ld)
-    nb, d = ld // 128, dw.get_device()
-    if not (dw.dtype in t.outs and ld % 128 == 0 and _is(dw, d, dw.dtype, (E, N, K)) and _is(a, d, t.u8, (N, ld)) and
-            _is(b, d, t.u8, (K, ld)) and _is(a_sc, d, t.f32, (N, nb)) and _is(b_sc, d, t.f32, (K, nb)) and
-            _is(offsets, d, t.i32, (E + 1,)) and t.current_device() == d):
+    nb, d, u8, f32 = ld // 128, dw.get_device(), t.u8, t.f32
+    if not (dw.dtype in t.outs and ld % 128 == 0 and dw.is_contiguous() and a.dtype is u8 and a.shape == (N, ld) and
+            a.is_contiguous() and a.get_device() == d and b.dtype is u8 and b.shape == (K, ld) and b.is_contiguous() and
+            b.get_device() == d and a_sc.dtype is f32 and a_sc.shape == (N, nb) and a_sc.is_contiguous() and
+            a_sc.get_device() == d and b_sc.dtype is f32 and b_sc.shape == (K, nb) and b_sc.is_contiguous() and
+            b_sc.get_device() == d and offsets.dtype is t.i32 and offsets.shape == (E + 1,) and offsets.is_contiguous() and
+            offsets.get_device() == d and (N | K | ld) <= _INT_MAX and t.current_device() == d):
+        _int(name, N, K, ld)
         if ld % 128:
             raise ValueError(f"{name}: a has {ld} columns, a multiple of 128 is expected")
-        _packed(name, "a", a, (t.u8,), (N, ld))
-        _packed(name, "b", b, (t.u8,), (K, ld))
-        _packed(name, "a_sc", a_sc, (t.f32,), (N, nb))
-        _packed(name, "b_sc", b_sc, (t.f32,), (K, nb))
+        _packed(name, "a", a, (u8,), (N, ld))
+        _packed(name, "b", b, (u8,), (K, ld))
+        _packed(name, "a_sc", a_sc, (f32,), (N, nb))
+        _packed(name, "b_sc", b_sc, (f32,), (K, nb))
         _packed(name, "offsets", offsets, (t.i32,), (E + 1,))
         _packed(name, "dw", dw, t.outs, (E, N, K))
         _here(name, a, a_sc, b, b_sc, offsets, dw)
