@@ -131,6 +131,65 @@ def dense_block_calls(times):
     print(json.dumps({"dense_block_calls": times}), flush=True)
 
 
+def block128_calls(times):
+    """Each call of the experts' tokens and of the products with a scale for each block of 128 that their kernel profile
+    lists, `times` times, on random data."""
+    import torch
+    from block_scaled_fp8xfp4_amd import mxmoe
+    from block_scaled_fp8xfp4_amd.layer import Route, quantize128, quantize128_t
+    torch.manual_seed(0)
+    bf16, u8 = torch.bfloat16, torch.uint8
+
+    def randn(*shape, dtype=bf16):
+        return torch.randn(shape, device="cuda", dtype=torch.float32).to(dtype)
+
+    def empty(*shape, dtype=bf16):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+    def repeat(name, call):
+        for _ in range(times):
+            call()
+        torch.cuda.synchronize()
+        log(f"{name}: {mxmoe.last_variant()}")
+
+    def routed(T, E, k):
+        route = Route(T, E, k)
+        route(torch.randn((T, E), device="cuda"))
+        return route
+
+    for T, E, H in ((48, 256, 5120), (8192, 256, 4096)):
+        r, x, o, y = routed(T, E, 8), randn(T, H), empty(T * 8, H), empty(T, H)
+        q, sc = quantize128(x)
+        qs, scs, d_o, dw = empty(T * 8, H, dtype=u8), empty(T * 8, H // 128, dtype=torch.float32), empty(T * 8, H), torch.empty_like(r.w)
+        repeat(f"sort {T} x {H}, 8 experts each", lambda: mxmoe.moe_permute(x, r.slot_pos, o))
+        repeat(f"sort {T} x {H} codes and scales, 8 experts each", lambda: mxmoe.moe_permute(q, r.slot_pos, qs, sc, scs))
+        repeat(f"back {T} x {H}, 8 experts each", lambda: mxmoe.moe_unpermute(o, r.w, r.slot_pos, y))
+        repeat(f"gradient {T} x {H}, 8 experts each", lambda: mxmoe.moe_unpermute_grad(y, o, r.w, r.slot_pos, d_o, dw))
+    x, gu = randn(8192, 4096), randn(8192, 8192)
+    q, sc = quantize128(x)
+    repeat("cast of rows 8192 x 4096", lambda: mxmoe.fp8_quantize128(x, q, sc))
+    repeat("SwiGLU cast 8192 x 4096", lambda: mxmoe.fp8_swiglu_quantize128(gu, q, sc))
+    wq, wsc = quantize128(x, 128)
+    repeat("cast of tiles 8192 x 4096", lambda: mxmoe.fp8_quantize128(x, wq, wsc, 128))
+    qt, sct = quantize128_t(x)
+    repeat("cast of columns 8192 x 4096", lambda: mxmoe.fp8_quantize128_t(x, qt, sct))
+    for M, N, K in ((1, 4096, 4096), (32, 4096, 4096), (48, 4096, 4096), (512, 4096, 4096), (1024, 4096, 4096), (2048, 4096, 4096),
+                    (8192, 4096, 4096)):
+        a, w, y = quantize128(randn(M, K)), quantize128(randn(N, K) * 0.02, 128), empty(M, N)
+        repeat(f"product {M} x {N} x {K}", lambda: mxmoe.fp8_block128_gemm(*a, *w, y))
+    w = [quantize128(randn(32, 1152, 4096) * 0.02, 128) for _ in range(8)]
+    w, w_sc = torch.cat([t for t, _ in w]), torch.cat([t for _, t in w])
+    for T in (1, 48, 1024, 2048, 8192):
+        r, a, y = routed(T, 256, 8), quantize128(randn(T * 8, 4096)), empty(T * 8, 1152)
+        repeat(f"256 experts' 1152 x 4096, {T} x 8 rows", lambda: mxmoe.fp8_block128_grouped_gemm(*a, w, w_sc, r.offsets, y))
+    del w, w_sc
+    r = routed(4096, 64, 8)
+    a, b, dw = quantize128_t(randn(32768, 1152), r.offsets), quantize128_t(randn(32768, 2048), r.offsets), empty(64, 1152, 2048)
+    repeat("64 experts' gradients 1152 x 2048 of 4096 x 8 rows",
+           lambda: mxmoe.fp8_block128_grouped_wgrad(*a, *b, r.offsets, dw))
+    print(json.dumps({"block128_calls": times}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -154,7 +213,12 @@ def main():
                     help="only copy a 256 MiB buffer 5 times (reference kernel for the HBM byte counters)")
     ap.add_argument("--dense-block-calls", type=int, default=0, metavar="N",
                     help="only make each call of the dense block N times (for its kernel profile)")
+    ap.add_argument("--block128-calls", type=int, default=0, metavar="N",
+                    help="only make each call of the experts' tokens and block-128 products N times (for their kernel profile)")
     args = ap.parse_args()
+    if args.block128_calls > 0:
+        block128_calls(args.block128_calls)
+        return
     if args.dense_block_calls > 0:
         dense_block_calls(args.dense_block_calls)
         return
