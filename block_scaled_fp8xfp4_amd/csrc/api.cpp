@@ -456,10 +456,10 @@ mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T,
 mx_status moe_permute(const void* x, int64_t x_ld, int64_t row_bytes, const void* x_sc, int64_t sc_bytes,
                       const int32_t* slot_pos, int T, int k, void* out, void* out_sc, int64_t out_rows, void* stream) {
   if (T < 0 || k < 1 || k > mx::MAX_K || row_bytes < 1 || sc_bytes < 0 || x_ld < row_bytes || out_rows < 0) return MX_EINVAL;
-  if (T == 0) { g_variant = "permute:empty"; return MX_OK; }
+  if (T == 0 || out_rows == 0) { g_variant = "permute:empty"; return MX_OK; }
   if (row_bytes > int64_t(1) << 40 || sc_bytes > int64_t(1) << 40 || x_ld > (int64_t(1) << 60) / T ||
       mx::permute_chunks(row_bytes, sc_bytes) > mx::TOKEN_MAX_CHUNKS / T ||
-      (out_rows > 0 && (row_bytes > (int64_t(1) << 60) / out_rows || sc_bytes > (int64_t(1) << 60) / out_rows)))
+      row_bytes > (int64_t(1) << 60) / out_rows || sc_bytes > (int64_t(1) << 60) / out_rows)
     return MX_EUNSUPPORTED;
   if (!x || !slot_pos || !out || (sc_bytes > 0 && (!x_sc || !out_sc)) || !aligned(slot_pos, 4)) return MX_EINVAL;
   const mx::PermuteArgs a{static_cast<const uint8_t*>(x), x_ld, row_bytes, static_cast<const uint8_t*>(x_sc), sc_bytes,
@@ -474,7 +474,7 @@ namespace {
 int unpermute_sizes(int64_t o_rows, int T, int k, int H) {
   if (T < 0 || k < 1 || k > mx::MAX_K || H < 1 || o_rows < 0) return MX_EINVAL;
   if (T == 0) return 1;
-  if (H > mx::TOKEN_MAX_CHUNKS / T || k > (int64_t(1) << 24) / T || o_rows > (int64_t(1) << 60) / H) return MX_EUNSUPPORTED;
+  if (H > mx::TOKEN_MAX_H || H > mx::TOKEN_MAX_CHUNKS / T || k > (int64_t(1) << 24) / T || o_rows > (int64_t(1) << 60) / H) return MX_EUNSUPPORTED;
   return MX_OK;
 }
 bool in_dtype(int d) { return d == MX_IN_F32 || d == MX_IN_BF16; }
@@ -503,6 +503,7 @@ mx_status moe_unpermute_grad(const void* dy, int dy_dtype, const void* o, int o_
   if (!in_dtype(o_dtype) || !in_dtype(dy_dtype) || r == MX_EINVAL) return MX_EINVAL;
   if (r == 1) { g_variant = "unpermute_grad:empty"; return MX_OK; }
   if (r != MX_OK) return r;
+  if (!dw && o_rows == 0) { g_variant = "unpermute_grad:empty"; return MX_OK; }
   if (!dy || !slot_pos || (!d_o && !dw) || (dw && !o && o_rows > 0)) return MX_EINVAL;
   if (!aligned(dy, size_of_in(dy_dtype)) || !aligned(o, size_of_in(o_dtype)) || !aligned(d_o, size_of_in(o_dtype)) ||
       !aligned(w, 4) || !aligned(slot_pos, 4) || !aligned(dw, 4))
@@ -571,7 +572,7 @@ namespace {
 mx_status b128(const mx::B128Args& a, mx::B128Mode mode, bool w_rows, void* stream) {
   // rows of a tile are addressed with 32-bit byte offsets
   if (a.ld > mx::B128_MAX_LD || !mx::b128_fits(a, mode)) return MX_EUNSUPPORTED;
-  if (!a.a || !a.a_sc || !a.w || !a.w_sc || !a.y || (mode != mx::B128Mode::dense && !a.offsets)) return MX_EINVAL;
+  if ((a.ld > 0 && (!a.a || !a.a_sc || !a.w || !a.w_sc)) || !a.y || (mode != mx::B128Mode::dense && !a.offsets)) return MX_EINVAL;
   if (!aligned(a.a, 16) || !aligned(a.w, 16) || !aligned(a.a_sc, 4) || !aligned(a.w_sc, 4) || !aligned(a.offsets, 4) ||
       !aligned(a.y, a.bf16_out ? 2 : 4))
     return MX_EINVAL;

@@ -9,6 +9,7 @@ namespace mx {
 
 constexpr int B128 = 128;                         // elements that share a scale along the reduction
 constexpr int64_t TOKEN_MAX_CHUNKS = int64_t(1) << 31;   // threads of one call
+constexpr int TOKEN_MAX_H = 1 << 30;              // columns, so that one a batch of pieces past the last is still an int
 
 struct PermuteArgs {
   const uint8_t* x; int64_t x_ld; int64_t row;    // rows of `row` bytes, x_ld bytes apart

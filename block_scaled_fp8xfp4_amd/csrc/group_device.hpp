@@ -34,7 +34,7 @@ __device__ __forceinline__ GroupTile find_tile_of(const int32_t* offsets, int E,
   uint32_t n[PER], sum = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    n[i] = o[i + 1] > o[i] ? (uint32_t)(o[i + 1] - o[i] + unit - 1) / (uint32_t)unit : 0u;
+    n[i] = o[i + 1] > o[i] ? ((uint32_t)(o[i + 1] - o[i]) + (uint32_t)unit - 1) / (uint32_t)unit : 0u;
     sum += n[i];
   }
   const uint32_t upto = lanes_upto(sum);           // tiles up to and with this lane's
@@ -71,7 +71,7 @@ __device__ __forceinline__ GroupSpan find_span_of(const int32_t* offsets, int E,
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int o = (int)max((int64_t)0, min((int64_t)offsets[min(lane * PER + i + 1, E)], R));
-    const uint32_t n = o > prev ? (uint32_t)(o - prev + unit - 1) / (uint32_t)unit : 0u;
+    const uint32_t n = o > prev ? ((uint32_t)(o - prev) + (uint32_t)unit - 1) / (uint32_t)unit : 0u;
     before += lane * PER + i < e ? n : 0u;
     mine += lane * PER + i == e ? n : 0u;
     prev = o;

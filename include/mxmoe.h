@@ -431,7 +431,8 @@ mx_status fp4_dense_ffn(const uint8_t* x, const uint8_t* x_sc, int x_fmt, int T,
  * row_bytes bytes without gaps.  With sc_bytes > 0 the rows' scales x_sc,
  * rows of sc_bytes bytes without gaps, go the same way into out_sc.  Rows and
  * scales are bytes of any type at any alignment (16-byte aligned rows are
- * fastest); out must not overlap x.  Each row is read once.  1 <= k <= 16;
+ * fastest); out must not overlap x, nor out_sc x_sc.  Each row is read once.
+ * 1 <= k <= 16;
  * T * (ceil(row_bytes / 16) + ceil(sc_bytes / 16)) <= 2^31.  The gradient of
  * x is moe_unpermute of the gradient of out, without weights.
  */
@@ -448,7 +449,7 @@ mx_status moe_permute(const void* x, int64_t x_ld, int64_t row_bytes, const void
  * is +0).  o [o_rows][H] fp32 or bf16 (MX_IN_*), w fp32 [T][k] or NULL
  * (ones), y [T][H] (MX_OUT_*), contiguous, at their types' alignment (16-byte
  * aligned rows are fastest); y must not overlap o.  1 <= k <= 16, any
- * H >= 1, T * H <= 2^31, T * k <= 2^24.
+ * H >= 1, H <= 2^30, T * H <= 2^31, T * k <= 2^24.
  */
 mx_status moe_unpermute(const void* o, int o_dtype, int64_t o_rows, const float* w, const int32_t* slot_pos, int T, int k,
                         int H, void* y, int y_dtype, void* stream);
@@ -461,7 +462,8 @@ mx_status moe_unpermute(const void* o, int o_dtype, int64_t o_rows, const float*
  * itself, otherwise outputs must not overlap inputs.  Products and sums are
  * fp32 in one fixed order; d_o is rounded once.  Slots that are nowhere or
  * past o_rows get dw = 0, and rows of d_o that no slot names are left as they
- * were.  Sizes and alignment as moe_unpermute.
+ * were; with d_o no two slots may name one row.  Sizes and alignment as
+ * moe_unpermute.
  */
 mx_status moe_unpermute_grad(const void* dy, int dy_dtype, const void* o, int o_dtype, int64_t o_rows, const float* w,
                              const int32_t* slot_pos, int T, int k, int H, void* d_o, float* dw, void* stream);
@@ -518,14 +520,13 @@ mx_status fp8_quantize128_t(const void* src, int src_dtype, int64_t src_ld, int6
  * [N][ceil(K / 128)] with n' = n (w_rows 1: e.g. the gradient of weights,
  * both operands from fp8_quantize128_t).  y [M][N] bf16 (RNE of the fp32
  * result) or fp32 (y_dtype MX_OUT_*).  A block's sum is one step of the matrix
- * cores (which cut E4M3 products as fp4_block_gemm describes: a few 1e-6 of
- * the result's norm); the blocks are added in order in fp32, one fma each, the
- * same for every M and kernel.  The gradient of a is the product of dy with
- * the transposed codes and scales of w (tiles of 128 x 128 are the same both
- * ways).  Any M >= 0, N >= 1, K % 16 == 0, 16 <= K <= 2^23; results of more
- * tiles than one launch holds (about 2^32 to 2^39, by the tile) return
- * MX_EUNSUPPORTED.  a, w 16-byte
- * aligned, scales 4-byte, y its type's.
+ * cores (which cut E4M3 products, see fp4_block_gemm: here about 3e-5 of the
+ * result's norm in all); the blocks are added in order in fp32, one fma each,
+ * the same for every M and kernel.  The gradient of a is the product of dy
+ * with the transposed codes and scales of w (tiles of 128 x 128 are the same
+ * both ways).  Any M >= 0, N >= 1, K % 16 == 0, 16 <= K <= 2^23; results of
+ * more tiles than one launch holds (about 2^32 to 2^39 results, by the tile)
+ * return MX_EUNSUPPORTED.  a, w 16-byte aligned, scales 4-byte, y its type's.
  */
 mx_status fp8_block128_gemm(const uint8_t* a, const float* a_sc, const uint8_t* w, const float* w_sc, int w_rows, int M, int N,
                             int K, void* y, int y_dtype, void* stream);
@@ -549,7 +550,7 @@ mx_status fp8_block128_grouped_gemm(const uint8_t* a, const float* a_sc, int R, 
  * products' rows; b [K][ld] + b_sc: of the rows that went in; both with the
  * same offsets (int32 [E + 1], device).  dw [E][N][K] bf16 or fp32, written
  * whole (experts without tokens: +0).  Any N, K >= 1; ld % 128 == 0,
- * ld <= 2^23; E <= 1024.
+ * ld <= 2^23 (0: no tokens, a and b and their scales may be NULL); E <= 1024.
  */
 mx_status fp8_block128_grouped_wgrad(const uint8_t* a, const float* a_sc, const uint8_t* b, const float* b_sc, int64_t ld,
                                      const int32_t* offsets, int E, int N, int K, void* dw, int dw_dtype, void* stream);

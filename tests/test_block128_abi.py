@@ -55,6 +55,15 @@ def test_unpermute_grad_rejects_bad_arguments(lib):
     assert call(T=0, dy=None, o=None, w=None, pos=None, d=None, dw=None) == MX_OK
 
 
+def test_tokens_columns_stay_below_2_31(lib):
+    """Rows of more than 2^30 columns, whose last pieces an int would not hold, and calls without experts' rows."""
+    H = (1 << 30) + 1
+    assert lib.moe_unpermute(FAKE, 1, 1, None, FAKE, 1, 1, H, FAKE, 0, None) == MX_EUNSUPPORTED
+    assert lib.moe_unpermute_grad(FAKE, 1, FAKE, 1, 1, None, FAKE, 1, 1, H, FAKE, None, None) == MX_EUNSUPPORTED
+    assert lib.moe_permute(FAKE, 64, 64, None, 0, FAKE, 4, 2, None, None, 0, None) == MX_OK
+    assert lib.moe_unpermute_grad(FAKE, 1, None, 1, 0, None, FAKE, 4, 2, 64, None, None, None) == MX_OK
+
+
 def test_quantize_rejects_bad_arguments(lib):
     def call(src=FAKE, dt=1, ld=64, n=2, rows=4, cols=64, br=1, q=FAKE, sc=FAKE):
         return lib.fp8_quantize128(src, dt, ld, n, rows, cols, br, q, sc, None)
