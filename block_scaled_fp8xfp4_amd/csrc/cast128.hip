@@ -52,46 +52,8 @@ __device__ __forceinline__ uint32_t row16_max_bits(uint32_t m) {
   return m;
 }
 
-// SwiGLU without double arithmetic where the result cannot depend on it.  Near values (fp32) are within 2^-20 of the values
-// that the cast is defined on, so a block's largest value is one of those whose near value is within 2^-19 of the largest
-// near one: one evaluation in double, in the lanes that hold such a one, gives the scale.  A code is that of a near value
-// times the reciprocal of the scale if it does not change within NEAR_EPS of it (2^-20 and the roundings of the reciprocal
-// and the product).  About one wavefront in 50 holds a code that does, or two such values in one lane, or a block out of
-// the range in which near values are good; it takes the double form.
-constexpr float NEAR_EPS = 1.25f * 9.5367431640625e-07f;
-struct Near128 { bool sure; Scale128 s; u32x2 codes; };
-__device__ __forceinline__ u32x2 codes8_times(const float* v, float f) {
-  uint32_t d[2];
-  codes_scaled<false, 8>(v, f, d);
-  return u32x2{d[0], d[1]};
-}
-__device__ __forceinline__ Near128 swiglu_near128(const float* g, const float* u, bool in) {
-  float a[8], amax = 0.0f, gmin = 0.0f, gbest = 0.0f, ubest = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    a[e] = in ? swiglu_near(g[e], u[e]) : 0.0f;
-    const bool more = __builtin_fabsf(a[e]) > amax;
-    gbest = more ? g[e] : gbest;
-    ubest = more ? u[e] : ubest;
-    amax = near_max(amax, a[e]);
-    gmin = in ? fminf(gmin, g[e]) : gmin;
-  }
-  const uint32_t top = row16_max_bits(__float_as_uint(amax) & 0x7FFFFFFFu);        // NaN is the largest
-  const float most = __uint_as_float(top), edge = most * (1.0f - 1.9073486328125e-06f);
-  int n = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) n += __builtin_fabsf(a[e]) >= edge;
-  bool sure = gmin > SWIGLU_MIN_G && most >= 3.5e-18f && most <= 1.3e36f && n <= 1;   // 2^-58, 2^120
-  uint32_t exact = 0;
-  if (n == 1) exact = __float_as_uint(swiglu(gbest, ubest)) & 0x7FFFFFFFu;
-  const Scale128 s = scale128(row16_max_bits(exact));
-  const u32x2 lo = codes8_times(a, s.inv * (1.0f - NEAR_EPS)), hi = codes8_times(a, s.inv * (1.0f + NEAR_EPS));
-  sure = sure && lo[0] == hi[0] && lo[1] == hi[1];
-  return Near128{sure, s, lo};
-}
-
 // Rows: 16 lanes hold a block, eight columns each; those past the row's end hold zeros and write nothing.
-template <bool BF16, bool SWIGLU>
+template <bool BF16>
 __global__ __launch_bounds__(256) void quantize128_rows_kernel(const void* __restrict__ src, int64_t ld, uint32_t n, uint32_t cols,
                                                                uint32_t nb, uint8_t* __restrict__ q, float* __restrict__ sc) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
@@ -100,21 +62,6 @@ __global__ __launch_bounds__(256) void quantize128_rows_kernel(const void* __res
   const bool in = c < cols;
   float v[8] = {};
   if (in) load8(src, BF16, (int64_t)r * ld + c, v);
-  if (SWIGLU) {
-    float u[8] = {};
-    if (in) load8(src, BF16, (int64_t)r * ld + cols + c, u);
-    const Near128 near = swiglu_near128(v, u, in);
-    if (__all(near.sure)) {
-      if (in) *reinterpret_cast<u32x2*>(q + (int64_t)r * cols + c) = near.codes;
-      if ((i & 15) == 0) sc[i >> 4] = near.s.sc;
-      return;
-    }
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h)                                       // four at a time: the double form is long
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e / 4 == h) v[e] = in ? swiglu(v[e], u[e]) : 0.0f;
-  }
   uint32_t amax = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) amax = bits_max(amax, v[e]);
@@ -123,14 +70,108 @@ __global__ __launch_bounds__(256) void quantize128_rows_kernel(const void* __res
   if ((i & 15) == 0) sc[i >> 4] = s.sc;
 }
 
+__device__ __forceinline__ float element(const void* p, bool bf16, int64_t i) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
+}
+
+// SwiGLU without double arithmetic where the result cannot depend on it.  Near values (fp32) are within 2^-20 of the values
+// that the cast is defined on, so a block's largest value is one of those whose near value is within 2^-19 of the largest
+// near one: where that is one value, its evaluation in double gives the scale.  A code is that of a near value times the
+// reciprocal of the scale if it does not change within NEAR_EPS of it (2^-20 and the roundings of the reciprocal and the
+// product); about one wavefront in 60 holds a code that does, and evaluates it in double.  Blocks with several such largest
+// values, or out of the range in which near values are good, take the double form as a whole.
+//
+// What bounds it is instructions (8192 x 4096 bf16 47 us, 3.6 TB/s; the loads and stores alone 37) and, for few rows, the
+// longest way through them (48 x 2048 3.3 us): the largest value is found with its place in its three lowest bits (2^-20
+// of it at most) and read again; a near value never reaches past 464, where a code would not be 448, so none is clamped;
+// and codes are mended one by one (whole blocks in double instead: 48 x 2048 4.3 us, 999 x 1376 fp32 6.9 from 5.9).  Several
+// blocks a lane, whose largest are evaluated at once, cost more registers than they save (8192 x 4096 46 us, 999 x 1376 6.7).
+constexpr float NEAR_EPS = 1.25f * 9.5367431640625e-07f;
+__device__ __forceinline__ u32x2 codes8_times(const float* v, float f) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * f, v[1] * f, 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * f, v[5] * f, 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * f, v[3] * f, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * f, v[7] * f, hi, true);
+  return u32x2{(uint32_t)lo, (uint32_t)hi};
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void swiglu_quantize128_kernel(const void* __restrict__ src, int64_t ld, uint32_t n, uint32_t cols,
+                                                                 uint32_t nb, uint8_t* __restrict__ q, float* __restrict__ sc) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n) return;                                                 // whole blocks are in or out
+  const int lane = threadIdx.x & 63, l = lane & 15;
+  const uint32_t r = i / (nb * 16), c = (i - r * nb * 16) * 8;
+  const bool in = c < cols;
+  const int64_t row = (int64_t)r * ld, at = row + c;
+  float a[8], gmin = 0.0f;
+  uint32_t first = 0, second = 0;                                     // the two largest, with their places
+  {
+    float g[8] = {}, u[8] = {};
+    if (in) {
+      load8(src, BF16, at, g);
+      load8(src, BF16, at + cols, u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = swiglu_near(g[e], u[e]);
+      gmin = fminf(gmin, g[e]);
+      const uint32_t key = (__float_as_uint(a[e]) & 0x7FFFFFF8u) | (uint32_t)e;                  // NaN is the largest
+      second = max(second, min(first, key));
+      first = max(first, key);
+    }
+  }
+  const uint32_t top = row16_max_bits(first);
+  const float most = __uint_as_float(top & ~7u);
+  const uint32_t edge = __float_as_uint(most * (1.0f - 3.814697265625e-06f));                    // 2^-18: 2^-19 and the places
+  const uint32_t holds = (uint32_t)(__ballot(first >= edge) >> (lane & 48)) & 0xFFFFu;           // the block's lanes that do
+  const bool sure = gmin > SWIGLU_MIN_G && most >= 3.5e-18f && most <= 1.3e36f &&                // 2^-58, 2^120
+                    second < edge && (holds & (holds - 1)) == 0;
+  const uint32_t place = min(c - l * 8 + __builtin_ctz(holds | 0x8000u) * 8 + (top & 7u), cols - 1);
+  const float exact = swiglu(element(src, BF16, row + place), element(src, BF16, row + cols + place));
+  Scale128 s = scale128(__float_as_uint(exact) & 0x7FFFFFFFu);
+  u32x2 d = codes8_times(a, s.inv * (1.0f - NEAR_EPS));
+  const u32x2 hi = codes8_times(a, s.inv * (1.0f + NEAR_EPS));
+  if (!__all(sure)) {
+    float v[8] = {}, u[8];
+    if (in) {                                                         // again, so that they need no registers until then
+      load8(src, BF16, at, v);
+      load8(src, BF16, at + cols, u);
+    }
+    uint32_t amax = 0;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h)                                       // four at a time: the double form is long
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e / 4 == h) v[e] = in ? swiglu(v[e], u[e]) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = bits_max(amax, v[e]);
+    s = scale128(row16_max_bits(amax));
+    d = codes8(v, s);
+  } else if (__any(d[0] != hi[0] || d[1] != hi[1])) {
+    uint64_t codes = (uint64_t)d[1] << 32 | d[0];
+    const uint64_t open = codes ^ ((uint64_t)hi[1] << 32 | hi[0]);
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const bool ask = (open >> (8 * e) & 0xFF) != 0;                 // never a lane past the row's end: its values are zeros
+      if (!__any(ask)) continue;
+      const float v = ask ? swiglu(element(src, BF16, at + e), element(src, BF16, at + cols + e)) : 0.0f;
+      const uint64_t code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient_side(v, s), 0.0f, 0, false) & 0xFFu;
+      if (ask) codes = (codes & ~(uint64_t(0xFF) << (8 * e))) | code << (8 * e);
+    }
+    d = u32x2{(uint32_t)codes, (uint32_t)(codes >> 32)};
+  }
+  if (in) *reinterpret_cast<u32x2*>(q + (int64_t)r * cols + c) = d;
+  if (l == 0) sc[i >> 4] = s.sc;
+}
+
 hipError_t launch_quantize128_rows(const void* src, bool bf16, int64_t ld, int64_t rows, int64_t cols, bool swiglu,
                                    uint8_t* q, float* sc, hipStream_t stream) {
   const int64_t nb = (cols + 127) / 128, n = rows * nb * 16;
   if (n == 0) return hipSuccess;
   const dim3 grid((unsigned)((n + 255) / 256)), block(256);
-#define MX_Q(B, S) hipLaunchKernelGGL((quantize128_rows_kernel<B, S>), grid, block, 0, stream, src, ld, (uint32_t)n, (uint32_t)cols, (uint32_t)nb, q, sc)
-  if (bf16) { if (swiglu) MX_Q(true, true); else MX_Q(true, false); }
-  else { if (swiglu) MX_Q(false, true); else MX_Q(false, false); }
+#define MX_Q(KERNEL) hipLaunchKernelGGL((KERNEL), grid, block, 0, stream, src, ld, (uint32_t)n, (uint32_t)cols, (uint32_t)nb, q, sc)
+  if (bf16) { if (swiglu) MX_Q(swiglu_quantize128_kernel<true>); else MX_Q(quantize128_rows_kernel<true>); }
+  else { if (swiglu) MX_Q(swiglu_quantize128_kernel<false>); else MX_Q(quantize128_rows_kernel<false>); }
 #undef MX_Q
   return hipGetLastError();
 }
@@ -180,9 +221,6 @@ hipError_t launch_quantize128_tiles(const void* src, bool bf16, int64_t ld, int6
 // largest values meet in LDS, where 64 threads make the scales; then each thread's codes go to LDS as dwords of four rows,
 // and come out as whole columns of 128 bytes.  A group's rows past its last are zeros.
 constexpr int TCOLS = 64;
-__device__ __forceinline__ float element(const void* p, bool bf16, int64_t i) {
-  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
-}
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize128_t_kernel(const void* __restrict__ src, int64_t ld, int64_t rows, int cols,
                                                             const int32_t* __restrict__ offsets, int E, uint8_t* __restrict__ q,

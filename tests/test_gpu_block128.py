@@ -112,6 +112,23 @@ def test_swiglu_quantize(dtype, T, I):
     assert torch.equal(q, q2) and torch.equal(sc, sc2)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_swiglu_quantize_many(dtype):
+    """A million values, some next to a border between codes, and blocks whose largest value is there twice."""
+    T, I = 1000, 1040
+    gu, v = typed(np.random.default_rng(5).standard_normal((T, 2 * I)) * 4, dtype)
+    for r in range(0, T, 50):
+        top = int(np.abs(v[r, :128] / (1 + np.exp(-v[r, :128])) * v[r, I:I + 128]).argmax())
+        for at in (0, I):
+            v[r, at + (top + 1 + r // 50 * 7) % 128] = v[r, at + top]
+    gu = torch.from_numpy(v).to(dtype).cuda()
+    q, sc = torch.zeros((T, I), dtype=U8, device="cuda"), torch.zeros((T, blocks(I)), device="cuda")
+    mxmoe.fp8_swiglu_quantize128(gu, q, sc)
+    a = (v[:, :I] / (1 + np.exp(-v[:, :I])) * v[:, I:]).astype(np.float32)
+    want_q, want_sc = ref.cast(a.astype(np.float64), 1, B)
+    assert np.array_equal(sc.cpu().numpy(), want_sc) and np.array_equal(q.cpu().numpy(), want_q)
+
+
 def test_swiglu_quantize_extremes():
     """Gates from far below to far above zero, subnormal ones, huge ones, and their ups; zero blocks."""
     g = np.concatenate([np.linspace(-110, 110, 97), [0, 1e-45, -1e-45, 1e-38, 3e38, -3e38, 88.8, -88.8, -745, -746],
