@@ -18,6 +18,8 @@
 
 namespace mx {
 
+typedef float v16f __attribute__((ext_vector_type(16)));
+
 // W (A side: 16 rows n) x X (B side: 16 rows m), K = 128, from zero: lane l holds row m = l % 16 and columns
 // n = 4 (l / 16) + [0, 4).
 __device__ __forceinline__ v4f block_product(const v8i& w, const v8i& x) {
@@ -318,8 +320,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
     } else {
       v8i xf[TM], wf[2];                          // operands of a column of products: this one's and the next one's
       v4f P[2][TM];                               // products on their way, and those of the column before
+      // OUTER: the matrix cores multiply the scales too, a column's 16 with the 64 of the rows, in fp32 as the vector unit
+      // does, bit for bit; a lane holds one of each.  It halves the vector instructions beside the products where both operands
+      // have scales by rows: 8192 x 4096 x 4096 170 us from 183, 4096 x 2048 x 8192 91 from 95, 64 experts' gradients 1152 x
+      // 2048 of 4096 x 8 rows 175 from 178; with a wavefront per SIMD it is slower (64 x 256: 1024 x 4096 x 4096 42 from 39)
+      constexpr bool OUTER = WROWS && TM == 4 && WM > 1;
       float f[TM], fn[TM], wn_ = 0.f;             // scales of the rows (times the tile's): the stage's, the next one's
       v4f sn{};                                   // WROWS: scales of the column's weight rows
+      v16f prods{};                               // OUTER: scales of the column before, all TM x 4
       auto load_x = [&](int i, uint32_t buf) {
         xf[i] = operand8(lds_read<u32x4>(xa + c0 + buf + i * 2048), lds_read<u32x4>(xa + c1 + buf + i * 2048));
       };
@@ -328,7 +336,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       };
       auto load_scales = [&](uint32_t buf) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fn[i] = lds_read<float>(lds0 + buf + S::OFF_S + ((wm * TM + i) * 16 + col) * 4);
+        for (int i = 0; i < (OUTER ? 1 : TM); ++i)
+          fn[i] = lds_read<float>(lds0 + buf + S::OFF_S + ((wm * TM + i) * 16 + (OUTER ? lane : col)) * 4);
         if (!WROWS) wn_ = lds_read<float>(lds0 + buf + S::OFF_S + (S::BM + wn) * 4);
       };
       // Holds the sums before the branches that follow (no instruction): the compiler would move them behind.
@@ -346,7 +355,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
         for (int j = 0; j < TN; ++j) {
           const bool end = j == TN - 1;
           const v4f sp = sn;                      // of the column before
-          if (WROWS) sn = lds_read<v4f>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + 4 * g) * 4);
+          if (OUTER) sn[0] = lds_read<float>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + col) * 4);
+          else if (WROWS) sn = lds_read<v4f>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + 4 * g) * 4);
           if (end && MORE == 1) {
             pin();
             landed(s + 1, nbuf);
@@ -367,7 +377,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
             const int jp = j == 0 ? TN - 1 : j - 1;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              acc[i][jp][r] = __builtin_fmaf(P[jp & 1][i][r], WROWS ? f[i] * sp[r] : f[i], acc[i][jp][r]);
+              acc[i][jp][r] = __builtin_fmaf(P[jp & 1][i][r], OUTER ? prods[i * 4 + r] : WROWS ? f[i] * sp[r] : f[i], acc[i][jp][r]);
             if (end && MORE) load_x(i, nbuf);
             if (end && MORE == 2 && i % 2 == 0 && i / 2 < S::FIRST) issue1(s + NST, buf, i / 2, 0);
             if (!end && MORE == 2 && j * TM + i < S::SPREAD) {
@@ -379,7 +389,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
           }
           if (j == 0) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) f[i] = WROWS ? fn[i] : fn[i] * wn_;
+            for (int i = 0; i < (OUTER ? 1 : TM); ++i) f[i] = WROWS ? fn[i] : fn[i] * wn_;
+          }
+          if (OUTER) {
+            prods = __builtin_amdgcn_mfma_f32_16x16x1f32(sn[0], f[0], v16f{}, 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
       };
@@ -408,7 +422,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][TN - 1][r] = __builtin_fmaf(P[(TN - 1) & 1][i][r], WROWS ? f[i] * sn[r] : f[i], acc[i][TN - 1][r]);
+          acc[i][TN - 1][r] = __builtin_fmaf(P[(TN - 1) & 1][i][r], OUTER ? prods[i * 4 + r] : WROWS ? f[i] * sn[r] : f[i], acc[i][TN - 1][r]);
     }
   }
 

@@ -331,3 +331,23 @@ def test_grouped_weight_gradient_in_order(bounds, N, K):
         dw = torch.full((E, N, K), 7.0, dtype=dtype, device="cuda")
         mxmoe.fp8_block128_grouped_wgrad(*[dev(v) for v in (a, a_sc, b, b_sc)], dev(np.array(bounds, np.int32)), dw)
         assert np.array_equal(dw.float().cpu().numpy(), want if dtype is F32 else ref.bf16(want))
+
+
+@pytest.mark.parametrize("M,N,variant", [(2048, 4096, "tile128x256"), (8000, 2000, "tile256x256")])
+def test_rows_scales_whose_products_are_tiny_or_not_numbers(M, N, variant):
+    """Scales by rows on both sides, whose products are subnormal in some blocks, huge, infinite or NaN in others: the large
+    tiles, which let the matrix cores multiply them, give the bits of the kernel of few rows."""
+    rng = np.random.default_rng(M)
+    K, nb = 272, 3
+    a, w = (dev(rng.integers(0, 0x7F, (n, K)).astype(np.uint8)) for n in (M, N))
+    sa, sw = (dev((rng.random((n, nb)) * 2.0 ** rng.integers(-75, -60, (n, nb))).astype(np.float32)) for n in (M, N))
+    sa[1::7] *= 2.0**125
+    sw[::5] *= 2.0**125
+    sa[3, 1], sa[9, 0], sw[4, 2], sw[6, 0] = float("nan"), float("inf"), float("nan"), 0.0
+    y = torch.empty((M, N), device="cuda")
+    mxmoe.fp8_block128_gemm(a, sa, w, sw, y)
+    assert mxmoe.last_variant() == "b128:" + variant
+    few = torch.empty((16, N), device="cuda")
+    for m in (0, 16, M - 16):
+        mxmoe.fp8_block128_gemm(a[m:m + 16], sa[m:m + 16], w, sw, few)
+        assert torch.equal(few.nan_to_num(7.0), y[m:m + 16].nan_to_num(7.0)) and torch.equal(few.isnan(), y[m:m + 16].isnan())
