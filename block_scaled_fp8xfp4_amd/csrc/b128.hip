@@ -309,7 +309,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
     else wait_vm<0>();
     cut(0, 0);
     lds_barrier();
-    if (wm * TM * 16 >= rows) {                   // nothing of this wavefront's is a result
+    // nothing of this wavefront's is a result (256 experts' 1152 x 4096, 8192 x 8 rows: 535 us, 552 with products of columns past N)
+    if (wm * TM * 16 >= rows || wn * TN * 16 >= cols) {
       uint32_t buf = 0;
       if (NST - 1 < nkb) issue(NST - 1, (NST - 1) * S::STAGE, S::FIRST, S::NV);
       for (int s = 0; s + 1 < nkb; ++s) {
