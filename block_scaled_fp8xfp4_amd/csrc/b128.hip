@@ -324,8 +324,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       // OUTER: the matrix cores multiply the scales too, a column's 16 with the 64 of the rows, in fp32 as the vector unit
       // does, bit for bit; a lane holds one of each.  It halves the vector instructions beside the products where both operands
       // have scales by rows: 8192 x 4096 x 4096 170 us from 183, 4096 x 2048 x 8192 91 from 95, 64 experts' gradients 1152 x
-      // 2048 of 4096 x 8 rows 175 from 178; with a wavefront per SIMD it is slower (64 x 256: 1024 x 4096 x 4096 42 from 39)
-      constexpr bool OUTER = WROWS && TM == 4 && WM > 1;
+      // 2048 of 4096 x 8 rows 175 from 178
+      constexpr bool OUTER = WROWS && TM == 4;
       float f[TM], fn[TM], wn_ = 0.f;             // scales of the rows (times the tile's): the stage's, the next one's
       v4f sn{};                                   // WROWS: scales of the column's weight rows
       v16f prods{};                               // OUTER: scales of the column before, all TM x 4
@@ -513,29 +513,43 @@ static void launch_tile(const B128Args& a, hipStream_t stream) {
 //   rows of 4096 x 4096:    1 rows16 8.2, 64 x 64 11.4; 32 rows32 9.8, 64 x 64 12.0; 48 64 x 64 13.5, rows32 13.7
 //           16384 x 4096:   1 rows16 18.8, 64 x 64 12.9 (DMA keeps more bytes on their way than registers)
 //           1152 x 4096:    48 rows16 7.1, 64 x 64 10.2; 96 rows32 8.7, 64 x 64 10.3
-//           4096 x 4096:    256 64 x 64 14.9, 64 x 128 20.5; 512 64 x 128 20.6, 64 x 64 23.3; 1024 64 x 256 29.9, 64 x 128 32.2,
-//                           128 x 256 36.9; 2048 128 x 256 41.2, 256 x 256 59.6; 4096 256 x 256 68.0, 128 x 256 79.5
+//           4096 x 4096:    256 64 x 64 14.9, 64 x 128 20.5; 512 64 x 128 18.6, 64 x 64 23.3; 700 128 x 128 22.3, 64 x 256 28.2; 1024
+//                           128 x 128 29.6, 64 x 128 32.2, 64 x 256 32.3, 128 x 256 36.9; 2048 128 x 256 41.2, 256 x 256 59.6; 4096 256 x 256 68.0, 128 x 256 79.5
 //   256 experts' 1152 x 4096, rows each: 4 64 x 64 209, 64 x 128 225, rows16 248; 32 64 x 128 248, 64 x 64 254, 128 x 256 259;
-//                           64 128 x 256 275, 64 x 128 295; 256 256 x 256 492, 128 x 256 510; one row of all: 12.7 rows16 and 64 x 64
+//                           64 128 x 256 275, 64 x 128 295; 192 256 x 256 395, 128 x 256 439; 256 256 x 256 492, 128 x 256
+//                           510; one row of all: 12.7 rows16 and 64 x 64
+//   8 experts' 4096 x 4096, rows each: 8 64 x 128 21.0, 64 x 64 21.1, 128 x 256 22.4; 64 128 x 256 30.1, 64 x 128 40.5; 128
+//                           128 x 256 37.7, 256 x 256 47.5; 256 256 x 256 60, 128 x 256 71; 1024 192, 208
+//   64 experts' 1152 x 2048, rows each: 128 128 x 256 44, 256 x 256 51; 256 256 x 256 73, 128 x 256 79; 512 128, 138
+//   gradients of 8 experts' 512 x 1024, 1024 tokens each: 128 x 128 12.8, 256 x 256 22.8
 //   256 experts' 4096 x 576, 48 rows of all: 64 x 128 95, 64 x 64 126, rows16 187 (few blocks of K: what a workgroup begins
 //                           and ends with counts)
-enum class B128Kernel { rows16, rows32, t64x64, t64x128, t64x256, t128x256, t256x256 };
+enum class B128Kernel { rows16, rows32, t64x64, t64x128, t128x128, t128x256, t256x256 };
 static int64_t row_groups(const B128Args& a, B128Mode mode, int rows) { return row_tiles(a, mode, rows) * (((int64_t)a.N + 15) / 16); }
+// Workgroups with rows that experts of about as many rows each make: half a tile more than whole ones, at least one each.
+static int64_t likely_groups(const B128Args& a, int bm, int bn) {
+  const int64_t e = a.E < a.M ? a.E : a.M, n = ((int64_t)a.M + (e - 1) * (bm / 2) + bm - 1) / bm;
+  return (n > e ? n : e) * (((int64_t)a.N + bn - 1) / bn);
+}
 static B128Kernel pick(const B128Args& a, B128Mode mode) {
-  if (mode == B128Mode::wgrad) return B128Kernel::t256x256;
+  if (mode == B128Mode::wgrad) return tile_groups(a, mode, 128, 128) <= 256 ? B128Kernel::t128x128 : B128Kernel::t256x256;
   if (row_groups(a, mode, 16) <= 256) return B128Kernel::rows16;
   if (mode == B128Mode::grouped) {
     if (row_groups(a, mode, 16) <= 512) return B128Kernel::rows16;
+    if (likely_groups(a, 64, 64) <= 256) return B128Kernel::t64x64;
+    if (likely_groups(a, 64, 128) <= 256) return B128Kernel::t64x128;
     const int64_t per = ((int64_t)a.M + a.E - 1) / a.E;               // rows of an expert, about; most fit one tile
     if (per <= 44) return per <= 24 && (a.K > 2048 || a.N <= 64) ? B128Kernel::t64x64 : B128Kernel::t64x128;
-    return per <= 96 ? B128Kernel::t128x256 : B128Kernel::t256x256;
+    // rounds of the largest two, at 3 to 2 (tiles of 256 rows are less full); past the second they run into one another
+    auto rounds = [](int64_t n) { return n <= 512 ? (n + 255) / 256 * 256 : n; };
+    return rounds(likely_groups(a, 256, 256)) * 3 <= rounds(likely_groups(a, 128, 256)) * 2 ? B128Kernel::t256x256 : B128Kernel::t128x256;
   }
   if (a.M > 16 && row_groups(a, mode, 32) <= 256) return B128Kernel::rows32;
   if (a.M <= 16 && row_groups(a, mode, 16) <= 512) return B128Kernel::rows16;
   // the smallest tiles that are one round; past them rounds of the largest two, at 5 to 3
   if (tile_groups(a, mode, 64, 64) <= 256) return B128Kernel::t64x64;
   if (tile_groups(a, mode, 64, 128) <= 256) return B128Kernel::t64x128;
-  if (tile_groups(a, mode, 64, 256) <= 256) return B128Kernel::t64x256;
+  if (tile_groups(a, mode, 128, 128) <= 256) return B128Kernel::t128x128;
   return (tile_groups(a, mode, 256, 256) + 255) / 256 * 5 <= (tile_groups(a, mode, 128, 256) + 255) / 256 * 3 ? B128Kernel::t256x256
                                                                                                               : B128Kernel::t128x256;
 }
@@ -545,18 +559,15 @@ template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args
     switch (pick(a, MODE)) {
       case B128Kernel::rows16: launch_rows<1, WROWS, MODE>(a, stream); return "b128:rows16";
       case B128Kernel::t64x64: launch_tile<WROWS, MODE, 2, 2, 2, 2, 4>(a, stream); return "b128:tile64x64";
-      case B128Kernel::t64x128: launch_tile<WROWS, MODE, 2, 4, 2, 2, 3>(a, stream); return "b128:tile64x128";
+      case B128Kernel::t64x128: launch_tile<WROWS, MODE, 2, 4, 2, 2, MODE == B128Mode::dense ? 4 : 3>(a, stream); return "b128:tile64x128";
       case B128Kernel::t128x256: launch_tile<WROWS, MODE, 2, 4, 4, 4, 3>(a, stream); return "b128:tile128x256";
       default: break;
     }
   }
-  if constexpr (MODE == B128Mode::dense) {
-    switch (pick(a, MODE)) {
-      case B128Kernel::rows32: launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32";
-      case B128Kernel::t64x256: launch_tile<WROWS, MODE, 1, 4, 4, 4, 3>(a, stream); return "b128:tile64x256";
-      default: break;
-    }
-  }
+  if constexpr (MODE == B128Mode::dense)
+    if (pick(a, MODE) == B128Kernel::rows32) { launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32"; }
+  if constexpr (MODE != B128Mode::grouped)
+    if (pick(a, MODE) == B128Kernel::t128x128) { launch_tile<WROWS, MODE, 2, 4, 4, 2, 4>(a, stream); return "b128:tile128x128"; }
   launch_tile<WROWS, MODE, 4, 2, 4, 8, 2>(a, stream);
   return "b128:tile256x256";
 }

@@ -182,7 +182,7 @@ def test_product_in_order(M, N, K, w_rows):
 
 @pytest.mark.parametrize("w_rows", [128, 1])
 @pytest.mark.parametrize("M,N,K,variant", [(9, 4100, 400, "rows16"), (31, 4080, 272, "rows32"), (300, 1030, 656, "tile64x64"),
-                                           (1030, 1100, 400, "tile64x128"), (2000, 1300, 272, "tile64x256"),
+                                           (1030, 1100, 400, "tile64x128"), (2000, 1300, 272, "tile128x128"),
                                            (3001, 1500, 528, "tile128x256"), (6001, 1502, 400, "tile256x256"),
                                            (6000, 1500, 128, "tile256x256"), (6000, 1500, 16, "tile256x256")])
 def test_every_kernel_in_order(M, N, K, variant, w_rows):
@@ -351,3 +351,43 @@ def test_rows_scales_whose_products_are_tiny_or_not_numbers(M, N, variant):
     for m in (0, 16, M - 16):
         mxmoe.fp8_block128_gemm(a[m:m + 16], sa[m:m + 16], w, sw, few)
         assert torch.equal(few.nan_to_num(7.0), y[m:m + 16].nan_to_num(7.0)) and torch.equal(few.isnan(), y[m:m + 16].isnan())
+
+
+@pytest.mark.parametrize("E,R,N,K,variant", [(16, 90, 60, 400, "rows16"), (16, 1000, 300, 656, "tile64x64"), (200, 900, 60, 144, "tile64x64"),
+                                             (16, 1000, 1030, 272, "tile64x128"), (200, 1000, 300, 400, "tile64x128"),
+                                             (16, 1600, 1500, 528, "tile128x256"), (1, 1300, 1500, 400, "tile64x128"),   # 21 x 12 workgroups
+                                             (4, 6000, 1500, 400, "tile256x256"), (16, 20000, 300, 144, "tile256x256")])
+def test_every_kernel_of_experts_in_order(E, R, N, K, variant):
+    rng = np.random.default_rng(E + R + N)
+    bounds = ragged(rng, E, R) if E > 1 else [0, R]
+    a, a_sc = ref.whole_codes(rng, R, K), ref.short_scales(rng, R, blocks(K))
+    w = ref.whole_codes(rng, E * N, K).reshape(E, N, K)
+    w_sc = ref.short_scales(rng, E * blocks(N), blocks(K)).reshape(E, blocks(N), blocks(K))
+    want = np.full((R, N), 7.0, np.float32)
+    for e, (i, j) in enumerate(zip(bounds, bounds[1:])):
+        if i < j:
+            want[i:j] = ref.in_order(a[i:j], a_sc[i:j], w[e], w_sc[e], B)
+    args = [dev(v) for v in (a, a_sc, w, w_sc)]
+    assert np.array_equal(grouped(*args, bounds, F32).cpu().numpy(), want)
+    assert mxmoe.last_variant() == "b128:" + variant
+    assert np.array_equal(grouped(*args, bounds, BF16).float().cpu().numpy(), ref.bf16(want))
+
+
+@pytest.mark.parametrize("E,rows,N,K,variant", [(8, 1500, 300, 270, "tile128x128"), (65, 6000, 300, 270, "tile256x256"),
+                                                (20, 9000, 520, 513, "tile256x256")])
+def test_every_kernel_of_weight_gradients_in_order(E, rows, N, K, variant):
+    rng = np.random.default_rng(E + N)
+    bounds = ragged(rng, E, rows)
+    ld = mxmoe.fp8_quantize128_t_cols(rows, E)
+    a, b = ref.whole_codes(rng, N, ld), ref.whole_codes(rng, K, ld)
+    a_sc, b_sc = ref.short_scales(rng, N, ld // B), ref.short_scales(rng, K, ld // B)
+    dw = torch.full((E, N, K), 7.0, device="cuda")
+    mxmoe.fp8_block128_grouped_wgrad(*[dev(v) for v in (a, a_sc, b, b_sc)], dev(np.array(bounds, np.int32)), dw)
+    assert mxmoe.last_variant() == "b128:" + variant
+    at = 0
+    for e, (i, j) in enumerate(zip(bounds, bounds[1:])):
+        n = blocks(j - i)
+        s, t = slice(at * B, (at + n) * B), slice(at, at + n)
+        want = ref.in_order(a[:, s], a_sc[:, t], b[:, s], b_sc[:, t], 1) if n else np.zeros((N, K), np.float32)
+        assert np.array_equal(dw[e].cpu().numpy(), want)
+        at += n
