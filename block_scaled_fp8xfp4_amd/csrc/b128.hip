@@ -170,7 +170,8 @@ __global__ __launch_bounds__(256, 4) void b128_rows_kernel(B128Args A) {
 template <bool WROWS, int WM, int WN, int TM, int TN, int NST>
 struct B128Shape {
   static constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
-  static constexpr int NSR = BM + (WROWS ? BN : WN), NS = (NSR + 64 * NW - 1) / (64 * NW);   // rows of scales; surplus ones repeat the last
+  // rows of scales, x's in whole 64s (a DMA instruction); surplus ones repeat the last
+  static constexpr int XS = (BM + 63) / 64 * 64, NS = (XS + (WROWS ? BN : WN) + 64 * NW - 1) / (64 * NW);
   static constexpr uint32_t OFF_W = BM * 128, OFF_S = OFF_W + BN * 128, STAGE = OFF_S + NS * NW * 256;
   static constexpr uint32_t LDS = STAGE * NST;
   static constexpr int NX = BM / 8 / NW, NWT = BN / 8 / NW, NV = NX + NWT + NS;    // DMA instructions per wavefront and stage
@@ -252,9 +253,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
   for (int i = 0; i < S::NWT; ++i) woff[i] = (uint32_t)min((i * S::NW + wave) * 8 + lane / 8, cols - 1) * (uint32_t)A.ld + (uint32_t)chunk;
 #pragma unroll
   for (int i = 0; i < S::NS; ++i) {
-    const int r = (i * S::NW + wave) * 64 + lane, c = min(r - S::BM, WROWS ? S::BN - 1 : WN - 1);
+    const int r = (i * S::NW + wave) * 64 + lane, c = min(r - S::XS, WROWS ? S::BN - 1 : WN - 1);
     const int wr = WROWS ? min(c, cols - 1) : (n0 % 128 + min(c * TN * 16, cols - 1)) / 128;
-    soff[i] = (uint32_t)(r < S::BM ? min(r, rows - 1) : wr) * (uint32_t)A.ld_sc * 4;
+    soff[i] = (uint32_t)(r < S::XS ? min(r, rows - 1) : wr) * (uint32_t)A.ld_sc * 4;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
   // the d-th DMA instruction of stage s; past: what this lane's chunk reaches past K (the row's last 16 are read again, and
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
   auto issue1 = [&](int s, uint32_t buf, int d, uint32_t past) {
     const int ix = min(max(d - S::NS, 0), S::NX - 1), iw = max(d - S::NS - S::NX, 0);
     if (d < S::NS)                                // 64 rows of scales are all x's or all w's
-      dma4_to_lds(((d * S::NW + wave) * 64 < S::BM ? xs : ws) + s, soff[min(d, S::NS - 1)], lds0 + buf + S::OFF_S + (d * S::NW + wave) * 256);
+      dma4_to_lds(((d * S::NW + wave) * 64 < S::XS ? xs : ws) + s, soff[min(d, S::NS - 1)], lds0 + buf + S::OFF_S + (d * S::NW + wave) * 256);
     else if (d < S::NS + S::NX) dma16_to_lds(x + (int64_t)s * 128, xoff[ix] - past, lds0 + buf + (ix * S::NW + wave) * 1024);
     else dma16_to_lds(w + (int64_t)s * 128, woff[iw] - past, lds0 + buf + S::OFF_W + (iw * S::NW + wave) * 1024);
   };
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
 #pragma unroll
         for (int i = 0; i < (OUTER ? 1 : TM); ++i)
           fn[i] = lds_read<float>(lds0 + buf + S::OFF_S + ((wm * TM + i) * 16 + (OUTER ? lane : col)) * 4);
-        if (!WROWS) wn_ = lds_read<float>(lds0 + buf + S::OFF_S + (S::BM + wn) * 4);
+        if (!WROWS) wn_ = lds_read<float>(lds0 + buf + S::OFF_S + (S::XS + wn) * 4);
       };
       // Holds the sums before the branches that follow (no instruction): the compiler would move them behind.
       auto pin = [&] {
@@ -356,8 +357,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
         for (int j = 0; j < TN; ++j) {
           const bool end = j == TN - 1;
           const v4f sp = sn;                      // of the column before
-          if (OUTER) sn[0] = lds_read<float>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + col) * 4);
-          else if (WROWS) sn = lds_read<v4f>(lds0 + buf + S::OFF_S + (S::BM + (wn * TN + j) * 16 + 4 * g) * 4);
+          if (OUTER) sn[0] = lds_read<float>(lds0 + buf + S::OFF_S + (S::XS + (wn * TN + j) * 16 + col) * 4);
+          else if (WROWS) sn = lds_read<v4f>(lds0 + buf + S::OFF_S + (S::XS + (wn * TN + j) * 16 + 4 * g) * 4);
           if (end && MORE == 1) {
             pin();
             landed(s + 1, nbuf);
@@ -517,14 +518,16 @@ static void launch_tile(const B128Args& a, hipStream_t stream) {
 //                           128 x 128 29.6, 64 x 128 32.2, 64 x 256 32.3, 128 x 256 36.9; 2048 128 x 256 41.2, 256 x 256 59.6; 4096 256 x 256 68.0, 128 x 256 79.5
 //   256 experts' 1152 x 4096, rows each: 4 64 x 64 209, 64 x 128 225, rows16 248; 32 64 x 128 248, 64 x 64 254, 128 x 256 259;
 //                           64 128 x 256 275, 64 x 128 295; 192 256 x 256 395, 128 x 256 439; 256 256 x 256 492, 128 x 256
-//                           510; one row of all: 12.7 rows16 and 64 x 64
+//                           510
+//                           8 rows of all 16 x 64 13.3, 64 x 64 15.7; 32 rows 30.3, 35.5; 64 56.5, 60.7; 384 179, 180; 1024 215, 214;
+//                           2048 224, 219 (16 x 64 in 8 stages, one workgroup a CU: 12.6, 36.4, 61, 189, 232, 236)
 //   8 experts' 4096 x 4096, rows each: 8 64 x 128 21.0, 64 x 64 21.1, 128 x 256 22.4; 64 128 x 256 30.1, 64 x 128 40.5; 128
 //                           128 x 256 37.7, 256 x 256 47.5; 256 256 x 256 60, 128 x 256 71; 1024 192, 208
 //   64 experts' 1152 x 2048, rows each: 128 128 x 256 44, 256 x 256 51; 256 256 x 256 73, 128 x 256 79; 512 128, 138
 //   gradients of 8 experts' 512 x 1024, 1024 tokens each: 128 x 128 12.8, 256 x 256 22.8
 //   256 experts' 4096 x 576, 48 rows of all: 64 x 128 95, 64 x 64 126, rows16 187 (few blocks of K: what a workgroup begins
 //                           and ends with counts)
-enum class B128Kernel { rows16, rows32, t64x64, t64x128, t128x128, t128x256, t256x256 };
+enum class B128Kernel { rows16, rows32, t16x64, t64x64, t64x128, t128x128, t128x256, t256x256 };
 static int64_t row_groups(const B128Args& a, B128Mode mode, int rows) { return row_tiles(a, mode, rows) * (((int64_t)a.N + 15) / 16); }
 // Workgroups with rows that experts of about as many rows each make: half a tile more than whole ones, at least one each.
 static int64_t likely_groups(const B128Args& a, int bm, int bn) {
@@ -536,6 +539,7 @@ static B128Kernel pick(const B128Args& a, B128Mode mode) {
   if (row_groups(a, mode, 16) <= 256) return B128Kernel::rows16;
   if (mode == B128Mode::grouped) {
     if (row_groups(a, mode, 16) <= 512) return B128Kernel::rows16;
+    if (a.M <= 2 * (int64_t)a.E) return B128Kernel::t16x64;           // two rows each, three workgroups a CU
     if (likely_groups(a, 64, 64) <= 256) return B128Kernel::t64x64;
     if (likely_groups(a, 64, 128) <= 256) return B128Kernel::t64x128;
     const int64_t per = ((int64_t)a.M + a.E - 1) / a.E;               // rows of an expert, about; most fit one tile
@@ -566,6 +570,8 @@ template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args
   }
   if constexpr (MODE == B128Mode::dense)
     if (pick(a, MODE) == B128Kernel::rows32) { launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32"; }
+  if constexpr (MODE == B128Mode::grouped)
+    if (pick(a, MODE) == B128Kernel::t16x64) { launch_tile<WROWS, MODE, 1, 2, 1, 2, 5>(a, stream); return "b128:tile16x64"; }
   if constexpr (MODE != B128Mode::grouped)
     if (pick(a, MODE) == B128Kernel::t128x128) { launch_tile<WROWS, MODE, 2, 4, 4, 2, 4>(a, stream); return "b128:tile128x128"; }
   launch_tile<WROWS, MODE, 4, 2, 4, 8, 2>(a, stream);
@@ -576,6 +582,7 @@ template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args
 bool b128_fits(const B128Args& a, B128Mode mode) {
   constexpr int64_t MOST = int64_t(1) << 23;
   switch (pick(a, mode)) {
+    case B128Kernel::t16x64: return tile_groups(a, mode, 16, 64) < MOST;
     case B128Kernel::t64x64: return tile_groups(a, mode, 64, 64) < MOST;
     case B128Kernel::t64x128: return tile_groups(a, mode, 64, 128) < MOST;
     case B128Kernel::t128x256: return tile_groups(a, mode, 128, 256) < MOST;

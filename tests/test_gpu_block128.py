@@ -354,6 +354,7 @@ def test_rows_scales_whose_products_are_tiny_or_not_numbers(M, N, variant):
 
 
 @pytest.mark.parametrize("E,R,N,K,variant", [(16, 90, 60, 400, "rows16"), (16, 1000, 300, 656, "tile64x64"), (200, 900, 60, 144, "tile64x64"),
+                                             (40, 70, 1100, 1040, "tile16x64"), (300, 600, 130, 272, "tile16x64"), (30, 60, 300, 144, "tile16x64"),
                                              (16, 1000, 1030, 272, "tile64x128"), (200, 1000, 300, 400, "tile64x128"),
                                              (16, 1600, 1500, 528, "tile128x256"), (1, 1300, 1500, 400, "tile64x128"),   # 21 x 12 workgroups
                                              (4, 6000, 1500, 400, "tile256x256"), (16, 20000, 300, 144, "tile256x256")])
