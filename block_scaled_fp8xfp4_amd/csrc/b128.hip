@@ -512,7 +512,8 @@ static void launch_tile(const B128Args& a, hipStream_t stream) {
 
 // Which kernel, by how many workgroups each shape gives and what a round of them takes.  us, weights from memory:
 //   rows of 4096 x 4096:    1 rows16 8.2, 64 x 64 11.4; 32 rows32 9.8, 64 x 64 12.0; 48 64 x 64 13.5, rows32 13.7
-//           16384 x 4096:   1 rows16 18.8, 64 x 64 12.9 (DMA keeps more bytes on their way than registers)
+//           16384 x 4096:   1 16 x 64 16.1, rows16 18.8 (DMA keeps more bytes on their way than registers); 9216 x 4096: 16 16 x 64
+//                           12.2, 64 x 64 13.6; 8192 x 4096: 1 rows16 9.9, 16 x 64 11.4; 129280 x 4096: 1 16 x 64 98.7, 128 x 256 104.5
 //           1152 x 4096:    48 rows16 7.1, 64 x 64 10.2; 96 rows32 8.7, 64 x 64 10.3
 //           4096 x 4096:    256 64 x 64 14.9, 64 x 128 20.5; 512 64 x 128 18.6, 64 x 64 23.3; 700 128 x 128 22.3, 64 x 256 28.2; 1024
 //                           128 x 128 29.6, 64 x 128 32.2, 64 x 256 32.3, 128 x 256 36.9; 2048 128 x 256 41.2, 256 x 256 59.6; 4096 256 x 256 68.0, 128 x 256 79.5
@@ -550,6 +551,7 @@ static B128Kernel pick(const B128Args& a, B128Mode mode) {
   }
   if (a.M > 16 && row_groups(a, mode, 32) <= 256) return B128Kernel::rows32;
   if (a.M <= 16 && row_groups(a, mode, 16) <= 512) return B128Kernel::rows16;
+  if (a.M <= 16) return B128Kernel::t16x64;                           // one row of tiles, three workgroups a CU
   // the smallest tiles that are one round; past them rounds of the largest two, at 5 to 3
   if (tile_groups(a, mode, 64, 64) <= 256) return B128Kernel::t64x64;
   if (tile_groups(a, mode, 64, 128) <= 256) return B128Kernel::t64x128;
@@ -570,7 +572,7 @@ template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args
   }
   if constexpr (MODE == B128Mode::dense)
     if (pick(a, MODE) == B128Kernel::rows32) { launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32"; }
-  if constexpr (MODE == B128Mode::grouped)
+  if constexpr (MODE != B128Mode::wgrad)
     if (pick(a, MODE) == B128Kernel::t16x64) { launch_tile<WROWS, MODE, 1, 2, 1, 2, 5>(a, stream); return "b128:tile16x64"; }
   if constexpr (MODE != B128Mode::grouped)
     if (pick(a, MODE) == B128Kernel::t128x128) { launch_tile<WROWS, MODE, 2, 4, 4, 2, 4>(a, stream); return "b128:tile128x128"; }

@@ -181,7 +181,7 @@ def test_product_in_order(M, N, K, w_rows):
 
 
 @pytest.mark.parametrize("w_rows", [128, 1])
-@pytest.mark.parametrize("M,N,K,variant", [(9, 4100, 400, "rows16"), (31, 4080, 272, "rows32"), (300, 1030, 656, "tile64x64"),
+@pytest.mark.parametrize("M,N,K,variant", [(9, 4100, 400, "rows16"), (3, 9010, 272, "tile16x64"), (31, 4080, 272, "rows32"), (300, 1030, 656, "tile64x64"),
                                            (1030, 1100, 400, "tile64x128"), (2000, 1300, 272, "tile128x128"),
                                            (3001, 1500, 528, "tile128x256"), (6001, 1502, 400, "tile256x256"),
                                            (6000, 1500, 128, "tile256x256"), (6000, 1500, 16, "tile256x256")])
