@@ -503,12 +503,6 @@ static int64_t tile_groups(const B128Args& a, B128Mode mode, int bm, int bn) {
   if (mode == B128Mode::grouped) return (n + XCDS - 1) / XCDS * XCDS * nct;
   return (n * nct * (mode == B128Mode::wgrad ? a.E : 1) + XCDS - 1) / XCDS * XCDS;
 }
-template <bool WROWS, B128Mode MODE, int WM, int WN, int TM, int TN, int NST>
-static void launch_tile(const B128Args& a, hipStream_t stream) {
-  using S = B128Shape<WROWS, WM, WN, TM, TN, NST>;
-  const int64_t n = tile_groups(a, MODE, S::BM, S::BN);
-  hipLaunchKernelGGL((b128_tile_kernel<WROWS, MODE, WM, WN, TM, TN, NST>), dim3((unsigned)n), dim3(64 * S::NW), 0, stream, a);
-}
 
 // Which kernel, by how many workgroups each shape gives and what a round of them takes.  us, weights from memory:
 //   rows of 4096 x 4096:    1 rows16 8.2, 64 x 64 11.4; 32 rows32 9.8, 64 x 64 12.0; 48 64 x 64 13.5, rows32 13.7
@@ -529,13 +523,31 @@ static void launch_tile(const B128Args& a, hipStream_t stream) {
 //   256 experts' 4096 x 576, 48 rows of all: 64 x 128 95, 64 x 64 126, rows16 187 (few blocks of K: what a workgroup begins
 //                           and ends with counts)
 enum class B128Kernel { rows16, rows32, t16x64, t64x64, t64x128, t128x128, t128x256, t256x256 };
+struct B128Group { int rows, cols, threads; };                        // of a workgroup
+static constexpr B128Group group_of(B128Kernel k) {
+  switch (k) {
+    case B128Kernel::rows16: return {16, 16, 256};
+    case B128Kernel::rows32: return {32, 16, 256};
+    case B128Kernel::t16x64: return {16, 64, 128};
+    case B128Kernel::t64x64: return {64, 64, 256};
+    case B128Kernel::t64x128: return {64, 128, 512};
+    case B128Kernel::t128x128: return {128, 128, 512};
+    case B128Kernel::t128x256: return {128, 256, 512};
+    default: return {256, 256, 512};
+  }
+}
+// A launch holds fewer than 2^32 threads.
+static bool launch_holds(const B128Args& a, B128Mode mode, B128Kernel k) {
+  const B128Group g = group_of(k);
+  return tile_groups(a, mode, g.rows, g.cols) < (int64_t(1) << 32) / g.threads;
+}
 static int64_t row_groups(const B128Args& a, B128Mode mode, int rows) { return row_tiles(a, mode, rows) * (((int64_t)a.N + 15) / 16); }
 // Workgroups with rows that experts of about as many rows each make: half a tile more than whole ones, at least one each.
 static int64_t likely_groups(const B128Args& a, int bm, int bn) {
   const int64_t e = a.E < a.M ? a.E : a.M, n = ((int64_t)a.M + (e - 1) * (bm / 2) + bm - 1) / bm;
   return (n > e ? n : e) * (((int64_t)a.N + bn - 1) / bn);
 }
-static B128Kernel pick(const B128Args& a, B128Mode mode) {
+static B128Kernel quickest(const B128Args& a, B128Mode mode) {
   if (mode == B128Mode::wgrad) return tile_groups(a, mode, 128, 128) <= 256 ? B128Kernel::t128x128 : B128Kernel::t256x256;
   if (row_groups(a, mode, 16) <= 256) return B128Kernel::rows16;
   if (mode == B128Mode::grouped) {
@@ -560,37 +572,42 @@ static B128Kernel pick(const B128Args& a, B128Mode mode) {
                                                                                                               : B128Kernel::t128x256;
 }
 
+// Where one launch does not hold the quickest kernel's workgroups (1024 experts' few rows by 2^20 columns), larger tiles;
+// weight gradients have no others.
+static B128Kernel pick(const B128Args& a, B128Mode mode) {
+  const B128Kernel k = quickest(a, mode);
+  if (launch_holds(a, mode, k)) return k;
+  return mode != B128Mode::wgrad && launch_holds(a, mode, B128Kernel::t128x256) ? B128Kernel::t128x256 : B128Kernel::t256x256;
+}
+bool b128_fits(const B128Args& a, B128Mode mode) { return launch_holds(a, mode, pick(a, mode)); }
+
+template <bool WROWS, B128Mode MODE, B128Kernel KERNEL, int WM, int WN, int TM, int TN, int NST>
+static void launch_tile(const B128Args& a, hipStream_t stream) {
+  using S = B128Shape<WROWS, WM, WN, TM, TN, NST>;
+  constexpr B128Group G = group_of(KERNEL);
+  static_assert(G.rows == S::BM && G.cols == S::BN && G.threads == 64 * S::NW, "what the limits are counted by");
+  const int64_t n = tile_groups(a, MODE, S::BM, S::BN);
+  hipLaunchKernelGGL((b128_tile_kernel<WROWS, MODE, WM, WN, TM, TN, NST>), dim3((unsigned)n), dim3(64 * S::NW), 0, stream, a);
+}
 template <bool WROWS, B128Mode MODE> static const char* launch_of(const B128Args& a, hipStream_t stream) {
+  using K = B128Kernel;
+  const K k = pick(a, MODE);
   if constexpr (MODE != B128Mode::wgrad) {
-    switch (pick(a, MODE)) {
-      case B128Kernel::rows16: launch_rows<1, WROWS, MODE>(a, stream); return "b128:rows16";
-      case B128Kernel::t64x64: launch_tile<WROWS, MODE, 2, 2, 2, 2, 4>(a, stream); return "b128:tile64x64";
-      case B128Kernel::t64x128: launch_tile<WROWS, MODE, 2, 4, 2, 2, MODE == B128Mode::dense ? 4 : 3>(a, stream); return "b128:tile64x128";
-      case B128Kernel::t128x256: launch_tile<WROWS, MODE, 2, 4, 4, 4, 3>(a, stream); return "b128:tile128x256";
+    switch (k) {
+      case K::rows16: launch_rows<1, WROWS, MODE>(a, stream); return "b128:rows16";
+      case K::t16x64: launch_tile<WROWS, MODE, K::t16x64, 1, 2, 1, 2, 5>(a, stream); return "b128:tile16x64";
+      case K::t64x64: launch_tile<WROWS, MODE, K::t64x64, 2, 2, 2, 2, 4>(a, stream); return "b128:tile64x64";
+      case K::t64x128: launch_tile<WROWS, MODE, K::t64x128, 2, 4, 2, 2, MODE == B128Mode::dense ? 4 : 3>(a, stream); return "b128:tile64x128";
+      case K::t128x256: launch_tile<WROWS, MODE, K::t128x256, 2, 4, 4, 4, 3>(a, stream); return "b128:tile128x256";
       default: break;
     }
   }
   if constexpr (MODE == B128Mode::dense)
-    if (pick(a, MODE) == B128Kernel::rows32) { launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32"; }
-  if constexpr (MODE != B128Mode::wgrad)
-    if (pick(a, MODE) == B128Kernel::t16x64) { launch_tile<WROWS, MODE, 1, 2, 1, 2, 5>(a, stream); return "b128:tile16x64"; }
+    if (k == K::rows32) { launch_rows<2, WROWS, MODE>(a, stream); return "b128:rows32"; }
   if constexpr (MODE != B128Mode::grouped)
-    if (pick(a, MODE) == B128Kernel::t128x128) { launch_tile<WROWS, MODE, 2, 4, 4, 2, 4>(a, stream); return "b128:tile128x128"; }
-  launch_tile<WROWS, MODE, 4, 2, 4, 8, 2>(a, stream);
+    if (k == K::t128x128) { launch_tile<WROWS, MODE, K::t128x128, 2, 4, 4, 2, 4>(a, stream); return "b128:tile128x128"; }
+  launch_tile<WROWS, MODE, K::t256x256, 4, 2, 4, 8, 2>(a, stream);
   return "b128:tile256x256";
-}
-
-// A launch holds fewer than 2^32 threads (at most 512 a workgroup).
-bool b128_fits(const B128Args& a, B128Mode mode) {
-  constexpr int64_t MOST = int64_t(1) << 23;
-  switch (pick(a, mode)) {
-    case B128Kernel::t16x64: return tile_groups(a, mode, 16, 64) < MOST;
-    case B128Kernel::t64x64: return tile_groups(a, mode, 64, 64) < MOST;
-    case B128Kernel::t64x128: return tile_groups(a, mode, 64, 128) < MOST;
-    case B128Kernel::t128x256: return tile_groups(a, mode, 128, 256) < MOST;
-    case B128Kernel::t256x256: return tile_groups(a, mode, 256, 256) < MOST;
-    default: return true;                                             // few
-  }
 }
 
 // Results of more than 64 MB go past the caches: nothing finds them there, and what they would push out is read again

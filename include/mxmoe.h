@@ -524,9 +524,11 @@ mx_status fp8_quantize128_t(const void* src, int src_dtype, int64_t src_ld, int6
  * result's norm in all); the blocks are added in order in fp32, one fma each,
  * the same for every M and kernel.  The gradient of a is the product of dy
  * with the transposed codes and scales of w (tiles of 128 x 128 are the same
- * both ways).  Any M >= 0, N >= 1, K % 16 == 0, 16 <= K <= 2^23; results of
- * more tiles than one launch holds (about 2^32 to 2^39 results, by the tile)
- * return MX_EUNSUPPORTED.  a, w 16-byte aligned, scales 4-byte, y its type's.
+ * both ways).  Any M >= 0, N >= 1, K % 16 == 0, 16 <= K <= 2^23.  A launch
+ * holds fewer than 2^23 tiles of 256 x 256 results, the last ones of a row or
+ * column (and of an expert's rows) counted whole, and up to 16 rows by fewer
+ * than 2^31 - 512 columns; larger calls return MX_EUNSUPPORTED.  a, w 16-byte
+ * aligned, scales 4-byte, y its type's.
  */
 mx_status fp8_block128_gemm(const uint8_t* a, const float* a_sc, const uint8_t* w, const float* w_sc, int w_rows, int M, int N,
                             int K, void* y, int y_dtype, void* stream);
