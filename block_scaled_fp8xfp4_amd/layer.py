@@ -193,13 +193,21 @@ def quantize128_t(v, offsets=None, stream=None):
     return q, sc
 
 
+def _whole16(v):
+    """v [..., n] with zeros up to whole 16s, which a cast along n takes: zero codes add nothing to a sum over n."""
+    n = -v.shape[-1] % 16
+    return torch.nn.functional.pad(v, (0, n)) if n else v
+
+
 class FP8Linear128:
-    """A dense projection with FP8 weights [N, K] + scales [ceil(N / 128), ceil(K / 128)] (fp8_block128_gemm), and its
-    gradients.  Rows come and go in bf16 or fp32 and are cast here; train: the transposed weights are laid out too."""
+    """A dense projection with FP8 weights [N, K] + scales [ceil(N / 128), ceil(K / 128)] (fp8_block128_gemm), K % 16 == 0,
+    any N, and its gradients.  Rows come and go in bf16 or fp32 and are cast here; input_grad copies dy first where N is
+    not a multiple of 16.  train: the transposed weights are laid out too, once, on the current stream (weights that
+    change take a new object; a call on another stream comes after that stream's work)."""
 
     def __init__(self, w, w_sc, train=False):
         self.w, self.w_sc = w, w_sc
-        self.w_t, self.w_t_sc = (w.t().contiguous(), w_sc.t().contiguous()) if train else (None, None)
+        self.w_t, self.w_t_sc = (_whole16(w.t()).contiguous(), w_sc.t().contiguous()) if train else (None, None)
 
     def _product(self, x, w, w_sc, dtype, stream):
         with _under(stream):
@@ -214,7 +222,10 @@ class FP8Linear128:
     def input_grad(self, dy, dtype=torch.bfloat16, stream=None):
         if self.w_t is None:
             raise ValueError("FP8Linear128: made without train")
-        return self._product(dy, self.w_t, self.w_t_sc, dtype, stream)
+        if dy.shape[-1] != self.w.shape[0]:
+            raise ValueError(f"FP8Linear128: dy has {dy.shape[-1]} columns, the weights {self.w.shape[0]} rows")
+        with _under(stream):
+            return self._product(_whole16(dy), self.w_t, self.w_t_sc, dtype, stream)
 
     def weight_grad(self, dy, x, dtype=torch.float32, stream=None):
         """dy^T x [N, K], both cast along their rows."""
@@ -230,11 +241,12 @@ class FP8Linear128:
 
 class ExpertLinear128:
     """The experts' projections [E, N, K] + scales [E, ceil(N / 128), ceil(K / 128)] of rows sorted by expert (offsets: a
-    Route's), and their gradients; rows in bf16 or fp32, cast here.  Rows behind offsets[E] are undefined in what comes out."""
+    Route's), and their gradients; rows in bf16 or fp32, cast here.  Rows behind offsets[E] are undefined in what comes out.
+    Sizes and train as FP8Linear128."""
 
     def __init__(self, w, w_sc, train=False):
         self.w, self.w_sc = w, w_sc
-        self.w_t, self.w_t_sc = (w.transpose(1, 2).contiguous(), w_sc.transpose(1, 2).contiguous()) if train else (None, None)
+        self.w_t, self.w_t_sc = (_whole16(w.transpose(1, 2)).contiguous(), w_sc.transpose(1, 2).contiguous()) if train else (None, None)
 
     def _product(self, x, w, w_sc, offsets, dtype, stream):
         with _under(stream):
@@ -249,7 +261,10 @@ class ExpertLinear128:
     def input_grad(self, dy, offsets, dtype=torch.bfloat16, stream=None):
         if self.w_t is None:
             raise ValueError("ExpertLinear128: made without train")
-        return self._product(dy, self.w_t, self.w_t_sc, offsets, dtype, stream)
+        if dy.shape[-1] != self.w.shape[1]:
+            raise ValueError(f"ExpertLinear128: dy has {dy.shape[-1]} columns, the weights {self.w.shape[1]} rows")
+        with _under(stream):
+            return self._product(_whole16(dy), self.w_t, self.w_t_sc, offsets, dtype, stream)
 
     def weight_grad(self, dy, x, offsets, dtype=torch.float32, stream=None):
         with _under(stream):

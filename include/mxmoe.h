@@ -524,7 +524,8 @@ mx_status fp8_quantize128_t(const void* src, int src_dtype, int64_t src_ld, int6
  * result's norm in all); the blocks are added in order in fp32, one fma each,
  * the same for every M and kernel.  The gradient of a is the product of dy
  * with the transposed codes and scales of w (tiles of 128 x 128 are the same
- * both ways).  Any M >= 0, N >= 1, K % 16 == 0, 16 <= K <= 2^23.  A launch
+ * both ways; where N % 16 != 0 both sides with zero codes up to whole 16s).
+ * Any M >= 0, N >= 1, K % 16 == 0, 16 <= K <= 2^23.  A launch
  * holds fewer than 2^23 tiles of 256 x 256 results, the last ones of a row or
  * column (and of an expert's rows) counted whole, and up to 16 rows by fewer
  * than 2^31 - 512 columns; larger calls return MX_EUNSUPPORTED.  a, w 16-byte
