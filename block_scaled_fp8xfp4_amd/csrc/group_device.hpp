@@ -21,7 +21,7 @@ __device__ __forceinline__ uint32_t lanes_upto(uint32_t v) {
   return v;
 }
 
-struct GroupTile { int e, tile, first, row0, rows; };    // e < 0: no such tile
+struct GroupTile { int e, tile, row0, rows; };    // the expert, which of its tiles, its rows; e < 0: no such tile
 
 // PER experts a lane (64 PER >= E).
 template <int PER>
@@ -39,23 +39,22 @@ __device__ __forceinline__ GroupTile find_tile_of(const int32_t* offsets, int E,
   }
   const uint32_t upto = lanes_upto(sum);           // tiles up to and with this lane's
   const uint64_t past = __ballot(upto > t);
-  if (past == 0) return GroupTile{-1, 0, 0, 0, 0};
+  if (past == 0) return GroupTile{-1, 0, 0, 0};
   uint32_t first = upto - sum;
-  GroupTile g{-1, 0, 0, 0, 0};
+  GroupTile g{-1, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (g.e < 0 && t < first + n[i]) g = GroupTile{lane * PER + i, (int)(t - first), (int)first, o[i], o[i + 1] - o[i]};
+    if (g.e < 0 && t < first + n[i]) g = GroupTile{lane * PER + i, (int)(t - first), o[i], o[i + 1] - o[i]};
     first += n[i];
   }
   const int src = __builtin_ctzll(past);
   g.e = __builtin_amdgcn_readlane(g.e, src);
   g.tile = __builtin_amdgcn_readlane(g.tile, src);
-  g.first = __builtin_amdgcn_readlane(g.first, src);
   g.row0 = __builtin_amdgcn_readlane(g.row0, src);
   g.rows = __builtin_amdgcn_readlane(g.rows, src);
   return g;
 }
-// The expert of tile t when each expert's rows are cut into tiles of `unit`; first is the expert's first tile.
+// The expert of tile t when each expert's rows are cut into tiles of `unit`.
 // All 64 lanes of the wavefront take part.
 __device__ __forceinline__ GroupTile find_tile(const int32_t* offsets, int E, int64_t R, int unit, uint32_t t) {
   return E <= 256 ? find_tile_of<4>(offsets, E, R, unit, t) : find_tile_of<16>(offsets, E, R, unit, t);
