@@ -11,6 +11,11 @@
 // blocks in order.  Every kernel keeps to it, so a row's bits do not depend on
 // M, on the other rows or on the kernel.  A block that K ends in is filled up
 // with zeros.
+//
+// Precision: that step cuts E4M3 products below the largest of their eight
+// (3.3e-5 of the result's norm on normal data; fp32 products of the decoded
+// values 1e-7).  In bf16 it decides the rounding of one result in a hundred: two
+// such results are 2.5e-4 of the norm apart, either 1.7e-3 from the exact one.
 #include "b128_launch.hpp"
 #include "group_device.hpp"
 #include "lds_device.hpp"
@@ -519,7 +524,17 @@ static int64_t tile_groups(const B128Args& a, B128Mode mode, int bm, int bn) {
 //   8 experts' 4096 x 4096, rows each: 8 64 x 128 21.0, 64 x 64 21.1, 128 x 256 22.4; 64 128 x 256 30.1, 64 x 128 40.5; 128
 //                           128 x 256 37.7, 256 x 256 47.5; 256 256 x 256 60, 128 x 256 71; 1024 192, 208
 //   64 experts' 1152 x 2048, rows each: 128 128 x 256 44, 256 x 256 51; 256 256 x 256 73, 128 x 256 79; 512 128, 138
-//   gradients of 8 experts' 512 x 1024, 1024 tokens each: 128 x 128 12.8, 256 x 256 22.8
+//   gradients, 1024 tokens each, by workgroups of 128 x 128: 8 experts' 512 x 1024 (256) 128 x 128 13.1, 256 x 256 22.7; 640 x 1024
+//                           (320) 23.4, 23.4; 12 of 512 x 1024 (384) 24.7, 25.8; 16 (512) 26.2, 26.8; 32 (1024) 48.8, 30.1
+//   256 experts, 64 x 64 and 64 x 128, 4 and 16 rows each: 1152 x 2048 104, 101 and 112, 108; x 2304 116, 114 and 126, 124; x 3328
+//                           163, 162 and 178, 174; x 4096 212, 228 and 223, 237; x 5120 246, 247 and 275, 266; 512 x 2304 58.4, 53.9;
+//                           64 experts of 3 rows x 2048 31.6, 32.7; x 2816 42.5, 44.0; x 4096 65.7, 73.3: the border of K lies where
+//                           neither is ahead by more than 3 % (8 at 512 columns)
+//                           12 rows each, K = 2048: 64 columns 10.9, 12.4; 128 16.6, 17.1; 256 29.6, 29.0
+//   scales by rows on both sides, K = 4096, 128 x 256 and 256 x 256: 2048 x 4096 49.6, 63.9; 2560 76.2, 65.0; 5120 117.7, 124.5; 6144
+//                           128.6, 128.0; 8192 183.6, 146.4
+//   256 experts' 1152 x 4096 chosen as 1 / rank: 8192 x 8 rows 256 x 256 501, 128 x 256 500; 2048 x 8 128 x 256 291, 64 x 128 299,
+//                           256 x 256 333; 512 x 8 64 x 64 227, 64 x 128 237
 //   256 experts' 4096 x 576, 48 rows of all: 64 x 128 95, 64 x 64 126, rows16 187 (few blocks of K: what a workgroup begins
 //                           and ends with counts)
 enum class B128Kernel { rows16, rows32, t16x64, t64x64, t64x128, t128x128, t128x256, t256x256 };
