@@ -14,8 +14,9 @@
 //
 // Precision: that step cuts E4M3 products below the largest of their eight
 // (3.3e-5 of the result's norm on normal data; fp32 products of the decoded
-// values 1e-7).  In bf16 it decides the rounding of one result in a hundred: two
-// such results are 2.5e-4 of the norm apart, either 1.7e-3 from the exact one.
+// values 1e-7).  In bf16 it decides the rounding of 1.4 % of the results: with it
+// and without they are 2.6e-4 of the norm apart, and 1.6559e-3 and 1.6558e-3 from
+// the exact ones (8192 x 4096 x 4096).
 #include "b128_launch.hpp"
 #include "group_device.hpp"
 #include "lds_device.hpp"
@@ -329,8 +330,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void b128_tile_kernel(B128Args A) 
       v4f P[2][TM];                               // products on their way, and those of the column before
       // OUTER: the matrix cores multiply the scales too, a column's 16 with the 64 of the rows, in fp32 as the vector unit
       // does, bit for bit; a lane holds one of each.  It halves the vector instructions beside the products where both operands
-      // have scales by rows: 8192 x 4096 x 4096 170 us from 183, 4096 x 2048 x 8192 91 from 95, 64 experts' gradients 1152 x
-      // 2048 of 4096 x 8 rows 175 from 178
+      // have scales by rows: 8192 x 4096 x 4096 again and again 170 us from 183 (with pauses 148), 4096 x 2048 x 8192 91 from 95,
+      // 64 experts' gradients 1152 x 2048 of 4096 x 8 rows 175 from 178
       constexpr bool OUTER = WROWS && TM == 4;
       float f[TM], fn[TM], wn_ = 0.f;             // scales of the rows (times the tile's): the stage's, the next one's
       v4f sn{};                                   // WROWS: scales of the column's weight rows

@@ -81,7 +81,7 @@ __device__ __forceinline__ float element(const void* p, bool bf16, int64_t i) {
 // product); about one wavefront in 60 holds a code that does, and evaluates it in double.  Blocks with several such largest
 // values, or out of the range in which near values are good, take the double form as a whole.
 //
-// What bounds it is instructions (8192 x 4096 bf16 47 us, 3.6 TB/s; the loads and stores alone 37) and, for few rows, the
+// What bounds it is instructions (8192 x 4096 bf16 42 to 47 us, 4.0 to 3.6 TB/s; the loads and stores alone 37) and, for few rows, the
 // longest way through them (48 x 2048 3.3 us): the largest value is found with its place in its three lowest bits (2^-20
 // of it at most) and read again; a near value never reaches past 464, where a code would not be 448, so none is clamped;
 // and codes are mended one by one (whole blocks in double instead: 48 x 2048 4.3 us, 999 x 1376 fp32 6.9 from 5.9).  Several
